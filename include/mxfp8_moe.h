@@ -27,8 +27,9 @@
  *    failure the call returns a non-zero mxfp8_status, records a message that
  *    mxfp8_last_error() returns on the calling thread, and leaves every output
  *    untouched.  No C++ exception crosses this interface.
- *  - Outputs are fully overwritten, except where moe_bwd_mxfp8's `accumulate`
- *    flag asks for the gradients to be added into them.
+ *  - Outputs are fully overwritten, except where the `accumulate` flag of
+ *    moe_bwd_mxfp8 or moe_balance_loss_bwd asks for the gradients to be added
+ *    into them.
  *
  * MXFP8 (P1: "32-element quantization group"): a group of 32 consecutive
  * elements along the quantised axis shares one E8M0 scale byte S (value
@@ -449,6 +450,7 @@ int moe_bwd_mxfp8_stage(const moe_bwd_mxfp8_args* args, void* workspace, size_t 
  *                read at the selected experts: exactly one of the two.
  *   renorm       0 or 1; non-zero only with MXFP8_ROUTER_TOPK_OVER_SOFTMAX.
  *   dlogits      [T,E] fp32 output, every entry written.
+ * A row whose entries are all outside [0,E) gets zeros, whatever its logits hold.
  * Arithmetic is fp32 (exp through the device math library).
  * Errors: INVALID_ARG for an unknown mode, a shape outside the bounds above,
  * renorm with another mode, both or neither of dscores/daff, a NULL pointer
@@ -463,6 +465,147 @@ typedef enum {
 int moe_router_bwd(int mode, int64_t T, int64_t E, int64_t K, const int32_t* topk_idx, const float* topk_scores,
                    const float* logits, const float* dscores, const uint16_t* daff, int renorm, float* dlogits,
                    void* stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_router_fwd -- the router forward: each token's K largest logits, their
+ * scores (the modes of moe_router_bwd, whose topk_idx, topk_scores and logits
+ * these are) and the scores in the masked layout of expert_affinities_masked.
+ *   Selections go by descending logit, equal logits (-0 and +0 among them) by
+ *   ascending expert.  An expert whose logit is -inf or NaN is closed: it is
+ *   never selected.  A token whose mask byte is 0 selects nothing, and its
+ *   logits are not read into any output.  Where fewer than K experts are open the
+ *   remaining selections hold id -1 (a dropped selection for moe_build_blocks
+ *   and moe_router_bwd) and score 0.
+ *   Scores: MXFP8_ROUTER_SOFTMAX_OVER_TOPK  softmax over the selected logits;
+ *     MXFP8_ROUTER_TOPK_OVER_SOFTMAX  the softmax over all E logits at the
+ *     selected ones, divided by their sum with renorm; MXFP8_ROUTER_TOPK  the
+ *     logits themselves.  A logit of +inf, or a NaN where the softmax is over
+ *     all E logits, makes its token's scores NaN.
+ * Arguments:
+ *   T, E, K      tokens, experts, selections; 1 <= K <= min(E, 32), E <= 4096.
+ *   logits       [T,E] fp32 or bf16 (logits_type); arithmetic is fp32.
+ *   token_mask   [T] bytes, or NULL: every token takes part.
+ *   renorm       0 or 1; 1 only with MXFP8_ROUTER_TOPK_OVER_SOFTMAX.
+ *   topk_idx     [T,K] int32, topk_scores [T,K] fp32: written.
+ *   affinities   [T,E] fp32, or NULL: the score at each selected expert, 0
+ *                elsewhere; every entry written.
+ * T == 0 is not an error: nothing is enqueued.
+ * Errors: INVALID_ARG for an unknown mode or type, a shape outside the bounds,
+ * renorm with another mode or outside {0,1}, a NULL pointer, or a tensor
+ * (token_mask excepted) not 16-byte aligned; UNSUPPORTED for E above
+ * MXFP8_ROUTER_MAX_EXPERTS or T above 2^31 - 1; HIP if the launch fails. */
+typedef enum { MXFP8_TYPE_F32 = 0, MXFP8_TYPE_BF16 = 1 } mxfp8_type;
+#define MXFP8_ROUTER_MAX_EXPERTS 4096
+int moe_router_fwd(int mode, int64_t T, int64_t E, int64_t K, const void* logits, int logits_type,
+                   const uint8_t* token_mask, int renorm, int32_t* topk_idx, float* topk_scores,
+                   float* affinities, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_balance_loss / moe_balance_loss_bwd -- the router's auxiliary losses.
+ * p_t = softmax over all E logits of token t, lse_t their log-sum-exp.  Token t
+ * takes part if it lies in a sequence, its mask byte is not 0 and one of its
+ * logits is above -inf.  With n_s the tokens of sequence s that take part, S'
+ * the sequences that have any, n the tokens in all and c_se how often those
+ * tokens of s select expert e (ids outside [0,E) count nowhere):
+ *   loss[0] = (balance_coef / S') sum_s E sum_e c_se / (K n_s) * (sum_{t in s} p_te) / n_s
+ *   loss[1] = (z_coef / n) sum_t lse_t^2
+ * (0 where no token takes part).  Evenly spread routing gives loss[0] =
+ * balance_coef.  The counts are constants of the gradient:
+ *   dlogits[t,e] = dloss[0] p_te (w_se - sum_j w_sj p_tj) + dloss[1] (2 z_coef / n) lse_t p_te,
+ *   w_se = balance_coef E c_se / (S' K n_s^2)
+ * Arguments (moe_balance_args):
+ *   T, E, K, S     tokens, experts, selections a token, sequences;
+ *                  1 <= K <= min(E, 32), S >= 1.
+ *   logits         [T,E] fp32 or bf16 (logits_type); arithmetic is fp32, the
+ *                  losses' last sums fp64.
+ *   topk_idx       [T,K] int32 (forward only).
+ *   token_mask     [T] bytes, or NULL.
+ *   seq_starts     [S+1] int32 in device memory: sequence s is the tokens
+ *                  [seq_starts[s], seq_starts[s+1]); entries must not
+ *                  decrease (values are kept in [0,T]; entries that do
+ *                  decrease give unspecified losses and gradients, no access out of
+ *                  range).  A sequence may be empty; tokens before the first
+ *                  or behind the last one take no part.  NULL: one sequence of
+ *                  all T tokens (S must be 1).
+ *   loss           [2] fp32.
+ *   counts         [S,E] int32: c_se.
+ *   num_tokens     [S+2] int32: n_s for each s, then S', then n.
+ *   The forward writes all of loss, counts and num_tokens; the backward reads
+ *   counts and num_tokens as the forward left them (loss is not read).
+ *   dloss          [2] fp32 in device memory, or NULL: both 1.
+ *   dlogits        [T,E] fp32.  accumulate 0: every entry written, tokens
+ *                  that take no part get 0; 1: the gradient is added to what
+ *                  dlogits holds (moe_router_bwd's output, say), and rows that
+ *                  take no part are left as they are.
+ * Workspace (forward): moe_balance_loss_workspace_size(T, E, S) bytes (0 on
+ * invalid sizes), 256-byte aligned; nothing in it outlives the call.  Sums run
+ * in an order that depends on the sizes alone: the results are the same bits
+ * on every run.
+ * T == 0 is not an error: the forward writes zeros.
+ * Errors: INVALID_ARG for an unknown type, a shape outside the bounds, S != 1 without
+ * seq_starts, a coefficient that is not finite, accumulate outside {0,1}, a
+ * NULL pointer, or a tensor (token_mask, seq_starts, dloss, loss: 4-byte, the
+ * mask any) not 16-byte aligned; UNSUPPORTED for E above MXFP8_ROUTER_MAX_EXPERTS,
+ * T * K or S * E above 2^31 - 1; WORKSPACE; HIP if a launch fails. */
+typedef struct {
+  int64_t T, E, K, S;
+  const void* logits;
+  int logits_type;
+  const int32_t* topk_idx;
+  const uint8_t* token_mask;
+  const int32_t* seq_starts;
+  float balance_coef, z_coef;
+  float* loss;
+  int32_t* counts;
+  int32_t* num_tokens;
+  const float* dloss;
+  float* dlogits;
+  int accumulate;
+} moe_balance_args;
+size_t moe_balance_loss_workspace_size(int64_t T, int64_t E, int64_t S);
+int moe_balance_loss(const moe_balance_args* args, void* workspace, size_t workspace_bytes, void* stream);
+int moe_balance_loss_bwd(const moe_balance_args* args, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * mxfp8_gated_act_fwd / mxfp8_gated_act_bwd -- the gated activation of an FFN
+ * whose gate/up checkpoint is kept in MXFP8 (2 + 2/32 bytes a gate/up pair
+ * instead of 4).
+ *   gate_up   [rows, 2, cols] bf16: row r's gate g = [r,0,c], up u = [r,1,c].
+ *   forward:  inter [rows, cols] bf16 = act(g) * u, from the bf16 values,
+ *             computed in fp32 and rounded once; codes [rows, 2, cols] and
+ *             scales [rows, 2, cols/32]: g and u quantised in groups of 32
+ *             along cols (the rule above).
+ *   backward: with g, u the values of codes and scales and d = dinter
+ *             [rows, cols] bf16:  dgate_up[r,0,c] = d u act'(g),
+ *             dgate_up[r,1,c] = d act(g), each rounded once to bf16.
+ * activation: MXFP8_ACT_SWIGLU or MXFP8_ACT_GEGLU (as in moe_bwd_mxfp8).
+ * A dense FFN's gate/up product is rows = tokens, cols = I.  The MoE layer's
+ * gate_up_proj_act_checkpoint_T [N,2,I,B] is rows = N, cols = I * B, whose
+ * groups of 32 are then 32 consecutive slots, and the codes and scales are
+ * what moe_bwd_mxfp8 takes as gate_up_checkpoint_codes / _scales.
+ *   token_position_to_id  [rows * period] int32, or NULL.  Element (r, c) is
+ *             slot c % period of block r; slots whose id is outside [0,T) are
+ *             padding: their elements count as zeros (whatever they hold), so
+ *             inter, the codes and dgate_up are 0 there, and they do not reach
+ *             a scale.  period % 32 == 0, cols % period == 0.
+ * Non-finite values: a group of g or u holding one has unspecified codes and
+ * scale; inter and dgate_up follow the formulas element by element.  A scale
+ * byte of 255 gives unspecified gradients in its group.
+ * rows == 0 is not an error: nothing is enqueued.
+ * Errors: INVALID_ARG for a negative size, cols % 32 != 0, a period that does
+ * not fit, a bad activation or fmt, T < 0, a NULL pointer, or a tensor not
+ * 16-byte aligned (scales: any alignment); UNSUPPORTED for rows * cols above 2^39; HIP if
+ * the launch fails. */
+typedef struct {
+  int64_t rows, cols;
+  int activation, fmt;                  /* fmt: MXFP8_E4M3 or MXFP8_E5M2          */
+  const int32_t* token_position_to_id;
+  int64_t period, T;                    /* read with token_position_to_id only    */
+} mxfp8_gated_act_args;
+int mxfp8_gated_act_fwd(const mxfp8_gated_act_args* args, const uint16_t* gate_up, uint16_t* inter,
+                        uint8_t* codes, uint8_t* scales, void* stream);
+int mxfp8_gated_act_bwd(const mxfp8_gated_act_args* args, const uint16_t* dinter, const uint8_t* codes,
+                        const uint8_t* scales, uint16_t* dgate_up, void* stream);
 
 #ifdef __cplusplus
 }

@@ -75,6 +75,18 @@ class MoeWorkspaceLayout(C.Structure):
     _fields_ = [(n, C.c_size_t) for n in LAYOUT_FIELDS]
 
 
+class BalanceArgs(C.Structure):
+    _fields_ = [("T", _i64), ("E", _i64), ("K", _i64), ("S", _i64), ("logits", _p), ("logits_type", C.c_int),
+                ("topk_idx", _p), ("token_mask", _p), ("seq_starts", _p), ("balance_coef", C.c_float),
+                ("z_coef", C.c_float), ("loss", _p), ("counts", _p), ("num_tokens", _p), ("dloss", _p),
+                ("dlogits", _p), ("accumulate", C.c_int)]
+
+
+class GatedActArgs(C.Structure):
+    _fields_ = [("rows", _i64), ("cols", _i64), ("activation", C.c_int), ("fmt", C.c_int),
+                ("token_position_to_id", _p), ("period", _i64), ("T", _i64)]
+
+
 def _declare(L):
     L.mxfp8_last_error.restype = C.c_char_p
     L.mxfp8_version.restype = C.c_char_p
@@ -97,6 +109,12 @@ def _declare(L):
         ("matmul_mxfp8_bwd_stage", C.c_int, [_p, _p, _p, _i64, _i64, _i64, C.c_int, C.c_int, C.c_int, _p, _p,
                                              _p, C.c_size_t, C.c_int, _p]),
         ("moe_router_bwd", C.c_int, [C.c_int, _i64, _i64, _i64, _p, _p, _p, _p, _p, C.c_int, _p, _p]),
+        ("moe_router_fwd", C.c_int, [C.c_int, _i64, _i64, _i64, _p, C.c_int, _p, C.c_int, _p, _p, _p, _p]),
+        ("moe_balance_loss_workspace_size", C.c_size_t, [_i64, _i64, _i64]),
+        ("moe_balance_loss", C.c_int, [C.POINTER(BalanceArgs), _p, C.c_size_t, _p]),
+        ("moe_balance_loss_bwd", C.c_int, [C.POINTER(BalanceArgs), _p]),
+        ("mxfp8_gated_act_fwd", C.c_int, [C.POINTER(GatedActArgs), _p, _p, _p, _p, _p]),
+        ("mxfp8_gated_act_bwd", C.c_int, [C.POINTER(GatedActArgs), _p, _p, _p, _p, _p]),
     ):
         if hasattr(L, name):
             f = getattr(L, name)
@@ -408,4 +426,181 @@ def moe_router_bwd(mode: int, topk_idx: torch.Tensor, *, dscores: Optional[torch
                                 _dev(dscores, torch.float32, "dscores"), _dev(daff, torch.bfloat16, "daff"),
                                 1 if renorm else 0, _dev(out, torch.float32, "out"), _stream(topk_idx)),
            "moe_router_bwd")
+    return out
+
+
+# ----------------------------------------------------------------------------- router forward, auxiliary losses
+def _tensor(t: Optional[torch.Tensor], dtype, shape, device, name):
+    """The address of an argument that must be a contiguous `dtype` tensor of `shape` on `device` (None: NULL)."""
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
+    return _dev(t, dtype, name)
+
+
+def _mask(t: Optional[torch.Tensor], T, device):
+    if t is not None and t.dtype == torch.bool:
+        t = t.view(torch.uint8)
+    return _tensor(t, torch.uint8, (T,), device, "token_mask")
+
+
+def _logits_type(logits: torch.Tensor, name):
+    if logits.dim() != 2:
+        raise ValueError(f"{name}: logits must be [T, E]")
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"{name}: logits must be float32 or bfloat16, got {logits.dtype}")
+    return 0 if logits.dtype == torch.float32 else 1
+
+
+def _call(device, name, *args):
+    """One library call on `device`'s current stream (the null stream stands for the current device's, so
+    that device is made current)."""
+    f = getattr(lib(), name)
+    if torch.cuda.current_device() == device.index:
+        rc = f(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = f(*args, torch.cuda.current_stream(device).cuda_stream)
+    _check(rc, name)
+
+
+def moe_router_fwd(mode: int, logits: torch.Tensor, K: int, renorm: bool = False,
+                   token_mask: Optional[torch.Tensor] = None, out=None):
+    """Top-k routing (include/mxfp8_moe.h: moe_router_fwd): logits [T, E] fp32 or bf16 ->
+    (topk_idx [T, K] int32, topk_scores [T, K] fp32, affinities [T*E] fp32).
+
+    The ids feed moe_build_blocks and moe_router_bwd, the affinities MoeBwd.  token_mask [T] bool or uint8:
+    a token with 0 selects nothing (ids -1, scores 0), as do selections that find no expert above -inf.
+    out: optional (topk_idx, topk_scores, affinities) to write into."""
+    typ = _logits_type(logits, "moe_router_fwd")
+    T, E = logits.shape
+    dev = logits.device
+    x = _dev(logits, logits.dtype, "logits")
+    m = _mask(token_mask, T, dev)
+    if out is None:
+        out = (torch.empty((T, K), dtype=torch.int32, device=dev), torch.empty((T, K), dtype=torch.float32, device=dev),
+               torch.empty(T * E, dtype=torch.float32, device=dev))
+    idx, scores, aff = out
+    _call(dev, "moe_router_fwd", mode, T, E, K, x, typ, m, 1 if renorm else 0,
+          _tensor(idx, torch.int32, (T, K), dev, "topk_idx"),
+          _tensor(scores, torch.float32, (T, K), dev, "topk_scores"),
+          _tensor(aff, torch.float32, (T * E,), dev, "affinities"))
+    return out
+
+
+def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, balance_coef: float, z_coef: float = 0.0,
+                     token_mask: Optional[torch.Tensor] = None, seq_starts: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, out=None):
+    """The router's load-balance and z losses with the per-expert counts (include/mxfp8_moe.h: moe_balance_loss).
+
+    logits [T, E] fp32 or bf16, topk_idx [T, K] int32, token_mask [T] bool or uint8, seq_starts [S+1] int32 ->
+    (loss [2] fp32, counts [S, E] int32, num_tokens [S+2] int32); S = 1 without seq_starts.  counts and
+    num_tokens are what moe_balance_loss_bwd needs."""
+    typ = _logits_type(logits, "moe_balance_loss")
+    T, E = logits.shape
+    dev = logits.device
+    x = _dev(logits, logits.dtype, "logits")
+    if topk_idx.dim() != 2:
+        raise ValueError("moe_balance_loss: topk_idx must be [T, K]")
+    K = topk_idx.shape[1]
+    S = 1 if seq_starts is None else seq_starts.numel() - 1
+    if out is None:
+        out = (torch.empty(2, dtype=torch.float32, device=dev),
+               torch.empty((max(S, 0), E), dtype=torch.int32, device=dev),
+               torch.empty(max(S, 0) + 2, dtype=torch.int32, device=dev))
+    loss, counts, num = out
+    if workspace is None:
+        workspace = torch.empty(lib().moe_balance_loss_workspace_size(T, E, S), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev:
+        raise ValueError(f"workspace: expected a tensor on {dev}, got {workspace.device}")
+    a = BalanceArgs(T, E, K, S, x, typ, _tensor(topk_idx, torch.int32, (T, K), dev, "topk_idx"),
+                    _mask(token_mask, T, dev), _tensor(seq_starts, torch.int32, (S + 1,), dev, "seq_starts"),
+                    balance_coef, z_coef, _tensor(loss, torch.float32, (2,), dev, "loss"),
+                    _tensor(counts, torch.int32, (S, E), dev, "counts"),
+                    _tensor(num, torch.int32, (S + 2,), dev, "num_tokens"), None, None, 0)
+    _call(dev, "moe_balance_loss", C.byref(a), _dev(workspace, torch.uint8, "workspace"), workspace.numel())
+    return out
+
+
+def moe_balance_loss_bwd(logits: torch.Tensor, counts: torch.Tensor, num_tokens: torch.Tensor, K: int,
+                         balance_coef: float, z_coef: float = 0.0, dloss: Optional[torch.Tensor] = None,
+                         token_mask: Optional[torch.Tensor] = None, seq_starts: Optional[torch.Tensor] = None,
+                         out: Optional[torch.Tensor] = None, accumulate: bool = False) -> torch.Tensor:
+    """Gradient of the auxiliary losses on the logits, [T, E] fp32 (include/mxfp8_moe.h: moe_balance_loss_bwd).
+
+    counts and num_tokens come from moe_balance_loss with the same logits, mask, sequences and coefficients;
+    dloss [2] fp32 (None: ones).  accumulate=True adds into `out`, moe_router_bwd's result for instance."""
+    typ = _logits_type(logits, "moe_balance_loss_bwd")
+    T, E = logits.shape
+    dev = logits.device
+    x = _dev(logits, logits.dtype, "logits")
+    S = 1 if seq_starts is None else seq_starts.numel() - 1
+    if out is None:
+        if accumulate:
+            raise ValueError("moe_balance_loss_bwd: accumulate needs out")
+        out = torch.empty((T, E), dtype=torch.float32, device=dev)
+    a = BalanceArgs(T, E, K, S, x, typ, None, _mask(token_mask, T, dev),
+                    _tensor(seq_starts, torch.int32, (S + 1,), dev, "seq_starts"), balance_coef, z_coef, None,
+                    _tensor(counts, torch.int32, (S, E), dev, "counts"),
+                    _tensor(num_tokens, torch.int32, (S + 2,), dev, "num_tokens"),
+                    _tensor(dloss, torch.float32, (2,), dev, "dloss"),
+                    _tensor(out, torch.float32, (T, E), dev, "out"), int(bool(accumulate)))
+    _call(dev, "moe_balance_loss_bwd", C.byref(a))
+    return out
+
+
+# ----------------------------------------------------------------------------- gated activation, MXFP8 checkpoint
+def _gated_act_args(shape, activation, fmt, token_position_to_id, T, device, name):
+    if len(shape) < 3 or shape[1] != 2:
+        raise ValueError(f"{name}: expected a gate/up pair [rows, 2, ..., n], got {tuple(shape)}")
+    rows, period = shape[0], shape[-1]
+    if period % 32:
+        raise ValueError(f"{name}: the last dimension must be a multiple of 32 (got {period})")
+    cols = 1
+    for n in shape[2:]:
+        cols *= n
+    return GatedActArgs(rows, cols, activation, fmt,
+                        _tensor(token_position_to_id, torch.int32, (rows * period,), device, "token_position_to_id"),
+                        period, T)
+
+
+def mxfp8_gated_act_fwd(gate_up: torch.Tensor, activation: int = ACT_SWIGLU, fmt: int = E4M3,
+                        token_position_to_id: Optional[torch.Tensor] = None, T: int = 0, out=None):
+    """Gated activation with its checkpoint in MXFP8 (include/mxfp8_moe.h: mxfp8_gated_act_fwd).
+
+    gate_up [rows, 2, ..., n] bf16 -- a dense FFN's [M, 2, I] or the MoE checkpoint layout [N, 2, I, B] -- ->
+    (inter [rows, ..., n] bf16, codes uint8 of gate_up's shape, scales uint8 [rows, 2, ..., n/32]), groups of 32
+    along the last axis.  token_position_to_id [rows*n] int32 with T tokens: slots with another id are padding
+    and count as zeros."""
+    shape = tuple(gate_up.shape)
+    dev = gate_up.device
+    x = _dev(gate_up, torch.bfloat16, "gate_up")
+    a = _gated_act_args(shape, activation, fmt, token_position_to_id, T, dev, "mxfp8_gated_act_fwd")
+    ishape, sshape = shape[:1] + shape[2:], shape[:-1] + (shape[-1] // 32,)
+    if out is None:
+        out = (torch.empty(ishape, dtype=torch.bfloat16, device=dev), torch.empty(shape, dtype=torch.uint8, device=dev),
+               torch.empty(sshape, dtype=torch.uint8, device=dev))
+    inter, codes, scales = out
+    _call(dev, "mxfp8_gated_act_fwd", C.byref(a), x, _tensor(inter, torch.bfloat16, ishape, dev, "inter"),
+          _tensor(codes, torch.uint8, shape, dev, "codes"), _tensor(scales, torch.uint8, sshape, dev, "scales"))
+    return out
+
+
+def mxfp8_gated_act_bwd(dinter: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, activation: int = ACT_SWIGLU,
+                        fmt: int = E4M3, token_position_to_id: Optional[torch.Tensor] = None, T: int = 0,
+                        out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gated activation's backward from its MXFP8 checkpoint (include/mxfp8_moe.h: mxfp8_gated_act_bwd):
+    dinter [rows, ..., n] bf16 with mxfp8_gated_act_fwd's codes and scales -> d(gate_up), bf16 of codes' shape."""
+    shape = tuple(codes.shape)
+    dev = codes.device
+    a = _gated_act_args(shape, activation, fmt, token_position_to_id, T, dev, "mxfp8_gated_act_bwd")
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    _call(dev, "mxfp8_gated_act_bwd", C.byref(a),
+          _tensor(dinter, torch.bfloat16, shape[:1] + shape[2:], dev, "dinter"), _dev(codes, torch.uint8, "codes"),
+          _tensor(scales, torch.uint8, shape[:-1] + (shape[-1] // 32,), dev, "scales"),
+          _tensor(out, torch.bfloat16, shape, dev, "out"))
     return out

@@ -3,6 +3,8 @@
 // allocated here and nothing is synchronised.
 #include <climits>
 #include <atomic>
+#include <cmath>
+#include <type_traits>
 #include <mutex>
 #include <cstdarg>
 #include <cstdio>
@@ -779,6 +781,188 @@ int moe_router_bwd(int mode, int64_t T, int64_t E, int64_t K, const int32_t* top
   r.idx = topk_idx; r.scores = topk_scores; r.logits = logits; r.dscores = dscores; r.daff = daff;
   r.dlogits = dlogits;
   return hip_status(mx::launch_router_bwd(r, static_cast<hipStream_t>(stream)), "router backward");
+}
+
+/* ---- router forward and auxiliary losses --------------------------------- */
+
+static bool valid_type(int t) { return t == MXFP8_TYPE_F32 || t == MXFP8_TYPE_BF16; }
+
+// The bounds that the router forward and the balance losses share.
+static int router_shape(const char* what, int64_t T, int64_t E, int64_t K, int type) {
+  if (!valid_type(type)) return fail(MXFP8_ERR_INVALID_ARG, "%s: logits_type %d is not F32/BF16", what, type);
+  if (T < 0 || E < 1 || K < 1 || K > E || K > MXFP8_ROUTER_MAX_K)
+    return fail(MXFP8_ERR_INVALID_ARG, "%s: need T >= 0 and 1 <= K <= min(E, %d) (T %lld, E %lld, K %lld)", what,
+                MXFP8_ROUTER_MAX_K, (long long)T, (long long)E, (long long)K);
+  if (E > MXFP8_ROUTER_MAX_EXPERTS)
+    return fail(MXFP8_ERR_UNSUPPORTED, "%s: E %lld above %d", what, (long long)E, MXFP8_ROUTER_MAX_EXPERTS);
+  if (T > INT32_MAX / K) return fail(MXFP8_ERR_UNSUPPORTED, "%s: T * K beyond 2^31 - 1", what);
+  return MXFP8_OK;
+}
+
+int moe_router_fwd(int mode, int64_t T, int64_t E, int64_t K, const void* logits, int logits_type,
+                   const uint8_t* token_mask, int renorm, int32_t* topk_idx, float* topk_scores,
+                   float* affinities, void* stream) {
+  static_assert(MXFP8_ROUTER_MAX_EXPERTS == mx::kRouterFwdMaxExperts, "the header's bound");
+  if (mode != MXFP8_ROUTER_SOFTMAX_OVER_TOPK && mode != MXFP8_ROUTER_TOPK_OVER_SOFTMAX && mode != MXFP8_ROUTER_TOPK)
+    return fail(MXFP8_ERR_INVALID_ARG, "moe_router_fwd: unknown mode %d", mode);
+  int rc = router_shape("moe_router_fwd", T, E, K, logits_type);
+  if (rc) return rc;
+  if (renorm != 0 && renorm != 1) return fail(MXFP8_ERR_INVALID_ARG, "moe_router_fwd: renorm must be 0/1");
+  if (renorm && mode != MXFP8_ROUTER_TOPK_OVER_SOFTMAX)
+    return fail(MXFP8_ERR_INVALID_ARG, "moe_router_fwd: renorm applies to the top-k-over-softmax mode only");
+  if (T == 0) return ok();
+  if (!logits || !topk_idx || !topk_scores) return fail(MXFP8_ERR_INVALID_ARG, "moe_router_fwd: null pointer");
+  const void* ptrs[4] = {logits, topk_idx, topk_scores, affinities};
+  for (const void* q : ptrs)
+    if (q && !aligned16(q)) return fail(MXFP8_ERR_INVALID_ARG, "moe_router_fwd: tensors must be 16-byte aligned");
+  mx::RouterFwdArgs r{};
+  r.mode = mode; r.renorm = renorm; r.bf16 = logits_type == MXFP8_TYPE_BF16;
+  r.T = T; r.E = E; r.K = K;
+  r.logits = logits; r.mask = token_mask; r.idx = topk_idx; r.scores = topk_scores; r.aff = affinities;
+  return hip_status(mx::launch_router_fwd(r, static_cast<hipStream_t>(stream)), "router forward");
+}
+
+// The workspace's regions, each 256-byte aligned; fills the record pointers of p where base is given.
+static size_t balance_regions(int64_t T, int64_t E, int64_t S, uint8_t* base, mx::BalanceArgs* p) {
+  const int64_t chunk = mx::balance_chunk_tokens(T, E);
+  const int64_t recs = (T + chunk - 1) / chunk + S;
+  size_t o = 0;
+  auto put = [&](auto*& field, int64_t n) {
+    using F = std::remove_reference_t<decltype(*field)>;
+    if (base) field = reinterpret_cast<F*>(base + o);
+    o = up256(o + size_t(n) * sizeof(F));
+  };
+  p->chunk = chunk;
+  put(p->part_p, recs * E);
+  put(p->part_c, recs * E);
+  put(p->part_z, recs);
+  put(p->part_n, recs);
+  put(p->term, S * ((E + 63) / 64));
+  put(p->term_z, S);
+  put(p->done, 1);
+  return o;
+}
+
+static int balance_shape(const char* what, int64_t T, int64_t E, int64_t K, int64_t S, int type) {
+  int rc = router_shape(what, T, E, K, type);
+  if (rc) return rc;
+  if (S < 1) return fail(MXFP8_ERR_INVALID_ARG, "%s: S must be positive (got %lld)", what, (long long)S);
+  if (S > INT32_MAX / E) return fail(MXFP8_ERR_UNSUPPORTED, "%s: S * E beyond 2^31 - 1", what);
+  return MXFP8_OK;
+}
+
+static int balance_check(const char* what, const moe_balance_args* a, mx::BalanceArgs& p) {
+  if (!a) return fail(MXFP8_ERR_INVALID_ARG, "%s: null args", what);
+  int rc = balance_shape(what, a->T, a->E, a->K, a->S, a->logits_type);
+  if (rc) return rc;
+  if (!a->seq_starts && a->S != 1) return fail(MXFP8_ERR_INVALID_ARG, "%s: S != 1 needs seq_starts", what);
+  if (!(std::isfinite(a->balance_coef) && std::isfinite(a->z_coef)))
+    return fail(MXFP8_ERR_INVALID_ARG, "%s: the coefficients must be finite", what);
+  if (!a->counts || !a->num_tokens || (a->T > 0 && !a->logits))
+    return fail(MXFP8_ERR_INVALID_ARG, "%s: null pointer", what);
+  const void* al[3] = {a->logits, a->counts, a->num_tokens};
+  for (const void* q : al)
+    if (q && !aligned16(q)) return fail(MXFP8_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", what);
+  const void* words[3] = {a->seq_starts, a->dloss, a->loss};
+  for (const void* q : words)
+    if (reinterpret_cast<uintptr_t>(q) & 3u)
+      return fail(MXFP8_ERR_INVALID_ARG, "%s: seq_starts, dloss and loss must be 4-byte aligned", what);
+  p.bf16 = a->logits_type == MXFP8_TYPE_BF16;
+  p.T = a->T; p.E = a->E; p.K = a->K; p.S = a->S;
+  p.logits = a->logits; p.idx = a->topk_idx; p.mask = a->token_mask; p.seq = a->seq_starts;
+  p.balance_coef = a->balance_coef; p.z_coef = a->z_coef;
+  p.loss = a->loss; p.counts = a->counts; p.num = a->num_tokens;
+  p.dloss = a->dloss; p.dlogits = a->dlogits;
+  return MXFP8_OK;
+}
+
+size_t moe_balance_loss_workspace_size(int64_t T, int64_t E, int64_t S) {
+  if (balance_shape("moe_balance_loss_workspace_size", T, E, 1, S, MXFP8_TYPE_F32)) return 0;
+  mx::BalanceArgs p{};
+  return balance_regions(T, E, S, nullptr, &p);
+}
+
+int moe_balance_loss(const moe_balance_args* a, void* ws, size_t ws_bytes, void* stream) {
+  mx::BalanceArgs p{};
+  int rc = balance_check("moe_balance_loss", a, p);
+  if (rc) return rc;
+  if (!a->loss || (a->T > 0 && !a->topk_idx)) return fail(MXFP8_ERR_INVALID_ARG, "moe_balance_loss: null pointer");
+  if (a->topk_idx && !aligned16(a->topk_idx))
+    return fail(MXFP8_ERR_INVALID_ARG, "moe_balance_loss: tensors must be 16-byte aligned");
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u))
+    return fail(MXFP8_ERR_INVALID_ARG, "moe_balance_loss: workspace must be non-null and 256-byte aligned");
+  const size_t need = balance_regions(a->T, a->E, a->S, static_cast<uint8_t*>(ws), &p);
+  if (ws_bytes < need)
+    return fail(MXFP8_ERR_WORKSPACE, "moe_balance_loss: workspace %zu < %zu bytes", ws_bytes, need);
+  return hip_status(mx::launch_balance_fwd(p, static_cast<hipStream_t>(stream)), "balance loss");
+}
+
+int moe_balance_loss_bwd(const moe_balance_args* a, void* stream) {
+  mx::BalanceArgs p{};
+  int rc = balance_check("moe_balance_loss_bwd", a, p);
+  if (rc) return rc;
+  if (a->accumulate != 0 && a->accumulate != 1)
+    return fail(MXFP8_ERR_INVALID_ARG, "moe_balance_loss_bwd: accumulate must be 0/1");
+  if (a->T == 0) return ok();
+  if (!a->dlogits) return fail(MXFP8_ERR_INVALID_ARG, "moe_balance_loss_bwd: null pointer");
+  if (!aligned16(a->dlogits))
+    return fail(MXFP8_ERR_INVALID_ARG, "moe_balance_loss_bwd: tensors must be 16-byte aligned");
+  p.accumulate = a->accumulate;
+  return hip_status(mx::launch_balance_bwd(p, static_cast<hipStream_t>(stream)), "balance loss backward");
+}
+
+/* ---- gated activation with an MXFP8 checkpoint --------------------------- */
+
+static int gated_act_check(const char* what, const mxfp8_gated_act_args* a, const void* const* ptrs, int n,
+                           const void* scales, mx::GatedActArgs& p, bool& empty) {
+  if (!a) return fail(MXFP8_ERR_INVALID_ARG, "%s: null args", what);
+  if (a->rows < 0 || a->cols < 0) return fail(MXFP8_ERR_INVALID_ARG, "%s: negative shape", what);
+  if (a->cols % 32)
+    return fail(MXFP8_ERR_INVALID_ARG, "%s: cols must be a multiple of 32 (got %lld)", what, (long long)a->cols);
+  if (!valid_fmt(a->fmt)) return fail(MXFP8_ERR_INVALID_ARG, "%s: fmt %d is not E4M3/E5M2", what, a->fmt);
+  if (a->activation != MXFP8_ACT_SWIGLU && a->activation != MXFP8_ACT_GEGLU)
+    return fail(MXFP8_ERR_INVALID_ARG, "%s: activation must be 0 (SwiGLU) or 1 (GeGLU)", what);
+  if (a->token_position_to_id && (a->period <= 0 || a->period % 32 || a->cols % a->period || a->T < 0))
+    return fail(MXFP8_ERR_INVALID_ARG, "%s: token_position_to_id needs T >= 0 and a period that is a multiple of 32 "
+                "and divides cols (got %lld)", what, (long long)a->period);
+  empty = a->rows == 0 || a->cols == 0;
+  if (empty) return MXFP8_OK;
+  if (a->rows > (int64_t(1) << 39) / a->cols)
+    return fail(MXFP8_ERR_UNSUPPORTED, "%s: rows * cols beyond 2^39", what);
+  if (!scales) return fail(MXFP8_ERR_INVALID_ARG, "%s: null pointer", what);
+  for (int i = 0; i < n; ++i)
+    if (!ptrs[i]) return fail(MXFP8_ERR_INVALID_ARG, "%s: null pointer", what);
+  for (int i = 0; i < n; ++i)
+    if (!aligned16(ptrs[i])) return fail(MXFP8_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", what);
+  if (a->token_position_to_id && !aligned16(a->token_position_to_id))
+    return fail(MXFP8_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", what);
+  p.R = a->rows; p.C = a->cols; p.fmt = a->fmt; p.geglu = a->activation == MXFP8_ACT_GEGLU;
+  p.slot_id = a->token_position_to_id; p.B = a->period; p.T = a->T;
+  return MXFP8_OK;
+}
+
+int mxfp8_gated_act_fwd(const mxfp8_gated_act_args* a, const uint16_t* gate_up, uint16_t* inter, uint8_t* codes,
+                        uint8_t* scales, void* stream) {
+  mx::GatedActArgs p{};
+  bool empty = false;
+  const void* ptrs[3] = {gate_up, inter, codes};
+  int rc = gated_act_check("mxfp8_gated_act_fwd", a, ptrs, 3, scales, p, empty);
+  if (rc) return rc;
+  if (empty) return ok();
+  p.gate_up = gate_up; p.inter = inter; p.codes = codes; p.scales = scales;
+  return hip_status(mx::launch_gated_act_fwd(p, static_cast<hipStream_t>(stream)), "gated activation");
+}
+
+int mxfp8_gated_act_bwd(const mxfp8_gated_act_args* a, const uint16_t* dinter, const uint8_t* codes,
+                        const uint8_t* scales, uint16_t* dgate_up, void* stream) {
+  mx::GatedActArgs p{};
+  bool empty = false;
+  const void* ptrs[3] = {dinter, codes, dgate_up};
+  int rc = gated_act_check("mxfp8_gated_act_bwd", a, ptrs, 3, scales, p, empty);
+  if (rc) return rc;
+  if (empty) return ok();
+  p.dinter = dinter; p.codes_in = codes; p.scales_in = scales; p.dgate_up = dgate_up;
+  return hip_status(mx::launch_gated_act_bwd(p, static_cast<hipStream_t>(stream)), "gated activation backward");
 }
 
 }  // extern "C"

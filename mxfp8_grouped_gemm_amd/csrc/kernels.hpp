@@ -100,6 +100,69 @@ struct RouterArgs {
 };
 hipError_t launch_router_bwd(const RouterArgs& p, hipStream_t st);
 
+// router_fwd.hip -- the router forward; balance.hip -- its auxiliary losses
+constexpr int64_t kRouterFwdMaxExperts = 4096;
+struct RouterFwdArgs {
+  int mode;                   // kRouter*
+  int renorm;
+  int bf16;                   // logits are bf16 (else fp32)
+  int64_t T, E, K;
+  const void* logits;         // [T,E]
+  const uint8_t* mask;        // [T], 0: the token selects nothing; or null
+  int32_t* idx;               // [T,K]
+  float* scores;              // [T,K]
+  float* aff;                 // [T,E], or null
+};
+hipError_t launch_router_fwd(const RouterFwdArgs& p, hipStream_t st);
+
+struct BalanceArgs {
+  int bf16;
+  int accumulate;             // backward: add to dlogits
+  int64_t T, E, K, S;
+  const void* logits;         // [T,E]
+  const int32_t* idx;         // [T,K] (forward)
+  const uint8_t* mask;        // [T] or null
+  const int32_t* seq;         // [S+1] or null (one sequence of all tokens)
+  float balance_coef, z_coef;
+  float* loss;                // [2]
+  int32_t* counts;            // [S,E]: written forward, read backward
+  int32_t* num;               // [S+2]: tokens per sequence, sequences with tokens, tokens
+  const float* dloss;         // [2] or null (ones)
+  float* dlogits;             // [T,E]
+  // forward workspace: records of (chunk, sequence) at chunk + sequence, the
+  // sequences' terms, the count of finished workgroups
+  int64_t chunk;              // tokens
+  float* part_p;              // [chunks+S][E]
+  int32_t* part_c;            // [chunks+S][E]
+  float* part_z;              // [chunks+S]
+  int32_t* part_n;            // [chunks+S]
+  double* term;               // [S][ceil(E/64)]
+  float* term_z;              // [S]
+  unsigned* done;
+};
+int64_t balance_chunk_tokens(int64_t T, int64_t E);
+hipError_t launch_balance_fwd(const BalanceArgs& p, hipStream_t st);
+hipError_t launch_balance_bwd(const BalanceArgs& p, hipStream_t st);
+
+// gated_act.hip -- the gated activation with an MXFP8 gate/up checkpoint
+struct GatedActArgs {
+  int64_t R, C;               // gate_up [R][2][C], C % 32 == 0
+  int64_t B;                  // slots of a row (C % B == 0, B % 32 == 0); with slot_id
+  int64_t T;
+  const int32_t* slot_id;     // [R*B]: a token in [0,T), else padding; or null
+  int fmt, geglu;
+  const uint16_t* gate_up;    // forward: [R][2][C]
+  uint16_t* inter;            //          [R][C]
+  uint8_t* codes;             //          [R][2][C]
+  uint8_t* scales;            //          [R][2][C/32]
+  const uint16_t* dinter;     // backward: [R][C]
+  const uint8_t* codes_in;
+  const uint8_t* scales_in;
+  uint16_t* dgate_up;         //           [R][2][C]
+};
+hipError_t launch_gated_act_fwd(const GatedActArgs& p, hipStream_t st);
+hipError_t launch_gated_act_bwd(const GatedActArgs& p, hipStream_t st);
+
 // moe_aux.hip
 hipError_t launch_fill_u32(void* p, int64_t n, uint32_t v, hipStream_t st);
 hipError_t launch_fill_u16(void* p, int64_t n, uint16_t v, hipStream_t st);

@@ -12,6 +12,7 @@
 //     dp_k = g_k, or (g_k - sum_m g_m s_m) / S renormalised;
 //     d[e] = p_e (dp(e) - sum_k dp_k p[idx_k]), dp(e) = dp_k at e = idx_k, else 0.
 //   top-k scatter        (scores = the selected logits): d[idx_k] = g_k; 0 elsewhere.
+// A row without a selection (every id outside [0, E)) gets zeros whatever its logits hold.
 // Every d[t][e] is written.  HBM-bound: a row is E fp32 logits read (top-k over
 // softmax only) and E fp32 gradients written, plus the K selections.
 //
@@ -110,9 +111,11 @@ __global__ void __launch_bounds__(kRouterThreads) router_bwd_kernel(RouterArgs p
     const float inv_s = 1.f / s;
     // the selected probabilities and the adjusted gradients at them
     float psum = 0.f, gdot = 0.f;
+    bool any = false;
     for (int k = 0; k < K; ++k) {
       const int e = idx[k];
       if (e < 0 || e >= E) continue;
+      any = true;
       psum += expf(z[e] - m) * inv_s;
       if (RENORM) gdot += grad(k) * p.scores[t * K + k];
     }
@@ -134,10 +137,10 @@ __global__ void __launch_bounds__(kRouterThreads) router_bwd_kernel(RouterArgs p
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
         const int e = lane + L * j;
-        if (e < E) out[e] = zv[j] * inv_s * (dp_at(e) - dot);
+        if (e < E) out[e] = any ? zv[j] * inv_s * (dp_at(e) - dot) : 0.f;
       }
     } else {
-      for (int e = lane; e < E; e += L) out[e] = expf(z[e] - m) * inv_s * (dp_at(e) - dot);
+      for (int e = lane; e < E; e += L) out[e] = any ? expf(z[e] - m) * inv_s * (dp_at(e) - dot) : 0.f;
     }
   }
 }

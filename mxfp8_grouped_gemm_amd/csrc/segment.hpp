@@ -1,0 +1,62 @@
+// segment.hpp -- reductions over segments of L consecutive lanes (L a power of
+// two, 8 to 64) that stay in the register file: quad_perm, row_half_mirror and
+// row_mirror DPP moves within 16 lanes, v_permlane16_swap / v_permlane32_swap
+// beyond.  After each step every lane of the reduced group holds the same
+// value, so a mirror serves as the exchange with the other half.  Each step
+// combines two values with a commutative operation: all lanes of a segment end
+// with the same bits.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace mx {
+namespace seg {
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t x) {
+  return uint32_t(__builtin_amdgcn_update_dpp(0, int(x), CTRL, 0xf, 0xf, true));
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;
+
+template <int L, class Op>
+__device__ __forceinline__ uint32_t reduce(uint32_t x, const Op& op) {
+  static_assert(L >= 1 && L <= 64 && (L & (L - 1)) == 0, "a power of two");
+#if defined(__HIP_DEVICE_COMPILE__)
+  if constexpr (L > 1) x = op(x, dpp<kXor1>(x));
+  if constexpr (L > 2) x = op(x, dpp<kXor2>(x));
+  if constexpr (L > 4) x = op(x, dpp<kHalfMirror>(x));
+  if constexpr (L > 8) x = op(x, dpp<kMirror>(x));
+  if constexpr (L > 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    x = op(r[0], r[1]);
+  }
+  if constexpr (L > 32) {
+    const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    x = op(r[0], r[1]);
+  }
+#endif
+  return x;
+}
+template <int L>
+__device__ __forceinline__ float sum(float v) {
+  return __uint_as_float(reduce<L>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
+}
+template <int L>
+__device__ __forceinline__ float max(float v) {   // NaN only where every value is NaN
+  return __uint_as_float(reduce<L>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }));
+}
+template <int L>
+__device__ __forceinline__ uint32_t umax(uint32_t v) {
+  return reduce<L>(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+template <int L>
+__device__ __forceinline__ uint32_t umin(uint32_t v) {
+  return reduce<L>(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
+}
+
+}  // namespace seg
+}  // namespace mx

@@ -129,3 +129,75 @@ def gather_scores(daff: np.ndarray, idx: np.ndarray) -> np.ndarray:
     """g [T, K] from an affinity gradient laid out [T, E] (the masked layout of
     the affinities, index t*E + e): g[t, k] = daff[t, idx[t, k]]."""
     return np.take_along_axis(np.asarray(daff, dtype=np.float64), np.asarray(idx, dtype=np.int64), axis=1)
+
+
+def topk(logits: np.ndarray, K: int, mask: np.ndarray | None = None):
+    """Top-k selection of each token: (idx [T, K], open [T, K] bool).
+
+    Descending logit, equal logits by ascending expert; an expert at -inf or
+    NaN is closed.  Selections that find no open expert (all of them for a
+    token whose mask is 0) hold id -1 and open False."""
+    z = np.array(logits, dtype=np.float64)
+    z[np.isnan(z)] = -np.inf
+    if mask is not None:
+        z[~np.asarray(mask, dtype=bool)] = -np.inf
+    idx = np.argsort(-z, axis=1, kind="stable")[:, :K]
+    is_open = np.take_along_axis(z, idx, axis=1) > -np.inf
+    return np.where(is_open, idx, -1).astype(np.int32), is_open
+
+
+def forward_topk(mode: int, logits: np.ndarray, K: int, renorm: bool = False, mask: np.ndarray | None = None):
+    """(idx [T, K], scores [T, K], affinities [T, E]) of the whole router
+    forward, token by token; closed selections score 0."""
+    z = np.asarray(logits, dtype=np.float64)
+    T, E = z.shape
+    idx, is_open = topk(z, K, mask)
+    scores, aff = np.zeros((T, K)), np.zeros((T, E))
+    for t in range(T):
+        n = int(is_open[t].sum())
+        if n:
+            scores[t, :n] = forward(mode, z[t:t + 1], idx[t:t + 1, :n], renorm)[0]
+            aff[t, idx[t, :n]] = scores[t, :n]
+    return idx, scores, aff
+
+
+def balance(logits, idx, balance_coef, z_coef, mask=None, seq_starts=None, dloss=(1.0, 1.0)):
+    """The load-balance and z losses: (loss [2], counts [S, E], num [S+2], d(logits) [T, E]).
+
+    Sequence by sequence: f_e = c_e / (K n) the share of the selections, P_e the
+    mean softmax probability, balance = coef E <f, P> averaged over the
+    sequences with tokens; z = coef mean(lse^2) over all tokens that take part
+    (in a sequence, mask not 0, some logit above -inf).  The gradient is the
+    softmax Jacobian's product with the constant f, and of lse^2."""
+    z = np.asarray(logits, dtype=np.float64)
+    T, E = z.shape
+    K = np.asarray(idx).shape[1]
+    bounds = [0, T] if seq_starts is None else list(seq_starts)
+    S = len(bounds) - 1
+    counts, num = np.zeros((S, E), dtype=np.int64), np.zeros(S + 2, dtype=np.int64)
+    rows = []
+    for s in range(S):
+        rows.append([t for t in range(bounds[s], bounds[s + 1])
+                     if (mask is None or mask[t]) and np.any(z[t] > -np.inf)])
+        num[s] = len(rows[s])
+        for t in rows[s]:
+            for e in np.asarray(idx)[t]:
+                if 0 <= e < E:
+                    counts[s, e] += 1
+    num[S], num[S + 1] = np.count_nonzero(num[:S]), num[:S].sum()
+    loss, d = np.zeros(2), np.zeros((T, E))
+    for s in range(S):
+        if not rows[s]:
+            continue
+        x = z[rows[s]]
+        m = x.max(axis=1, keepdims=True)
+        p = np.exp(x - m)
+        lse = m[:, 0] + np.log(p.sum(axis=1))
+        p /= p.sum(axis=1, keepdims=True)
+        f = counts[s] / (K * num[s])
+        loss[0] += balance_coef * E * (f * p.mean(axis=0)).sum() / num[S]
+        loss[1] += z_coef * (lse ** 2).sum() / num[S + 1]
+        g = dloss[0] * balance_coef * E * f / (num[S] * num[s])
+        d[rows[s]] = p * (g - (p * g).sum(axis=1, keepdims=True)) + \
+            dloss[1] * z_coef * 2 / num[S + 1] * lse[:, None] * p
+    return loss, counts, num, d
