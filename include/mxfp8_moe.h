@@ -258,7 +258,8 @@ typedef struct {
   const int32_t*  token_position_to_id;           /* [N*B]; outside [0,T) = padding slot */
   const int32_t*  block_to_expert;                /* [N], each in [0,E)                  */
   const uint16_t* output_hidden_states_grad;      /* [T,H] bf16                          */
-  const uint16_t* gate_up_proj_act_checkpoint_T;  /* [N,2,I,B] bf16, required:
+  const uint16_t* gate_up_proj_act_checkpoint_T;  /* [N,2,I,B] bf16, required unless the
+                                                     MXFP8 one below is given:
                                                      [b,0,i,p] = gate_pre, [b,1,i,p] = up;
                                                      padding slots' values are ignored  */
   const uint16_t* down_proj_bias;                 /* [E,H] bf16, required iff has_bias   */
@@ -309,6 +310,16 @@ typedef struct {
    * definition).  inter = act(gate_pre) * up, dGate = dInter * up * act'(g),
    * dUp = dInter * act(g); gate_act_checkpoint_T then holds bf16(act(g)).   */
   int activation;
+  /* The gate/up checkpoint in MXFP8, instead of gate_up_proj_act_checkpoint_T
+   * (NULL then): codes [N,2,I,B] in fmt_checkpoint and scales [N,2,I,B/32],
+   * groups of 32 consecutive slots, as mxfp8_gated_act_fwd writes them: 2 + 2/32
+   * bytes a gate/up pair instead of 4.  The backward works on the values they
+   * stand for: the same results as with a bf16 checkpoint holding those values.
+   * Padding slots' codes, and the scales of groups of padding alone, are
+   * ignored.  Not together with the [N,I,B] checkpoints above (UNSUPPORTED). */
+  const uint8_t* gate_up_checkpoint_codes;
+  const uint8_t* gate_up_checkpoint_scales;
+  int fmt_checkpoint;   /* MXFP8_E4M3 or MXFP8_E5M2; read with gate_up_checkpoint_codes only */
 } moe_bwd_mxfp8_args;
 typedef enum { MXFP8_ACT_SWIGLU = 0, MXFP8_ACT_GEGLU = 1 } mxfp8_activation;
 
@@ -334,8 +345,9 @@ typedef enum { MXFP8_ACT_SWIGLU = 0, MXFP8_ACT_GEGLU = 1 } mxfp8_activation;
  *                                                     (slots past a block's extent unwritten;
  *                                                     empty, like phase1_tiles, where Phase 1
  *                                                     runs with its epilogue in one kernel:
- *                                                     H % 128 == 0, H <= 2048, I <= 512 and
- *                                                     no caller checkpoints)
+ *                                                     H % 128 == 0, H <= 2048, I <= 512,
+ *                                                     no [N,I,B] checkpoints and no E5M2
+ *                                                     gate/up checkpoint)
  *   phase1_tiles/phase3_tiles [N+1 + tiles] int32     first tile of each block over its
  *                                                     live slot tiles (with round-robin tile
  *                                                     order the blocks whose slot tiles are

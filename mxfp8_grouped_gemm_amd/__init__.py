@@ -61,7 +61,8 @@ class MoeBwdArgs(C.Structure):
                 ("gate_and_up_proj_bias_grad", _p), ("down_proj_bias_grad", _p),
                 ("gate_act_checkpoint_T", _p), ("intermediate_checkpoint_T", _p),
                 ("scaled_intermediate_checkpoint_T", _p), ("down_proj_act_checkpoint", _p),
-                ("num_valid_tokens", _p), ("accumulate", C.c_int), ("activation", C.c_int)]
+                ("num_valid_tokens", _p), ("accumulate", C.c_int), ("activation", C.c_int),
+                ("gate_up_checkpoint_codes", _p), ("gate_up_checkpoint_scales", _p), ("fmt_checkpoint", C.c_int)]
 
 
 LAYOUT_FIELDS = ("dy_codes", "dy_scales", "dy_deq", "wd_deq", "x_tok_codes", "x_tok_scales", "gy_tok_codes", "gy_tok_scales",
@@ -317,14 +318,19 @@ class MoeBwd:
     Allocates the outputs and the workspace once; ``run()`` enqueues the whole
     backward on the current stream.  With ``accumulate=True`` the outputs are
     allocated zeroed and each ``run()`` adds its gradients into what they hold
-    (write priors into ``self.out`` to start from other values)."""
+    (write priors into ``self.out`` to start from other values).
+    ``gate_up_checkpoint=(codes [N, 2, I, B], scales [N, 2, I, B/32])`` is the
+    gate/up checkpoint in MXFP8 (mxfp8_gated_act_fwd's, format
+    ``fmt_checkpoint``) in place of the bf16 ``gate_up_proj_act_checkpoint_T``,
+    which is then None."""
 
     def __init__(self, hidden_states, expert_affinities_masked, gate_up_codes, gate_up_scales, down_codes,
                  down_scales, token_position_to_id, block_to_expert, output_hidden_states_grad, block_size,
                  gate_up_proj_act_checkpoint_T, down_proj_bias=None, affinity_on=0, fmt_weight=E4M3,
                  fmt_act=E4M3, fmt_grad=E5M2, workspace=None, gate_act_checkpoint_T=None,
                  intermediate_checkpoint_T=None, scaled_intermediate_checkpoint_T=None,
-                 down_proj_act_checkpoint=None, num_valid_tokens=None, accumulate=False, activation=0):
+                 down_proj_act_checkpoint=None, num_valid_tokens=None, accumulate=False, activation=0,
+                 gate_up_checkpoint=None, fmt_checkpoint=E4M3):
         T, H = hidden_states.shape
         E, _, _, I = gate_up_codes.shape
         N = block_to_expert.numel()
@@ -332,7 +338,9 @@ class MoeBwd:
         self.keep = [hidden_states, expert_affinities_masked, gate_up_codes, gate_up_scales, down_codes,
                      down_scales, token_position_to_id, block_to_expert, output_hidden_states_grad,
                      gate_up_proj_act_checkpoint_T, down_proj_bias, gate_act_checkpoint_T, intermediate_checkpoint_T,
-                     scaled_intermediate_checkpoint_T, down_proj_act_checkpoint, num_valid_tokens]
+                     scaled_intermediate_checkpoint_T, down_proj_act_checkpoint, num_valid_tokens,
+                     gate_up_checkpoint]
+        ck_codes, ck_scales = (None, None) if gate_up_checkpoint is None else gate_up_checkpoint
         has_bias = down_proj_bias is not None
         alloc = torch.zeros if accumulate else torch.empty
         self.out = dict(
@@ -361,7 +369,10 @@ class MoeBwd:
             _dev(intermediate_checkpoint_T, torch.bfloat16, "intermediate_checkpoint_T"),
             _dev(scaled_intermediate_checkpoint_T, torch.bfloat16, "scaled_intermediate_checkpoint_T"),
             _dev(down_proj_act_checkpoint, torch.bfloat16, "down_proj_act_checkpoint"),
-            _dev(num_valid_tokens, torch.int32, "num_valid_tokens"), int(bool(accumulate)), int(activation))
+            _dev(num_valid_tokens, torch.int32, "num_valid_tokens"), int(bool(accumulate)), int(activation),
+            _tensor(ck_codes, torch.uint8, (N, 2, I, block_size), dev, "gate_up_checkpoint codes"),
+            _tensor(ck_scales, torch.uint8, (N, 2, I, block_size // 32), dev, "gate_up_checkpoint scales"),
+            int(fmt_checkpoint))
         L = lib()
         lay = MoeWorkspaceLayout()
         _check(L.moe_bwd_mxfp8_workspace_query(C.byref(self.args), C.byref(lay)), "moe_bwd_mxfp8_workspace_query")

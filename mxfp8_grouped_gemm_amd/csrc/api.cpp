@@ -408,7 +408,8 @@ static bool moe_fuse_bias(const moe_bwd_mxfp8_args* a) {
 // which its launcher checks again): no dS in HBM, and no tile ranges.
 static bool moe_phase1_fused(const moe_bwd_mxfp8_args* a) {
   return a->H % 128 == 0 && a->H <= 2048 && a->I <= 512 && !a->gate_act_checkpoint_T &&
-         !a->intermediate_checkpoint_T && !a->scaled_intermediate_checkpoint_T;
+         !a->intermediate_checkpoint_T && !a->scaled_intermediate_checkpoint_T &&
+         (!a->gate_up_checkpoint_codes || a->fmt_checkpoint == MXFP8_E4M3);
 }
 
 static int moe_layout(const moe_bwd_mxfp8_args* a, moe_bwd_mxfp8_workspace_layout* L) {
@@ -519,7 +520,10 @@ static int moe_run(const moe_bwd_mxfp8_args* a, void* ws, size_t ws_bytes, void*
     return fail(MXFP8_ERR_UNSUPPORTED, "moe_bwd_mxfp8: a bias with the affinity on I is not supported");
   const void* req[] = {a->hidden_states, a->expert_affinities_masked, a->gate_up_codes, a->gate_up_scales,
                        a->down_codes, a->down_scales, a->token_position_to_id, a->block_to_expert,
-                       a->output_hidden_states_grad, a->gate_up_proj_act_checkpoint_T, a->hidden_states_grad,
+                       a->output_hidden_states_grad,
+                       a->gate_up_checkpoint_codes ? static_cast<const void*>(a->gate_up_checkpoint_codes)
+                                                   : a->gate_up_proj_act_checkpoint_T,
+                       a->hidden_states_grad,
                        a->expert_affinities_masked_grad, a->gate_up_proj_weight_grad, a->down_proj_weight_grad};
   for (const void* q : req)
     if (!q) return fail(MXFP8_ERR_INVALID_ARG, "moe_bwd_mxfp8: a required pointer is null");
@@ -531,6 +535,20 @@ static int moe_run(const moe_bwd_mxfp8_args* a, void* ws, size_t ws_bytes, void*
     if (!aligned16(a->down_proj_bias) || !aligned16(a->gate_and_up_proj_bias_grad) ||
         !aligned16(a->down_proj_bias_grad))
       return fail(MXFP8_ERR_INVALID_ARG, "moe_bwd_mxfp8: bias tensors must be 16-byte aligned");
+  }
+  if (a->gate_up_checkpoint_codes) {
+    if (a->gate_up_proj_act_checkpoint_T)
+      return fail(MXFP8_ERR_INVALID_ARG, "moe_bwd_mxfp8: pass the gate/up checkpoint in bf16 or in MXFP8, not both");
+    if (!a->gate_up_checkpoint_scales)
+      return fail(MXFP8_ERR_INVALID_ARG, "moe_bwd_mxfp8: gate_up_checkpoint_codes and _scales go together");
+    if (!aligned16(a->gate_up_checkpoint_scales))
+      return fail(MXFP8_ERR_INVALID_ARG, "moe_bwd_mxfp8: tensors must be 16-byte aligned");
+    if (!valid_fmt(a->fmt_checkpoint))
+      return fail(MXFP8_ERR_INVALID_ARG, "moe_bwd_mxfp8: fmt_checkpoint must be E4M3 (0) or E5M2 (1)");
+    if (a->gate_act_checkpoint_T || a->intermediate_checkpoint_T || a->scaled_intermediate_checkpoint_T)
+      return fail(MXFP8_ERR_UNSUPPORTED, "moe_bwd_mxfp8: the [N,I,B] checkpoints go with the bf16 gate/up checkpoint");
+  } else if (a->gate_up_checkpoint_scales) {
+    return fail(MXFP8_ERR_INVALID_ARG, "moe_bwd_mxfp8: gate_up_checkpoint_codes and _scales go together");
   }
   if (a->scaled_intermediate_checkpoint_T && a->affinity_on != 1)
     return fail(MXFP8_ERR_INVALID_ARG, "moe_bwd_mxfp8: scaled_intermediate_checkpoint_T needs the affinity on I");
@@ -662,6 +680,8 @@ static int moe_run(const moe_bwd_mxfp8_args* a, void* ws, size_t ws_bytes, void*
   p1.tile_start = reinterpret_cast<int32_t*>(at(L.phase1_tiles));
   p1.slot_tok = slot_tok; p1.slot_aff = slot_aff; p1.b2e = a->block_to_expert; p1.flag = flag;
   p1.ckpt = a->gate_up_proj_act_checkpoint_T;
+  p1.ck8_codes = a->gate_up_checkpoint_codes; p1.ck8_scales = a->gate_up_checkpoint_scales;
+  p1.ck8_fmt = a->fmt_checkpoint;
   p1.ga_ckpt = a->gate_act_checkpoint_T;
   p1.in_ckpt = a->intermediate_checkpoint_T;
   p1.sc_ckpt = a->scaled_intermediate_checkpoint_T;

@@ -209,7 +209,10 @@ struct Phase1Args {
   const int32_t* b2e;           // [N]
   const int32_t* flag;          // [N]: the block's extent (one past its last routed slot)
   int32_t* tile_start;          // [N+1]: tile ranges over the blocks' live slot tiles (moe_tiles.hpp)
-  const uint16_t* ckpt;         // [N][2][I][B]
+  const uint16_t* ckpt;         // [N][2][I][B] bf16, or null and the same in MXFP8 (groups along the slots):
+  const uint8_t* ck8_codes;     // [N][2][I][B], format ck8_fmt
+  const uint8_t* ck8_scales;    // [N][2][I][B/32]
+  int ck8_fmt;
   // optional checkpoints supplied by the caller ([N][I][B] bf16 each), read in
   // place of recomputing the value: silu(gate), the intermediate, and the
   // intermediate times the affinity (affinity on I)

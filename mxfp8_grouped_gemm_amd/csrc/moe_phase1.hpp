@@ -155,7 +155,7 @@ hipError_t phase1_launch(Phase1Args p, int fg, int fw, hipStream_t st) {
 // tiles past a block's extent skip the product (all padding, dS = 0) but still
 // write the padding's codes and scales; blocks without tokens write their zero
 // intermediate operand.  Tile order as in phase1_kernel, over all tiles.
-template <int BM, int BN, int FG, int FW, bool GEGLU>
+template <int BM, int BN, int FG, int FW, bool GEGLU, int C8>
 __global__ void __launch_bounds__(v2::kThreads) phase1_fused_kernel(Phase1Args p) {
   constexpr int SMEM = phase1_ring_smem<BM, BN>();
   static_assert(SMEM >= EpiLds<BN>::BYTES, "the epilogue's chunk fits the ring's LDS");
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(v2::kThreads) phase1_fused_kernel(Phase1Args p
   // ring leaves registers for them (128 x 128), else right after it
   constexpr bool EARLY = BM * BN <= 128 * 128;
   EpiGU pre[2];
-  if (EARLY) epi_load_gu<BN>(p, b, chunk_row0(0), GSTRIDE, n0, pre[0]);
+  if (EARLY) epi_load_gu<BN, C8>(p, b, chunk_row0(0), GSTRIDE, n0, pre[0]);
   v16f acc[FM][FN];
   if (n0 < ext) {
     const int32_t* st = p.slot_tok + int64_t(b) * p.B;
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(v2::kThreads) phase1_fused_kernel(Phase1Args p
       });
     });
   }
-  if (!EARLY) epi_load_gu<BN>(p, b, chunk_row0(0), GSTRIDE, n0, pre[0]);
+  if (!EARLY) epi_load_gu<BN, C8>(p, b, chunk_row0(0), GSTRIDE, n0, pre[0]);
   __syncthreads();   // every wave is done reading the ring
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int h = lane >> 5, r = lane & 31, wm = wave >> 1;
@@ -219,17 +219,22 @@ __global__ void __launch_bounds__(v2::kThreads) phase1_fused_kernel(Phase1Args p
         v2::static_for<FN>([&](auto FJ) { row[32 * int(FJ)] = acc[FI][FJ][int(Q)]; });
       });
     }
-    if constexpr (c + 1 < NCH) epi_load_gu<BN>(p, b, chunk_row0(c + 1), GSTRIDE, n0, pre[(c + 1) & 1]);
+    if constexpr (c + 1 < NCH) epi_load_gu<BN, C8>(p, b, chunk_row0(c + 1), GSTRIDE, n0, pre[(c + 1) & 1]);
     __syncthreads();
-    epi_chunk<FG, 2, BN, false, GEGLU, true>(p, b, chunk_row0(c), GSTRIDE, n0, smem, &pre[c & 1]);
+    epi_chunk<FG, 2, BN, false, GEGLU, true, C8>(p, b, chunk_row0(c), GSTRIDE, n0, smem, &pre[c & 1]);
     __syncthreads();   // pass 2 is done with the staging before the next chunk's dS
   });
 }
 
 template <int BM, int BN, int FG, int FW>
 inline void phase1_fused_go(const Phase1Args& p, unsigned blocks, hipStream_t st) {
-  if (p.geglu) phase1_fused_kernel<BM, BN, FG, FW, true><<<blocks, v2::kThreads, 0, st>>>(p);
-  else phase1_fused_kernel<BM, BN, FG, FW, false><<<blocks, v2::kThreads, 0, st>>>(p);
+  if (p.ck8_codes) {   // E4M3 (phase1_fusable)
+    if (p.geglu) phase1_fused_kernel<BM, BN, FG, FW, true, kE4M3><<<blocks, v2::kThreads, 0, st>>>(p);
+    else phase1_fused_kernel<BM, BN, FG, FW, false, kE4M3><<<blocks, v2::kThreads, 0, st>>>(p);
+  } else {
+    if (p.geglu) phase1_fused_kernel<BM, BN, FG, FW, true, -1><<<blocks, v2::kThreads, 0, st>>>(p);
+    else phase1_fused_kernel<BM, BN, FG, FW, false, -1><<<blocks, v2::kThreads, 0, st>>>(p);
+  }
 }
 
 template <int BM, int BN>

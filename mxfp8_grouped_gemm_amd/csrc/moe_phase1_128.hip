@@ -35,8 +35,10 @@ hipError_t launch_phase1(const Phase1Args& p, int fg, int fw, hipStream_t st) {
 // 128 x 128 / 256 x 256 tiles: the epilogue's loads and stores do not overlap
 // the other workgroup's MFMAs, and the product itself needs both workgroups
 // to hide its latency, so the element-wise work adds to the product's time.
+// An E5M2 checkpoint takes the two kernels (the fused one is built for bf16 and E4M3 checkpoints).
 bool phase1_fusable(const Phase1Args& p) {
-  return p.H % 128 == 0 && p.H <= 2048 && p.I <= 512 && !p.ga_ckpt && !p.in_ckpt && !p.sc_ckpt;
+  return p.H % 128 == 0 && p.H <= 2048 && p.I <= 512 && !p.ga_ckpt && !p.in_ckpt && !p.sc_ckpt &&
+         (!p.ck8_codes || p.ck8_fmt == kE4M3);
 }
 
 hipError_t launch_phase1_fused(const Phase1Args& p, int fg, int fw, hipStream_t st) {

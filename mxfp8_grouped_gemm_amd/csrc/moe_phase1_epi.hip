@@ -10,7 +10,7 @@ namespace mx {
 // row chunks that share a slot's 128-byte run of dgu_row codes and its scale
 // words are consecutive, and consecutive chunks run on one XCD, so those lines
 // fill up in one L2 instead of reaching HBM in pieces from several.
-template <int FG, bool ON_I, int TS, bool CK, bool GEGLU>
+template <int FG, bool ON_I, int TS, bool CK, bool GEGLU, int C8>
 __global__ void __launch_bounds__(kEpiThreads) phase1_epi_kernel(Phase1Args p) {
   constexpr int TI = kEpiElems / TS;
   __shared__ __attribute__((aligned(16))) uint8_t lds[EpiLds<TS>::BYTES];
@@ -26,28 +26,34 @@ __global__ void __launch_bounds__(kEpiThreads) phase1_epi_kernel(Phase1Args p) {
     epi_empty_chunk<TS>(p, b, ti0, s0);
     return;
   }
-  epi_chunk<FG, ON_I ? 1 : 0, TS, CK, GEGLU, false>(p, b, ti0, 32, s0, lds);
+  epi_chunk<FG, ON_I ? 1 : 0, TS, CK, GEGLU, false, C8>(p, b, ti0, 32, s0, lds);
 }
 
-template <int TS, bool CK, bool GEGLU>
+template <int TS, bool CK, bool GEGLU, int C8>
 static hipError_t epi_launch(const Phase1Args& p, int fg, hipStream_t st) {
   constexpr int TI = kEpiElems / TS;
   const int64_t grid = int64_t(p.N) * ((p.I + TI - 1) / TI) * (p.B / TS);
   if (grid > INT32_MAX) return hipErrorInvalidValue;
   const bool on_i = p.affinity_on_i != 0;
   if (fg == kE4M3) {
-    if (on_i) phase1_epi_kernel<kE4M3, true, TS, CK, GEGLU><<<unsigned(grid), kEpiThreads, 0, st>>>(p);
-    else phase1_epi_kernel<kE4M3, false, TS, CK, GEGLU><<<unsigned(grid), kEpiThreads, 0, st>>>(p);
+    if (on_i) phase1_epi_kernel<kE4M3, true, TS, CK, GEGLU, C8><<<unsigned(grid), kEpiThreads, 0, st>>>(p);
+    else phase1_epi_kernel<kE4M3, false, TS, CK, GEGLU, C8><<<unsigned(grid), kEpiThreads, 0, st>>>(p);
   } else {
-    if (on_i) phase1_epi_kernel<kE5M2, true, TS, CK, GEGLU><<<unsigned(grid), kEpiThreads, 0, st>>>(p);
-    else phase1_epi_kernel<kE5M2, false, TS, CK, GEGLU><<<unsigned(grid), kEpiThreads, 0, st>>>(p);
+    if (on_i) phase1_epi_kernel<kE5M2, true, TS, CK, GEGLU, C8><<<unsigned(grid), kEpiThreads, 0, st>>>(p);
+    else phase1_epi_kernel<kE5M2, false, TS, CK, GEGLU, C8><<<unsigned(grid), kEpiThreads, 0, st>>>(p);
   }
   return hipGetLastError();
 }
 template <int TS, bool GEGLU>
 static hipError_t epi_launch(const Phase1Args& p, int fg, hipStream_t st) {
-  if (p.ga_ckpt || p.in_ckpt || p.sc_ckpt) return epi_launch<TS, true, GEGLU>(p, fg, st);
-  return epi_launch<TS, false, GEGLU>(p, fg, st);
+  const bool ck = p.ga_ckpt || p.in_ckpt || p.sc_ckpt;
+  if (p.ck8_codes) {   // comes alone
+    if (ck) return hipErrorInvalidValue;
+    if (p.ck8_fmt == kE4M3) return epi_launch<TS, false, GEGLU, kE4M3>(p, fg, st);
+    return epi_launch<TS, false, GEGLU, kE5M2>(p, fg, st);
+  }
+  if (ck) return epi_launch<TS, true, GEGLU, -1>(p, fg, st);
+  return epi_launch<TS, false, GEGLU, -1>(p, fg, st);
 }
 template <int TS>
 static hipError_t epi_launch(const Phase1Args& p, int fg, hipStream_t st) {

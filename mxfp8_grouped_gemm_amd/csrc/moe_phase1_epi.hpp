@@ -113,10 +113,48 @@ __device__ __forceinline__ void epi_empty_chunk(const Phase1Args& p, int b, int6
 // chunk: slot (t % TS) of the chunk, the 32 rows of its group (t / TS).  The
 // fused kernel loads the next chunk's while it works on the current one.
 struct EpiGU {
-  uint32_t gu[32];   // bf16 gate | bf16 up << 16 (the d16 and d16_hi loads fill one register)
+  uint32_t gu[32];   // bf16 gate | bf16 up << 16 (the d16 and d16_hi loads fill one register); codes likewise
+  uint32_t sc;       // MXFP8 checkpoint: the scales of one row (epi_load_scales)
 };
 typedef unsigned short epi_us2 __attribute__((ext_vector_type(2)));
+
+// The MXFP8 checkpoint (C8 >= 0: its element format).  Its groups run along
+// the slots, so a wave's 64 slots x 32 rows hold two groups a row: lane l loads
+// the scale bytes of row i0 + l % 32 for the group its own slot is in, as the
+// bf16 values 2^X (gate | up << 16; byte 0: the subnormal 2^-127), and row k's
+// reach its 32 lanes by one swizzle each.  A code times its scale is exact
+// in fp32, and is the value a bf16 checkpoint of the dequantised tensor holds:
+// the two checkpoints give the same bits.
 template <int TS>
+__device__ __forceinline__ uint32_t epi_load_scales(const Phase1Args& p, int b, int64_t i0, int64_t s0, uint32_t live) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const uint32_t G = uint32_t(p.B / 32), plane = uint32_t(p.I) * G;
+  const auto rs = MX_RSRC(v2::make_rsrc(p.ck8_scales + int64_t(b) * 2 * plane, live * 2 * plane));
+  const uint32_t v = (uint32_t(i0) + (threadIdx.x & 31)) * G + uint32_t(s0 + threadIdx.x % TS) / 32;
+  const uint32_t g = __builtin_amdgcn_raw_buffer_load_b8(rs, v, 0, 0);
+  const uint32_t u = __builtin_amdgcn_raw_buffer_load_b8(rs, v, plane, 0);
+  return (g ? g << 7 : 0x40u) | (u ? u << 7 : 0x40u) << 16;
+#else
+  return 0;
+#endif
+}
+// gate and up from the codes w (gate | up << 16) of row K; ok 0 (a padding slot): zeros, whatever
+// the scale holds
+template <int C8, int K>
+__device__ __forceinline__ void epi_decode(uint32_t w, uint32_t sc, uint32_t ok, float& g, float& u) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const uint32_t s = uint32_t(__builtin_amdgcn_ds_swizzle(int(sc), K << 5)) & ok;
+  if constexpr (C8 == kE4M3) {
+    g = __builtin_amdgcn_cvt_f32_fp8(int(w), 0) * lo_bf16(s);
+    u = __builtin_amdgcn_cvt_f32_fp8(int(w), 2) * hi_bf16(s);
+  } else {
+    g = __builtin_amdgcn_cvt_f32_bf8(int(w), 0) * lo_bf16(s);
+    u = __builtin_amdgcn_cvt_f32_bf8(int(w), 2) * hi_bf16(s);
+  }
+#endif
+}
+
+template <int TS, int C8 = -1>
 __device__ __forceinline__ void epi_load_gu(const Phase1Args& p, int b, int64_t ti0, int64_t gstride, int64_t s0,
                                             EpiGU& x) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -125,6 +163,20 @@ __device__ __forceinline__ void epi_load_gu(const Phase1Args& p, int b, int64_t 
   if (i0 < p.I) {
     const bool ok = p.slot_tok[slot] >= 0;
     const uint32_t live = s0 < p.flag[b] ? 1u : 0u;
+    if constexpr (C8 >= 0) {
+      const uint32_t plane = uint32_t(p.I * p.B);
+      const auto rc = MX_RSRC(v2::make_rsrc(p.ck8_codes + int64_t(b) * 2 * p.I * p.B, live * 2 * plane));
+      const uint32_t vc = ok ? uint32_t(s0 + sl) : v2::kOOB;
+      x.sc = epi_load_scales<TS>(p, b, i0, s0, live);
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        const uint32_t row = __builtin_amdgcn_readfirstlane(uint32_t((i0 + k) * p.B));
+        const uint16_t g = __builtin_amdgcn_raw_buffer_load_b8(rc, vc, row, kNT);
+        const uint16_t u = __builtin_amdgcn_raw_buffer_load_b8(rc, vc, row + plane, kNT);
+        x.gu[k] = __builtin_bit_cast(uint32_t, epi_us2{g, u});
+      }
+      return;
+    }
     const auto rc = MX_RSRC(v2::make_rsrc(p.ckpt + int64_t(b) * 2 * p.I * p.B, live * uint32_t(p.I * p.B * 4)));
     const uint32_t vc = ok ? uint32_t((s0 + sl) * 2) : v2::kOOB;
 #pragma unroll
@@ -146,12 +198,13 @@ __device__ __forceinline__ void epi_load_gu(const Phase1Args& p, int b, int64_t 
 // pass 1 then runs its 32 rows in two halves so that the extra loads fit in
 // registers.  lds: EpiLds<TS>::BYTES bytes (16-byte aligned), holding the
 // chunk's dS on entry when DS_LDS, which also takes the checkpoint values from
-// pre (loaded by epi_load_gu).  Ends with pass 2's stores issued; the caller
+// pre (loaded by epi_load_gu).  C8: the MXFP8 checkpoint's format, -1: bf16.  Ends with pass 2's stores issued; the caller
 // synchronises before it reuses the LDS.
-template <int FG, int ONI, int TS, bool CK, bool GEGLU, bool DS_LDS>
+template <int FG, int ONI, int TS, bool CK, bool GEGLU, bool DS_LDS, int C8 = -1>
 __device__ __forceinline__ void epi_chunk(const Phase1Args& p, int b, int64_t ti0, int64_t gstride, int64_t s0,
                                           uint8_t* lds, const EpiGU* pre = nullptr) {
   static_assert(!(CK && DS_LDS), "supplied checkpoints take the stand-alone epilogue");
+  static_assert(!CK || C8 < 0, "the MXFP8 checkpoint comes alone");
   using L = EpiLds<TS>;
   constexpr int NG = L::NG, GSW = L::GSW, ISH = L::ISH;
   uint32_t* stg_gu = reinterpret_cast<uint32_t*>(lds);
@@ -183,29 +236,52 @@ __device__ __forceinline__ void epi_chunk(const Phase1Args& p, int b, int64_t ti
     // descriptors have no records, so every load reads zero without memory traffic
     const uint32_t live = s0 < p.flag[b] ? 1u : 0u;
     const auto rd = MX_RSRC(v2::make_rsrc(p.ds + int64_t(b) * p.I * p.B, live * uint32_t(p.I * p.B * 4)));
-    const auto rc = MX_RSRC(v2::make_rsrc(p.ckpt + int64_t(b) * 2 * p.I * p.B, live * uint32_t(p.I * p.B * 4)));
+    const auto rc = MX_RSRC(C8 >= 0 ? v2::make_rsrc(p.ck8_codes + int64_t(b) * 2 * p.I * p.B, live * uint32_t(p.I * p.B * 2))
+                                    : v2::make_rsrc(p.ckpt + int64_t(b) * 2 * p.I * p.B, live * uint32_t(p.I * p.B * 4)));
     // padding slots read dS and the checkpoint as zeros (their dS may be unwritten)
     const uint32_t vd = ok ? uint32_t((s0 + sl) * 4) : v2::kOOB, vc = ok ? uint32_t((s0 + sl) * 2) : v2::kOOB;
     // element k of the 32: its intermediate operand goes to half k & 1 of itp[k / 2]
     auto put_it = [&](int k, uint16_t v) {
       itp[k >> 1] = (k & 1) ? (itp[k >> 1] & 0xffffu) | (uint32_t(v) << 16) : uint32_t(v);
     };
+    // gate and up of element K from the checkpoint word w
+    const uint32_t okm = ok ? 0xffffffffu : 0u;
+    auto put = [&](auto K, uint32_t w, uint32_t sc, float d) {
+      constexpr int k = K;
+      float g = lo_bf16(w), u = hi_bf16(w);
+      if constexpr (C8 >= 0) epi_decode<C8, k>(w, sc, okm, g, u);
+      uint16_t v;
+      gu[k] = swiglu_bwd<GEGLU>(on_i, d, g, u, a, false, 0.f, false, 0.f, false, 0, daff, v);
+      put_it(k, v);
+      amg = fmaxf(amg, fabsf(lo_bf16(gu[k])));
+      amu = fmaxf(amu, fabsf(hi_bf16(gu[k])));
+    };
     if constexpr (!CK && DS_LDS) {
       // dS from LDS, read as it is used; all of it is read before the barrier,
       // after which the staging overwrites it
       if (rows) {
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const float x = dsl[(r0 + k) * L::DSW + sl];
-          uint16_t v;
-          gu[k] = swiglu_bwd<GEGLU>(on_i, ok ? x : 0.f, lo_bf16(pre->gu[k]), hi_bf16(pre->gu[k]), a, false,
-                                    0.f, false, 0.f, false, 0, daff, v);
-          put_it(k, v);
-          amg = fmaxf(amg, fabsf(lo_bf16(gu[k])));
-          amu = fmaxf(amu, fabsf(hi_bf16(gu[k])));
-        }
+        v2::static_for<32>([&](auto K) {
+          const float x = dsl[(r0 + int(K)) * L::DSW + sl];
+          put(K, pre->gu[int(K)], pre->sc, ok ? x : 0.f);
+        });
       }
       __syncthreads();
+    } else if constexpr (C8 >= 0) {
+      uint32_t cw[32];   // codes: gate | up << 16
+      float dv[32];
+      if (rows) {
+        const uint32_t vb = ok ? uint32_t(s0 + sl) : v2::kOOB;
+        const uint32_t sc = epi_load_scales<TS>(p, b, i0, s0, live);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const uint32_t row = __builtin_amdgcn_readfirstlane(uint32_t((i0 + k) * p.B));
+          dv[k] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rd, vd, row * 4, kNT));
+          const uint16_t g = __builtin_amdgcn_raw_buffer_load_b8(rc, vb, row, kNT);
+          const uint16_t u = __builtin_amdgcn_raw_buffer_load_b8(rc, vb, row + uint32_t(p.I * p.B), kNT);
+          cw[k] = __builtin_bit_cast(uint32_t, epi_us2{g, u});
+        }
+        v2::static_for<32>([&](auto K) { put(K, cw[int(K)], sc, dv[int(K)]); });
+      }
     } else if constexpr (!CK) {
       uint16_t gb[32], ub[32];
       float dv[32];

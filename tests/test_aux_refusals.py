@@ -132,3 +132,31 @@ def test_bindings_check_their_tensors():
         mx.mxfp8_gated_act_bwd(x, c, s)
     with pytest.raises(ValueError, match="token_position_to_id"):
         mx.mxfp8_gated_act_bwd(x[:, 0].contiguous(), c, s, token_position_to_id=torch.zeros(64, dtype=torch.int32), T=1)
+
+
+def test_moe_bwd_checkpoint_refusals():
+    """The MXFP8 gate/up checkpoint of moe_bwd_mxfp8: in validation, before any device access."""
+    from test_abi import _fake_args
+    L = mx.lib()
+    f = 0x10000
+
+    def run(**kw):
+        a = _fake_args(mx, L)
+        for k, v in kw.items():
+            setattr(a, k, v)
+        return L.moe_bwd_mxfp8(C.byref(a), C.c_void_p(f), 1024, None)
+
+    ck = dict(gate_up_proj_act_checkpoint_T=None, gate_up_checkpoint_codes=f, gate_up_checkpoint_scales=f)
+    assert run(**ck) == 3                                     # accepted up to the workspace
+    assert run(gate_up_proj_act_checkpoint_T=None) == 1
+    assert run(**{**ck, "gate_up_proj_act_checkpoint_T": f}) == 1 and "not both" in mx.last_error()
+    assert run(**{**ck, "gate_up_checkpoint_scales": None}) == 1 and "together" in mx.last_error()
+    assert run(gate_up_checkpoint_scales=f) == 1 and "together" in mx.last_error()
+    assert run(**ck, fmt_checkpoint=2) == 1 and "fmt_checkpoint" in mx.last_error()
+    assert run(**{**ck, "gate_up_checkpoint_codes": f + 8}) == 1 and "aligned" in mx.last_error()
+    assert run(**{**ck, "gate_up_checkpoint_scales": f + 4}) == 1 and "aligned" in mx.last_error()
+    assert run(**ck, gate_act_checkpoint_T=f) == 2 and run(**ck, intermediate_checkpoint_T=f) == 2
+    # the workspace of an E5M2 checkpoint holds the product that its epilogue reads
+    a, b = _fake_args(mx, L), _fake_args(mx, L)
+    b.gate_up_checkpoint_codes, b.fmt_checkpoint = f, mx.E5M2
+    assert L.moe_bwd_mxfp8_workspace_size(C.byref(b)) > L.moe_bwd_mxfp8_workspace_size(C.byref(a))
