@@ -822,7 +822,8 @@ static int router_shape(const char* what, int64_t T, int64_t E, int64_t K, int t
 int moe_router_fwd(int mode, int64_t T, int64_t E, int64_t K, const void* logits, int logits_type,
                    const uint8_t* token_mask, int renorm, int32_t* topk_idx, float* topk_scores,
                    float* affinities, void* stream) {
-  static_assert(MXFP8_ROUTER_MAX_EXPERTS == mx::kRouterFwdMaxExperts, "the header's bound");
+  static_assert(MXFP8_ROUTER_MAX_EXPERTS == mx::kRouterFwdMaxExperts && MXFP8_ROUTER_MAX_K == mx::kRouterMaxK,
+                "the header's bounds");
   if (mode != MXFP8_ROUTER_SOFTMAX_OVER_TOPK && mode != MXFP8_ROUTER_TOPK_OVER_SOFTMAX && mode != MXFP8_ROUTER_TOPK)
     return fail(MXFP8_ERR_INVALID_ARG, "moe_router_fwd: unknown mode %d", mode);
   int rc = router_shape("moe_router_fwd", T, E, K, logits_type);
@@ -857,7 +858,7 @@ static size_t balance_regions(int64_t T, int64_t E, int64_t S, uint8_t* base, mx
   put(p->part_c, recs * E);
   put(p->part_z, recs);
   put(p->part_n, recs);
-  put(p->term, S * ((E + 63) / 64));
+  put(p->term, S * ((E + 31) / 32));
   put(p->term_z, S);
   put(p->done, 1);
   return o;

@@ -20,21 +20,20 @@
 // finish the sequences' terms in sequence order: no floating-point atomics, the
 // same bits on every run.
 // HBM-bound: E logits and K ids a token; backward E logits read, E gradients
-// written.
-#include <type_traits>
-
+// written (rows in registers, router_rows.hpp).
 #include "kernels.hpp"
-#include "mx_device.hpp"
-#include "segment.hpp"
+#include "router_rows.hpp"
 
 namespace mx {
 
 namespace {
-constexpr int kThreads = 256;
-constexpr int kTile = 64;   // experts of one workgroup of the second launch
+constexpr int kBwdThreads = 256;
+constexpr int kSumThreads = 1024;
+constexpr int kTile = 32;        // experts of one workgroup of the second launch
+constexpr int kChunks = 512;     // two workgroups of the first launch per CU
 
-__device__ __forceinline__ float load_logit(const float* p) { return *p; }
-__device__ __forceinline__ float load_logit(const uint16_t* p) { return bf16_to_f32(*p); }
+// threads of the chunk kernel: its LDS holds a row of E sums per wave
+constexpr int chunk_threads(int EPL) { return EPL > 8 ? 256 : 512; }
 
 // first token of sequence s (s in [0, S]), kept in [0, T]
 __device__ __forceinline__ int64_t seq_at(const BalanceArgs& p, int64_t s) {
@@ -42,51 +41,80 @@ __device__ __forceinline__ int64_t seq_at(const BalanceArgs& p, int64_t s) {
   const int64_t v = p.seq[s];
   return v < 0 ? 0 : v > p.T ? p.T : v;
 }
-// the last s in [0, S] whose sequence starts at or before token t; -1 if none
-__device__ __forceinline__ int64_t seq_of(const BalanceArgs& p, int64_t t) {
-  if (!p.seq) return t < p.T ? 0 : 1;
-  int64_t lo = 0, hi = p.S + 1;   // entries before lo are <= t, from hi on > t
-  while (lo < hi) {
-    const int64_t mid = (lo + hi) >> 1;
-    if (seq_at(p, mid) <= t) lo = mid + 1;
-    else hi = mid;
-  }
-  return lo - 1;
-}
 
-// One row's softmax over all experts by L lanes: x[j] becomes p at column
-// lane + L j; returns false where no logit is above -inf (x is 0 then).
-template <int L, int EPL, class LT>
-__device__ __forceinline__ bool row_softmax(const LT* row, int E, int lane, float (&x)[EPL], float& lse) {
-  float m = -INFINITY;
-#pragma unroll
-  for (int j = 0; j < EPL; ++j) {
-    const int e = lane + L * j;
-    x[j] = e < E ? load_logit(row + e) : -INFINITY;
+// The part of seq_starts around token t, found by the whole wave, 64 entries a
+// step: `lo` and this lane's entry lo + lane (past every token behind the last
+// one), such that lo = 0 or entry lo is at or before t, and the first entry past
+// t is among the 64 or just behind them.
+__device__ __forceinline__ int64_t seq_window(const BalanceArgs& p, int64_t t, int64_t& v) {
+  const int lane = threadIdx.x & 63;
+  int64_t lo = 0, n = p.S + 1;
+  while (n > 64) {
+    const int64_t step = (n + 63) / 64;
+    const int c = __popcll(__ballot(lane * step < n && seq_at(p, lo + lane * step) <= t));
+    if (c == 0) break;   // entry 0 is past t
+    n = n - (c - 1) * step < step ? n - (c - 1) * step : step;
+    lo += (c - 1) * step;
   }
-#pragma unroll
-  for (int j = 0; j < EPL; ++j) m = fmaxf(m, x[j]);
-  m = seg::max<L>(m);
-  const bool some = m > -INFINITY;
-  float s = 0.f;
-#pragma unroll
-  for (int j = 0; j < EPL; ++j) {
-    x[j] = some && lane + L * j < E ? expf(x[j] - m) : 0.f;
-    s += x[j];
+  v = lo + lane <= p.S ? seq_at(p, lo + lane) : p.T + 1;
+  return lo;
+}
+// The first sequence that may hold token t (the last one that starts at or before it, or
+// the first) and its bounds a, b, for the whole wave.
+__device__ __forceinline__ int64_t seq_of_wave(const BalanceArgs& p, int64_t t, int64_t& a, int64_t& b) {
+  a = 0;
+  b = p.T;
+  if (!p.seq) return 0;
+  int64_t v;
+  const int64_t lo = seq_window(p, t, v);
+  const int c = __popcll(__ballot(v <= t));
+  const int64_t s = lo + c > 0 ? lo + c - 1 : 0;
+  if (c > 0 && c < 64) {
+    a = __shfl(int(v), c - 1, 64);   // T < 2^31; the sentinel T + 1 only where s = S
+    b = __shfl(int(v), c, 64);
+  } else {
+    a = seq_at(p, s);
+    b = seq_at(p, s < p.S ? s + 1 : s);
   }
-  s = seg::sum<L>(s);
-  const float inv = some ? 1.f / s : 0.f;
-#pragma unroll
-  for (int j = 0; j < EPL; ++j) x[j] *= inv;
-  lse = some ? m + logf(s) : 0.f;
-  return some;
+  return s;
+}
+// The same for each of the wave's 64 / L rows t0, t0 + 1, ... by its own lanes.
+template <int L>
+__device__ __forceinline__ int64_t seq_of_rows(const BalanceArgs& p, int64_t t0) {
+  if (!p.seq) return t0 < p.T ? 0 : 1;   // rows past T are not looked at
+  constexpr int R = 64 / L;
+  const int lane = threadIdx.x & 63;
+  int64_t v;
+  const int64_t lo = seq_window(p, t0, v);
+  int c = __popcll(__ballot(v <= t0));
+  const uint64_t end = __ballot(v <= t0 + R - 1);
+  if (end == ~uint64_t(0)) {   // starts past the window may lie among these rows: each row by itself
+    const int64_t t = t0 + lane / L;
+    int64_t l = lo, h = p.S + 1;
+    while (l < h) {
+      const int64_t mid = (l + h) >> 1;
+      if (seq_at(p, mid) <= t) l = mid + 1;
+      else h = mid;
+    }
+    return l - 1;
+  }
+  if (__popcll(end) != c) {
+#pragma unroll 4
+    for (int r = 1; r < R; ++r) {
+      const int k = __popcll(__ballot(v <= t0 + r));
+      if (lane / L == r) c = k;
+    }
+  }
+  return lo - 1 + c;
 }
 }  // namespace
 
-template <int L, int EPL, class LT>
-__global__ void __launch_bounds__(kThreads) balance_chunk_kernel(BalanceArgs p) {
-  constexpr int R = kThreads / L;          // rows at a time
-  constexpr int W = kThreads / 64;
+template <int L, int EPL, bool VEC, class LT>
+__global__ void __launch_bounds__(chunk_threads(EPL)) balance_chunk_kernel(BalanceArgs p) {
+  constexpr int THREADS = chunk_threads(EPL);
+  constexpr int R = THREADS / L;   // rows at a time
+  constexpr int W = THREADS / 64;
+  constexpr int IDS = (kRouterMaxK + L - 1) / L;   // ids of one lane, K <= 32
   __shared__ float lp[W][L * EPL];
   __shared__ int hist[L * EPL];
   __shared__ float lz[W];
@@ -97,49 +125,67 @@ __global__ void __launch_bounds__(kThreads) balance_chunk_kernel(BalanceArgs p) 
   const int64_t c0 = int64_t(blockIdx.x) * p.chunk;
   const int64_t c1 = c0 + p.chunk < p.T ? c0 + p.chunk : p.T;
   if (c0 >= c1) return;
-  int64_t s = seq_of(p, c0);
-  for (s = s < 0 ? 0 : s; s < p.S; ++s) {
-    const int64_t a = seq_at(p, s), b = seq_at(p, s + 1);
+  const LT* logits = static_cast<const LT*>(p.logits);
+  // a row and its ids are loaded one round ahead, the first ones while the
+  // sequence is looked up
+  float nx[EPL];
+  int nid[IDS];
+  bool nlive = false;
+  int64_t nt = -1;
+  auto fetch = [&](int64_t t) {
+    nt = t;
+    if (t >= c1) return;
+    rows::load<EPL, VEC>(logits + t * p.E, E, lane, nx);
+#pragma unroll
+    for (int k = 0; k < IDS; ++k) nid[k] = lane + L * k < K ? p.idx[t * K + lane + L * k] : -1;
+    nlive = !p.mask || p.mask[t] != 0;
+  };
+  fetch(c0 + slot);
+  int64_t a, b;
+  int64_t s = seq_of_wave(p, c0, a, b);
+  for (; s < p.S; ++s, a = b, b = seq_at(p, s < p.S ? s + 1 : s)) {
     if (a >= c1) break;
     const int64_t lo = a > c0 ? a : c0, hi = b < c1 ? b : c1;
     if (lo >= hi) continue;
-    for (int e = threadIdx.x; e < E; e += kThreads) hist[e] = 0;
+    for (int e = threadIdx.x; e < E; e += THREADS) hist[e] = 0;
     __syncthreads();
     float acc[EPL];
 #pragma unroll
     for (int j = 0; j < EPL; ++j) acc[j] = 0.f;
-    float z2 = 0.f;
-    int n = 0;
+    float z2 = 0.f, n = 0.f;   // n: whole numbers, at most a chunk's tokens
     for (int64_t t = lo + slot; t < hi; t += R) {
-      if (p.mask && !p.mask[t]) continue;
+      if (t != nt) fetch(t);
       float x[EPL], lse;
-      if (!row_softmax<L, EPL>(static_cast<const LT*>(p.logits) + t * p.E, E, lane, x, lse)) continue;
+      int id[IDS];
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) x[j] = nx[j];
+#pragma unroll
+      for (int k = 0; k < IDS; ++k) id[k] = nid[k];
+      const bool live = nlive;
+      fetch(t + R);
+      if (!live || !rows::softmax<L, EPL>(x, lse)) continue;
 #pragma unroll
       for (int j = 0; j < EPL; ++j) acc[j] += x[j];
       if (lane == 0) {
         z2 += lse * lse;
-        ++n;
+        n += 1.f;
       }
-      for (int k = lane; k < K; k += L) {
-        const int e = p.idx[t * K + k];
-        if (e >= 0 && e < E) atomicAdd(&hist[e], 1);
-      }
+#pragma unroll
+      for (int k = 0; k < IDS; ++k)
+        if (id[k] >= 0 && id[k] < E) atomicAdd(&hist[id[k]], 1);
     }
     // the wave's row slots, then the waves
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
-      float v = acc[j];
-      for (int o = L; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
-      if ((threadIdx.x & 63) < L) lp[wave][lane + L * j] = v;
+      const float v = seg::across<L>(acc[j]);
+      if ((threadIdx.x & 63) < L) lp[wave][lane * EPL + j] = v;
     }
-    for (int o = 1; o < 64; o <<= 1) {
-      z2 += __shfl_xor(z2, o, 64);
-      n += __shfl_xor(n, o, 64);
-    }
-    if ((threadIdx.x & 63) == 0) { lz[wave] = z2; ln[wave] = n; }
+    z2 = seg::sum<64>(z2);
+    n = seg::sum<64>(n);
+    if ((threadIdx.x & 63) == 0) { lz[wave] = z2; ln[wave] = int(n); }
     __syncthreads();
     const int64_t rec = int64_t(blockIdx.x) + s;
-    for (int e = threadIdx.x; e < E; e += kThreads) {
+    for (int e = threadIdx.x; e < E; e += THREADS) {
       float v = lp[0][e];
 #pragma unroll
       for (int w = 1; w < W; ++w) v += lp[w][e];
@@ -158,188 +204,221 @@ __global__ void __launch_bounds__(kThreads) balance_chunk_kernel(BalanceArgs p) 
   }
 }
 
-// Grid (S, tiles of kTile experts): thread (q, e) adds every fourth record of
-// its sequence for expert e.
-__global__ void __launch_bounds__(kThreads) balance_sum_kernel(BalanceArgs p) {
-  constexpr int Q = kThreads / kTile;
-  __shared__ float sp[Q][kTile];
-  __shared__ int sc[Q][kTile];
-  __shared__ int sn[kThreads];
-  __shared__ float sz[kThreads];
+// Values that the last workgroup reads from the others: stored and loaded as
+// agent-scope atomics, which pass through the XCDs' L2s, and waited for before
+// the workgroup counts itself as done.  (Fences would write back and
+// invalidate whole L2s: 3 of the kernel's 8 us.)
+template <class T>
+__device__ __forceinline__ void publish(T* p, T v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <class T>
+__device__ __forceinline__ T published(const T* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Grid (S, tiles of kTile experts): thread (q, col) adds every 32nd record of
+// its sequence for one expert, so that 512 records are 16 loads in flight.
+__global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(BalanceArgs p) {
+  constexpr int Q = kSumThreads / kTile, W = kSumThreads / 64;
+  static_assert(kTile == 32, "two record groups a wave");
+  __shared__ float sp[W][kTile], sz[W];
+  __shared__ int sc[W][kTile], sn[W];
   __shared__ bool last;
   const int64_t s = blockIdx.x;
-  const int tid = threadIdx.x, q = tid / kTile, col = tid % kTile;
+  const int tid = threadIdx.x, q = tid / kTile, col = tid % kTile, wave = tid >> 6;
   const int64_t e = int64_t(blockIdx.y) * kTile + col;
   const int64_t a = seq_at(p, s), b = seq_at(p, s + 1);
   const int64_t f = a < b ? a / p.chunk : 0, l = a < b ? (b - 1) / p.chunk : -1;   // its chunks
   float v = 0.f;
   int c = 0;
-  if (e < p.E)
+  if (e < p.E) {
+#pragma unroll 8
     for (int64_t k = f + q; k <= l; k += Q) {
       v += p.part_p[(k + s) * p.E + e];
       c += p.part_c[(k + s) * p.E + e];
     }
-  sp[q][col] = v;
-  sc[q][col] = c;
+  }
   int n = 0;
   float z = 0.f;
-  for (int64_t k = f + tid; k <= l; k += kThreads) {
+  for (int64_t k = f + tid; k <= l; k += kSumThreads) {
     n += p.part_n[k + s];
     z += p.part_z[k + s];
   }
-  sn[tid] = n;
-  sz[tid] = z;
-  __syncthreads();
-  for (int o = kThreads / 2; o; o >>= 1) {
-    if (tid < o) {
-      sn[tid] += sn[tid + o];
-      sz[tid] += sz[tid + o];
-    }
-    __syncthreads();
+  v += __shfl_xor(v, 32, 64);
+  c += __shfl_xor(c, 32, 64);
+  for (int o = 1; o < 64; o <<= 1) {
+    n += __shfl_xor(n, o, 64);
+    z += __shfl_xor(z, o, 64);
   }
-  n = sn[0];
-  if (q == 0) {
-    for (int i = 1; i < Q; ++i) {
+  if ((tid & 63) < kTile) {
+    sp[wave][col] = v;
+    sc[wave][col] = c;
+  }
+  if ((tid & 63) == 0) { sn[wave] = n; sz[wave] = z; }
+  __syncthreads();
+  if (tid < kTile) {
+    n = 0;
+    z = v = 0.f;
+    c = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
       v += sp[i][col];
       c += sc[i][col];
+      n += sn[i];
+      z += sz[i];
     }
     if (e < p.E) p.counts[s * p.E + e] = c;
     // the tile's share of sum_e c_se sum_t p_te / n_s^2
     double d = n > 0 ? double(c) * double(v) / (double(n) * double(n)) : 0.;
     for (int o = 1; o < kTile; o <<= 1) d += __shfl_xor(d, o, 64);
     if (tid == 0) {
-      p.term[s * gridDim.y + blockIdx.y] = d;
+      publish(&p.term[s * gridDim.y + blockIdx.y], d);
       if (blockIdx.y == 0) {
-        p.num[s] = n;
-        p.term_z[s] = sz[0];
+        publish(&p.num[s], n);
+        publish(&p.term_z[s], z);
       }
-      __threadfence();
-      last = atomicAdd(p.done, 1u) == gridDim.x * gridDim.y - 1;
+      last = gridDim.x * gridDim.y == 1;
+      if (!last) {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the published values have reached memory
+        last = __hip_atomic_fetch_add(p.done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x * gridDim.y - 1;
+      }
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
   }
   __syncthreads();
   if (!last) return;
-  __threadfence();
   // all sequences' terms, in an order that does not depend on who is last
-  __shared__ double db[kThreads], dz[kThreads];
-  __shared__ int di[kThreads], dl[kThreads];
+  __shared__ double db[W], dz[W];
+  __shared__ int di[W], dl[W];
   double tb = 0., tz = 0.;
   int all = 0, live = 0;
-  const volatile double* term = p.term;
-  const volatile float* term_z = p.term_z;
-  const volatile int32_t* num = p.num;
-  for (int64_t i = tid; i < p.S * gridDim.y; i += kThreads) tb += term[i];
-  for (int64_t i = tid; i < p.S; i += kThreads) {
-    tz += term_z[i];
-    all += num[i];
-    live += num[i] > 0;
+  for (int64_t i = tid; i < p.S * gridDim.y; i += kSumThreads) tb += published(&p.term[i]);
+  for (int64_t i = tid; i < p.S; i += kSumThreads) {
+    tz += published(&p.term_z[i]);
+    const int k = published(&p.num[i]);
+    all += k;
+    live += k > 0;
   }
-  db[tid] = tb; dz[tid] = tz; di[tid] = all; dl[tid] = live;
+  for (int o = 1; o < 64; o <<= 1) {
+    tb += __shfl_xor(tb, o, 64);
+    tz += __shfl_xor(tz, o, 64);
+    all += __shfl_xor(all, o, 64);
+    live += __shfl_xor(live, o, 64);
+  }
+  if ((tid & 63) == 0) { db[wave] = tb; dz[wave] = tz; di[wave] = all; dl[wave] = live; }
   __syncthreads();
-  for (int o = kThreads / 2; o; o >>= 1) {
-    if (tid < o) {
-      db[tid] += db[tid + o];
-      dz[tid] += dz[tid + o];
-      di[tid] += di[tid + o];
-      dl[tid] += dl[tid + o];
+  if (tid < W) {
+    tb = db[tid]; tz = dz[tid]; all = di[tid]; live = dl[tid];
+    for (int o = 1; o < W; o <<= 1) {
+      tb += __shfl_xor(tb, o, 64);
+      tz += __shfl_xor(tz, o, 64);
+      all += __shfl_xor(all, o, 64);
+      live += __shfl_xor(live, o, 64);
     }
-    __syncthreads();
-  }
-  if (tid == 0) {
-    all = di[0];
-    live = dl[0];
-    p.num[p.S] = live;
-    p.num[p.S + 1] = all;
-    p.loss[0] = live ? float(double(p.balance_coef) * double(p.E) * db[0] / (double(p.K) * live)) : 0.f;
-    p.loss[1] = all ? float(double(p.z_coef) * dz[0] / all) : 0.f;
+    if (tid == 0) {
+      p.num[p.S] = live;
+      p.num[p.S + 1] = all;
+      p.loss[0] = live ? float(double(p.balance_coef) * double(p.E) * tb / (double(p.K) * live)) : 0.f;
+      p.loss[1] = all ? float(double(p.z_coef) * tz / all) : 0.f;
+    }
   }
 }
 
-template <int L, int EPL, class LT>
-__global__ void __launch_bounds__(kThreads) balance_bwd_kernel(BalanceArgs p) {
-  const int lane = threadIdx.x % L;
-  const int64_t t = int64_t(blockIdx.x) * (kThreads / L) + threadIdx.x / L;
-  if (t >= p.T) return;   // whole segments leave together
-  const int E = int(p.E);
-  float* out = p.dlogits + t * p.E;
-  const int64_t s = seq_of(p, t);
+template <int L, int EPL, bool VEC, class LT>
+__global__ void __launch_bounds__(kBwdThreads) balance_bwd_kernel(BalanceArgs p) {
+  const int lane = threadIdx.x % L, slot = (threadIdx.x & 63) / L;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t0 = int64_t(blockIdx.x) * (kBwdThreads / L) + wave * (64 / L);   // the wave's first row
+  if (t0 >= p.T) return;   // whole waves leave
+  const bool in = slot < p.T - t0;
+  const int E = int(p.E), off = slot * E;   // 32-bit offsets from the wave's rows
+  const LT* logits = static_cast<const LT*>(p.logits) + t0 * p.E;
+  float* out = p.dlogits + t0 * p.E;
+  // the row is under way while its sequence is looked up
   float x[EPL], lse = 0.f;
-  bool part = s >= 0 && s < p.S && t < seq_at(p, s + 1) && (!p.mask || p.mask[t] != 0);
-  if (part) part = row_softmax<L, EPL>(static_cast<const LT*>(p.logits) + t * p.E, E, lane, x, lse);
-  if (!part) {
-    if (!p.accumulate)
-      for (int e = lane; e < E; e += L) out[e] = 0.f;
-    return;
+  bool part = in && (!p.mask || p.mask[t0 + slot] != 0);
+  if (in) {
+    rows::load<EPL, VEC>(logits + off, E, lane, x);
+  } else {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) x[j] = -INFINITY;
   }
   const float gb = p.dloss ? p.dloss[0] : 1.f, gz = p.dloss ? p.dloss[1] : 1.f;
-  const float n = float(p.num[s]), live = float(p.num[p.S]), all = float(p.num[p.S + 1]);
-  const float fb = gb * (p.balance_coef * float(p.E) / (live * float(p.K) * n)) / n;
-  const float fz = gz * (2.f * p.z_coef / all) * lse;
+  const float live = float(p.num[p.S]), all = float(p.num[p.S + 1]);
+  const int64_t s = seq_of_rows<L>(p, t0);
+  if (!in) return;
+  part = part && s >= 0 && s < p.S;
+  const float n = part ? float(p.num[s]) : 1.f;
+  part = rows::softmax<L, EPL>(x, lse) && part;
+  if (!part) {
+    if (!p.accumulate) {
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) x[j] = 0.f;
+      rows::store<EPL, VEC>(out + off, E, lane, x);
+    }
+    return;
+  }
+  const float rn = rows::rcp_fast(n);
+  const float fb = gb * (p.balance_coef * float(p.E) * rows::rcp_fast(live * float(p.K))) * rn * rn;
+  const float fz = gz * (2.f * p.z_coef * rows::rcp_fast(all)) * lse;
+  const int32_t* counts = p.counts + s * p.E + lane * EPL;
   float w[EPL], dot = 0.f;
+  if constexpr (VEC) {
+#pragma unroll
+    for (int q = 0; q < EPL; q += 4) {
+      const int4 c = lane * EPL + q < E ? *reinterpret_cast<const int4*>(counts + q) : int4{0, 0, 0, 0};
+      w[q] = float(c.x); w[q + 1] = float(c.y); w[q + 2] = float(c.z); w[q + 3] = float(c.w);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) w[j] = lane * EPL + j < E ? float(counts[j]) : 0.f;
+  }
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
-    const int e = lane + L * j;
-    w[j] = e < E ? fb * float(p.counts[s * p.E + e]) : 0.f;
+    w[j] *= fb;
     dot += w[j] * x[j];
   }
   dot = seg::sum<L>(dot) - fz;
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) {
-    const int e = lane + L * j;
-    if (e < E) {
-      const float d = x[j] * (w[j] - dot);
-      out[e] = p.accumulate ? out[e] + d : d;
-    }
+  for (int j = 0; j < EPL; ++j) x[j] *= w[j] - dot;
+  if (p.accumulate) {
+    rows::load<EPL, VEC>(static_cast<const float*>(out + off), E, lane, w);
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) x[j] += w[j];
   }
+  rows::store<EPL, VEC>(out + off, E, lane, x);
 }
 
-namespace {
-// f(L, EPL) for E experts: L = E / 8 rounded up to a power of two in [8, 64]
-template <int N> using Int = std::integral_constant<int, N>;
-template <class F>
-void by_experts(int64_t E, const F& f) {
-  if (E <= 8) f(Int<8>{}, Int<1>{});
-  else if (E <= 16) f(Int<8>{}, Int<2>{});
-  else if (E <= 32) f(Int<8>{}, Int<4>{});
-  else if (E <= 64) f(Int<8>{}, Int<8>{});
-  else if (E <= 128) f(Int<16>{}, Int<8>{});
-  else if (E <= 256) f(Int<32>{}, Int<8>{});
-  else if (E <= 512) f(Int<64>{}, Int<8>{});
-  else if (E <= 1024) f(Int<64>{}, Int<16>{});
-  else if (E <= 2048) f(Int<64>{}, Int<32>{});
-  else f(Int<64>{}, Int<64>{});
-}
-int rows_at_a_time(int64_t E) { return E <= 64 ? 32 : E <= 128 ? 16 : E <= 256 ? 8 : 4; }
-}  // namespace
-
-// Tokens of one chunk: one round of rows, or more where that would make over
-// 1024 chunks.
+// Tokens of one chunk: a round of the workgroup's rows, or as many as keep to
+// kChunks chunks.
 int64_t balance_chunk_tokens(int64_t T, int64_t E) {
-  const int64_t r = rows_at_a_time(E);
-  const int64_t c = (T + 1023) / 1024;
+  const int64_t r = chunk_threads(E > 512 ? 16 : 8) / rows::lanes(E);
+  const int64_t c = (T + kChunks - 1) / kChunks;
   return c <= r ? r : (c + r - 1) / r * r;
 }
 
 hipError_t launch_balance_fwd(const BalanceArgs& p, hipStream_t st) {
   const int64_t chunks = (p.T + p.chunk - 1) / p.chunk;
   const unsigned grid = unsigned(chunks > 0 ? chunks : 1);
-  by_experts(p.E, [&](auto L, auto EPL) {
-    if (p.bf16) balance_chunk_kernel<L(), EPL(), uint16_t><<<grid, kThreads, 0, st>>>(p);
-    else balance_chunk_kernel<L(), EPL(), float><<<grid, kThreads, 0, st>>>(p);
+  rows::by_experts(p.E, [&](auto L, auto EPL, auto vec) {
+    constexpr int threads = chunk_threads(EPL());
+    if (p.bf16) balance_chunk_kernel<L(), EPL(), vec(), uint16_t><<<grid, threads, 0, st>>>(p);
+    else balance_chunk_kernel<L(), EPL(), vec(), float><<<grid, threads, 0, st>>>(p);
   });
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  balance_sum_kernel<<<dim3(unsigned(p.S), unsigned((p.E + kTile - 1) / kTile)), kThreads, 0, st>>>(p);
+  balance_sum_kernel<<<dim3(unsigned(p.S), unsigned((p.E + kTile - 1) / kTile)), kSumThreads, 0, st>>>(p);
   return hipGetLastError();
 }
 
 hipError_t launch_balance_bwd(const BalanceArgs& p, hipStream_t st) {
   if (p.T <= 0) return hipSuccess;
-  const int64_t rows = rows_at_a_time(p.E);
-  const unsigned grid = unsigned((p.T + rows - 1) / rows);
-  by_experts(p.E, [&](auto L, auto EPL) {
-    if (p.bf16) balance_bwd_kernel<L(), EPL(), uint16_t><<<grid, kThreads, 0, st>>>(p);
-    else balance_bwd_kernel<L(), EPL(), float><<<grid, kThreads, 0, st>>>(p);
+  const int64_t r = kBwdThreads / rows::lanes(p.E);
+  const unsigned grid = unsigned((p.T + r - 1) / r);
+  rows::by_experts(p.E, [&](auto L, auto EPL, auto vec) {
+    if (p.bf16) balance_bwd_kernel<L(), EPL(), vec(), uint16_t><<<grid, kBwdThreads, 0, st>>>(p);
+    else balance_bwd_kernel<L(), EPL(), vec(), float><<<grid, kBwdThreads, 0, st>>>(p);
   });
   return hipGetLastError();
 }

@@ -102,6 +102,7 @@ hipError_t launch_router_bwd(const RouterArgs& p, hipStream_t st);
 
 // router_fwd.hip -- the router forward; balance.hip -- its auxiliary losses
 constexpr int64_t kRouterFwdMaxExperts = 4096;
+constexpr int kRouterMaxK = 32;
 struct RouterFwdArgs {
   int mode;                   // kRouter*
   int renorm;
@@ -136,7 +137,7 @@ struct BalanceArgs {
   int32_t* part_c;            // [chunks+S][E]
   float* part_z;              // [chunks+S]
   int32_t* part_n;            // [chunks+S]
-  double* term;               // [S][ceil(E/64)]
+  double* term;               // [S][ceil(E/32)]
   float* term_z;              // [S]
   unsigned* done;
 };

@@ -1,0 +1,129 @@
+// router_rows.hpp -- rows of router logits in registers, shared by the router
+// forward and the auxiliary losses.  L lanes take one row, EPL consecutive
+// columns each: 8 (L = E / 8 rounded up to a power of two, from one lane for 8
+// experts to a whole wave for 512), more past 512 experts.  Eight columns are
+// one 16-byte access of bf16 or two of fp32 where E % 8 == 0 (VEC: every row
+// and every lane's run is then aligned, and a lane holds 8 columns or none).
+#pragma once
+#include <type_traits>
+
+#include "kernels.hpp"
+#include "mx_device.hpp"
+#include "segment.hpp"
+
+namespace mx {
+namespace rows {
+
+// exp(d) for d <= 0 through v_exp_f32: d * log2 e rounds once, 2^-24 |d| of the
+// result (results under 2^-126 may be 0).
+__device__ __forceinline__ float exp_fast(float d) { return __builtin_amdgcn_exp2f(d * 1.4426950408889634f); }
+
+// log(s) through v_log_f32, 1 / s through v_rcp_f32: within about an ulp, s in [1, 4096]
+__device__ __forceinline__ float log_fast(float s) { return __builtin_amdgcn_logf(s) * 0.6931471805599453f; }
+__device__ __forceinline__ float rcp_fast(float s) { return __builtin_amdgcn_rcpf(s); }
+
+__device__ __forceinline__ float value(float v) { return v; }
+__device__ __forceinline__ float value(uint16_t v) { return bf16_to_f32(v); }
+
+// x[j] = logit of column lane * EPL + j, -inf past E
+template <int EPL, bool VEC, class LT>
+__device__ __forceinline__ void load(const LT* row, int E, int lane, float (&x)[EPL]) {
+  const int c0 = lane * EPL;
+  if constexpr (VEC) {
+#pragma unroll
+    for (int q = 0; q < EPL; q += 8) {
+      if (c0 + q < E) {
+        if constexpr (std::is_same_v<LT, float>) {
+          const float4 a = *reinterpret_cast<const float4*>(row + c0 + q);
+          const float4 b = *reinterpret_cast<const float4*>(row + c0 + q + 4);
+          x[q] = a.x; x[q + 1] = a.y; x[q + 2] = a.z; x[q + 3] = a.w;
+          x[q + 4] = b.x; x[q + 5] = b.y; x[q + 6] = b.z; x[q + 7] = b.w;
+        } else {
+          const uint4 a = *reinterpret_cast<const uint4*>(row + c0 + q);
+          const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            x[q + 2 * k] = __uint_as_float(w[k] << 16);
+            x[q + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[q + j] = -INFINITY;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {   // past E: the last column again, so that no load hangs on a branch
+      const float v = value(row[c0 + j < E ? c0 + j : E - 1]);
+      x[j] = c0 + j < E ? v : -INFINITY;
+    }
+  }
+}
+
+// columns lane * EPL + j of an fp32 row
+template <int EPL, bool VEC>
+__device__ __forceinline__ void store(float* row, int E, int lane, const float (&x)[EPL]) {
+  const int c0 = lane * EPL;
+  if constexpr (VEC) {
+#pragma unroll
+    for (int q = 0; q < EPL; q += 4)
+      if (c0 + q < E) *reinterpret_cast<float4*>(row + c0 + q) = float4{x[q], x[q + 1], x[q + 2], x[q + 3]};
+  } else {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+      if (c0 + j < E) row[c0 + j] = x[j];
+  }
+}
+
+// Softmax of a row over its L lanes: x becomes p; false (x = 0) where no logit
+// is above -inf.
+template <int L, int EPL>
+__device__ __forceinline__ bool softmax(float (&x)[EPL], float& lse) {
+  float m = x[0];
+#pragma unroll
+  for (int j = 1; j < EPL; ++j) m = fmaxf(m, x[j]);
+  m = seg::max<L>(m);
+  const bool some = m > -INFINITY;
+  if (!some) m = 0.f;   // exp(-inf - 0) = 0
+  float s = 0.f;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    x[j] = exp_fast(x[j] - m);
+    s += x[j];
+  }
+  s = seg::sum<L>(s);
+  const float inv = some ? rcp_fast(s) : 0.f;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) x[j] *= inv;
+  lse = some ? m + log_fast(s) : 0.f;
+  return some;
+}
+
+// f(L, EPL, VEC) for E experts
+template <int N> using Int = std::integral_constant<int, N>;
+template <class F>
+void by_experts(int64_t E, const F& f) {
+  auto go = [&](auto L, auto EPL) {
+    if (E % 8 == 0) f(L, EPL, std::true_type{});
+    else f(L, EPL, std::false_type{});
+  };
+  if (E <= 8) go(Int<1>{}, Int<8>{});
+  else if (E <= 16) go(Int<2>{}, Int<8>{});
+  else if (E <= 32) go(Int<4>{}, Int<8>{});
+  else if (E <= 64) go(Int<8>{}, Int<8>{});
+  else if (E <= 128) go(Int<16>{}, Int<8>{});
+  else if (E <= 256) go(Int<32>{}, Int<8>{});
+  else if (E <= 512) go(Int<64>{}, Int<8>{});
+  else if (E <= 1024) go(Int<64>{}, Int<16>{});
+  else if (E <= 2048) go(Int<64>{}, Int<32>{});
+  else go(Int<64>{}, Int<64>{});
+}
+inline int lanes(int64_t E) {
+  int l = 1;
+  while (l < 64 && l * 8 < E) l *= 2;
+  return l;
+}
+
+}  // namespace rows
+}  // namespace mx

@@ -58,5 +58,30 @@ __device__ __forceinline__ uint32_t umin(uint32_t v) {
   return reduce<L>(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
 }
 
+
+// Sum over the lanes of a wave that are congruent modulo L (the same column of
+// the wave's 64 / L segments), in every lane: exact exchanges (quad_perm,
+// rotations within 16 lanes, row swaps), since lanes of a segment differ.
+constexpr int kRor4 = 0x124, kRor8 = 0x128;
+template <int L>
+__device__ __forceinline__ float across(float v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  auto add = [&](uint32_t b) { v += __uint_as_float(b); };
+  if constexpr (L <= 1) add(dpp<kXor1>(__float_as_uint(v)));
+  if constexpr (L <= 2) add(dpp<kXor2>(__float_as_uint(v)));
+  if constexpr (L <= 8) add(dpp<kRor8>(__float_as_uint(v)));
+  if constexpr (L <= 4) add(dpp<kRor4>(__float_as_uint(v)));
+  if constexpr (L <= 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  if constexpr (L <= 32) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+#endif
+  return v;
+}
+
 }  // namespace seg
 }  // namespace mx
