@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+from functools import lru_cache
 from typing import Optional
 
 import torch
@@ -441,10 +442,17 @@ def moe_router_bwd(mode: int, topk_idx: torch.Tensor, *, dscores: Optional[torch
 
 
 # ----------------------------------------------------------------------------- router forward, auxiliary losses
+# Small calls cost more on the host than on the GPU: arguments that are right
+# take one comparison each, tensors made here none.
+_empty = torch.empty
+
+
 def _tensor(t: Optional[torch.Tensor], dtype, shape, device, name):
     """The address of an argument that must be a contiguous `dtype` tensor of `shape` on `device` (None: NULL)."""
     if t is None:
         return None
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
@@ -453,29 +461,46 @@ def _tensor(t: Optional[torch.Tensor], dtype, shape, device, name):
 
 
 def _mask(t: Optional[torch.Tensor], T, device):
-    if t is not None and t.dtype == torch.bool:
-        t = t.view(torch.uint8)
-    return _tensor(t, torch.uint8, (T,), device, "token_mask")
+    if t is None:
+        return None
+    return _tensor(t, torch.bool if t.dtype is torch.bool else torch.uint8, (T,), device, "token_mask")
 
 
-def _logits_type(logits: torch.Tensor, name):
+def _logits(logits: torch.Tensor, name):
+    """(T, E, device, address, type) of a [T, E] logits argument."""
     if logits.dim() != 2:
         raise ValueError(f"{name}: logits must be [T, E]")
-    if logits.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"{name}: logits must be float32 or bfloat16, got {logits.dtype}")
-    return 0 if logits.dtype == torch.float32 else 1
+    dtype = logits.dtype
+    if dtype is torch.float32:
+        typ = 0
+    elif dtype is torch.bfloat16:
+        typ = 1
+    else:
+        raise TypeError(f"{name}: logits must be float32 or bfloat16, got {dtype}")
+    T, E = logits.shape
+    return T, E, logits.device, _dev(logits, dtype, "logits"), typ
+
+
+def _sequences(seq_starts: Optional[torch.Tensor], device):
+    """(S, address) of an optional [S+1] tensor of sequence starts."""
+    if seq_starts is None:
+        return 1, None
+    n = seq_starts.numel()
+    return n - 1, _tensor(seq_starts, torch.int32, (n,), device, "seq_starts")
 
 
 def _call(device, name, *args):
     """One library call on `device`'s current stream (the null stream stands for the current device's, so
     that device is made current)."""
     f = getattr(lib(), name)
-    if torch.cuda.current_device() == device.index:
-        rc = f(*args, torch.cuda.current_stream(device).cuda_stream)
+    index = device.index
+    if torch.cuda.current_device() == index:
+        rc = f(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            rc = f(*args, torch.cuda.current_stream(device).cuda_stream)
-    _check(rc, name)
+            rc = f(*args, torch._C._cuda_getCurrentRawStream(index))
+    if rc:
+        _check(rc, name)
 
 
 def moe_router_fwd(mode: int, logits: torch.Tensor, K: int, renorm: bool = False,
@@ -486,20 +511,25 @@ def moe_router_fwd(mode: int, logits: torch.Tensor, K: int, renorm: bool = False
     The ids feed moe_build_blocks and moe_router_bwd, the affinities MoeBwd.  token_mask [T] bool or uint8:
     a token with 0 selects nothing (ids -1, scores 0), as do selections that find no expert above -inf.
     out: optional (topk_idx, topk_scores, affinities) to write into."""
-    typ = _logits_type(logits, "moe_router_fwd")
-    T, E = logits.shape
-    dev = logits.device
-    x = _dev(logits, logits.dtype, "logits")
+    T, E, dev, x, typ = _logits(logits, "moe_router_fwd")
     m = _mask(token_mask, T, dev)
     if out is None:
-        out = (torch.empty((T, K), dtype=torch.int32, device=dev), torch.empty((T, K), dtype=torch.float32, device=dev),
-               torch.empty(T * E, dtype=torch.float32, device=dev))
-    idx, scores, aff = out
-    _call(dev, "moe_router_fwd", mode, T, E, K, x, typ, m, 1 if renorm else 0,
-          _tensor(idx, torch.int32, (T, K), dev, "topk_idx"),
-          _tensor(scores, torch.float32, (T, K), dev, "topk_scores"),
-          _tensor(aff, torch.float32, (T * E,), dev, "affinities"))
+        idx, scores, aff = out = (_empty((T, K), dtype=torch.int32, device=dev),
+                                  _empty((T, K), dtype=torch.float32, device=dev),
+                                  _empty(T * E, dtype=torch.float32, device=dev))
+        ptrs = idx.data_ptr(), scores.data_ptr(), aff.data_ptr()
+    else:
+        idx, scores, aff = out
+        ptrs = (_tensor(idx, torch.int32, (T, K), dev, "topk_idx"),
+                _tensor(scores, torch.float32, (T, K), dev, "topk_scores"),
+                _tensor(aff, torch.float32, (T * E,), dev, "affinities"))
+    _call(dev, "moe_router_fwd", mode, T, E, K, x, typ, m, 1 if renorm else 0, *ptrs)
     return out
+
+
+@lru_cache(maxsize=256)
+def _balance_workspace_size(T, E, S):
+    return lib().moe_balance_loss_workspace_size(T, E, S)
 
 
 def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, balance_coef: float, z_coef: float = 0.0,
@@ -510,29 +540,30 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, balance_coef:
     logits [T, E] fp32 or bf16, topk_idx [T, K] int32, token_mask [T] bool or uint8, seq_starts [S+1] int32 ->
     (loss [2] fp32, counts [S, E] int32, num_tokens [S+2] int32); S = 1 without seq_starts.  counts and
     num_tokens are what moe_balance_loss_bwd needs."""
-    typ = _logits_type(logits, "moe_balance_loss")
-    T, E = logits.shape
-    dev = logits.device
-    x = _dev(logits, logits.dtype, "logits")
+    T, E, dev, x, typ = _logits(logits, "moe_balance_loss")
     if topk_idx.dim() != 2:
         raise ValueError("moe_balance_loss: topk_idx must be [T, K]")
     K = topk_idx.shape[1]
-    S = 1 if seq_starts is None else seq_starts.numel() - 1
+    S, seq = _sequences(seq_starts, dev)
     if out is None:
-        out = (torch.empty(2, dtype=torch.float32, device=dev),
-               torch.empty((max(S, 0), E), dtype=torch.int32, device=dev),
-               torch.empty(max(S, 0) + 2, dtype=torch.int32, device=dev))
-    loss, counts, num = out
+        n = S if S > 0 else 0
+        loss, counts, num = out = (_empty(2, dtype=torch.float32, device=dev),
+                                   _empty((n, E), dtype=torch.int32, device=dev),
+                                   _empty(n + 2, dtype=torch.int32, device=dev))
+        ptrs = loss.data_ptr(), counts.data_ptr(), num.data_ptr()
+    else:
+        loss, counts, num = out
+        ptrs = (_tensor(loss, torch.float32, (2,), dev, "loss"), _tensor(counts, torch.int32, (S, E), dev, "counts"),
+                _tensor(num, torch.int32, (S + 2,), dev, "num_tokens"))
     if workspace is None:
-        workspace = torch.empty(lib().moe_balance_loss_workspace_size(T, E, S), dtype=torch.uint8, device=dev)
-    elif workspace.device != dev:
-        raise ValueError(f"workspace: expected a tensor on {dev}, got {workspace.device}")
+        size = _balance_workspace_size(T, E, S)
+        ws = _empty(size, dtype=torch.uint8, device=dev).data_ptr() if size else None   # 0: refused below
+    else:
+        size = workspace.numel()
+        ws = _tensor(workspace, torch.uint8, workspace.shape, dev, "workspace")
     a = BalanceArgs(T, E, K, S, x, typ, _tensor(topk_idx, torch.int32, (T, K), dev, "topk_idx"),
-                    _mask(token_mask, T, dev), _tensor(seq_starts, torch.int32, (S + 1,), dev, "seq_starts"),
-                    balance_coef, z_coef, _tensor(loss, torch.float32, (2,), dev, "loss"),
-                    _tensor(counts, torch.int32, (S, E), dev, "counts"),
-                    _tensor(num, torch.int32, (S + 2,), dev, "num_tokens"), None, None, 0)
-    _call(dev, "moe_balance_loss", C.byref(a), _dev(workspace, torch.uint8, "workspace"), workspace.numel())
+                    _mask(token_mask, T, dev), seq, balance_coef, z_coef, *ptrs)
+    _call(dev, "moe_balance_loss", C.byref(a), ws, size)
     return out
 
 
@@ -544,21 +575,19 @@ def moe_balance_loss_bwd(logits: torch.Tensor, counts: torch.Tensor, num_tokens:
 
     counts and num_tokens come from moe_balance_loss with the same logits, mask, sequences and coefficients;
     dloss [2] fp32 (None: ones).  accumulate=True adds into `out`, moe_router_bwd's result for instance."""
-    typ = _logits_type(logits, "moe_balance_loss_bwd")
-    T, E = logits.shape
-    dev = logits.device
-    x = _dev(logits, logits.dtype, "logits")
-    S = 1 if seq_starts is None else seq_starts.numel() - 1
+    T, E, dev, x, typ = _logits(logits, "moe_balance_loss_bwd")
+    S, seq = _sequences(seq_starts, dev)
     if out is None:
         if accumulate:
             raise ValueError("moe_balance_loss_bwd: accumulate needs out")
-        out = torch.empty((T, E), dtype=torch.float32, device=dev)
-    a = BalanceArgs(T, E, K, S, x, typ, None, _mask(token_mask, T, dev),
-                    _tensor(seq_starts, torch.int32, (S + 1,), dev, "seq_starts"), balance_coef, z_coef, None,
+        out = _empty((T, E), dtype=torch.float32, device=dev)
+        d = out.data_ptr()
+    else:
+        d = _tensor(out, torch.float32, (T, E), dev, "out")
+    a = BalanceArgs(T, E, K, S, x, typ, None, _mask(token_mask, T, dev), seq, balance_coef, z_coef, None,
                     _tensor(counts, torch.int32, (S, E), dev, "counts"),
                     _tensor(num_tokens, torch.int32, (S + 2,), dev, "num_tokens"),
-                    _tensor(dloss, torch.float32, (2,), dev, "dloss"),
-                    _tensor(out, torch.float32, (T, E), dev, "out"), int(bool(accumulate)))
+                    _tensor(dloss, torch.float32, (2,), dev, "dloss"), d, 1 if accumulate else 0)
     _call(dev, "moe_balance_loss_bwd", C.byref(a))
     return out
 
@@ -570,9 +599,11 @@ def _gated_act_args(shape, activation, fmt, token_position_to_id, T, device, nam
     rows, period = shape[0], shape[-1]
     if period % 32:
         raise ValueError(f"{name}: the last dimension must be a multiple of 32 (got {period})")
-    cols = 1
-    for n in shape[2:]:
+    cols = period
+    for n in shape[2:-1]:
         cols *= n
+    if token_position_to_id is None:
+        return GatedActArgs(rows, cols, activation, fmt)
     return GatedActArgs(rows, cols, activation, fmt,
                         _tensor(token_position_to_id, torch.int32, (rows * period,), device, "token_position_to_id"),
                         period, T)
@@ -586,17 +617,21 @@ def mxfp8_gated_act_fwd(gate_up: torch.Tensor, activation: int = ACT_SWIGLU, fmt
     (inter [rows, ..., n] bf16, codes uint8 of gate_up's shape, scales uint8 [rows, 2, ..., n/32]), groups of 32
     along the last axis.  token_position_to_id [rows*n] int32 with T tokens: slots with another id are padding
     and count as zeros."""
-    shape = tuple(gate_up.shape)
+    shape = gate_up.shape
     dev = gate_up.device
     x = _dev(gate_up, torch.bfloat16, "gate_up")
     a = _gated_act_args(shape, activation, fmt, token_position_to_id, T, dev, "mxfp8_gated_act_fwd")
-    ishape, sshape = shape[:1] + shape[2:], shape[:-1] + (shape[-1] // 32,)
+    ishape, sshape = shape[:1] + shape[2:], (*shape[:-1], shape[-1] // 32)
     if out is None:
-        out = (torch.empty(ishape, dtype=torch.bfloat16, device=dev), torch.empty(shape, dtype=torch.uint8, device=dev),
-               torch.empty(sshape, dtype=torch.uint8, device=dev))
-    inter, codes, scales = out
-    _call(dev, "mxfp8_gated_act_fwd", C.byref(a), x, _tensor(inter, torch.bfloat16, ishape, dev, "inter"),
-          _tensor(codes, torch.uint8, shape, dev, "codes"), _tensor(scales, torch.uint8, sshape, dev, "scales"))
+        inter, codes, scales = out = (_empty(ishape, dtype=torch.bfloat16, device=dev),
+                                      _empty(shape, dtype=torch.uint8, device=dev),
+                                      _empty(sshape, dtype=torch.uint8, device=dev))
+        ptrs = inter.data_ptr(), codes.data_ptr(), scales.data_ptr()
+    else:
+        inter, codes, scales = out
+        ptrs = (_tensor(inter, torch.bfloat16, ishape, dev, "inter"), _tensor(codes, torch.uint8, shape, dev, "codes"),
+                _tensor(scales, torch.uint8, sshape, dev, "scales"))
+    _call(dev, "mxfp8_gated_act_fwd", C.byref(a), x, *ptrs)
     return out
 
 
@@ -605,13 +640,15 @@ def mxfp8_gated_act_bwd(dinter: torch.Tensor, codes: torch.Tensor, scales: torch
                         out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The gated activation's backward from its MXFP8 checkpoint (include/mxfp8_moe.h: mxfp8_gated_act_bwd):
     dinter [rows, ..., n] bf16 with mxfp8_gated_act_fwd's codes and scales -> d(gate_up), bf16 of codes' shape."""
-    shape = tuple(codes.shape)
+    shape = codes.shape
     dev = codes.device
     a = _gated_act_args(shape, activation, fmt, token_position_to_id, T, dev, "mxfp8_gated_act_bwd")
+    ptrs = (_tensor(dinter, torch.bfloat16, shape[:1] + shape[2:], dev, "dinter"), _dev(codes, torch.uint8, "codes"),
+            _tensor(scales, torch.uint8, (*shape[:-1], shape[-1] // 32), dev, "scales"))
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    _call(dev, "mxfp8_gated_act_bwd", C.byref(a),
-          _tensor(dinter, torch.bfloat16, shape[:1] + shape[2:], dev, "dinter"), _dev(codes, torch.uint8, "codes"),
-          _tensor(scales, torch.uint8, shape[:-1] + (shape[-1] // 32,), dev, "scales"),
-          _tensor(out, torch.bfloat16, shape, dev, "out"))
+        out = _empty(shape, dtype=torch.bfloat16, device=dev)
+        d = out.data_ptr()
+    else:
+        d = _tensor(out, torch.bfloat16, shape, dev, "out")
+    _call(dev, "mxfp8_gated_act_bwd", C.byref(a), *ptrs, d)
     return out
