@@ -204,6 +204,7 @@ __global__ void __launch_bounds__(v2::kThreads) phase1_fused_kernel(Phase1Args p
   }
   if (!EARLY) epi_load_gu<BN, C8>(p, b, chunk_row0(0), GSTRIDE, n0, pre[0]);
   __syncthreads();   // every wave is done reading the ring
+  saturate_fp8_conversions();   // for the epilogue's groups
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int h = lane >> 5, r = lane & 31, wm = wave >> 1;
   float* dsl = reinterpret_cast<float*>(smem);

@@ -26,6 +26,7 @@ __global__ void __launch_bounds__(kEpiThreads) phase1_epi_kernel(Phase1Args p) {
     epi_empty_chunk<TS>(p, b, ti0, s0);
     return;
   }
+  saturate_fp8_conversions();
   epi_chunk<FG, ON_I ? 1 : 0, TS, CK, GEGLU, false, C8>(p, b, ti0, 32, s0, lds);
 }
 

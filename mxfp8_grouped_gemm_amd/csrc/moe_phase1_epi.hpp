@@ -27,7 +27,9 @@
 // as 32-byte runs.  dS comes either from HBM (the stand-alone epilogue kernel)
 // or from LDS, where the fused Phase-1 kernel leaves each chunk of its tile's
 // product (DS_LDS); the arithmetic is the same either way, so the two give
-// identical bits.
+// identical bits.  The kernels that run it have the fp8 converters saturate
+// (saturate_fp8_conversions), so that groups are encoded from bf16 pairs as they
+// are, one conversion per two values.
 #pragma once
 #include "kernels.hpp"
 #include "gemm_v2.hpp"
@@ -120,11 +122,16 @@ typedef unsigned short epi_us2 __attribute__((ext_vector_type(2)));
 
 // The MXFP8 checkpoint (C8 >= 0: its element format).  Its groups run along
 // the slots, so a wave's 64 slots x 32 rows hold two groups a row: lane l loads
-// the scale bytes of row i0 + l % 32 for the group its own slot is in, as the
-// bf16 values 2^X (gate | up << 16; byte 0: the subnormal 2^-127), and row k's
-// reach its 32 lanes by one swizzle each.  A code times its scale is exact
-// in fp32, and is the value a bf16 checkpoint of the dequantised tensor holds:
-// the two checkpoints give the same bits.
+// the two scale bytes of row i0 + l % 32 for the group its own slot is in, and
+// row k's reach its 32 lanes by one swizzle.  v_cvt_scalef32_f32_fp8 / _bf8
+// multiply a code by the power of two whose E8M0 byte is the exponent field of
+// their scale operand and ignore the other bits (byte 0 is 2^-127; checked for
+// every code and scale), so the word gate << 23 | up is the gate's operand as
+// it stands, and shifted by 23 the up's: 4 instructions a row, one more than the
+// bf16 checkpoint's unpacking.  A code times its scale is exact in fp32, and is
+// the value a bf16 checkpoint of the dequantised tensor holds: the two
+// checkpoints give the same bits.  Padding slots load code 0; byte 255 (NaN) is
+// read as 254, so that a group of padding alone may hold anything.
 template <int TS>
 __device__ __forceinline__ uint32_t epi_load_scales(const Phase1Args& p, int b, int64_t i0, int64_t s0, uint32_t live) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -133,23 +140,22 @@ __device__ __forceinline__ uint32_t epi_load_scales(const Phase1Args& p, int b, 
   const uint32_t v = (uint32_t(i0) + (threadIdx.x & 31)) * G + uint32_t(s0 + threadIdx.x % TS) / 32;
   const uint32_t g = __builtin_amdgcn_raw_buffer_load_b8(rs, v, 0, 0);
   const uint32_t u = __builtin_amdgcn_raw_buffer_load_b8(rs, v, plane, 0);
-  return (g ? g << 7 : 0x40u) | (u ? u << 7 : 0x40u) << 16;
+  return min(g, 254u) << 23 | min(u, 254u);
 #else
   return 0;
 #endif
 }
-// gate and up from the codes w (gate | up << 16) of row K; ok 0 (a padding slot): zeros, whatever
-// the scale holds
+// gate and up from the codes w (gate | up << 16) of row K
 template <int C8, int K>
-__device__ __forceinline__ void epi_decode(uint32_t w, uint32_t sc, uint32_t ok, float& g, float& u) {
+__device__ __forceinline__ void epi_decode(uint32_t w, uint32_t sc, float& g, float& u) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  const uint32_t s = uint32_t(__builtin_amdgcn_ds_swizzle(int(sc), K << 5)) & ok;
+  const uint32_t s = uint32_t(__builtin_amdgcn_ds_swizzle(int(sc), K << 5));
   if constexpr (C8 == kE4M3) {
-    g = __builtin_amdgcn_cvt_f32_fp8(int(w), 0) * lo_bf16(s);
-    u = __builtin_amdgcn_cvt_f32_fp8(int(w), 2) * hi_bf16(s);
+    g = __builtin_amdgcn_cvt_scalef32_f32_fp8(int(w), __uint_as_float(s), 0);
+    u = __builtin_amdgcn_cvt_scalef32_f32_fp8(int(w), __uint_as_float(s << 23), 2);
   } else {
-    g = __builtin_amdgcn_cvt_f32_bf8(int(w), 0) * lo_bf16(s);
-    u = __builtin_amdgcn_cvt_f32_bf8(int(w), 2) * hi_bf16(s);
+    g = __builtin_amdgcn_cvt_scalef32_f32_bf8(int(w), __uint_as_float(s), 0);
+    u = __builtin_amdgcn_cvt_scalef32_f32_bf8(int(w), __uint_as_float(s << 23), 2);
   }
 #endif
 }
@@ -171,8 +177,8 @@ __device__ __forceinline__ void epi_load_gu(const Phase1Args& p, int b, int64_t 
 #pragma unroll
       for (int k = 0; k < 32; ++k) {
         const uint32_t row = __builtin_amdgcn_readfirstlane(uint32_t((i0 + k) * p.B));
-        const uint16_t g = __builtin_amdgcn_raw_buffer_load_b8(rc, vc, row, kNT);
-        const uint16_t u = __builtin_amdgcn_raw_buffer_load_b8(rc, vc, row + plane, kNT);
+        const uint16_t g = __builtin_amdgcn_raw_buffer_load_b8(rc, vc, row, 0);
+        const uint16_t u = __builtin_amdgcn_raw_buffer_load_b8(rc, vc, row + plane, 0);
         x.gu[k] = __builtin_bit_cast(uint32_t, epi_us2{g, u});
       }
       return;
@@ -230,7 +236,8 @@ __device__ __forceinline__ void epi_chunk(const Phase1Args& p, int b, int64_t ti
     // own wait, serialising the 96 loads a thread keeps in flight).
     uint32_t gu[32];   // bf16(dGate) | bf16(dUp) << 16
     uint32_t itp[16];  // bf16 intermediate operand, rows 2k | 2k + 1 << 16
-    float daff = 0.f, amg = 0.f, amu = 0.f;
+    float daff = 0.f;
+    uint32_t am = 0;   // largest |dGate| and |dUp| so far, bf16 pair
 #if defined(__HIP_DEVICE_COMPILE__)
     // a chunk past the block's extent is all padding (dS unwritten there): its
     // descriptors have no records, so every load reads zero without memory traffic
@@ -245,16 +252,14 @@ __device__ __forceinline__ void epi_chunk(const Phase1Args& p, int b, int64_t ti
       itp[k >> 1] = (k & 1) ? (itp[k >> 1] & 0xffffu) | (uint32_t(v) << 16) : uint32_t(v);
     };
     // gate and up of element K from the checkpoint word w
-    const uint32_t okm = ok ? 0xffffffffu : 0u;
     auto put = [&](auto K, uint32_t w, uint32_t sc, float d) {
       constexpr int k = K;
       float g = lo_bf16(w), u = hi_bf16(w);
-      if constexpr (C8 >= 0) epi_decode<C8, k>(w, sc, okm, g, u);
+      if constexpr (C8 >= 0) epi_decode<C8, k>(w, sc, g, u);
       uint16_t v;
       gu[k] = swiglu_bwd<GEGLU>(on_i, d, g, u, a, false, 0.f, false, 0.f, false, 0, daff, v);
       put_it(k, v);
-      amg = fmaxf(amg, fabsf(lo_bf16(gu[k])));
-      amu = fmaxf(amu, fabsf(hi_bf16(gu[k])));
+      am = absmax_bf16x2(am, gu[k]);
     };
     if constexpr (!CK && DS_LDS) {
       // dS from LDS, read as it is used; all of it is read before the barrier,
@@ -276,8 +281,8 @@ __device__ __forceinline__ void epi_chunk(const Phase1Args& p, int b, int64_t ti
         for (int k = 0; k < 32; ++k) {
           const uint32_t row = __builtin_amdgcn_readfirstlane(uint32_t((i0 + k) * p.B));
           dv[k] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rd, vd, row * 4, kNT));
-          const uint16_t g = __builtin_amdgcn_raw_buffer_load_b8(rc, vb, row, kNT);
-          const uint16_t u = __builtin_amdgcn_raw_buffer_load_b8(rc, vb, row + uint32_t(p.I * p.B), kNT);
+          const uint16_t g = __builtin_amdgcn_raw_buffer_load_b8(rc, vb, row, 0);
+          const uint16_t u = __builtin_amdgcn_raw_buffer_load_b8(rc, vb, row + uint32_t(p.I * p.B), 0);
           cw[k] = __builtin_bit_cast(uint32_t, epi_us2{g, u});
         }
         v2::static_for<32>([&](auto K) { put(K, cw[int(K)], sc, dv[int(K)]); });
@@ -299,8 +304,7 @@ __device__ __forceinline__ void epi_chunk(const Phase1Args& p, int b, int64_t ti
           gu[k] = swiglu_bwd<GEGLU>(on_i, dv[k], bf16_to_f32(gb[k]), bf16_to_f32(ub[k]), a, false, 0.f, false, 0.f,
                                     false, 0, daff, v);
           put_it(k, v);
-          amg = fmaxf(amg, fabsf(lo_bf16(gu[k])));
-          amu = fmaxf(amu, fabsf(hi_bf16(gu[k])));
+          am = absmax_bf16x2(am, gu[k]);
         }
       }
     } else if (rows) {
@@ -333,8 +337,7 @@ __device__ __forceinline__ void epi_chunk(const Phase1Args& p, int b, int64_t ti
           gu[kk] = swiglu_bwd<GEGLU>(on_i, dv[k], bf16_to_f32(gb[k]), bf16_to_f32(ub[k]), a, has_ga,
                                      bf16_to_f32(gab[k]), has_in, bf16_to_f32(inb[k]), has_sc, scb[k], daff, v);
           put_it(kk, v);
-          amg = fmaxf(amg, fabsf(lo_bf16(gu[kk])));
-          amu = fmaxf(amu, fabsf(hi_bf16(gu[kk])));
+          am = absmax_bf16x2(am, gu[kk]);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -342,15 +345,14 @@ __device__ __forceinline__ void epi_chunk(const Phase1Args& p, int b, int64_t ti
 #endif
     if (rows) {
       // I-axis groups: the thread's 32 rows are one group of dGate and one of dUp
-      const int Xg = scale_exp<FG>(__float_as_uint(amg)), Xu = scale_exp<FG>(__float_as_uint(amu));
-      const float ig = inv_scale(Xg), iu = inv_scale(Xu);
+      const int Xg = scale_exp<FG>(am << 16), Xu = scale_exp<FG>(am & 0xffff0000u);
+      const float cg = cvt_scale(Xg), cu = cvt_scale(Xu);
       uint32_t wg[8], wu[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        wg[k] = encode4<FG>(lo_bf16(gu[4 * k]), lo_bf16(gu[4 * k + 1]), lo_bf16(gu[4 * k + 2]), lo_bf16(gu[4 * k + 3]),
-                            ig);
-        wu[k] = encode4<FG>(hi_bf16(gu[4 * k]), hi_bf16(gu[4 * k + 1]), hi_bf16(gu[4 * k + 2]), hi_bf16(gu[4 * k + 3]),
-                            iu);
+        const uint32_t x0 = gu[4 * k], x1 = gu[4 * k + 1], x2 = gu[4 * k + 2], x3 = gu[4 * k + 3];
+        wg[k] = encode_bf16x4<FG>(lo_halves(x0, x1), lo_halves(x2, x3), cg);
+        wu[k] = encode_bf16x4<FG>(hi_halves(x0, x1), hi_halves(x2, x3), cu);
       }
       // stage-major (P rows over 2I) for the ring loop, else row-major [P][2I]
       uint4* rg = reinterpret_cast<uint4*>(
@@ -387,26 +389,25 @@ __device__ __forceinline__ void epi_chunk(const Phase1Args& p, int b, int64_t ti
     if (i < p.I) {
       const int64_t p0 = sbase + s0 + 32 * c;
       const uint32_t* src = stg_gu + r * GSW + 33 * c;
-      uint32_t mg = 0, mu = 0;
+      uint32_t am = 0;
       float sg = 0.f, su = 0.f;
 #pragma unroll
       for (int k = 0; k < 32; ++k) {
         const uint32_t x = src[k];
-        mg = max(mg, (x << 16) & 0x7fffffffu);
-        mu = max(mu, x & 0x7fff0000u);
+        am = absmax_bf16x2(am, x);
         if (p.has_bias) {
           sg += __uint_as_float(x << 16);
           su += __uint_as_float(x & 0xffff0000u);
         }
       }
-      const int Xg = scale_exp<FG>(mg), Xu = scale_exp<FG>(mu);
-      const float ig = inv_scale(Xg), iu = inv_scale(Xu);
+      const int Xg = scale_exp<FG>(am << 16), Xu = scale_exp<FG>(am & 0xffff0000u);
+      const float sc_g = cvt_scale(Xg), sc_u = cvt_scale(Xu);
       uint32_t cg[8], cu[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const uint32_t x0 = src[4 * k], x1 = src[4 * k + 1], x2 = src[4 * k + 2], x3 = src[4 * k + 3];
-        cg[k] = encode4<FG>(lo_bf16(x0), lo_bf16(x1), lo_bf16(x2), lo_bf16(x3), ig);
-        cu[k] = encode4<FG>(hi_bf16(x0), hi_bf16(x1), hi_bf16(x2), hi_bf16(x3), iu);
+        cg[k] = encode_bf16x4<FG>(lo_halves(x0, x1), lo_halves(x2, x3), sc_g);
+        cu[k] = encode_bf16x4<FG>(hi_halves(x0, x1), hi_halves(x2, x3), sc_u);
       }
       uint4* og = reinterpret_cast<uint4*>(p.dgu_tok_codes + stage_major_off(i, p0, twoI, P));   // 2I rows over P
       uint4* ou = reinterpret_cast<uint4*>(p.dgu_tok_codes + stage_major_off(p.I + i, p0, twoI, P));
@@ -428,20 +429,22 @@ __device__ __forceinline__ void epi_chunk(const Phase1Args& p, int b, int64_t ti
         }
       }
       // the intermediate operand (activation format)
-      const uint16_t* isrc = stg_in + r * ISH + 34 * c;
-      uint32_t mi = 0;
+      static_assert(ISH % 2 == 0, "a run of 32 values is 16 aligned words");
+      const uint32_t* isrc = reinterpret_cast<const uint32_t*>(stg_in + r * ISH + 34 * c);
+      uint32_t iw[16], mi = 0;
 #pragma unroll
-      for (int k = 0; k < 32; ++k) mi = max(mi, (uint32_t(isrc[k]) << 16) & 0x7fffffffu);
+      for (int k = 0; k < 16; ++k) {
+        iw[k] = isrc[k];
+        mi = absmax_bf16x2(mi, iw[k]);
+      }
+      mi = max(mi & 0xffffu, mi >> 16) << 16;
       const bool e5 = p.fmt_act == kE5M2;   // uniform
       const int Xi = e5 ? scale_exp<kE5M2>(mi) : scale_exp<kE4M3>(mi);
-      const float ii = inv_scale(Xi);
+      const float sc_i = cvt_scale(Xi);
       uint32_t ci[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float v0 = bf16_to_f32(isrc[4 * k]), v1 = bf16_to_f32(isrc[4 * k + 1]);
-        const float v2 = bf16_to_f32(isrc[4 * k + 2]), v3 = bf16_to_f32(isrc[4 * k + 3]);
-        ci[k] = e5 ? encode4<kE5M2>(v0, v1, v2, v3, ii) : encode4<kE4M3>(v0, v1, v2, v3, ii);
-      }
+      for (int k = 0; k < 8; ++k)
+        ci[k] = e5 ? encode_bf16x4<kE5M2>(iw[2 * k], iw[2 * k + 1], sc_i) : encode_bf16x4<kE4M3>(iw[2 * k], iw[2 * k + 1], sc_i);
       uint4* oi = reinterpret_cast<uint4*>(p.inter_tok_codes + stage_major_off(i, p0, p.I, P));   // I rows over P
       oi[0] = uint4{ci[0], ci[1], ci[2], ci[3]};
       oi[1] = uint4{ci[4], ci[5], ci[6], ci[7]};

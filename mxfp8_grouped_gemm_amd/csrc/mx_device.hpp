@@ -194,6 +194,15 @@ __device__ __forceinline__ uint32_t encode_bf16x4(uint32_t p01, uint32_t p23, fl
   }
   return __builtin_bit_cast(uint32_t, r);
 }
+// A wave that has called this (the FP16_OVFL bit of its mode register, which
+// also governs the fp8 conversions) gets saturation from the converters
+// themselves: encode_bf16x4 then needs no clamped inputs.  Checked on the GPU
+// like the above: every bf16 pattern x every scale the group rule can produce.
+__device__ __forceinline__ void saturate_fp8_conversions() {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_s_setreg(1 | 23 << 6, 1);   // hwreg(MODE, bit 23, 1 bit)
+#endif
+}
 // low / high halves of two words, packed (a's in the low half)
 __device__ __forceinline__ uint32_t lo_halves(uint32_t a, uint32_t b) { return (a & 0xffffu) | (b << 16); }
 __device__ __forceinline__ uint32_t hi_halves(uint32_t a, uint32_t b) { return (a >> 16) | (b & 0xffff0000u); }
