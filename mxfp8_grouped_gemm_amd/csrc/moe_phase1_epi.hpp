@@ -91,6 +91,28 @@ __device__ __forceinline__ uint32_t swiglu_bwd(bool on_i, float d, float g, floa
   }
 }
 
+// Two elements at once, nothing supplied: the same roundings, two values a
+// conversion.  gu: each element's bf16(dGate) | bf16(dUp) << 16; returns the
+// two intermediate operands, the first in the low half.
+template <bool GEGLU>
+__device__ __forceinline__ uint32_t swiglu_bwd2(bool on_i, const float (&d)[2], const float (&g)[2], const float (&u)[2],
+                                                float a, float& daff, uint32_t (&gu)[2]) {
+  float s[2];   // the gate's factor: sigmoid, or the normal CDF
+#pragma unroll
+  for (int h = 0; h < 2; ++h) s[h] = GEGLU ? normal_cdf(g[h]) : sigmoid_fast(g[h]);
+  const uint32_t ga = bf16x2_rne(g[0] * s[0], g[1] * s[1]);
+  const float gf[2] = {lo_bf16(ga), hi_bf16(ga)};
+  const uint32_t in = bf16x2_rne(gf[0] * u[0], gf[1] * u[1]);
+  const float nf[2] = {lo_bf16(in), hi_bf16(in)};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    daff += d[h] * nf[h];
+    const float di = a * d[h];   // d(intermediate)
+    gu[h] = bf16x2_rne(di * u[h] * (GEGLU ? dgelu_from(g[h], s[h]) : dsilu_from(g[h], s[h])), di * gf[h]);
+  }
+  return on_i ? bf16x2_rne(a * nf[0], a * nf[1]) : in;
+}
+
 // A chunk of a block without tokens: its intermediate operand is all zeros
 // (codes 0, scale byte 0; scales pair-major [P/128][I][4]).
 template <int TS>
@@ -145,17 +167,17 @@ __device__ __forceinline__ uint32_t epi_load_scales(const Phase1Args& p, int b, 
   return 0;
 #endif
 }
-// gate and up from the codes w (gate | up << 16) of row K
-template <int C8, int K>
-__device__ __forceinline__ void epi_decode(uint32_t w, uint32_t sc, float& g, float& u) {
+// gate and up from the codes of row K: byte 0 of wg and byte UB of wu
+template <int C8, int K, int UB>
+__device__ __forceinline__ void epi_decode(uint32_t wg, uint32_t wu, uint32_t sc, float& g, float& u) {
 #if defined(__HIP_DEVICE_COMPILE__)
   const uint32_t s = uint32_t(__builtin_amdgcn_ds_swizzle(int(sc), K << 5));
   if constexpr (C8 == kE4M3) {
-    g = __builtin_amdgcn_cvt_scalef32_f32_fp8(int(w), __uint_as_float(s), 0);
-    u = __builtin_amdgcn_cvt_scalef32_f32_fp8(int(w), __uint_as_float(s << 23), 2);
+    g = __builtin_amdgcn_cvt_scalef32_f32_fp8(int(wg), __uint_as_float(s), 0);
+    u = __builtin_amdgcn_cvt_scalef32_f32_fp8(int(wu), __uint_as_float(s << 23), UB);
   } else {
-    g = __builtin_amdgcn_cvt_scalef32_f32_bf8(int(w), __uint_as_float(s), 0);
-    u = __builtin_amdgcn_cvt_scalef32_f32_bf8(int(w), __uint_as_float(s << 23), 2);
+    g = __builtin_amdgcn_cvt_scalef32_f32_bf8(int(wg), __uint_as_float(s), 0);
+    u = __builtin_amdgcn_cvt_scalef32_f32_bf8(int(wu), __uint_as_float(s << 23), UB);
   }
 #endif
 }
@@ -251,61 +273,62 @@ __device__ __forceinline__ void epi_chunk(const Phase1Args& p, int b, int64_t ti
     auto put_it = [&](int k, uint16_t v) {
       itp[k >> 1] = (k & 1) ? (itp[k >> 1] & 0xffffu) | (uint32_t(v) << 16) : uint32_t(v);
     };
-    // gate and up of element K from the checkpoint word w
-    auto put = [&](auto K, uint32_t w, uint32_t sc, float d) {
-      constexpr int k = K;
-      float g = lo_bf16(w), u = hi_bf16(w);
-      if constexpr (C8 >= 0) epi_decode<C8, k>(w, sc, g, u);
-      uint16_t v;
-      gu[k] = swiglu_bwd<GEGLU>(on_i, d, g, u, a, false, 0.f, false, 0.f, false, 0, daff, v);
-      put_it(k, v);
-      am = absmax_bf16x2(am, gu[k]);
+    // elements 2 K and 2 K + 1 from their gates and ups and dS
+    auto put2 = [&](auto K, const float (&g)[2], const float (&u)[2], float d0, float d1) {
+      constexpr int k = 2 * int(K);
+      const float d[2] = {d0, d1};
+      uint32_t o[2];
+      itp[int(K)] = swiglu_bwd2<GEGLU>(on_i, d, g, u, a, daff, o);
+      gu[k] = o[0];
+      gu[k + 1] = o[1];
+      am = absmax_bf16x2(absmax_bf16x2(am, o[0]), o[1]);
     };
     if constexpr (!CK && DS_LDS) {
       // dS from LDS, read as it is used; all of it is read before the barrier,
       // after which the staging overwrites it
       if (rows) {
-        v2::static_for<32>([&](auto K) {
-          const float x = dsl[(r0 + int(K)) * L::DSW + sl];
-          put(K, pre->gu[int(K)], pre->sc, ok ? x : 0.f);
+        v2::static_for<16>([&](auto K) {
+          const float* x = dsl + (r0 + 2 * int(K)) * L::DSW + sl;
+          const float x0 = x[0], x1 = x[L::DSW];
+          constexpr int k = 2 * int(K);
+          const uint32_t w0 = pre->gu[k], w1 = pre->gu[k + 1];
+          float g[2] = {lo_bf16(w0), lo_bf16(w1)}, u[2] = {hi_bf16(w0), hi_bf16(w1)};
+          if constexpr (C8 >= 0) {
+            epi_decode<C8, k, 2>(w0, w0, pre->sc, g[0], u[0]);
+            epi_decode<C8, k + 1, 2>(w1, w1, pre->sc, g[1], u[1]);
+          }
+          put2(K, g, u, ok ? x0 : 0.f, ok ? x1 : 0.f);
         });
       }
       __syncthreads();
-    } else if constexpr (C8 >= 0) {
-      uint32_t cw[32];   // codes: gate | up << 16
+    } else if constexpr (!CK) {
+      uint16_t gb[32], ub[32];   // bf16, or codes
       float dv[32];
+      uint32_t sc = 0;
       if (rows) {
         const uint32_t vb = ok ? uint32_t(s0 + sl) : v2::kOOB;
-        const uint32_t sc = epi_load_scales<TS>(p, b, i0, s0, live);
+        if constexpr (C8 >= 0) sc = epi_load_scales<TS>(p, b, i0, s0, live);
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
           const uint32_t row = __builtin_amdgcn_readfirstlane(uint32_t((i0 + k) * p.B));
           dv[k] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rd, vd, row * 4, kNT));
-          const uint16_t g = __builtin_amdgcn_raw_buffer_load_b8(rc, vb, row, 0);
-          const uint16_t u = __builtin_amdgcn_raw_buffer_load_b8(rc, vb, row + uint32_t(p.I * p.B), 0);
-          cw[k] = __builtin_bit_cast(uint32_t, epi_us2{g, u});
+          if constexpr (C8 >= 0) {   // 64 bytes a load: the line's other half is another wave's, so no kNT
+            gb[k] = __builtin_amdgcn_raw_buffer_load_b8(rc, vb, row, 0);
+            ub[k] = __builtin_amdgcn_raw_buffer_load_b8(rc, vb, row + uint32_t(p.I * p.B), 0);
+          } else {
+            gb[k] = __builtin_amdgcn_raw_buffer_load_b16(rc, vc, row * 2, kNT);
+            ub[k] = __builtin_amdgcn_raw_buffer_load_b16(rc, vc, (row + uint32_t(p.I * p.B)) * 2, kNT);
+          }
         }
-        v2::static_for<32>([&](auto K) { put(K, cw[int(K)], sc, dv[int(K)]); });
-      }
-    } else if constexpr (!CK) {
-      uint16_t gb[32], ub[32];
-      float dv[32];
-      if (rows) {
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const uint32_t row = __builtin_amdgcn_readfirstlane(uint32_t((i0 + k) * p.B));
-          dv[k] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rd, vd, row * 4, kNT));
-          gb[k] = __builtin_amdgcn_raw_buffer_load_b16(rc, vc, row * 2, kNT);
-          ub[k] = __builtin_amdgcn_raw_buffer_load_b16(rc, vc, (row + uint32_t(p.I * p.B)) * 2, kNT);
-        }
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          uint16_t v;
-          gu[k] = swiglu_bwd<GEGLU>(on_i, dv[k], bf16_to_f32(gb[k]), bf16_to_f32(ub[k]), a, false, 0.f, false, 0.f,
-                                    false, 0, daff, v);
-          put_it(k, v);
-          am = absmax_bf16x2(am, gu[k]);
-        }
+        v2::static_for<16>([&](auto K) {
+          constexpr int k = 2 * int(K);
+          float g[2] = {bf16_to_f32(gb[k]), bf16_to_f32(gb[k + 1])}, u[2] = {bf16_to_f32(ub[k]), bf16_to_f32(ub[k + 1])};
+          if constexpr (C8 >= 0) {
+            epi_decode<C8, k, 0>(gb[k], ub[k], sc, g[0], u[0]);
+            epi_decode<C8, k + 1, 0>(gb[k + 1], ub[k + 1], sc, g[1], u[1]);
+          }
+          put2(K, g, u, dv[k], dv[k + 1]);
+        });
       }
     } else if (rows) {
       // a checkpoint that was not supplied is read through a descriptor with
