@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
-from functools import lru_cache
+from functools import cached_property, lru_cache
 from typing import Optional
 
 import torch
@@ -374,19 +374,21 @@ class MoeBwd:
             _tensor(ck_codes, torch.uint8, (N, 2, I, block_size), dev, "gate_up_checkpoint codes"),
             _tensor(ck_scales, torch.uint8, (N, 2, I, block_size // 32), dev, "gate_up_checkpoint scales"),
             int(fmt_checkpoint))
-        L = lib()
-        lay = MoeWorkspaceLayout()
-        _check(L.moe_bwd_mxfp8_workspace_query(C.byref(self.args), C.byref(lay)), "moe_bwd_mxfp8_workspace_query")
-        self.layout = {n: getattr(lay, n) for n in LAYOUT_FIELDS}
+        self._lay = MoeWorkspaceLayout()
+        _check(lib().moe_bwd_mxfp8_workspace_query(C.byref(self.args), C.byref(self._lay)),
+               "moe_bwd_mxfp8_workspace_query")
         if workspace is None:
-            workspace = torch.empty(self.layout["total"], dtype=torch.uint8, device=dev)
+            workspace = torch.empty(self._lay.total, dtype=torch.uint8, device=dev)
         self.workspace = workspace
         self.device = dev
 
+    @cached_property
+    def layout(self):
+        """Byte offset of each workspace region, by name."""
+        return {n: getattr(self._lay, n) for n in LAYOUT_FIELDS}
+
     def run(self):
-        _check(lib().moe_bwd_mxfp8(C.byref(self.args), self.workspace.data_ptr(), self.workspace.numel(),
-                                   C.c_void_p(torch.cuda.current_stream(self.device).cuda_stream)),
-               "moe_bwd_mxfp8")
+        _call(self.device, "moe_bwd_mxfp8", C.byref(self.args), self.workspace.data_ptr(), self.workspace.numel())
         return self.out
 
     NUM_STAGES = 10

@@ -210,7 +210,10 @@ static int dense_run(const matmul_mxfp8_bwd_args* a, void* ws, size_t ws_bytes, 
       }
     }
     if (i == 0 || swz[i]) {   // GEMM layout: at most the row-major scales become pair-major
-      if (pairs && !a->use_scale_packing) return mx::launch_scales_to_pairs(ps[i], 1, rows[i], kdim[i], wsc, st);
+      if (pairs && !a->use_scale_packing) {
+        const mx::ScalesToPairs job{ps[i], 1, rows[i], kdim[i], wsc};
+        return mx::launch_scales_to_pairs(&job, 1, st);
+      }
       return hipSuccess;
     }
     hipError_t r = mx::launch_transpose_codes(pc[i], kdim[i], rows[i], wc, st);
@@ -609,13 +612,12 @@ static int moe_run(const moe_bwd_mxfp8_args* a, void* ws, size_t ws_bytes, void*
   if (stage >= lo && stage <= hi && (e = (call)) != hipSuccess) return hip_status(e, what);
 
   stage = 0;
-  STEP(mx::launch_fill_u32(daff_slot, P, 0u, st), "zero the d(affinity) bias term");
   if (a->has_bias) {
     STEP(mx::launch_fill_u32(db1_acc, E * 2 * I, 0u, st), "zero db1 accumulator");
     STEP(mx::launch_fill_u32(db2_acc, E * H, 0u, st), "zero db2 accumulator");
   }
   STEP(mx::launch_slot_setup(a->token_position_to_id, a->block_to_expert, a->expert_affinities_masked, T, E, N, B,
-                             a->num_valid_tokens, slot_tok, slot_aff, slot_of, flag, boff, blist, st),
+                             a->num_valid_tokens, slot_tok, slot_aff, slot_of, daff_slot, flag, boff, blist, st),
        "slot setup");
   stage = 1;
   // S1: dY quantised along H per token row (Phase-1 operand, gathered by token later).
@@ -625,18 +627,17 @@ static int moe_run(const moe_bwd_mxfp8_args* a, void* ws, size_t ws_bytes, void*
   STEP(mx::launch_quant_rows(a->output_hidden_states_grad, T, H, a->fmt_grad, at(L.dy_codes), at(L.dy_scales), st,
                              h_pairs ? nullptr : reinterpret_cast<uint16_t*>(at(L.dy_deq)), h_pairs),
        "quantize dY");
-  if (h_pairs) {
-    STEP(mx::launch_scales_to_pairs(a->down_scales, E, I, H, at(L.wd_scales_pairs), st), "W_down scales to pairs");
-  } else {
+  // Phase 3 on the ring loop reads W_gate_up's scales pair-major, Phase 1 W_down's
+  const bool gu_pairs = (2 * I) % 128 == 0;
+  mx::ScalesToPairs jobs[2];
+  int njobs = 0;
+  if (h_pairs) jobs[njobs++] = {a->down_scales, E, I, H, at(L.wd_scales_pairs)};
+  if (gu_pairs) jobs[njobs++] = {a->gate_up_scales, E, H, 2 * I, at(L.wgu_scales_pairs)};
+  if (njobs) STEP(mx::launch_scales_to_pairs(jobs, njobs, st), "weight scales to pairs");
+  if (!h_pairs)
     STEP(mx::launch_dequant_rows(a->down_codes, a->down_scales, E * I, H, a->fmt_weight,
                                  reinterpret_cast<uint16_t*>(at(L.wd_deq)), st),
          "dequantize W_down");
-  }
-  // Phase 3 on the ring loop reads W_gate_up's scales pair-major
-  const bool gu_pairs = (2 * I) % 128 == 0;
-  if (gu_pairs)
-    STEP(mx::launch_scales_to_pairs(a->gate_up_scales, E, H, 2 * I, at(L.wgu_scales_pairs), st),
-         "W_gate_up scales to pairs");
   stage = 2;
   STEP(order(side ? &side->ev[0] : nullptr, st, s2), "second stream after the set-up");
   // token-axis operands of Phases 2 and 4: X, a*dY (on H) or dY (on I); the intermediate
@@ -749,11 +750,11 @@ static int moe_run(const moe_bwd_mxfp8_args* a, void* ws, size_t ws_bytes, void*
   if (side && stage >= lo && stage <= hi && (e = hipStreamWaitEvent(st, side->ev[2], 0)) != hipSuccess)
     return hip_status(e, "caller's stream after the gathers");
   const bool acc = a->accumulate != 0;
-  STEP(mx::launch_dx_reduce(dx_slot, slot_of, T, E, H, a->hidden_states_grad, st, acc), "dX per-token sums");
+  STEP(mx::launch_dx_reduce(dx_slot, slot_of, T, E, H, a->hidden_states_grad, a->expert_affinities_masked_grad, st, acc),
+       "dX per-token sums");
   STEP(mx::launch_daff_scatter(daff_slot, reinterpret_cast<const float*>(at(L.daff_part)),
                                I / 32 + (moe_fuse_bias(a) ? H / 128 : 0), slot_tok,
-                               a->block_to_expert, T, E, B, N, a->expert_affinities_masked_grad,
-                               st, acc),
+                               a->block_to_expert, E, B, N, a->expert_affinities_masked_grad, st, acc),
        "d(affinity) scatter");
   if (a->has_bias) {
     STEP(mx::launch_f32_to_bf16(db1_acc, a->gate_and_up_proj_bias_grad, E * 2 * I, st, acc), "db1 to bf16");

@@ -45,9 +45,14 @@ hipError_t launch_quant_tok(const uint16_t* x, int64_t src_rows, int64_t cols, c
 // [R/128][C][4] (pairs) or row-major [C][R/32]
 hipError_t launch_transpose_codes(const uint8_t* in, int64_t R, int64_t C, uint8_t* out, hipStream_t st);
 hipError_t launch_scales_axis0(const uint8_t* in, int64_t R, int64_t C, uint8_t* out, bool pairs, hipStream_t st);
-// gate/up weight scales [E][H][2I/32] -> pair-major per expert [E][2I/128][H][4]
-hipError_t launch_scales_to_pairs(const uint8_t* in, int64_t groups, int64_t rows, int64_t k, uint8_t* out,
-                                  hipStream_t st);
+// weight scales [groups][rows][k/32] -> pair-major per expert [groups][k/128][rows][4],
+// one or two tensors in one launch
+struct ScalesToPairs {
+  const uint8_t* in;
+  int64_t groups, rows, k;
+  uint8_t* out;
+};
+hipError_t launch_scales_to_pairs(const ScalesToPairs* jobs, int n, hipStream_t st);
 
 // gemm_dense.hip: C[m][n] = sum_k A[m][k] B[n][k] -> bf16 out[g][m][n].
 // A [M][lda] and B [N][ldb] fp8 codes, K-contiguous.  Scales pair-major
@@ -166,7 +171,6 @@ hipError_t launch_gated_act_bwd(const GatedActArgs& p, hipStream_t st);
 
 // moe_aux.hip
 hipError_t launch_fill_u32(void* p, int64_t n, uint32_t v, hipStream_t st);
-hipError_t launch_fill_u16(void* p, int64_t n, uint16_t v, hipStream_t st);
 // ws: build_blocks_workspace_bytes(E) bytes (per expert and token chunk: counts, first slots)
 int64_t build_blocks_workspace_bytes(int64_t E);
 hipError_t launch_build_blocks(const int32_t* topk, int64_t T, int64_t K, int64_t E, int64_t B, int64_t N,
@@ -182,17 +186,19 @@ hipError_t launch_tile_ranges(const int32_t* ext, int64_t N, int W, int other, i
                               TailCut* cut, int conc, int npairs, int rr, int blk);
 hipError_t launch_slot_setup(const int32_t* tpid, const int32_t* b2e, const float* aff, int64_t T, int64_t E,
                              int64_t N, int64_t B, const int32_t* nvalid, int32_t* slot_tok, float* slot_aff,
-                             int32_t* slot_of, int32_t* flag, int32_t* off, int32_t* list, hipStream_t st);
-// accumulate: each bf16 output becomes bf16(old + value) (else bf16(value))
+                             int32_t* slot_of, float* daff_slot, int32_t* flag, int32_t* off, int32_t* list,
+                             hipStream_t st);
+// accumulate: each bf16 output becomes bf16(old + value) (else bf16(value), and
+// launch_dx_reduce zeroes daff [T*E] for the scatter that follows it)
 hipError_t launch_dx_reduce(const float* dx_slot, const int32_t* slot_of, int64_t T, int64_t E, int64_t H,
-                            uint16_t* dx, hipStream_t st, bool accumulate = false);
+                            uint16_t* dx, uint16_t* daff, hipStream_t st, bool accumulate = false);
 hipError_t launch_bias(const uint16_t* dy, const uint16_t* b2, const int32_t* slot_tok, const float* slot_aff,
                        const int32_t* b2e, const int32_t* flag, int64_t H, int64_t B, int64_t N, float* daff_slot,
                        float* db2_acc, hipStream_t st);
 hipError_t launch_f32_to_bf16(const float* src, uint16_t* dst, int64_t n, hipStream_t st, bool accumulate = false);
 hipError_t launch_daff_scatter(const float* daff_slot, const float* daff_part, int64_t nparts,
-                               const int32_t* slot_tok, const int32_t* b2e, int64_t T, int64_t E, int64_t B,
-                               int64_t N, uint16_t* daff, hipStream_t st, bool accumulate = false);
+                               const int32_t* slot_tok, const int32_t* b2e, int64_t E, int64_t B, int64_t N,
+                               uint16_t* daff, hipStream_t st, bool accumulate = false);
 
 // moe_phase1_*.hip (product, epilogue), moe_phase3.hip
 struct Phase1Args {

@@ -24,18 +24,6 @@ __global__ void fill_u32_kernel(uint32_t* p, int64_t n, uint32_t v) {
     p[i] = v;
 }
 
-__global__ void fill_u16_kernel(uint16_t* p, int64_t n, uint16_t v) {
-  for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += int64_t(gridDim.x) * blockDim.x)
-    p[i] = v;
-}
-
-hipError_t launch_fill_u16(void* p, int64_t n, uint16_t v, hipStream_t st) {
-  if (n <= 0) return hipSuccess;
-  const int64_t want = (n + 255) / 256;
-  fill_u16_kernel<<<unsigned(want < 8192 ? want : 8192), 256, 0, st>>>(static_cast<uint16_t*>(p), n, v);
-  return hipGetLastError();
-}
-
 hipError_t launch_fill_u32(void* p, int64_t n, uint32_t v, hipStream_t st) {
   if (n <= 0) return hipSuccess;
   const int64_t want = (n + 255) / 256;
@@ -340,39 +328,89 @@ hipError_t launch_build_blocks(const int32_t* topk, int64_t T, int64_t K, int64_
 // of pair (t, e) (a pair occupies at most one slot; -1 where none, filled
 // beforehand).  Outside [0,T) is padding, and with a device count of valid
 // tokens (P1's num_valid_tokens: the real tokens are the leading rows, a count
-// above T means T) so is every token at or past it.
-__global__ void slot_info_kernel(const int32_t* __restrict__ tpid, const int32_t* __restrict__ b2e,
-                                 const float* __restrict__ aff, int64_t T, int64_t E, int64_t B, int64_t P,
-                                 const int32_t* __restrict__ nvalid, int32_t* __restrict__ slot_tok,
-                                 float* __restrict__ slot_aff, int32_t* __restrict__ slot_of) {
+// above T means T) so is every token at or past it.  Then the block's extent:
+// one past its last routed slot (0: no routed slot, the block takes no part in
+// the GEMMs).  Slots at or past the extent are padding, so the GEMMs skip tiles
+// that start there.  One workgroup per block; daff_slot starts as zeros.
+__global__ void __launch_bounds__(256) slot_block_kernel(const int32_t* __restrict__ tpid,
+                                                         const int32_t* __restrict__ b2e,
+                                                         const float* __restrict__ aff, int64_t T, int64_t E, int64_t B,
+                                                         const int32_t* __restrict__ nvalid,
+                                                         int32_t* __restrict__ slot_tok, float* __restrict__ slot_aff,
+                                                         int32_t* __restrict__ slot_of, float* __restrict__ daff_slot,
+                                                         int32_t* __restrict__ flag) {
+  __shared__ int red[4];
   const int64_t n = nvalid ? int64_t(*nvalid) : T;
   const int64_t Tv = n < 0 ? 0 : (n < T ? n : T);
-  for (int64_t s = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; s < P; s += int64_t(gridDim.x) * blockDim.x) {
-    const int64_t e = b2e[s / B];
+  const int64_t e = b2e[blockIdx.x];
+  int ext = 0;
+  for (int64_t p = threadIdx.x; p < B; p += 256) {
+    const int64_t s = int64_t(blockIdx.x) * B + p;
     const int64_t t = tpid[s];
     const bool ok = t >= 0 && t < Tv && e >= 0 && e < E;
     slot_tok[s] = ok ? int32_t(t) : -1;
     slot_aff[s] = ok ? aff[t * E + e] : 0.f;
-    if (ok) slot_of[t * E + e] = int32_t(s);
+    daff_slot[s] = 0.f;
+    if (ok) {
+      slot_of[t * E + e] = int32_t(s);
+      ext = int(p) + 1;   // p ascends per thread
+    }
   }
-}
-
-// A block's extent: one past its last routed slot (0: no routed slot, the block
-// takes no part in the GEMMs).  Slots at or past the extent are padding, so
-// the GEMMs skip tiles that start there.
-__global__ void __launch_bounds__(256) block_flag_kernel(const int32_t* __restrict__ slot_tok, int64_t B,
-                                                         int32_t* __restrict__ flag) {
-  __shared__ int red[4];
-  int ext = 0;
-  for (int64_t p = threadIdx.x; p < B; p += 256)
-    if (slot_tok[int64_t(blockIdx.x) * B + p] >= 0) ext = int(p) + 1;   // p ascends per thread
   for (int o = 32; o > 0; o >>= 1) ext = max(ext, __shfl_xor(ext, o, 64));
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = ext;
   __syncthreads();
   if (threadIdx.x == 0) flag[blockIdx.x] = max(max(red[0], red[1]), max(red[2], red[3]));
 }
 
-// Per-expert lists of occupied blocks in ascending order: counts (one
+// Per-expert lists of occupied blocks in ascending order, for up to 1024 blocks
+// and experts: one workgroup, a thread per block.  The counts by LDS atomics,
+// the offsets by a scan over the experts, and a block's place in its list by
+// counting the blocks before it with its expert (N / 4 reads of four at a
+// time, the same address in every lane).
+constexpr int kListMax = 1024;
+__global__ void __launch_bounds__(kListMax) expert_lists_kernel(const int32_t* __restrict__ b2e,
+                                                                const int32_t* __restrict__ flag, int N, int E,
+                                                                int32_t* __restrict__ off, int32_t* __restrict__ list) {
+  __shared__ __attribute__((aligned(16))) int32_t eb[kListMax];   // an occupied block's expert, else -1
+  __shared__ int32_t cnt[kListMax];
+  __shared__ int32_t wsum[kListMax / 64];
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  int e = -1;
+  if (t < N && flag[t] != 0) e = b2e[t];
+  if (e < 0 || e >= E) e = -1;
+  eb[t] = e;
+  cnt[t] = 0;
+  __syncthreads();
+  if (e >= 0) atomicAdd(&cnt[e], 1);
+  __syncthreads();
+  const int c = cnt[t];
+  int x = c;
+  for (int o = 1; o < 64; o <<= 1) {
+    const int y = __shfl_up(x, o, 64);
+    if (lane >= o) x += y;
+  }
+  if (lane == 63) wsum[wave] = x;
+  __syncthreads();
+  int before = 0;
+  for (int w = 0; w < wave; ++w) before += wsum[w];
+  const int pos = before + x - c;   // expert t's first entry
+  cnt[t] = pos;
+  if (t < E) off[t] = pos;
+  if (t == E - 1) off[E] = pos + c;
+  __syncthreads();
+  if (e >= 0) {
+    int rank = 0;
+    const int4* q = reinterpret_cast<const int4*>(eb);
+#pragma unroll 4
+    for (int b = 0; b < N; b += 4) {
+      const int4 v = q[b >> 2];
+      rank += (v.x == e && b < t) + (v.y == e && b + 1 < t) + (v.z == e && b + 2 < t) + (v.w == e && b + 3 < t);
+    }
+    list[cnt[e] + rank] = t;
+  }
+}
+
+// The same for more blocks or experts: counts (one
 // workgroup per expert, coalesced scans of the blocks), offsets (one
 // workgroup), then each expert's list in block order (one workgroup each).
 __global__ void __launch_bounds__(256) expert_count_kernel(const int32_t* __restrict__ b2e,
@@ -486,14 +524,16 @@ hipError_t launch_tile_ranges(const int32_t* ext, int64_t N, int W, int other, i
 
 hipError_t launch_slot_setup(const int32_t* tpid, const int32_t* b2e, const float* aff, int64_t T, int64_t E,
                              int64_t N, int64_t B, const int32_t* nvalid, int32_t* slot_tok, float* slot_aff,
-                             int32_t* slot_of, int32_t* flag, int32_t* off, int32_t* list, hipStream_t st) {
-  const int64_t P = N * B;
-  const int64_t want = (P + 255) / 256;
+                             int32_t* slot_of, float* daff_slot, int32_t* flag, int32_t* off, int32_t* list,
+                             hipStream_t st) {
   hipError_t err = launch_fill_u32(reinterpret_cast<uint32_t*>(slot_of), T * E, 0xffffffffu, st);
   if (err != hipSuccess) return err;
-  slot_info_kernel<<<unsigned(want < 4096 ? want : 4096), 256, 0, st>>>(tpid, b2e, aff, T, E, B, P, nvalid,
-                                                                           slot_tok, slot_aff, slot_of);
-  block_flag_kernel<<<unsigned(N), 256, 0, st>>>(slot_tok, B, flag);
+  slot_block_kernel<<<unsigned(N), 256, 0, st>>>(tpid, b2e, aff, T, E, B, nvalid, slot_tok, slot_aff, slot_of, daff_slot,
+                                                 flag);
+  if (N <= kListMax && E <= kListMax) {
+    expert_lists_kernel<<<1, kListMax, 0, st>>>(b2e, flag, int(N), int(E), off, list);
+    return hipGetLastError();
+  }
   // the counts go to off[1..E] and become offsets in place: in each 256-expert
   // chunk every count is read before the scan's barrier and every offset
   // written after it, and a chunk writes only indices the later chunks do not read
@@ -605,14 +645,27 @@ hipError_t launch_f32_to_bf16(const float* src, uint16_t* dst, int64_t n, hipStr
 // experts at a time (a block scan keeps expert order), then each thread sums
 // up to four 4-column groups over them.  The rows are read and dX is stored
 // with the nontemporal hint (the rows are read once, dX is the final output):
-// 7-10% faster for each.
+// 7-10% faster for each.  Without ACC the workgroups past the tokens zero
+// d(affinity) [T*E], kZeroRun values each, for the pairs that the scatter after
+// this kernel does not write.
+constexpr int kZeroRun = 256 * 8;
 template <bool ACC>
 __global__ void __launch_bounds__(256) dx_reduce_kernel(const float* __restrict__ dx_slot,
-                                                        const int32_t* __restrict__ slot_of, int64_t E, int64_t H,
-                                                        uint16_t* __restrict__ dx) {
+                                                        const int32_t* __restrict__ slot_of, int64_t T, int64_t E,
+                                                        int64_t H, uint16_t* __restrict__ dx,
+                                                        uint16_t* __restrict__ daff) {
   __shared__ int red[4];
   __shared__ int32_t list[256];
   const int64_t t = blockIdx.x;
+  if (!ACC && t >= T) {
+    const int64_t i = (t - T) * kZeroRun + int64_t(threadIdx.x) * 8, n = T * E;
+    if (i + 8 <= n) {
+      *reinterpret_cast<uint4*>(daff + i) = uint4{0, 0, 0, 0};
+    } else {
+      for (int64_t k = i; k < n; ++k) daff[k] = 0;
+    }
+    return;
+  }
   const int32_t* so = slot_of + t * E;
   const int64_t C = H / 4;   // 4-column groups
   for (int64_t c0 = 0; c0 < C; c0 += 4 * 256) {
@@ -657,10 +710,15 @@ __global__ void __launch_bounds__(256) dx_reduce_kernel(const float* __restrict_
 }
 
 hipError_t launch_dx_reduce(const float* dx_slot, const int32_t* slot_of, int64_t T, int64_t E, int64_t H,
-                            uint16_t* dx, hipStream_t st, bool accumulate) {
+                            uint16_t* dx, uint16_t* daff, hipStream_t st, bool accumulate) {
   if (T <= 0) return hipSuccess;
-  if (accumulate) dx_reduce_kernel<true><<<unsigned(T), 256, 0, st>>>(dx_slot, slot_of, E, H, dx);
-  else dx_reduce_kernel<false><<<unsigned(T), 256, 0, st>>>(dx_slot, slot_of, E, H, dx);
+  if (accumulate) {   // pairs without a slot keep their value
+    dx_reduce_kernel<true><<<unsigned(T), 256, 0, st>>>(dx_slot, slot_of, T, E, H, dx, daff);
+    return hipGetLastError();
+  }
+  const int64_t grid = T + (T * E + kZeroRun - 1) / kZeroRun;
+  if (grid > INT32_MAX) return hipErrorInvalidValue;
+  dx_reduce_kernel<false><<<unsigned(grid), 256, 0, st>>>(dx_slot, slot_of, T, E, H, dx, daff);
   return hipGetLastError();
 }
 
@@ -696,12 +754,8 @@ __global__ void __launch_bounds__(256) daff_scatter_kernel(const float* __restri
 }
 
 hipError_t launch_daff_scatter(const float* daff_slot, const float* daff_part, int64_t nparts,
-                               const int32_t* slot_tok, const int32_t* b2e, int64_t T, int64_t E, int64_t B,
-                               int64_t N, uint16_t* daff, hipStream_t st, bool accumulate) {
-  if (!accumulate) {   // pairs without a slot are 0; accumulating, they keep their value
-    hipError_t err = launch_fill_u16(daff, T * E, 0, st);
-    if (err != hipSuccess) return err;
-  }
+                               const int32_t* slot_tok, const int32_t* b2e, int64_t E, int64_t B, int64_t N,
+                               uint16_t* daff, hipStream_t st, bool accumulate) {
   const int64_t P = N * B;
   daff_scatter_kernel<<<unsigned((P + 63) / 64), 256, 0, st>>>(daff_slot, daff_part, nparts, slot_tok, b2e, E, B, P,
                                                                 accumulate ? 1 : 0, daff);

@@ -431,12 +431,21 @@ __global__ void __launch_bounds__(256) quant_dual_kernel(const uint16_t* __restr
 // [groups][k/128][rows][4]; k % 128 == 0.  A transpose of 4-byte words
 // ([rows][kp] -> [kp][rows] per group) through LDS: a workgroup moves 64 rows x
 // 32 words, reading 128-byte row runs and writing 256-byte column runs.
-__global__ void __launch_bounds__(256) scales_to_pairs_kernel(const uint32_t* __restrict__ in, int64_t rows,
-                                                              int64_t kp, uint32_t* __restrict__ out) {
+struct PairsJob {
+  const uint32_t* in;
+  uint32_t* out;
+  int64_t rows, kp;
+  unsigned gx, gy;      // workgroups along the words and the rows of a group
+  unsigned first;       // the job's first workgroup
+};
+__global__ void __launch_bounds__(256) scales_to_pairs_kernel(PairsJob j0, PairsJob j1) {
   __shared__ uint32_t tile[32][65];
-  const int64_t p0 = int64_t(blockIdx.x) * 32, r0 = int64_t(blockIdx.y) * 64, g = blockIdx.z;
-  const uint32_t* src = in + g * rows * kp;
-  uint32_t* dst = out + g * rows * kp;
+  const PairsJob& j = blockIdx.x < j1.first ? j0 : j1;
+  const unsigned id = blockIdx.x - j.first, per = j.gx * j.gy;
+  const unsigned g = id / per, yx = id - g * per, y = yx / j.gx, x = yx - y * j.gx;
+  const int64_t rows = j.rows, kp = j.kp, p0 = int64_t(x) * 32, r0 = int64_t(y) * 64;
+  const uint32_t* src = j.in + g * rows * kp;
+  uint32_t* dst = j.out + g * rows * kp;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const int i = threadIdx.x + 256 * k, r = i >> 5, p = i & 31;
@@ -485,15 +494,29 @@ hipError_t launch_quant_rows(const uint16_t* x, int64_t rows, int64_t cols, int 
   return hipGetLastError();
 }
 
-hipError_t launch_scales_to_pairs(const uint8_t* in, int64_t groups, int64_t rows, int64_t k, uint8_t* out,
-                                  hipStream_t st) {
-  if (k % 128) return hipErrorInvalidValue;
-  const int64_t kp = k / 128;
-  if (groups == 0 || rows == 0 || kp == 0) return hipSuccess;
-  if (groups > 65535 || (rows + 63) / 64 > 65535 || (kp + 31) / 32 > INT32_MAX) return hipErrorInvalidValue;
-  const dim3 grid(unsigned((kp + 31) / 32), unsigned((rows + 63) / 64), unsigned(groups));
-  scales_to_pairs_kernel<<<grid, 256, 0, st>>>(reinterpret_cast<const uint32_t*>(in), rows, kp,
-                                               reinterpret_cast<uint32_t*>(out));
+hipError_t launch_scales_to_pairs(const ScalesToPairs* jobs, int n, hipStream_t st) {
+  PairsJob j[2] = {};
+  int64_t total = 0;
+  for (int i = 0; i < 2; ++i) {
+    j[i].first = unsigned(total);
+    if (i >= n) continue;
+    const ScalesToPairs& q = jobs[i];
+    if (q.k % 128) return hipErrorInvalidValue;
+    const int64_t kp = q.k / 128, gx = (kp + 31) / 32, gy = (q.rows + 63) / 64;
+    j[i].in = reinterpret_cast<const uint32_t*>(q.in);
+    j[i].out = reinterpret_cast<uint32_t*>(q.out);
+    j[i].rows = q.rows;
+    j[i].kp = kp;
+    if (gx > INT32_MAX || gy > INT32_MAX || gx * gy > INT32_MAX || (gx * gy > 0 && q.groups > INT32_MAX / (gx * gy)))
+      return hipErrorInvalidValue;
+    j[i].gx = unsigned(gx);
+    j[i].gy = unsigned(gy);
+    total += gx * gy * q.groups;
+  }
+  if (total > INT32_MAX) return hipErrorInvalidValue;
+  if (total == 0) return hipSuccess;
+  if (n < 2) j[1].first = unsigned(total);
+  scales_to_pairs_kernel<<<unsigned(total), 256, 0, st>>>(j[0], j[1]);
   return hipGetLastError();
 }
 

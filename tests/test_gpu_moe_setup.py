@@ -1,0 +1,74 @@
+"""The MoE backward's set-up regions against plain recomputation: slots, block
+extents, expert lists (in one workgroup up to 1024 blocks and experts, in three
+kernels past that), the inverse map, and d(affinity)'s zeros."""
+import numpy as np
+import pytest
+import torch
+
+import mxfp8_grouped_gemm_amd as mx
+import synthetic as S
+from moe_gpu_common import gpu_problem
+
+pytestmark = pytest.mark.gpu
+
+
+def _bound(gp, tpid, b2e, **kw):
+    t, cfg = gp["t"], gp["cfg"]
+    gu_c, gu_s, d_c, d_s = gp["wq"]
+    E, H, I = cfg.E, cfg.H, cfg.I
+    return mx.MoeBwd(t["hidden"], torch.from_numpy(gp["aff"]).cuda(), gu_c.view(E, H, 2, I), gu_s.view(E, H, 2, I // 32),
+                     d_c.view(E, I, H), d_s.view(E, I, H // 32), tpid, b2e, t["dy"], cfg.B, t["ckpt"],
+                     down_proj_bias=t["b2"], affinity_on=cfg.affinity_on, **kw)
+
+
+def _check(cfg, op, tpid, b2e, N):
+    L, ws, B, E, T = op.layout, op.workspace.cpu().numpy(), cfg.B, cfg.E, cfg.T
+    i32 = lambda name, n: ws[L[name]:L[name] + 4 * n].view(np.int32)
+    ok = (tpid >= 0) & (tpid < T) & (np.repeat(b2e, B) >= 0) & (np.repeat(b2e, B) < E)
+    tok = np.where(ok, tpid, -1)
+    assert np.array_equal(i32("slot_token", N * B), tok)
+    aff = np.where(ok, op_aff(op, T, E)[np.maximum(tok, 0), np.clip(np.repeat(b2e, B), 0, E - 1)], 0)
+    assert np.array_equal(ws[L["slot_affinity"]:L["slot_affinity"] + 4 * N * B].view(np.float32), aff.astype(np.float32))
+    ext = np.array([(np.nonzero(row)[0][-1] + 1) if row.any() else 0 for row in ok.reshape(N, B)])
+    assert np.array_equal(i32("block_flag", N), ext)
+    lists = [[b for b in range(N) if b2e[b] == e and ext[b]] for e in range(E)]
+    off = np.concatenate([[0], np.cumsum([len(x) for x in lists])])
+    assert np.array_equal(i32("expert_block_offsets", E + 1), off)
+    assert i32("expert_block_list", N)[:off[-1]].tolist() == [b for x in lists for b in x]
+    inv = np.full((T, E), -1)
+    s = np.nonzero(ok)[0]
+    inv[tok[s], np.repeat(b2e, B)[s]] = s
+    assert np.array_equal(i32("slot_of", T * E).reshape(T, E), inv)
+    daff = op.out["daff"].float().cpu().numpy().reshape(T, E)
+    assert not daff[inv < 0].any() and daff[inv >= 0].any()
+
+
+def op_aff(op, T, E):
+    return op.keep[1].cpu().numpy().reshape(T, E)
+
+
+@pytest.mark.parametrize("T,E,N,order", [(256, 4, None, "sorted"), (300, 7, 40, "shuffled"), (64, 3, 1024, "shuffled"),
+                                         (64, 3, 1025, "shuffled"), (200, 130, 190, "shuffled"),
+                                         (31, 5, None, "sorted")])
+def test_setup_regions(T, E, N, order):
+    """Blocks in the builder's order and in any other, with empty blocks between,
+    blocks of no expert, and odd T * E."""
+    cfg = S.scaled(S.TINY, T=T, H=128, I=64, E=E, K=2, B=128)
+    print("setup", T, E, N, order, flush=True)
+    gp = gpu_problem(cfg, N=N)
+    N = gp["N"]
+    tpid, b2e = gp["tpid"].cpu().numpy().reshape(N, cfg.B), gp["b2e"].cpu().numpy().copy()
+    if order == "shuffled":
+        perm = np.random.default_rng(N).permutation(N)
+        tpid, b2e = tpid[perm], b2e[perm]
+        empty = np.nonzero((tpid < 0).all(1))[0]
+        b2e[empty[::2]] = np.array([-1, E, 2 ** 30])[np.arange(len(empty[::2])) % 3]
+        used = np.nonzero((tpid >= 0).any(1))[0]
+        tpid[used[0]] = np.where(tpid[used[0]] >= 0, -5, T + 3)          # a block of ids out of range
+        tpid[used[1], ::3] = -1                                          # holes inside a block
+    tpid = np.ascontiguousarray(tpid.reshape(-1))
+    op = _bound(gp, torch.from_numpy(tpid).cuda(), torch.from_numpy(np.ascontiguousarray(b2e)).cuda())
+    op.out["daff"].fill_(3.0)
+    op.run()
+    torch.cuda.synchronize()
+    _check(cfg, op, tpid, b2e, N)
