@@ -182,3 +182,21 @@ def test_in_a_graph_with_a_shared_workspace():
             g.replay()
             torch.cuda.synchronize()
             _check(z, idx, mask, seq, (0.1, 0.1), None, out, d)
+
+
+@pytest.mark.parametrize("E", [8, 60, 128, 700])
+def test_both_sides_of_the_one_workgroup_rule(E):
+    """One round of a workgroup's rows in up to 64 sequences, or two in up to four,
+    take one launch: sizes just inside and past the limits, against the oracle."""
+    threads, lanes = (256, 64) if E > 512 else (512, max(1, 2 ** int(np.ceil(np.log2(E / 8)))))
+    edge = threads // lanes
+    for T in (edge - 1, edge, edge + 1, 2 * edge - 1, 2 * edge, 2 * edge + 1):
+        for S in (1, 4, 5, 64, 65):
+            z, idx, mask, seq = _problem(T, E, 3, S, torch.float32, T + S)
+            kw = dict(token_mask=_dev(mask), seq_starts=_dev(seq))
+            got = mx.moe_balance_loss(_dev(z), _dev(idx), 0.02, 0.003, **kw)
+            _check(z, idx, mask, seq, (0.02, 0.003), None, got, None)
+    z, idx, mask, seq = _problem(1, E, 3, 9, torch.float32, 0, masked=0, closed=0, dropped=0)
+    none = torch.zeros(10, dtype=torch.int32, device="cuda")
+    loss, counts, num = mx.moe_balance_loss(_dev(z)[:0], _dev(idx)[:0], 1.0, 1.0, seq_starts=none)
+    assert counts.shape == (9, E) and not loss.any() and not counts.any() and not num.any()
