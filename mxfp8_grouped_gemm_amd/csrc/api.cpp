@@ -642,22 +642,30 @@ static int moe_run(const moe_bwd_mxfp8_args* a, void* ws, size_t ws_bytes, void*
   STEP(order(side ? &side->ev[0] : nullptr, st, s2), "second stream after the set-up");
   // token-axis operands of Phases 2 and 4: X, a*dY (on H) or dY (on I); the intermediate
   // operand comes out of the Phase-1 epilogue
-  STEP(mx::launch_quant_tok(a->hidden_states, T, H, slot_tok, nullptr, P, a->fmt_act, at(L.x_tok_codes),
-                            at(L.x_tok_scales), s2, true, false, nullptr, true),
-       "gather-quantize X");
-  if (a->down_proj_act_checkpoint) {   // a*dY supplied per slot: each routed slot reads its own row
-    STEP(mx::launch_quant_tok(a->down_proj_act_checkpoint, P, H, slot_tok, nullptr, P, a->fmt_grad,
-                              at(L.gy_tok_codes), at(L.gy_tok_scales), s2, true, true, nullptr, true),
-         "quantize the a*dY checkpoint");
+  // (one launch where neither carries more: no fused bias reductions, no a*dY checkpoint)
+  if (!a->down_proj_act_checkpoint && !moe_fuse_bias(a) && mx::quant_tok_xy_fits(T, H, P)) {
+    STEP(mx::launch_quant_tok_xy(a->hidden_states, a->output_hidden_states_grad, T, H, slot_tok,
+                                 a->affinity_on == 0 ? slot_aff : nullptr, P, a->fmt_act, a->fmt_grad,
+                                 at(L.x_tok_codes), at(L.x_tok_scales), at(L.gy_tok_codes), at(L.gy_tok_scales), s2),
+         "gather-quantize X and dY");
   } else {
-    // with a bias: db2 and the <dY, b2> shares of d(a) from the same row reads
-    // (rows I/32 .. I/32 + H/128 of daff_part)
-    const mx::TokBias tb{a->down_proj_bias, a->block_to_expert, B, db2_acc,
-                         reinterpret_cast<float*>(at(L.daff_part)) + (I / 32) * P};
-    STEP(mx::launch_quant_tok(a->output_hidden_states_grad, T, H, slot_tok, a->affinity_on == 0 ? slot_aff : nullptr,
-                              P, a->fmt_grad, at(L.gy_tok_codes), at(L.gy_tok_scales), s2, true, false,
-                              moe_fuse_bias(a) ? &tb : nullptr, true),
-         "gather-quantize dY");
+    STEP(mx::launch_quant_tok(a->hidden_states, T, H, slot_tok, nullptr, P, a->fmt_act, at(L.x_tok_codes),
+                              at(L.x_tok_scales), s2, true, false, nullptr, true),
+         "gather-quantize X");
+    if (a->down_proj_act_checkpoint) {   // a*dY supplied per slot: each routed slot reads its own row
+      STEP(mx::launch_quant_tok(a->down_proj_act_checkpoint, P, H, slot_tok, nullptr, P, a->fmt_grad,
+                                at(L.gy_tok_codes), at(L.gy_tok_scales), s2, true, true, nullptr, true),
+           "quantize the a*dY checkpoint");
+    } else {
+      // with a bias: db2 and the <dY, b2> shares of d(a) from the same row reads
+      // (rows I/32 .. I/32 + H/128 of daff_part)
+      const mx::TokBias tb{a->down_proj_bias, a->block_to_expert, B, db2_acc,
+                           reinterpret_cast<float*>(at(L.daff_part)) + (I / 32) * P};
+      STEP(mx::launch_quant_tok(a->output_hidden_states_grad, T, H, slot_tok, a->affinity_on == 0 ? slot_aff : nullptr,
+                                P, a->fmt_grad, at(L.gy_tok_codes), at(L.gy_tok_scales), s2, true, false,
+                                moe_fuse_bias(a) ? &tb : nullptr, true),
+           "gather-quantize dY");
+    }
   }
   stage = 3;
   if (a->has_bias && !moe_fuse_bias(a))

@@ -40,6 +40,14 @@ hipError_t launch_quant_tok(const uint16_t* x, int64_t src_rows, int64_t cols, c
                             const float* rowscale, int64_t rows, int fmt, uint8_t* codes_t,
                             uint8_t* scales_t, hipStream_t st, bool pairs = false, bool self_rows = false,
                             const TokBias* bias = nullptr, bool stage_major = false);
+// the MoE backward's two gathers, X and dY (times rowscale, or null), by the same
+// index in one launch, codes stage-major and scales pair-major; for short gathers
+// from sources under 2 GiB, rows % 128 == 0
+bool quant_tok_xy_fits(int64_t src_rows, int64_t cols, int64_t rows);
+hipError_t launch_quant_tok_xy(const uint16_t* x, const uint16_t* dy, int64_t src_rows, int64_t cols,
+                               const int32_t* idx, const float* rowscale, int64_t rows, int fmt_x, int fmt_y,
+                               uint8_t* x_codes, uint8_t* x_scales, uint8_t* y_codes, uint8_t* y_scales,
+                               hipStream_t st);
 // prequant.hip: an operand quantised along its rows (codes [R][C], scales
 // [R/32][C]) into the GEMM layout: codes [C][R]; scales pair-major
 // [R/128][C][4] (pairs) or row-major [C][R/32]

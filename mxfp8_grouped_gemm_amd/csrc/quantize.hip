@@ -262,13 +262,11 @@ constexpr int kTokCols = 128;
 // P3 (sonic-moe functional/backward.py, db2_and_ds_kernel): db2 and the bias
 // term of the affinity gradient.
 template <int FMT, bool GATHER, bool ROWSCALE, bool PAIRS, bool OFF32, bool BIAS>
-__global__ void __launch_bounds__(256) quant_tok_kernel(const uint16_t* __restrict__ x,
-                                                         int64_t src_rows, int64_t cols,
-                                                         const int32_t* __restrict__ idx,
-                                                         const float* __restrict__ rowscale,
-                                                         int64_t rows, uint8_t* __restrict__ codes_t,
-                                                         uint8_t* __restrict__ scales_t, int self_rows,
-                                                         TokBias bias, int stage_major) {
+__device__ __forceinline__ void quant_tok_tile(const uint16_t* __restrict__ x, int64_t src_rows, int64_t cols,
+                                               const int32_t* __restrict__ idx, const float* __restrict__ rowscale,
+                                               int64_t rows, uint8_t* __restrict__ codes_t,
+                                               uint8_t* __restrict__ scales_t, int self_rows, const TokBias& bias,
+                                               int stage_major) {
   const int cp = threadIdx.x & 63;
   const int grp = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t row0 = int64_t(blockIdx.y) * kTokRows + grp * 32;
@@ -360,6 +358,34 @@ __global__ void __launch_bounds__(256) quant_tok_kernel(const uint16_t* __restri
     }
   }
   tok_encode_pair<FMT, PAIRS>(w, rows, cols, colA, row0, codes_t, scales_t, stage_major != 0);
+}
+
+template <int FMT, bool GATHER, bool ROWSCALE, bool PAIRS, bool OFF32, bool BIAS>
+__global__ void __launch_bounds__(256) quant_tok_kernel(const uint16_t* __restrict__ x, int64_t src_rows, int64_t cols,
+                                                        const int32_t* __restrict__ idx,
+                                                        const float* __restrict__ rowscale, int64_t rows,
+                                                        uint8_t* __restrict__ codes_t, uint8_t* __restrict__ scales_t,
+                                                        int self_rows, TokBias bias, int stage_major) {
+  quant_tok_tile<FMT, GATHER, ROWSCALE, PAIRS, OFF32, BIAS>(x, src_rows, cols, idx, rowscale, rows, codes_t, scales_t,
+                                                            self_rows, bias, stage_major);
+}
+
+// X (blockIdx.z 0) and dY (1, with the affinities where ROWSCALE) gathered in
+// one launch, both pair-major and stage-major.
+template <int FX, int FY, bool ROWSCALE>
+__global__ void __launch_bounds__(256) quant_tok_xy_kernel(const uint16_t* __restrict__ x,
+                                                           const uint16_t* __restrict__ dy, int64_t src_rows,
+                                                           int64_t cols, const int32_t* __restrict__ idx,
+                                                           const float* __restrict__ rowscale, int64_t rows,
+                                                           uint8_t* __restrict__ x_codes, uint8_t* __restrict__ x_scales,
+                                                           uint8_t* __restrict__ y_codes,
+                                                           uint8_t* __restrict__ y_scales) {
+  if (blockIdx.z == 0)
+    quant_tok_tile<FX, true, false, true, true, false>(x, src_rows, cols, idx, nullptr, rows, x_codes, x_scales, 0,
+                                                       TokBias{}, 1);
+  else
+    quant_tok_tile<FY, true, ROWSCALE, true, true, false>(dy, src_rows, cols, idx, rowscale, rows, y_codes, y_scales, 0,
+                                                          TokBias{}, 1);
 }
 
 // ---------------------------------------------------------------------------
@@ -609,6 +635,40 @@ hipError_t launch_quant_tok(const uint16_t* x, int64_t src_rows, int64_t cols, c
   } else {
     if (pairs) go(E5{}, std::true_type{});
     else go(E5{}, std::false_type{});
+  }
+  return hipGetLastError();
+}
+
+// One launch for both pays where a gather is short, up to 8 workgroups per CU
+// (7 workgroups each: the tiny step 69 -> 65 us); with 5120 (the medium workload)
+// its step was 0.3% slower.
+bool quant_tok_xy_fits(int64_t src_rows, int64_t cols, int64_t rows) {
+  const int64_t tiles = (cols + kTokCols - 1) / kTokCols * ((rows + kTokRows - 1) / kTokRows);
+  return tiles <= 2048 && src_rows * cols * 2 < int64_t(v2::kOOB) && rows <= int64_t(INT32_MAX) && rows % 128 == 0;
+}
+hipError_t launch_quant_tok_xy(const uint16_t* x, const uint16_t* dy, int64_t src_rows, int64_t cols,
+                               const int32_t* idx, const float* rowscale, int64_t rows, int fmt_x, int fmt_y,
+                               uint8_t* x_codes, uint8_t* x_scales, uint8_t* y_codes, uint8_t* y_scales,
+                               hipStream_t st) {
+  if (rows == 0 || cols == 0) return hipSuccess;
+  if (!quant_tok_xy_fits(src_rows, cols, rows)) return hipErrorInvalidValue;
+  const dim3 grid(unsigned((cols + kTokCols - 1) / kTokCols), unsigned((rows + kTokRows - 1) / kTokRows), 2);
+  auto go = [&](auto fx, auto fy) {
+    if (rowscale)
+      quant_tok_xy_kernel<fx(), fy(), true><<<grid, 256, 0, st>>>(x, dy, src_rows, cols, idx, rowscale, rows, x_codes,
+                                                                  x_scales, y_codes, y_scales);
+    else
+      quant_tok_xy_kernel<fx(), fy(), false><<<grid, 256, 0, st>>>(x, dy, src_rows, cols, idx, rowscale, rows, x_codes,
+                                                                   x_scales, y_codes, y_scales);
+  };
+  using E4 = std::integral_constant<int, kE4M3>;
+  using E5 = std::integral_constant<int, kE5M2>;
+  if (fmt_x == kE4M3) {
+    if (fmt_y == kE4M3) go(E4{}, E4{});
+    else go(E4{}, E5{});
+  } else {
+    if (fmt_y == kE4M3) go(E5{}, E4{});
+    else go(E5{}, E5{});
   }
   return hipGetLastError();
 }
