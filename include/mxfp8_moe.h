@@ -505,7 +505,9 @@ int moe_router_bwd(int mode, int64_t T, int64_t E, int64_t K, const int32_t* top
  * Errors: INVALID_ARG for an unknown mode or type, a shape outside the bounds,
  * renorm with another mode or outside {0,1}, a NULL pointer, or a tensor
  * (token_mask excepted) not 16-byte aligned; UNSUPPORTED for E above
- * MXFP8_ROUTER_MAX_EXPERTS or T above 2^31 - 1; HIP if the launch fails. */
+ * MXFP8_ROUTER_MAX_EXPERTS, T * K above 2^31 - 1, or more tokens than one launch
+ * takes (2^32 - 65536 threads, E / 8 rounded up to a power of two, at most 64, for
+ * each: 2^26 - 1024 tokens of more than 256 experts); HIP if the launch fails. */
 typedef enum { MXFP8_TYPE_F32 = 0, MXFP8_TYPE_BF16 = 1 } mxfp8_type;
 #define MXFP8_ROUTER_MAX_EXPERTS 4096
 int moe_router_fwd(int mode, int64_t T, int64_t E, int64_t K, const void* logits, int logits_type,
@@ -557,8 +559,10 @@ int moe_router_fwd(int mode, int64_t T, int64_t E, int64_t K, const void* logits
  * Errors: INVALID_ARG for an unknown type, a shape outside the bounds, S != 1 without
  * seq_starts, a coefficient that is not finite, accumulate outside {0,1}, a
  * NULL pointer, or a tensor (token_mask, seq_starts, dloss, loss: 4-byte, the
- * mask any) not 16-byte aligned; UNSUPPORTED for E above MXFP8_ROUTER_MAX_EXPERTS,
- * T * K or S * E above 2^31 - 1; WORKSPACE; HIP if a launch fails. */
+ * mask any) not 16-byte aligned; UNSUPPORTED for the sizes that moe_router_fwd
+ * refuses so, S above MOE_BALANCE_MAX_SEQUENCES or S * E above 2^31 - 1;
+ * WORKSPACE; HIP if a launch fails. */
+#define MOE_BALANCE_MAX_SEQUENCES 1048576
 typedef struct {
   int64_t T, E, K, S;
   const void* logits;
@@ -606,7 +610,7 @@ int moe_balance_loss_bwd(const moe_balance_args* args, void* stream);
  * rows == 0 is not an error: nothing is enqueued.
  * Errors: INVALID_ARG for a negative size, cols % 32 != 0, a period that does
  * not fit, a bad activation or fmt, T < 0, a NULL pointer, or a tensor not
- * 16-byte aligned (scales: any alignment); UNSUPPORTED for rows * cols above 2^39; HIP if
+ * 16-byte aligned (scales: any alignment); UNSUPPORTED for rows * cols above 2^34; HIP if
  * the launch fails. */
 typedef struct {
   int64_t rows, cols;

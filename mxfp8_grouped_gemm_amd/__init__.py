@@ -606,13 +606,15 @@ def _gated_act_args(shape, activation, fmt, token_position_to_id, T, device, nam
         cols *= n
     if token_position_to_id is None:
         return GatedActArgs(rows, cols, activation, fmt)
+    if T is None:
+        raise ValueError(f"{name}: token_position_to_id needs T, the number of tokens")
     return GatedActArgs(rows, cols, activation, fmt,
                         _tensor(token_position_to_id, torch.int32, (rows * period,), device, "token_position_to_id"),
                         period, T)
 
 
 def mxfp8_gated_act_fwd(gate_up: torch.Tensor, activation: int = ACT_SWIGLU, fmt: int = E4M3,
-                        token_position_to_id: Optional[torch.Tensor] = None, T: int = 0, out=None):
+                        token_position_to_id: Optional[torch.Tensor] = None, T: Optional[int] = None, out=None):
     """Gated activation with its checkpoint in MXFP8 (include/mxfp8_moe.h: mxfp8_gated_act_fwd).
 
     gate_up [rows, 2, ..., n] bf16 -- a dense FFN's [M, 2, I] or the MoE checkpoint layout [N, 2, I, B] -- ->
@@ -638,8 +640,8 @@ def mxfp8_gated_act_fwd(gate_up: torch.Tensor, activation: int = ACT_SWIGLU, fmt
 
 
 def mxfp8_gated_act_bwd(dinter: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, activation: int = ACT_SWIGLU,
-                        fmt: int = E4M3, token_position_to_id: Optional[torch.Tensor] = None, T: int = 0,
-                        out: Optional[torch.Tensor] = None) -> torch.Tensor:
+                        fmt: int = E4M3, token_position_to_id: Optional[torch.Tensor] = None,
+                        T: Optional[int] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The gated activation's backward from its MXFP8 checkpoint (include/mxfp8_moe.h: mxfp8_gated_act_bwd):
     dinter [rows, ..., n] bf16 with mxfp8_gated_act_fwd's codes and scales -> d(gate_up), bf16 of codes' shape."""
     shape = codes.shape

@@ -825,6 +825,9 @@ static int router_shape(const char* what, int64_t T, int64_t E, int64_t K, int t
   if (E > MXFP8_ROUTER_MAX_EXPERTS)
     return fail(MXFP8_ERR_UNSUPPORTED, "%s: E %lld above %d", what, (long long)E, MXFP8_ROUTER_MAX_EXPERTS);
   if (T > INT32_MAX / K) return fail(MXFP8_ERR_UNSUPPORTED, "%s: T * K beyond 2^31 - 1", what);
+  if (T > mx::router_max_tokens(E))
+    return fail(MXFP8_ERR_UNSUPPORTED, "%s: T %lld beyond one launch with E %lld (%lld)", what, (long long)T, (long long)E,
+                (long long)mx::router_max_tokens(E));
   return MXFP8_OK;
 }
 
@@ -877,7 +880,8 @@ static int balance_shape(const char* what, int64_t T, int64_t E, int64_t K, int6
   int rc = router_shape(what, T, E, K, type);
   if (rc) return rc;
   if (S < 1) return fail(MXFP8_ERR_INVALID_ARG, "%s: S must be positive (got %lld)", what, (long long)S);
-  if (S > INT32_MAX / E) return fail(MXFP8_ERR_UNSUPPORTED, "%s: S * E beyond 2^31 - 1", what);
+  if (S > MOE_BALANCE_MAX_SEQUENCES || S > INT32_MAX / E)
+    return fail(MXFP8_ERR_UNSUPPORTED, "%s: S above %d or S * E beyond 2^31 - 1", what, MOE_BALANCE_MAX_SEQUENCES);
   return MXFP8_OK;
 }
 
@@ -957,8 +961,8 @@ static int gated_act_check(const char* what, const mxfp8_gated_act_args* a, cons
                 "and divides cols (got %lld)", what, (long long)a->period);
   empty = a->rows == 0 || a->cols == 0;
   if (empty) return MXFP8_OK;
-  if (a->rows > (int64_t(1) << 39) / a->cols)
-    return fail(MXFP8_ERR_UNSUPPORTED, "%s: rows * cols beyond 2^39", what);
+  if (a->rows > (int64_t(1) << 34) / a->cols)   // one launch, a thread for 8 elements
+    return fail(MXFP8_ERR_UNSUPPORTED, "%s: rows * cols beyond 2^34", what);
   if (!scales) return fail(MXFP8_ERR_INVALID_ARG, "%s: null pointer", what);
   for (int i = 0; i < n; ++i)
     if (!ptrs[i]) return fail(MXFP8_ERR_INVALID_ARG, "%s: null pointer", what);

@@ -127,6 +127,7 @@ struct RouterFwdArgs {
   float* scores;              // [T,K]
   float* aff;                 // [T,E], or null
 };
+int64_t router_max_tokens(int64_t E);   // of one launch, the losses' too
 hipError_t launch_router_fwd(const RouterFwdArgs& p, hipStream_t st);
 
 struct BalanceArgs {

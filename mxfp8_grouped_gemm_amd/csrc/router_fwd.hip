@@ -301,10 +301,12 @@ __global__ void __launch_bounds__(kThreads) router_merge_kernel(RouterFwdArgs p)
   if (in) rows::store<8, VEC>(p.aff + t0 * p.E + slot * E, E, lane, w);
 }
 
+int64_t router_max_tokens(int64_t E) { return rows::max_tokens(E); }
+
 hipError_t launch_router_fwd(const RouterFwdArgs& p, hipStream_t st) {
   if (p.T <= 0) return hipSuccess;
   const int64_t r = kThreads / rows::lanes(p.E);
-  if (p.E > kRouterFwdMaxExperts || (p.T + r - 1) / r > int64_t(INT32_MAX)) return hipErrorInvalidValue;
+  if (p.E > kRouterFwdMaxExperts || p.T > rows::max_tokens(p.E)) return hipErrorInvalidValue;
   const unsigned grid = unsigned((p.T + r - 1) / r);
   const int score = p.mode == kRouterTopk ? kRaw
                     : p.mode == kRouterSoftmaxOverTopk || p.renorm ? kOverSelection : kOverAll;

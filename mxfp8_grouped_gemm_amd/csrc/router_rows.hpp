@@ -125,5 +125,8 @@ inline int lanes(int64_t E) {
   return l;
 }
 
+// tokens of one launch: L threads each, under 2^32 in all
+inline int64_t max_tokens(int64_t E) { return ((int64_t(1) << 32) - 65536) / lanes(E); }
+
 }  // namespace rows
 }  // namespace mx

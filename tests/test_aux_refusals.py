@@ -34,6 +34,7 @@ def test_router_fwd_refusals():
         assert run(**bad) == 1, bad
     assert run(E=4097) == 2 and "4096" in mx.last_error()
     assert run(T=2 ** 30) == 2
+    assert run(T=2 ** 26 - 1023, E=257, K=1) == 2 and "one launch" in mx.last_error()
     assert run(renorm=1) == 1 and "renorm" in mx.last_error()
     assert run(mode=1, renorm=2) == 1
     for k in ("logits", "idx", "scores"):
@@ -68,7 +69,7 @@ def test_balance_refusals():
             assert f(**bad) == 1, bad
         assert f(E=4097, K=1) == 2
         assert f(T=2 ** 30) == 2
-        assert f(S=2 ** 28, seq_starts=F) == 2
+        assert f(S=2 ** 28, seq_starts=F) == 2 and f(S=2 ** 20 + 1, seq_starts=F) == 2
     assert fwd(loss=None) == 1 and fwd(topk_idx=None) == 1 and fwd(topk_idx=0x10004) == 1 and fwd(loss=0x10002) == 1
     assert bwd(dlogits=None) == 1 and bwd(dlogits=0x10004) == 1 and bwd(dloss=0x10002) == 1
     assert bwd(accumulate=2) == 1 and "accumulate" in mx.last_error()
@@ -130,6 +131,8 @@ def test_bindings_check_their_tensors():
             mx.mxfp8_gated_act_bwd(x[:, 0].contiguous(), bad, s)
     with pytest.raises(ValueError, match="shape"):
         mx.mxfp8_gated_act_bwd(x, c, s)
+    with pytest.raises(ValueError, match="needs T"):
+        mx.mxfp8_gated_act_bwd(x[:, 0].contiguous(), c, s, token_position_to_id=torch.zeros(128, dtype=torch.int32))
     with pytest.raises(ValueError, match="token_position_to_id"):
         mx.mxfp8_gated_act_bwd(x[:, 0].contiguous(), c, s, token_position_to_id=torch.zeros(64, dtype=torch.int32), T=1)
 

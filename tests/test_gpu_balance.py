@@ -200,3 +200,60 @@ def test_both_sides_of_the_one_workgroup_rule(E):
     none = torch.zeros(10, dtype=torch.int32, device="cuda")
     loss, counts, num = mx.moe_balance_loss(_dev(z)[:0], _dev(idx)[:0], 1.0, 1.0, seq_starts=none)
     assert counts.shape == (9, E) and not loss.any() and not counts.any() and not num.any()
+
+
+@pytest.mark.parametrize("T,E,S", [(2000, 24, 5000), (300, 8, 5000), (1500, 130, 700), (40, 16, 300)])
+def test_many_sequences_most_of_them_empty(T, E, S):
+    """More sequences than one look-up step holds, hundreds that start at one token."""
+    rng = np.random.default_rng(S)
+    z, idx, mask, _ = _problem(T, E, 3, 1, torch.float32, S)
+    seq = np.sort(np.concatenate([rng.integers(0, T + 1, S + 1 - 2 * 150), np.full(150, T // 3), np.full(150, T // 2)]))
+    seq = seq.astype(np.int32)
+    kw = dict(token_mask=_dev(mask), seq_starts=_dev(seq))
+    dloss = torch.tensor([1.3, 0.4])
+    got = mx.moe_balance_loss(_dev(z), _dev(idx), 0.02, 0.003, **kw)
+    d = mx.moe_balance_loss_bwd(_dev(z), got[1], got[2], 3, 0.02, 0.003, dloss=_dev(dloss), **kw)
+    _check(z, idx, mask, seq, (0.02, 0.003), dloss, got, d)
+
+
+def test_starts_that_decrease_stay_in_range():
+    """Unspecified results, but no access out of range: guard words around every output."""
+    T, E, K, S = 500, 12, 2, 40
+    z, idx, _, _ = _problem(T, E, K, 1, torch.float32, 5, masked=0)
+    rng = np.random.default_rng(1)
+    for seq in (rng.integers(-10 ** 6, 10 ** 6, S + 1), np.arange(S, -1, -1) * 12, rng.integers(0, T, S + 1)):
+        q = _dev(seq.astype(np.int32))
+        bufs = [torch.full((n + 128,), 7, dtype=dt, device="cuda")
+                for n, dt in ((2, torch.float32), (S * E, torch.int32), (S + 2, torch.int32), (T * E, torch.float32))]
+        out = (bufs[0][:2], bufs[1][:S * E].view(S, E), bufs[2][:S + 2])
+        mx.moe_balance_loss(_dev(z), _dev(idx), 0.1, 0.1, seq_starts=q, out=out)
+        mx.moe_balance_loss_bwd(_dev(z), out[1], out[2], K, 0.1, 0.1, seq_starts=q, out=bufs[3][:T * E].view(T, E))
+        torch.cuda.synchronize()
+        for b, n in zip(bufs, (2, S * E, S + 2, T * E)):
+            assert b[n:].eq(7).all()
+
+
+def test_repeated_ids_count_as_often_as_they_stand():
+    z = torch.randn(64, 8, device="cuda")
+    idx = torch.full((64, 3), 5, dtype=torch.int32, device="cuda")
+    _, counts, _ = mx.moe_balance_loss(z, idx, 1.0)
+    assert counts.tolist() == [[0, 0, 0, 0, 0, 192, 0, 0]]
+
+
+def test_two_streams_at_once():
+    T, E, K = 9000, 40, 4
+    probs = [_problem(T, E, K, 6, torch.float32, s) for s in (1, 2)]
+    args = [[_dev(x) for x in p] for p in probs]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(8):
+        for i, s in enumerate(streams):
+            z, idx, mask, seq = args[i]
+            with torch.cuda.stream(s):
+                outs[i].append(mx.moe_balance_loss(z, idx, 0.1, 0.1, token_mask=mask, seq_starts=seq))
+    torch.cuda.synchronize()
+    for i in range(2):
+        _check(*probs[i], (0.1, 0.1), None, outs[i][0], None)
+        for o in outs[i][1:]:
+            assert all(torch.equal(a, b) for a, b in zip(o, outs[i][0]))

@@ -236,3 +236,18 @@ def test_a_captured_backward_replays():
         ref = _bound(gp, None, _checkpoint(gp, mx.E4M3)).run()
         torch.cuda.synchronize()
         _same(cfg, got, ref)
+
+
+@pytest.mark.parametrize("name", ["medium_s", "fine_s"])
+def test_beside_the_down_projection_checkpoint(name):
+    """The a * dY checkpoint goes with either form of the gate/up checkpoint."""
+    cfg = CFGS[name]
+    gp = gpu_problem(cfg)
+    ck = _checkpoint(gp, mx.E4M3)
+    tok = gp["tpid"].long().clamp(0, cfg.T - 1)
+    a = torch.from_numpy(gp["aff"]).cuda().view(cfg.T, cfg.E)[tok, gp["b2e"].long().repeat_interleave(cfg.B)]
+    ady = (a[:, None] * gp["t"]["dy"].float()[tok]).to(torch.bfloat16).view(gp["N"], cfg.B, cfg.H)
+    got = _bound(gp, None, ck, down_proj_act_checkpoint=ady).run()
+    ref = _bound(gp, _dequant(*ck, mx.E4M3), down_proj_act_checkpoint=ady).run()
+    torch.cuda.synchronize()
+    _same(cfg, got, ref)

@@ -152,3 +152,57 @@ def test_router_backward_of_a_token_without_a_selection(mode, renorm):
     dead = (idx < 0).all(1)
     assert int(dead.sum()) == 13
     assert not d[dead].any() and torch.isfinite(d).all() and d[~dead].any(1).all()
+
+
+@pytest.mark.parametrize("E,K", [(7, 3), (64, 8), (128, 8), (128, 5), (256, 1), (512, 8), (512, 2), (700, 8)])
+def test_logits_an_ulp_apart(E, K):
+    """fp32 logits that differ in their last bits, inside the selection and across its
+    end, of both signs: the order is by value, not by expert."""
+    g = torch.Generator().manual_seed(E + K)
+    T = 400
+    z = torch.randn(T, E, generator=g)
+    base = torch.randn(T, 1, generator=g) + torch.where(torch.arange(T) % 2 == 0, 4.0, -4.0)[:, None]
+    steps = torch.randint(-40, 40, (T, E), generator=g, dtype=torch.int32)
+    close = (base.view(torch.int32) + steps).view(torch.float32)
+    some = torch.rand(T, E, generator=g) < 0.5
+    z = torch.where(some, close, z - 8).cuda()
+    z[::5] = close[::5].cuda()
+    for mode, renorm in MODES:
+        _check(mode, renorm, z, K, mx.moe_router_fwd(mode, z, K, renorm=renorm))
+
+
+@pytest.mark.parametrize("E", [5, 8, 40, 128, 300, 600])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_fewer_open_experts_than_selections(E, dtype):
+    """0 .. K open experts beside each other in a wave, NaN among the closed ones."""
+    K, T = min(E, 8), 200
+    g = torch.Generator().manual_seed(E)
+    z = torch.full((T, E), -torch.inf)
+    for t in range(T):
+        n = t % (K + 1)
+        at = torch.randperm(E, generator=g)[:n]
+        z[t, at] = torch.randn(n, generator=g)
+    z = z.to(dtype)
+    for mode, renorm in MODES:
+        _check(mode, renorm, z.cuda(), K, mx.moe_router_fwd(mode, z.cuda(), K, renorm=renorm))
+    nan = torch.where((z == -torch.inf) & (torch.rand(T, E, generator=g) < 0.3), torch.nan, z.float()).to(dtype)
+    for mode in (R.SOFTMAX_OVER_TOPK, R.TOPK):   # over the selection alone, NaN is closed like -inf
+        _check(mode, False, z.cuda(), K, mx.moe_router_fwd(mode, nan.cuda(), K))
+
+
+def test_two_streams_at_once():
+    """Calls on two streams with inputs of their own, interleaved."""
+    T, E, K = 4000, 96, 6
+    zs = [_logits(T, E, torch.float32, s) for s in (1, 2)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(8):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[i].append(mx.moe_router_fwd(0, zs[i], K))
+    torch.cuda.synchronize()
+    for i in range(2):
+        _check(0, False, zs[i], K, outs[i][0])
+        for o in outs[i][1:]:
+            assert all(torch.equal(a, b) for a, b in zip(o, outs[i][0]))
