@@ -494,9 +494,9 @@ def _sequences(seq_starts: Optional[torch.Tensor], device):
 def _call(device, name, *args):
     """One library call on `device`'s current stream (the null stream stands for the current device's, so
     that device is made current)."""
-    f = getattr(lib(), name)
+    f = getattr(_lib or lib(), name)
     index = device.index
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:   # the tensors exist, so the runtime is up
         rc = f(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
