@@ -607,6 +607,58 @@ static int moe_run(const moe_bwd_mxfp8_args* a, void* ws, size_t ws_bytes, void*
     hipError_t r = hipEventRecord(*ev, from);
     return r != hipSuccess ? r : hipStreamWaitEvent(to, *ev, 0);
   };
+  const bool h_pairs = H % 128 == 0;
+  // Phase 3 on the ring loop reads W_gate_up's scales pair-major, Phase 1 W_down's
+  const bool gu_pairs = (2 * I) % 128 == 0;
+  const bool fused = moe_phase1_fused(a);
+  mx::Phase1Args p1{};
+  if (h_pairs) {
+    p1.wd_codes = a->down_codes; p1.wd_scales = at(L.wd_scales_pairs);
+    p1.dy_codes = at(L.dy_codes); p1.dy_scales = at(L.dy_scales);
+  } else {
+    p1.wd_deq = reinterpret_cast<const uint16_t*>(at(L.wd_deq));
+    p1.dy_deq = reinterpret_cast<const uint16_t*>(at(L.dy_deq));
+  }
+  p1.ds = reinterpret_cast<float*>(at(L.phase1_ds));
+  p1.tile_start = reinterpret_cast<int32_t*>(at(L.phase1_tiles));
+  p1.slot_tok = slot_tok; p1.slot_aff = slot_aff; p1.b2e = a->block_to_expert; p1.flag = flag;
+  p1.ckpt = a->gate_up_proj_act_checkpoint_T;
+  p1.ck8_codes = a->gate_up_checkpoint_codes; p1.ck8_scales = a->gate_up_checkpoint_scales;
+  p1.ck8_fmt = a->fmt_checkpoint;
+  p1.ga_ckpt = a->gate_act_checkpoint_T;
+  p1.in_ckpt = a->intermediate_checkpoint_T;
+  p1.sc_ckpt = a->scaled_intermediate_checkpoint_T;
+  p1.T = T; p1.H = H; p1.I = I; p1.E = E; p1.N = N; p1.B = B;
+  p1.dgu_row_codes = at(L.dgu_row_codes); p1.dgu_row_scales = at(L.dgu_row_scales);
+  p1.dgu_tok_codes = at(L.dgu_tok_codes); p1.dgu_tok_scales = at(L.dgu_tok_scales);
+  p1.inter_tok_codes = at(L.inter_tok_codes); p1.inter_tok_scales = at(L.inter_tok_scales);
+  p1.daff_part = reinterpret_cast<float*>(at(L.daff_part)); p1.db1_acc = db1_acc;
+  p1.affinity_on_i = a->affinity_on; p1.has_bias = a->has_bias; p1.fmt_act = a->fmt_act;
+  p1.geglu = a->activation == MXFP8_ACT_GEGLU;
+  p1.dgu_row_pairs = gu_pairs;
+  // Tile order over the XCDs (measured: round robin 2.6% faster on Phase 1 with
+  // 58 MB W_down experts; the contiguous ranges 6% faster with 0.4-3 MB ones)
+  p1.rr_tiles = I * H >= kRoundRobinWeightBytes;
+  mx::Phase3Args p3{};
+  p3.dgu_row_codes = at(L.dgu_row_codes); p3.dgu_row_scales = at(L.dgu_row_scales);
+  p3.wgu_codes = a->gate_up_codes; p3.wgu_scales = gu_pairs ? at(L.wgu_scales_pairs) : a->gate_up_scales;
+  p3.slot_tok = slot_tok; p3.b2e = a->block_to_expert; p3.flag = flag;
+  p3.tile_start = reinterpret_cast<int32_t*>(at(L.phase3_tiles));
+  p3.H = H; p3.I = I; p3.N = N; p3.B = B; p3.dx_slot = dx_slot;
+  // the last round of tiles cut along K over the device's CUs
+  p3.conc = device_cus(st);
+  p3.parts = mx::phase3_parts_bytes(p3) > 0 ? at(L.phase3_parts) : nullptr;
+  // measured: round robin 4.8% faster with 117 MB W_gate_up experts, the
+  // contiguous ranges 6-14% faster with 0.8-6 MB ones
+  p3.rr_tiles = H * 2 * I >= kRoundRobinWeightBytes;
+  // the tile ranges of Phases 1 (its own kernel) and 3, by the set-up's last kernel
+  mx::TileRangeJob ranges[2];
+  int nranges = 0;
+  p1.ranges_done = p3.ranges_done = mx::setup_makes_ranges(N, E);
+  if (p1.ranges_done) {
+    ranges[nranges++] = mx::phase3_ranges(p3);
+    if (!fused) ranges[nranges++] = mx::phase1_ranges(p1);
+  }
   int stage = -1;
 #define STEP(call, what) \
   if (stage >= lo && stage <= hi && (e = (call)) != hipSuccess) return hip_status(e, what);
@@ -617,18 +669,16 @@ static int moe_run(const moe_bwd_mxfp8_args* a, void* ws, size_t ws_bytes, void*
     STEP(mx::launch_fill_u32(db2_acc, E * H, 0u, st), "zero db2 accumulator");
   }
   STEP(mx::launch_slot_setup(a->token_position_to_id, a->block_to_expert, a->expert_affinities_masked, T, E, N, B,
-                             a->num_valid_tokens, slot_tok, slot_aff, slot_of, daff_slot, flag, boff, blist, st),
+                             a->num_valid_tokens, slot_tok, slot_aff, slot_of, daff_slot, flag, boff, blist,
+                             ranges, nranges, st),
        "slot setup");
   stage = 1;
   // S1: dY quantised along H per token row (Phase-1 operand, gathered by token later).
   // H % 128 == 0: Phase 1 streams the codes with pair-major scales (dY's written so,
   // W_down's re-laid); otherwise it reads their exact bf16 values.
-  const bool h_pairs = H % 128 == 0;
   STEP(mx::launch_quant_rows(a->output_hidden_states_grad, T, H, a->fmt_grad, at(L.dy_codes), at(L.dy_scales), st,
                              h_pairs ? nullptr : reinterpret_cast<uint16_t*>(at(L.dy_deq)), h_pairs),
        "quantize dY");
-  // Phase 3 on the ring loop reads W_gate_up's scales pair-major, Phase 1 W_down's
-  const bool gu_pairs = (2 * I) % 128 == 0;
   mx::ScalesToPairs jobs[2];
   int njobs = 0;
   if (h_pairs) jobs[njobs++] = {a->down_scales, E, I, H, at(L.wd_scales_pairs)};
@@ -676,37 +726,8 @@ static int moe_run(const moe_bwd_mxfp8_args* a, void* ws, size_t ws_bytes, void*
   if (side && stage >= lo && stage <= hi && (e = hipEventRecord(side->ev[2], s2)) != hipSuccess)
     return hip_status(e, "second stream after the gathers");
   stage = 4;
-  // Phase 1: the product dS, fp32
-  mx::Phase1Args p1{};
-  if (h_pairs) {
-    p1.wd_codes = a->down_codes; p1.wd_scales = at(L.wd_scales_pairs);
-    p1.dy_codes = at(L.dy_codes); p1.dy_scales = at(L.dy_scales);
-  } else {
-    p1.wd_deq = reinterpret_cast<const uint16_t*>(at(L.wd_deq));
-    p1.dy_deq = reinterpret_cast<const uint16_t*>(at(L.dy_deq));
-  }
-  p1.ds = reinterpret_cast<float*>(at(L.phase1_ds));
-  p1.tile_start = reinterpret_cast<int32_t*>(at(L.phase1_tiles));
-  p1.slot_tok = slot_tok; p1.slot_aff = slot_aff; p1.b2e = a->block_to_expert; p1.flag = flag;
-  p1.ckpt = a->gate_up_proj_act_checkpoint_T;
-  p1.ck8_codes = a->gate_up_checkpoint_codes; p1.ck8_scales = a->gate_up_checkpoint_scales;
-  p1.ck8_fmt = a->fmt_checkpoint;
-  p1.ga_ckpt = a->gate_act_checkpoint_T;
-  p1.in_ckpt = a->intermediate_checkpoint_T;
-  p1.sc_ckpt = a->scaled_intermediate_checkpoint_T;
-  p1.T = T; p1.H = H; p1.I = I; p1.E = E; p1.N = N; p1.B = B;
-  p1.dgu_row_codes = at(L.dgu_row_codes); p1.dgu_row_scales = at(L.dgu_row_scales);
-  p1.dgu_tok_codes = at(L.dgu_tok_codes); p1.dgu_tok_scales = at(L.dgu_tok_scales);
-  p1.inter_tok_codes = at(L.inter_tok_codes); p1.inter_tok_scales = at(L.inter_tok_scales);
-  p1.daff_part = reinterpret_cast<float*>(at(L.daff_part)); p1.db1_acc = db1_acc;
-  p1.affinity_on_i = a->affinity_on; p1.has_bias = a->has_bias; p1.fmt_act = a->fmt_act;
-  p1.geglu = a->activation == MXFP8_ACT_GEGLU;
-  p1.dgu_row_pairs = gu_pairs;
-  // Tile order over the XCDs (measured: round robin 2.6% faster on Phase 1 with
-  // 58 MB W_down experts; the contiguous ranges 6% faster with 0.4-3 MB ones)
-  p1.rr_tiles = I * H >= kRoundRobinWeightBytes;
   // With the epilogue fused stage 4 does both and stage 5 nothing.
-  const bool fused = moe_phase1_fused(a);
+  // Phase 1: the product dS, fp32
   if (fused) {
     STEP(mx::launch_phase1_fused(p1, a->fmt_grad, a->fmt_weight, st), "phase 1 (with its epilogue)");
   } else {
@@ -718,18 +739,6 @@ static int moe_run(const moe_bwd_mxfp8_args* a, void* ws, size_t ws_bytes, void*
   stage = 6;
   STEP(order(side ? &side->ev[1] : nullptr, st, s2), "second stream after the epilogue");
   // Phase 3: dX scatter-add
-  mx::Phase3Args p3{};
-  p3.dgu_row_codes = at(L.dgu_row_codes); p3.dgu_row_scales = at(L.dgu_row_scales);
-  p3.wgu_codes = a->gate_up_codes; p3.wgu_scales = gu_pairs ? at(L.wgu_scales_pairs) : a->gate_up_scales;
-  p3.slot_tok = slot_tok; p3.b2e = a->block_to_expert; p3.flag = flag;
-  p3.tile_start = reinterpret_cast<int32_t*>(at(L.phase3_tiles));
-  p3.H = H; p3.I = I; p3.N = N; p3.B = B; p3.dx_slot = dx_slot;
-  // the last round of tiles cut along K over the device's CUs
-  p3.conc = device_cus(st);
-  p3.parts = mx::phase3_parts_bytes(p3) > 0 ? at(L.phase3_parts) : nullptr;
-  // measured: round robin 4.8% faster with 117 MB W_gate_up experts, the
-  // contiguous ranges 6-14% faster with 0.8-6 MB ones
-  p3.rr_tiles = H * 2 * I >= kRoundRobinWeightBytes;
   STEP(mx::launch_phase3(p3, a->fmt_grad, a->fmt_weight, st), "phase 3");
   stage = 7;
   // Phase 2: dW_gate_up[e] = X_tok . dGU_tok^T over the expert's blocks

@@ -189,14 +189,25 @@ hipError_t launch_build_blocks(const int32_t* topk, int64_t T, int64_t K, int64_
 int64_t build_blocks_noalloc_max_experts();
 hipError_t build_blocks_scratch(int device, int32_t** out);
 struct TailCut;
+// The tile ranges of one GEMM over the blocks' live slot tiles (moe_tiles.hpp).
 // rr: the tiles handed out round robin over the XCDs (the blocks whose slot
-// tiles are all live first, blk = the block size); cut: Phase 3's tail cut
-hipError_t launch_tile_ranges(const int32_t* ext, int64_t N, int W, int other, int32_t* start, hipStream_t st,
-                              TailCut* cut, int conc, int npairs, int rr, int blk);
+// tiles are all live first); cut: Phase 3's tail cut, or null
+struct TileRangeJob {
+  int W, other;        // slots of a slot tile, tiles along the other dimension
+  int blk;             // the block size
+  int32_t* start;
+  TailCut* cut;
+  int conc, npairs, rr;
+};
+hipError_t launch_tile_ranges(const int32_t* ext, int64_t N, const TileRangeJob& job, hipStream_t st);
+// Up to kListMax blocks and experts, the set-up's last kernel makes the ranges
+// of the GEMMs that follow as well (their launchers are told so: ranges_done).
+constexpr int kListMax = 1024;
+inline bool setup_makes_ranges(int64_t N, int64_t E) { return N <= kListMax && E <= kListMax; }
 hipError_t launch_slot_setup(const int32_t* tpid, const int32_t* b2e, const float* aff, int64_t T, int64_t E,
                              int64_t N, int64_t B, const int32_t* nvalid, int32_t* slot_tok, float* slot_aff,
                              int32_t* slot_of, float* daff_slot, int32_t* flag, int32_t* off, int32_t* list,
-                             hipStream_t st);
+                             const TileRangeJob* jobs, int njobs, hipStream_t st);
 // accumulate: each bf16 output becomes bf16(old + value) (else bf16(value), and
 // launch_dx_reduce zeroes daff [T*E] for the scatter that follows it)
 hipError_t launch_dx_reduce(const float* dx_slot, const int32_t* slot_of, int64_t T, int64_t E, int64_t H,
@@ -253,8 +264,10 @@ struct Phase1Args {
   int dgu_row_pairs;            // 1: dGU along I feeds the ring loop (2I % 128 == 0): stage-major
                                 // codes, pair-major scales
   int rr_tiles;                 // tile order over the XCDs (moe_tiles.hpp)
+  int ranges_done;              // 1: tile_start is filled already
   int tiles_m, tiles_n;
 };
+TileRangeJob phase1_ranges(const Phase1Args& p);   // launch_phase1's
 hipError_t launch_phase1(const Phase1Args& p, int fmt_grad, int fmt_weight, hipStream_t st);
 hipError_t launch_phase1_epi(const Phase1Args& p, int fmt_grad, hipStream_t st);
 // Phase 1 and its epilogue in one kernel, where phase1_fusable: the same outputs
@@ -280,8 +293,10 @@ struct Phase3Args {
   // fp32 tiles
   int conc;
   uint8_t* parts;
+  int ranges_done;                // 1: tile_start (and the cut) are filled already
   int tiles_m, tiles_n, grid_main, npairs;   // set by the launcher
 };
+TileRangeJob phase3_ranges(const Phase3Args& p);   // launch_phase3's
 hipError_t launch_phase3(const Phase3Args& p, int fg, int fw, hipStream_t st);
 // Phase 3 tiles when every slot tile of every block is live (an upper bound)
 int64_t phase3_max_tiles(const Phase3Args& p);

@@ -367,13 +367,10 @@ __global__ void __launch_bounds__(256) slot_block_kernel(const int32_t* __restri
 // the offsets by a scan over the experts, and a block's place in its list by
 // counting the blocks before it with its expert (N / 4 reads of four at a
 // time, the same address in every lane).
-constexpr int kListMax = 1024;
-__global__ void __launch_bounds__(kListMax) expert_lists_kernel(const int32_t* __restrict__ b2e,
-                                                                const int32_t* __restrict__ flag, int N, int E,
-                                                                int32_t* __restrict__ off, int32_t* __restrict__ list) {
-  __shared__ __attribute__((aligned(16))) int32_t eb[kListMax];   // an occupied block's expert, else -1
-  __shared__ int32_t cnt[kListMax];
-  __shared__ int32_t wsum[kListMax / 64];
+// eb: LDS for an occupied block's expert, else -1 (16-byte aligned); cnt, wsum: LDS
+__device__ __forceinline__ void expert_lists(const int32_t* __restrict__ b2e, const int32_t* __restrict__ flag, int N,
+                                             int E, int32_t* __restrict__ off, int32_t* __restrict__ list, int32_t* eb,
+                                             int32_t* cnt, int32_t* wsum) {
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   int e = -1;
   if (t < N && flag[t] != 0) e = b2e[t];
@@ -515,23 +512,90 @@ __global__ void __launch_bounds__(256) tile_ranges_kernel(const int32_t* __restr
   }
 }
 
-hipError_t launch_tile_ranges(const int32_t* ext, int64_t N, int W, int other, int32_t* start, hipStream_t st,
-                              TailCut* cut, int conc, int npairs, int rr, int blk) {
-  const int cmax = (blk + W - 1) / W * other;   // tiles of a block whose slot tiles are all live
-  tile_ranges_kernel<<<1, 256, 0, st>>>(ext, int(N), W, other, start, cut, conc, npairs, rr, cmax);
+static int full_tiles(const TileRangeJob& j) { return (j.blk + j.W - 1) / j.W * j.other; }   // of a block all live
+
+hipError_t launch_tile_ranges(const int32_t* ext, int64_t N, const TileRangeJob& j, hipStream_t st) {
+  tile_ranges_kernel<<<1, 256, 0, st>>>(ext, int(N), j.W, j.other, j.start, j.cut, j.conc, j.npairs, j.rr, full_tiles(j));
   return hipGetLastError();
+}
+
+// tile_ranges_kernel's results for up to kListMax blocks, a thread each
+__device__ __forceinline__ void tile_ranges_of(const int32_t* __restrict__ ext, int N, const TileRangeJob& j, int cmax,
+                                               int32_t* wfull, int32_t* wpart) {
+  const int b = threadIdx.x, lane = b & 63, wave = b >> 6;
+  const int c = b < N ? (ext[b] + j.W - 1) / j.W * j.other : 0;
+  const bool full = j.rr && c == cmax;
+  int xf = full ? c : 0, xp = full ? 0 : c;
+  for (int o = 1; o < 64; o <<= 1) {
+    const int yf = __shfl_up(xf, o, 64), yp = __shfl_up(xp, o, 64);
+    if (lane >= o) {
+      xf += yf;
+      xp += yp;
+    }
+  }
+  if (lane == 63) {
+    wfull[wave] = xf;
+    wpart[wave] = xp;
+  }
+  __syncthreads();
+  int bf = 0, bp = 0, tf = 0, tp = 0;
+  for (int w = 0; w < kListMax / 64; ++w) {
+    bf += w < wave ? wfull[w] : 0;
+    bp += w < wave ? wpart[w] : 0;
+    tf += wfull[w];
+    tp += wpart[w];
+  }
+  const int total = tf + tp;
+  const int t0 = full ? bf + xf - c : tf + bp + xp - c;   // partly filled blocks after the full ones
+  if (b < N) {
+    j.start[b] = t0;
+    int32_t* map = j.start + N + 1;
+    for (int t = t0; t < t0 + c; ++t) map[t] = b;
+  }
+  if (b == 0) {
+    j.start[N] = total;
+    if (j.cut) {   // the tail cut of each XCD
+      int base = 0;
+      for (int x = 0; x < 8; ++x) {
+        TailCut k = tail_cut_one(total, x, j.rr, j.conc, j.npairs);
+        k.base = base;
+        base += k.tail * (k.S - 1);
+        j.cut[x] = k;
+      }
+    }
+  }
+}
+
+// The expert lists (workgroup 0) and the tile ranges of up to two GEMMs (1, 2).
+__global__ void __launch_bounds__(kListMax) block_lists_kernel(const int32_t* __restrict__ b2e,
+                                                               const int32_t* __restrict__ flag, int N, int E,
+                                                               int32_t* __restrict__ off, int32_t* __restrict__ list,
+                                                               TileRangeJob j0, TileRangeJob j1, int cmax0, int cmax1) {
+  __shared__ __attribute__((aligned(16))) int32_t eb[kListMax];
+  __shared__ int32_t cnt[kListMax];
+  __shared__ int32_t wsum[kListMax / 64];
+  if (blockIdx.x == 0) expert_lists(b2e, flag, N, E, off, list, eb, cnt, wsum);
+  else if (blockIdx.x == 1) tile_ranges_of(flag, N, j0, cmax0, eb, cnt);
+  else tile_ranges_of(flag, N, j1, cmax1, eb, cnt);
 }
 
 hipError_t launch_slot_setup(const int32_t* tpid, const int32_t* b2e, const float* aff, int64_t T, int64_t E,
                              int64_t N, int64_t B, const int32_t* nvalid, int32_t* slot_tok, float* slot_aff,
                              int32_t* slot_of, float* daff_slot, int32_t* flag, int32_t* off, int32_t* list,
-                             hipStream_t st) {
+                             const TileRangeJob* jobs, int njobs, hipStream_t st) {
   hipError_t err = launch_fill_u32(reinterpret_cast<uint32_t*>(slot_of), T * E, 0xffffffffu, st);
   if (err != hipSuccess) return err;
   slot_block_kernel<<<unsigned(N), 256, 0, st>>>(tpid, b2e, aff, T, E, B, nvalid, slot_tok, slot_aff, slot_of, daff_slot,
                                                  flag);
-  if (N <= kListMax && E <= kListMax) {
-    expert_lists_kernel<<<1, kListMax, 0, st>>>(b2e, flag, int(N), int(E), off, list);
+  if (setup_makes_ranges(N, E)) {
+    TileRangeJob j[2] = {};
+    int cmax[2] = {};
+    for (int i = 0; i < njobs && i < 2; ++i) {
+      j[i] = jobs[i];
+      cmax[i] = full_tiles(j[i]);
+    }
+    block_lists_kernel<<<unsigned(1 + njobs), kListMax, 0, st>>>(b2e, flag, int(N), int(E), off, list, j[0], j[1], cmax[0],
+                                                                 cmax[1]);
     return hipGetLastError();
   }
   // the counts go to off[1..E] and become offsets in place: in each 256-expert

@@ -125,9 +125,10 @@ hipError_t phase1_launch(Phase1Args p, int fg, int fw, hipStream_t st) {
   const int64_t blocks = (int64_t(p.tiles_m) * p.tiles_n * p.N + 7) & ~int64_t(7);   // every tile, rounded to 8
   if (blocks > INT32_MAX) return hipErrorInvalidValue;
   const unsigned grid = unsigned(blocks);
-  hipError_t e = launch_tile_ranges(p.flag, p.N, BN, p.tiles_m, p.tile_start, st, nullptr, 0, 0, p.rr_tiles,
-                                    int(p.B));
-  if (e != hipSuccess) return e;
+  if (!p.ranges_done) {
+    hipError_t e = launch_tile_ranges(p.flag, p.N, phase1_ranges(p), st);
+    if (e != hipSuccess) return e;
+  }
   if (G) {   // the bf16 values carry no format
     phase1_go<BM, BN, G, kE4M3, kE4M3>(p, grid, st);
   } else if (fg == kE4M3) {

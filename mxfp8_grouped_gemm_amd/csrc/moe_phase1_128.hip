@@ -19,12 +19,23 @@ extern template hipError_t phase1_launch<256, 128, false>(Phase1Args, int, int, 
 // 256 x 256 tiles' longer loop amortises its start and end).
 // H not a multiple of 128 (a ragged last K stage, scale rows not in whole
 // pairs): the v2 loop on bf16 values, 128 x 128.
+struct Phase1Tile {
+  int m, n;
+};
+static Phase1Tile phase1_tile(const Phase1Args& p) {
+  if (p.H % 128 != 0 || p.H <= 2048 || p.I < 256) return {128, 128};
+  return {256, p.B >= 256 ? 256 : 128};
+}
 hipError_t launch_phase1(const Phase1Args& p, int fg, int fw, hipStream_t st) {
   if (p.H % 128 != 0) return phase1_launch<128, 128, true>(p, fg, fw, st);
-  if (p.H <= 2048) return phase1_launch<128, 128, false>(p, fg, fw, st);
-  if (p.I >= 256 && p.B >= 256) return phase1_launch<256, 256, false>(p, fg, fw, st);
-  if (p.I >= 256) return phase1_launch<256, 128, false>(p, fg, fw, st);
+  const Phase1Tile t = phase1_tile(p);
+  if (t.m == 256 && t.n == 256) return phase1_launch<256, 256, false>(p, fg, fw, st);
+  if (t.m == 256) return phase1_launch<256, 128, false>(p, fg, fw, st);
   return phase1_launch<128, 128, false>(p, fg, fw, st);
+}
+TileRangeJob phase1_ranges(const Phase1Args& p) {
+  const Phase1Tile t = phase1_tile(p);
+  return {t.n, int((p.I + t.m - 1) / t.m), int(p.B), p.tile_start, nullptr, 0, 0, p.rr_tiles};
 }
 
 // Where Phase 1 runs with its epilogue in the same kernel (phase1_fused_kernel):

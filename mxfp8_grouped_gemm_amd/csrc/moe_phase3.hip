@@ -277,16 +277,12 @@ static hipError_t phase3_launch(Phase3Args p, int fg, int fw, bool generic, hipS
   if (total + kP3MaxExtra > INT32_MAX) return hipErrorInvalidValue;
   p.grid_main = int(total);
   p.npairs = int(2 * p.I / 128);
-  // the cut needs the ring, the parts buffer, whole XCDs of CUs (at most
-  // kP3MaxExtra: the extra workgroups and part tiles) and at least two parts'
-  // worth of stage pairs
-  const bool cut = !generic && p.parts && phase3_parts_bytes(p) > 0 && p.conc >= 8 && p.conc % 8 == 0 &&
-                   p.conc <= kP3MaxExtra && p.npairs >= 2 * kCutMinPairs;
-  if (!cut) p.conc = 0;
-  hipError_t e = launch_tile_ranges(p.flag, p.N, BM, p.tiles_n, p.tile_start, st,
-                                    cut ? reinterpret_cast<TailCut*>(p.parts) : nullptr, p.conc, p.npairs,
-                                    p.rr_tiles, int(p.B));
-  if (e != hipSuccess) return e;
+  const TileRangeJob job = phase3_ranges(p);
+  p.conc = job.conc;
+  if (!p.ranges_done) {
+    hipError_t e = launch_tile_ranges(p.flag, p.N, job, st);
+    if (e != hipSuccess) return e;
+  }
   if (generic) {
     const unsigned grid = unsigned(total);
     if (fg == 0 && fw == 0) phase3_generic<BM, BN, 0, 0><<<grid, v2::kThreads, 0, st>>>(p);
@@ -311,6 +307,15 @@ static hipError_t phase3_launch(Phase3Args p, int fg, int fw, bool generic, hipS
 // measured 5% faster at 2I = 512 than 128 x 128 tiles at two per CU.
 static bool phase3_wide(const Phase3Args& p) {
   return (2 * p.I) % v2::BK == 0 && 2 * p.I >= 1024 && p.B >= 256 && p.H >= 256;
+}
+TileRangeJob phase3_ranges(const Phase3Args& p) {
+  const int bm = phase3_wide(p) ? 256 : 128, bn = 256, npairs = int(2 * p.I / 128);
+  // the cut needs the ring, the parts buffer, whole XCDs of CUs (at most
+  // kP3MaxExtra: the extra workgroups and part tiles) and at least two parts'
+  // worth of stage pairs
+  const bool cut = p.parts && phase3_parts_bytes(p) > 0 && p.conc >= 8 && p.conc % 8 == 0 && p.conc <= kP3MaxExtra;
+  return {bm, int((p.H + bn - 1) / bn), int(p.B), p.tile_start, cut ? reinterpret_cast<TailCut*>(p.parts) : nullptr,
+          cut ? p.conc : 0, npairs, p.rr_tiles};
 }
 hipError_t launch_phase3(const Phase3Args& p, int fg, int fw, hipStream_t st) {
   if (phase3_wide(p)) return phase3_launch<256, 256>(p, fg, fw, false, st);

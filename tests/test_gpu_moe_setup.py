@@ -72,3 +72,37 @@ def test_setup_regions(T, E, N, order):
     op.run()
     torch.cuda.synchronize()
     _check(cfg, op, tpid, b2e, N)
+
+
+def _ranges(ext, W, other, rr, B):
+    """Tile starts, total and tile -> block map over the blocks' live slot tiles (round robin: whole blocks first)."""
+    c = -(-ext // W) * other
+    full = np.logical_and(rr, c == -(-B // W) * other)
+    order = np.concatenate([np.nonzero(full)[0], np.nonzero(~full)[0]])
+    start = np.zeros(len(ext) + 1, dtype=np.int64)
+    start[order] = np.cumsum(c[order]) - c[order]
+    start[-1] = c.sum()
+    return np.concatenate([start, np.repeat(order, c[order])])
+
+
+@pytest.mark.parametrize("H,I,B,E,N", [(128, 576, 128, 4, None), (256, 544, 512, 5, 30), (192, 96, 256, 3, 1024),
+                                       (128, 576, 128, 3, 1025), (4096, 8192, 256, 2, None)])
+def test_tile_ranges(H, I, B, E, N):
+    """Phases 1 and 3 over short, partly filled and full blocks, in both tile orders
+    (the last case: experts of 32 MiB and more, round robin)."""
+    cfg = S.scaled(S.TINY, T=900, H=H, I=I, E=E, K=2, B=B)
+    print("ranges", H, I, B, E, N, flush=True)
+    gp = gpu_problem(cfg, N=N)
+    op = _bound(gp, gp["tpid"], gp["b2e"])
+    op.run()
+    torch.cuda.synchronize()
+    L, ws, N = op.layout, op.workspace.cpu().numpy(), gp["N"]
+    i32 = lambda name, n: ws[L[name]:L[name] + 4 * n].view(np.int32)
+    ext = i32("block_flag", N).astype(np.int64)
+    m1, n1 = (128, 128) if H % 128 or H <= 2048 or I < 256 else (256, min(B, 256))
+    if not (H % 128 == 0 and H <= 2048 and I <= 512):   # else Phase 1 takes every tile
+        want = _ranges(ext, n1, -(-I // m1), I * H >= 2 ** 25, B)
+        assert np.array_equal(i32("phase1_tiles", len(want)), want)
+    wide = 2 * I % 128 == 0 and 2 * I >= 1024 and B >= 256 and H >= 256
+    want = _ranges(ext, 256 if wide else 128, -(-H // 256), 2 * I * H >= 2 ** 25, B)
+    assert np.array_equal(i32("phase3_tiles", len(want)), want)
