@@ -46,7 +46,8 @@ PROFILES = os.path.join(ROOT, "profiles")
 KERNEL_SOURCES = os.path.join(ROOT, "mxfp8_grouped_gemm_amd", "csrc")
 
 
-NOT_MOE_SOURCES = ("router.hip",)   # kernels no MoE-backward stage is built from
+# kernels and headers no MoE-backward stage is built from
+NOT_MOE_SOURCES = ("router.hip", "router_fwd.hip", "router_rows.hpp", "segment.hpp", "balance.hip", "gated_act.hip")
 
 
 def sources_sha256():

@@ -19,8 +19,12 @@
 // adds a sequence's records in chunk order, and the last of its workgroups to
 // finish the sequences' terms in sequence order: no floating-point atomics, the
 // same bits on every run.
-// HBM-bound: E logits and K ids a token; backward E logits read, E gradients
-// written (rows in registers, router_rows.hpp).
+// HBM-bound by its bytes: E logits and K ids a token; backward E logits read, E
+// gradients written (rows in registers, router_rows.hpp).  T = 32768, E = 128, K = 8,
+// 16 sequences: chunks 8.3 us (17.8 MB), sums 6.8 us (latency: records, one
+// atomic, the last workgroup's terms), gradient 9.8 us (33.6 MB, 3.4 TB/s; an
+// elementwise pass over as many bytes takes 6.4 us).  T = 16384, E = 8: 5.6 and 5.5 us, all
+// of it latency.
 #include "kernels.hpp"
 #include "router_rows.hpp"
 

@@ -12,8 +12,10 @@
 // no expert left holds id -1 (what the routing blocks drop) and score 0.
 //
 // HBM-bound by its bytes: a row is E logits read and E affinities written, plus
-// K ids and scores.  What it has to be kept from is the arithmetic of the
-// selection: K rounds of a maximum over a row cost more than the traffic.  So, for
+// K ids and scores (T = 32768, E = 128, K = 8: 35.7 MB in 11.4 us on the GPU, 10.3 us a
+// call in a row of calls, 3.5 TB/s; an elementwise pass over as many bytes takes
+// 6.4 us).  What it has to be kept from is the arithmetic of the selection: K
+// rounds of a maximum over a row cost more than the traffic (16.6 us).  So, for
 // up to 8 selections of up to 512 experts, each lane sorts its 8 columns
 // (router_rows.hpp) and log2 L exchanges merge the lanes' lists, keeping 8:
 // the elementwise maxima of one list and the other reversed are the 8 largest
@@ -22,7 +24,9 @@
 // An fp32 logit loses log2(8 L) low bits to the column; rows where that could
 // have changed the selection or its order (two candidates equal in the bits
 // left, which is seen after the merge) send their wave to the exact rounds, as
-// do more selections or experts.
+// do more selections or experts.  What bounds it now: about 350 vector instructions
+// a wave of four rows (half of the time), then the load, the four LDS exchanges and
+// the store of a single round of waves, which do not overlap.
 #include "kernels.hpp"
 #include "router_rows.hpp"
 

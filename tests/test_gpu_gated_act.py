@@ -198,3 +198,26 @@ def test_empty_stream_graph_and_guard_bytes():
         _check_fwd(x, 0, 0, out)
         _check_bwd(d, out[1], out[2], 0, 0, dx)
     assert guard[n:].eq(0xAB).all() and sguard[n // 32:].eq(0xAB).all() and iguard[n // 2:].eq(7).all()
+
+
+def test_geglu_over_the_whole_range():
+    """Every bf16 gate in (-16, 16) and some far outside, with ups and upstreams of 1:
+    g Phi(g) and its slope, relatively also in the left tail, where both fall
+    below 1e-38 at g = -13."""
+    from scipy.special import ndtr
+    bits = np.arange(1 << 16, dtype=np.uint32).astype(np.uint16)
+    bits = bits[(bits & 0x7FFF) < 0x4180]
+    bits = np.concatenate([bits, np.array([0x7F00, 0xFF00, 0x4300, 0xC300, 0x4200, 0xC200], dtype=np.uint16)])
+    g = np.resize(bits, (-(-bits.size // 32) * 32,)).reshape(-1, 1, 32)
+    x = S.from_bits(np.concatenate([g, np.full_like(g, 0x3F80)], 1), "cuda")
+    inter, codes, scales = mx.mxfp8_gated_act_fwd(x, mx.ACT_GEGLU)
+    v = _f64(x)[:, 0]
+    with np.errstate(over="ignore"):
+        ref = v * ndtr(v)
+    assert np.all(np.abs(_f64(inter) - ref) <= REL * np.abs(ref) + 2.0 ** -120)
+    # the backward on gates that the codes hold exactly: 4 significant bits, one scale a group
+    c = np.resize(np.arange(256, dtype=np.uint8)[(np.arange(256) & 0x7F) != 0x7F], 256).reshape(1, 256)
+    cc = torch.from_numpy(np.stack([c, np.full_like(c, 0x38)], 1)).cuda()      # ups: 1
+    ss = torch.from_numpy(np.stack([np.full((1, 8), 122, np.uint8), np.full((1, 8), 127, np.uint8)], 1)).cuda()
+    d = torch.ones(1, 256, dtype=torch.bfloat16, device="cuda")
+    _check_bwd(d, cc, ss, 1, 0, mx.mxfp8_gated_act_bwd(d, cc, ss, mx.ACT_GEGLU))
