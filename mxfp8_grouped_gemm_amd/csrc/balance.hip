@@ -11,20 +11,21 @@
 // A token takes part if it lies in a sequence, its mask byte is not 0 and one of
 // its logits is above -inf.
 //
-// Forward, two launches.  The first cuts the tokens into chunks, one workgroup
-// each; a workgroup goes through its rows a round at a time and through the
-// sequences that meet each round, and writes, for each sequence, the sums of p per expert, the counts, the tokens and the sum of
-// lse^2 to record chunk + sequence (moving along the tokens raises one of the
-// two each time, so the records of different pairs never meet).  The second
-// adds a sequence's records in chunk order, and the last of its workgroups to
-// finish the sequences' terms in sequence order: no floating-point atomics, the
-// same bits on every run.
+// Forward, two launches (one for few tokens, see balance_one).  The first cuts
+// the tokens into chunks, one workgroup each; a workgroup goes through its rows
+// a round at a time and through the sequences that meet each round, and writes,
+// for each sequence, the sums of p per expert, the counts, the tokens and the
+// sum of lse^2 to record chunk + sequence (moving along the tokens raises one
+// of the two each time, so the records of different pairs never meet).  The
+// second adds a sequence's records in an order fixed by the sizes, and the last
+// of its workgroups to finish the sequences' terms likewise: no floating-point
+// atomics, the same bits on every run.
 // HBM-bound by its bytes: E logits and K ids a token; backward E logits read, E
-// gradients written (rows in registers, router_rows.hpp).  T = 32768, E = 128, K = 8,
-// 16 sequences: chunks 8.3 us (17.8 MB), sums 6.8 us (latency: records, one
-// atomic, the last workgroup's terms), gradient 9.8 us (33.6 MB, 3.4 TB/s; an
-// elementwise pass over as many bytes takes 6.4 us).  T = 16384, E = 8: 5.6 and 5.5 us, all
-// of it latency.
+// gradients written (rows in registers, router_rows.hpp).  T = 32768, E = 128,
+// K = 8, 16 sequences: chunks 8.7 us (17.8 MB), sums 6.8 us (latency: records,
+// one atomic, the last workgroup's terms), gradient 9.8 us (33.6 MB, 3.4 TB/s;
+// an elementwise pass over as many bytes takes 6.4 us).  T = 16384, E = 8: 5.7
+// and 5.8 us, all of it latency.
 #include "kernels.hpp"
 #include "router_rows.hpp"
 

@@ -1,5 +1,5 @@
 // segment.hpp -- reductions over segments of L consecutive lanes (L a power of
-// two, 8 to 64) that stay in the register file: quad_perm, row_half_mirror and
+// two up to 64) that stay in the register file: quad_perm, row_half_mirror and
 // row_mirror DPP moves within 16 lanes, v_permlane16_swap / v_permlane32_swap
 // beyond.  After each step every lane of the reduced group holds the same
 // value, so a mirror serves as the exchange with the other half.  Each step
