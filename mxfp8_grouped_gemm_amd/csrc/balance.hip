@@ -25,7 +25,7 @@
 // K = 8, 16 sequences: chunks 8.7 us (17.8 MB), sums 6.8 us (latency: records,
 // one atomic, the last workgroup's terms), gradient 9.8 us (33.6 MB, 3.4 TB/s;
 // an elementwise pass over as many bytes takes 6.4 us).  T = 16384, E = 8: 5.7
-// and 5.8 us, all of it latency.
+// and 3.1 us (one workgroup, which needs no one else's terms), all of it latency.
 #include "kernels.hpp"
 #include "router_rows.hpp"
 
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(chunk_threads(EPL)) balance_chunk_kernel(Balan
   bool nlive = false;
   auto fetch = [&](int64_t t) {
     if (t >= c1) return;
-    rows::load<EPL, VEC>(logits + t * p.E, E, lane, nx);
+    rows::load<L, EPL, VEC>(logits + t * p.E, E, lane, nx);
 #pragma unroll
     for (int k = 0; k < IDS; ++k) nid[k] = lane + L * k < K ? p.idx[t * K + lane + L * k] : -1;
     nlive = !p.mask || p.mask[t] != 0;
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(chunk_threads(EPL)) balance_chunk_kernel(Balan
     for (int j = 0; j < EPL; ++j) {
       const float v = seg::across<L>(acc[j]);
       acc[j] = 0.f;
-      if ((threadIdx.x & 63) < L) lp[wave][lane * EPL + j] = v;
+      if ((threadIdx.x & 63) < L) lp[wave][rows::column<L>(lane, j)] = v;
     }
     z2 = seg::sum<64>(z2);
     n = seg::sum<64>(n);
@@ -286,6 +286,7 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(BalanceArgs p)
   __shared__ float sp[W][kTile], sz[W];
   __shared__ int sc[W][kTile], sn[W];
   __shared__ bool last;
+  const bool only = gridDim.x * gridDim.y == 1;
   const int64_t s = blockIdx.x;
   const int tid = threadIdx.x, q = tid / kTile, col = tid % kTile, wave = tid >> 6;
   const int64_t e = int64_t(blockIdx.y) * kTile + col;
@@ -333,20 +334,21 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(BalanceArgs p)
     // the tile's share of sum_e c_se sum_t p_te / n_s^2
     double d = n > 0 ? double(c) * double(v) / (double(n) * double(n)) : 0.;
     for (int o = 1; o < kTile; o <<= 1) d += __shfl_xor(d, o, 64);
-    if (tid == 0) {
+    if (tid == 0 && only) {   // all there is
+      p.num[s] = n;
+      write_totals(p, d, z, n, n > 0);
+    } else if (tid == 0) {
       publish(&p.term[s * gridDim.y + blockIdx.y], d);
       if (blockIdx.y == 0) {
         publish(&p.num[s], n);
         publish(&p.term_z[s], z);
       }
-      last = gridDim.x * gridDim.y == 1;
-      if (!last) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the published values have reached memory
-        last = __hip_atomic_fetch_add(p.done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x * gridDim.y - 1;
-      }
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the published values have reached memory
+      last = __hip_atomic_fetch_add(p.done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x * gridDim.y - 1;
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
   }
+  if (only) return;
   __syncthreads();
   if (!last) return;
   // all sequences' terms, in an order that does not depend on who is last
@@ -397,7 +399,7 @@ __global__ void __launch_bounds__(kBwdThreads) balance_bwd_kernel(BalanceArgs p)
   float x[EPL], lse = 0.f;
   bool part = in && (!p.mask || p.mask[t0 + slot] != 0);
   if (in) {
-    rows::load<EPL, VEC>(logits + off, E, lane, x);
+    rows::load<L, EPL, VEC>(logits + off, E, lane, x);
   } else {
 #pragma unroll
     for (int j = 0; j < EPL; ++j) x[j] = -INFINITY;
@@ -413,24 +415,25 @@ __global__ void __launch_bounds__(kBwdThreads) balance_bwd_kernel(BalanceArgs p)
     if (!p.accumulate) {
 #pragma unroll
       for (int j = 0; j < EPL; ++j) x[j] = 0.f;
-      rows::store<EPL, VEC>(out + off, E, lane, x);
+      rows::store<L, EPL, VEC>(out + off, E, lane, x);
     }
     return;
   }
   const float rn = rows::rcp_fast(n);
   const float fb = gb * (p.balance_coef * float(p.E) * rows::rcp_fast(live * float(p.K))) * rn * rn;
   const float fz = gz * (2.f * p.z_coef * rows::rcp_fast(all)) * lse;
-  const int32_t* counts = p.counts + s * p.E + lane * EPL;
+  const int32_t* counts = p.counts + s * p.E;
   float w[EPL], dot = 0.f;
-  if constexpr (VEC) {
 #pragma unroll
-    for (int q = 0; q < EPL; q += 4) {
-      const int4 c = lane * EPL + q < E ? *reinterpret_cast<const int4*>(counts + q) : int4{0, 0, 0, 0};
-      w[q] = float(c.x); w[q + 1] = float(c.y); w[q + 2] = float(c.z); w[q + 3] = float(c.w);
+  for (int j = 0; j < EPL; j += 4) {
+    const int c = rows::column<L>(lane, j);
+    if constexpr (VEC) {
+      const int4 k = c < E ? *reinterpret_cast<const int4*>(counts + c) : int4{0, 0, 0, 0};
+      w[j] = float(k.x); w[j + 1] = float(k.y); w[j + 2] = float(k.z); w[j + 3] = float(k.w);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[j + k] = c + k < E ? float(counts[c + k]) : 0.f;
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) w[j] = lane * EPL + j < E ? float(counts[j]) : 0.f;
   }
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
@@ -441,11 +444,11 @@ __global__ void __launch_bounds__(kBwdThreads) balance_bwd_kernel(BalanceArgs p)
 #pragma unroll
   for (int j = 0; j < EPL; ++j) x[j] *= w[j] - dot;
   if (p.accumulate) {
-    rows::load<EPL, VEC>(static_cast<const float*>(out + off), E, lane, w);
+    rows::load<L, EPL, VEC>(static_cast<const float*>(out + off), E, lane, w);
 #pragma unroll
     for (int j = 0; j < EPL; ++j) x[j] += w[j];
   }
-  rows::store<EPL, VEC>(out + off, E, lane, x);
+  rows::store<L, EPL, VEC>(out + off, E, lane, x);
 }
 
 // Tokens of one chunk: a round of the workgroup's rows, or as many as keep to

@@ -131,7 +131,7 @@ __device__ __forceinline__ void select_rounds(const RouterFwdArgs& p, int64_t t,
       if (key[j] > best) { best = key[j]; at = j; }
     const uint32_t most = seg::umax<L>(best);
     if (most == 0) break;   // nothing open is left (the same in the whole segment)
-    const uint32_t mine = best == most ? uint32_t(lane * EPL + at) : 0xffffffffu;
+    const uint32_t mine = best == most ? uint32_t(rows::column<L>(lane, at)) : 0xffffffffu;
     const bool won = seg::umin<L>(mine) == mine && best == most;
 #pragma unroll
     for (int j = 0; j < EPL; ++j)
@@ -153,11 +153,11 @@ __device__ __forceinline__ void select_rounds(const RouterFwdArgs& p, int64_t t,
   for (int j = 0; j < EPL; ++j) {
     z[j] = rank[j] < 0 ? 0.f : SCORE == kRaw ? z[j] + 0.f : z[j] * inv;
     if (rank[j] >= 0) {
-      p.idx[t * K + rank[j]] = lane * EPL + j;
+      p.idx[t * K + rank[j]] = rows::column<L>(lane, j);
       p.scores[t * K + rank[j]] = z[j];
     }
   }
-  if (p.aff) rows::store<EPL, VEC>(p.aff + t * p.E, E, lane, z);
+  if (p.aff) rows::store<L, EPL, VEC>(p.aff + t * p.E, E, lane, z);
   for (int k = found + lane; k < K; k += L) {
     p.idx[t * K + k] = -1;
     p.scores[t * K + k] = 0.f;
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kThreads) router_fwd_kernel(RouterFwdArgs p) {
   const int64_t t = int64_t(blockIdx.x) * (kThreads / L) + threadIdx.x / L;
   if (t >= p.T) return;   // whole segments leave together
   float z[EPL];
-  rows::load<EPL, VEC>(static_cast<const LT*>(p.logits) + t * p.E, int(p.E), lane, z);
+  rows::load<L, EPL, VEC>(static_cast<const LT*>(p.logits) + t * p.E, int(p.E), lane, z);
   if (p.mask && !p.mask[t]) {
 #pragma unroll
     for (int j = 0; j < EPL; ++j) z[j] = -INFINITY;
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kThreads) router_merge_kernel(RouterFwdArgs p)
   const int E = int(p.E), K = int(p.K);
   float z[8];
   const int row = in ? slot : 0;
-  rows::load<8, VEC>(static_cast<const LT*>(p.logits) + t0 * p.E + row * E, E, lane, z);
+  rows::load<L, 8, VEC>(static_cast<const LT*>(p.logits) + t0 * p.E + row * E, E, lane, z);
   if (!in || (p.mask && !p.mask[t0 + slot])) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) z[j] = -INFINITY;
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kThreads) router_merge_kernel(RouterFwdArgs p)
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const uint32_t b = __float_as_uint(fmaxf(z[j] + 0.f, -INFINITY));   // -0 + 0 = +0, NaN: -inf
-    own[j] = v[j] = ((b ^ (uint32_t(int32_t(b) >> 31) | 0x80000000u)) & ~COLS) | (COLS - lane * 8 - j);
+    own[j] = v[j] = ((b ^ (uint32_t(int32_t(b) >> 31) | 0x80000000u)) & ~COLS) | (COLS - rows::column<L>(lane, j));
   }
   sort8(v);
   merge_lanes<L>(v);
@@ -241,8 +241,10 @@ __global__ void __launch_bounds__(kThreads) router_merge_kernel(RouterFwdArgs p)
   // The selections go to one lane each (several where L < 8), which reads
   // their logits from the row in LDS.  All within the wave.
   float* zr = zs + (wave * R + slot) * 8 * L;
-  *reinterpret_cast<float4*>(zr + lane * 8) = float4{z[0], z[1], z[2], z[3]};
-  *reinterpret_cast<float4*>(zr + lane * 8 + 4) = float4{z[4], z[5], z[6], z[7]};
+  float4* lo = reinterpret_cast<float4*>(zr) + lane;   // the lane's two runs
+  float4* hi = lo + L;
+  *lo = float4{z[0], z[1], z[2], z[3]};
+  *hi = float4{z[4], z[5], z[6], z[7]};
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
   int col[KL];
@@ -290,8 +292,7 @@ __global__ void __launch_bounds__(kThreads) router_merge_kernel(RouterFwdArgs p)
   // the row again: zeros, the scores, and back
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
-  *reinterpret_cast<float4*>(zr + lane * 8) = float4{0.f, 0.f, 0.f, 0.f};
-  *reinterpret_cast<float4*>(zr + lane * 8 + 4) = float4{0.f, 0.f, 0.f, 0.f};
+  *lo = *hi = float4{0.f, 0.f, 0.f, 0.f};
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
 #pragma unroll
@@ -299,10 +300,9 @@ __global__ void __launch_bounds__(kThreads) router_merge_kernel(RouterFwdArgs p)
     if (lane + i * L < K && col[i] >= 0) zr[col[i]] = y[i];
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
-  const float4 a = *reinterpret_cast<const float4*>(zr + lane * 8);
-  const float4 b = *reinterpret_cast<const float4*>(zr + lane * 8 + 4);
+  const float4 a = *lo, b = *hi;
   const float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  if (in) rows::store<8, VEC>(p.aff + t0 * p.E + slot * E, E, lane, w);
+  if (in) rows::store<L, 8, VEC>(p.aff + t0 * p.E + slot * E, E, lane, w);
 }
 
 int64_t router_max_tokens(int64_t E) { return rows::max_tokens(E); }

@@ -1,9 +1,10 @@
 // router_rows.hpp -- rows of router logits in registers, shared by the router
-// forward and the auxiliary losses.  L lanes take one row, EPL consecutive
-// columns each: 8 (L = E / 8 rounded up to a power of two, from one lane for 8
-// experts to a whole wave for 512), more past 512 experts.  Eight columns are
-// one 16-byte access of bf16 or two of fp32 where E % 8 == 0 (VEC: every row
-// and every lane's run is then aligned, and a lane holds 8 columns or none).
+// forward and the auxiliary losses.  L lanes take one row, EPL columns each: 8
+// (L = E / 8 rounded up to a power of two, from one lane for 8 experts to a
+// whole wave for 512), more past 512 experts.  A lane holds runs of four columns,
+// run q of lane l at column 4 (l + L q): the lanes of a row read and write
+// consecutive runs (16 bytes of fp32, 8 of bf16) where E % 4 == 0 (VEC: every run is
+// then aligned, and inside the row or past it).
 #pragma once
 #include <type_traits>
 
@@ -25,54 +26,54 @@ __device__ __forceinline__ float rcp_fast(float s) { return __builtin_amdgcn_rcp
 __device__ __forceinline__ float value(float v) { return v; }
 __device__ __forceinline__ float value(uint16_t v) { return bf16_to_f32(v); }
 
-// x[j] = logit of column lane * EPL + j, -inf past E
-template <int EPL, bool VEC, class LT>
+// the column that lane holds in x[j]
+template <int L>
+__device__ __forceinline__ int column(int lane, int j) {
+  return 4 * (lane + L * (j >> 2)) + (j & 3);
+}
+
+// x[j] = logit of column<L>(lane, j), -inf past E
+template <int L, int EPL, bool VEC, class LT>
 __device__ __forceinline__ void load(const LT* row, int E, int lane, float (&x)[EPL]) {
-  const int c0 = lane * EPL;
-  if constexpr (VEC) {
 #pragma unroll
-    for (int q = 0; q < EPL; q += 8) {
-      if (c0 + q < E) {
+  for (int j = 0; j < EPL; j += 4) {
+    const int c = column<L>(lane, j);
+    if constexpr (VEC) {
+      if (c < E) {
         if constexpr (std::is_same_v<LT, float>) {
-          const float4 a = *reinterpret_cast<const float4*>(row + c0 + q);
-          const float4 b = *reinterpret_cast<const float4*>(row + c0 + q + 4);
-          x[q] = a.x; x[q + 1] = a.y; x[q + 2] = a.z; x[q + 3] = a.w;
-          x[q + 4] = b.x; x[q + 5] = b.y; x[q + 6] = b.z; x[q + 7] = b.w;
+          const float4 a = *reinterpret_cast<const float4*>(row + c);
+          x[j] = a.x; x[j + 1] = a.y; x[j + 2] = a.z; x[j + 3] = a.w;
         } else {
-          const uint4 a = *reinterpret_cast<const uint4*>(row + c0 + q);
-          const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            x[q + 2 * k] = __uint_as_float(w[k] << 16);
-            x[q + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-          }
+          const uint2 a = *reinterpret_cast<const uint2*>(row + c);
+          x[j] = __uint_as_float(a.x << 16); x[j + 1] = __uint_as_float(a.x & 0xffff0000u);
+          x[j + 2] = __uint_as_float(a.y << 16); x[j + 3] = __uint_as_float(a.y & 0xffff0000u);
         }
       } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[q + j] = -INFINITY;
+        x[j] = x[j + 1] = x[j + 2] = x[j + 3] = -INFINITY;
       }
-    }
-  } else {
+    } else {
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) {   // past E: the last column again, so that no load hangs on a branch
-      const float v = value(row[c0 + j < E ? c0 + j : E - 1]);
-      x[j] = c0 + j < E ? v : -INFINITY;
+      for (int k = 0; k < 4; ++k) {   // past E: the last column again, so that no load hangs on a branch
+        const float v = value(row[c + k < E ? c + k : E - 1]);
+        x[j + k] = c + k < E ? v : -INFINITY;
+      }
     }
   }
 }
 
-// columns lane * EPL + j of an fp32 row
-template <int EPL, bool VEC>
+// the same columns of an fp32 row
+template <int L, int EPL, bool VEC>
 __device__ __forceinline__ void store(float* row, int E, int lane, const float (&x)[EPL]) {
-  const int c0 = lane * EPL;
-  if constexpr (VEC) {
 #pragma unroll
-    for (int q = 0; q < EPL; q += 4)
-      if (c0 + q < E) *reinterpret_cast<float4*>(row + c0 + q) = float4{x[q], x[q + 1], x[q + 2], x[q + 3]};
-  } else {
+  for (int j = 0; j < EPL; j += 4) {
+    const int c = column<L>(lane, j);
+    if constexpr (VEC) {
+      if (c < E) *reinterpret_cast<float4*>(row + c) = float4{x[j], x[j + 1], x[j + 2], x[j + 3]};
+    } else {
 #pragma unroll
-    for (int j = 0; j < EPL; ++j)
-      if (c0 + j < E) row[c0 + j] = x[j];
+      for (int k = 0; k < 4; ++k)
+        if (c + k < E) row[c + k] = x[j + k];
+    }
   }
 }
 
@@ -105,7 +106,7 @@ template <int N> using Int = std::integral_constant<int, N>;
 template <class F>
 void by_experts(int64_t E, const F& f) {
   auto go = [&](auto L, auto EPL) {
-    if (E % 8 == 0) f(L, EPL, std::true_type{});
+    if (E % 4 == 0) f(L, EPL, std::true_type{});
     else f(L, EPL, std::false_type{});
   };
   if (E <= 8) go(Int<1>{}, Int<8>{});
