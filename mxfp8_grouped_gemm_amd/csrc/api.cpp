@@ -589,7 +589,8 @@ static int moe_run(const moe_bwd_mxfp8_args* a, void* ws, size_t ws_bytes, void*
   // the second stream, for a whole backward (stages in order keep to the caller's)
   SideStream* side = nullptr;
   std::unique_lock<std::mutex> side_lock;
-  if (lo == 0 && hi == MOE_BWD_NUM_STAGES - 1) {
+  const bool whole = lo == 0 && hi == MOE_BWD_NUM_STAGES - 1;
+  if (whole) {
     int device = -1, cus = 0;
     if ((st ? hipStreamGetDevice(st, &device) : hipGetDevice(&device)) == hipSuccess &&
         hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, device) == hipSuccess && cus > 0) {
@@ -659,6 +660,27 @@ static int moe_run(const moe_bwd_mxfp8_args* a, void* ws, size_t ws_bytes, void*
     ranges[nranges++] = mx::phase3_ranges(p3);
     if (!fused) ranges[nranges++] = mx::phase1_ranges(p1);
   }
+  // Phase 2: dW_gate_up[e] = X_tok . dGU_tok^T over the expert's blocks
+  mx::GemmStoreArgs g2{};
+  g2.a_codes = at(L.x_tok_codes); g2.a_scales = at(L.x_tok_scales); g2.lda = P;
+  g2.b_codes = at(L.dgu_tok_codes); g2.b_scales = at(L.dgu_tok_scales); g2.ldb = P;
+  g2.M = H; g2.N = 2 * I; g2.K = 0; g2.out = a->gate_up_proj_weight_grad; g2.ldo = 2 * I; g2.out_gstride = H * 2 * I;
+  g2.blk_off = boff; g2.blk_list = blist; g2.blk = int(B);
+  g2.blk_ext = flag;   // the expert's last block ends at its last routed slot (rounded up to 128)
+  // the token-axis operands are stage-major (whole cache lines per DMA
+  // instruction), which only the four-slot ring reads; measured on the large
+  // workload against row-major operands, Phase 2 on the pair-slot ring and
+  // Phase 4 on the four-slot ring: 9% and 10% faster
+  g2.pair = 0;
+  g2.stage_major = 1;
+  g2.accumulate = a->accumulate;
+  // Phase 4: dW_down[e] = inter_tok . gy_tok^T
+  mx::GemmStoreArgs g4 = g2;
+  g4.a_codes = at(L.inter_tok_codes); g4.a_scales = at(L.inter_tok_scales); g4.lda = P;
+  g4.b_codes = at(L.gy_tok_codes); g4.b_scales = at(L.gy_tok_scales); g4.ldb = P;
+  g4.M = I; g4.N = H; g4.out = a->down_proj_weight_grad; g4.ldo = H; g4.out_gstride = I * H;
+  // the three products in one launch, for a whole backward of a small layer
+  const bool joint = whole && !side && mx::moe_grads_fit(p3, g2, g4, int(E), device_cus(st));
   int stage = -1;
 #define STEP(call, what) \
   if (stage >= lo && stage <= hi && (e = (call)) != hipSuccess) return hip_status(e, what);
@@ -738,30 +760,16 @@ static int moe_run(const moe_bwd_mxfp8_args* a, void* ws, size_t ws_bytes, void*
   if (!fused) STEP(mx::launch_phase1_epi(p1, a->fmt_grad, st), "phase 1 epilogue");
   stage = 6;
   STEP(order(side ? &side->ev[1] : nullptr, st, s2), "second stream after the epilogue");
-  // Phase 3: dX scatter-add
-  STEP(mx::launch_phase3(p3, a->fmt_grad, a->fmt_weight, st), "phase 3");
-  stage = 7;
-  // Phase 2: dW_gate_up[e] = X_tok . dGU_tok^T over the expert's blocks
-  mx::GemmStoreArgs g{};
-  g.a_codes = at(L.x_tok_codes); g.a_scales = at(L.x_tok_scales); g.lda = P;
-  g.b_codes = at(L.dgu_tok_codes); g.b_scales = at(L.dgu_tok_scales); g.ldb = P;
-  g.M = H; g.N = 2 * I; g.K = 0; g.out = a->gate_up_proj_weight_grad; g.ldo = 2 * I; g.out_gstride = H * 2 * I;
-  g.blk_off = boff; g.blk_list = blist; g.blk = int(B);
-  g.blk_ext = flag;   // the expert's last block ends at its last routed slot (rounded up to 128)
-  // the token-axis operands are stage-major (whole cache lines per DMA
-  // instruction), which only the four-slot ring reads; measured on the large
-  // workload against row-major operands, Phase 2 on the pair-slot ring and
-  // Phase 4 on the four-slot ring: 9% and 10% faster
-  g.pair = 0;
-  g.stage_major = 1;
-  g.accumulate = a->accumulate;
-  STEP(mx::launch_gemm_store(g, int(E), a->fmt_act, a->fmt_grad, s2), "phase 2");
-  stage = 8;
-  // Phase 4: dW_down[e] = inter_tok . gy_tok^T
-  g.a_codes = at(L.inter_tok_codes); g.a_scales = at(L.inter_tok_scales); g.lda = P;
-  g.b_codes = at(L.gy_tok_codes); g.b_scales = at(L.gy_tok_scales); g.ldb = P;
-  g.M = I; g.N = H; g.out = a->down_proj_weight_grad; g.ldo = H; g.out_gstride = I * H;
-  STEP(mx::launch_gemm_store(g, int(E), a->fmt_act, a->fmt_grad, s2), "phase 4");
+  if (joint) {
+    STEP(mx::launch_moe_grads(p3, g2, g4, int(E), a->fmt_grad, a->fmt_weight, a->fmt_act, st), "phases 3, 2 and 4");
+  } else {
+    // Phase 3: dX scatter-add
+    STEP(mx::launch_phase3(p3, a->fmt_grad, a->fmt_weight, st), "phase 3");
+    stage = 7;
+    STEP(mx::launch_gemm_store(g2, int(E), a->fmt_act, a->fmt_grad, s2), "phase 2");
+    stage = 8;
+    STEP(mx::launch_gemm_store(g4, int(E), a->fmt_act, a->fmt_grad, s2), "phase 4");
+  }
   stage = 9;
   // finalisation (after the second stream's gathers and bias terms)
   if (side && stage >= lo && stage <= hi && (e = hipStreamWaitEvent(st, side->ev[2], 0)) != hipSuccess)

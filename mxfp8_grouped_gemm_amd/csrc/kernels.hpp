@@ -95,6 +95,9 @@ struct GemmStoreArgs {
   int groups;                     // set by the launcher
 };
 hipError_t launch_gemm_store(GemmStoreArgs p, int groups, int fa, int fb, hipStream_t st);
+// whether p runs 128 x 128 ring tiles over block lists, completed for them if so
+// (operands swapped): grid workgroups
+bool gemm_store_small(GemmStoreArgs& p, int groups, unsigned& grid);
 
 // router.hip -- the router backward (modes as mxfp8_router_mode in the public header)
 constexpr int kRouterSoftmaxOverTopk = 0;
@@ -298,6 +301,14 @@ struct Phase3Args {
 };
 TileRangeJob phase3_ranges(const Phase3Args& p);   // launch_phase3's
 hipError_t launch_phase3(const Phase3Args& p, int fg, int fw, hipStream_t st);
+// whether p runs uncut 128 x 256 ring tiles on ranges that the set-up made, completed for them if so
+bool phase3_small(Phase3Args& p, unsigned& grid);
+// moe_grads.hip -- Phases 3, 2 and 4 (g2, g4 as for launch_gemm_store, formats
+// fmt_act x fmt_grad) in one launch, where each fits as above and all their
+// workgroups run at once on cus CUs
+bool moe_grads_fit(Phase3Args p3, GemmStoreArgs g2, GemmStoreArgs g4, int groups, int cus);
+hipError_t launch_moe_grads(Phase3Args p3, GemmStoreArgs g2, GemmStoreArgs g4, int groups, int fg, int fw, int fa,
+                            hipStream_t st);
 // Phase 3 tiles when every slot tile of every block is live (an upper bound)
 int64_t phase3_max_tiles(const Phase3Args& p);
 // bytes of the parts buffer (H, I, N, B set)
