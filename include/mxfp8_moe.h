@@ -346,6 +346,7 @@ typedef enum { MXFP8_ACT_SWIGLU = 0, MXFP8_ACT_GEGLU = 1 } mxfp8_activation;
  *                                                     empty, like phase1_tiles, where Phase 1
  *                                                     runs with its epilogue in one kernel:
  *                                                     H % 128 == 0, H <= 2048, I <= 512,
+ *                                                     ceil(I/128) * ceil(B/128) * N >= 256,
  *                                                     no [N,I,B] checkpoints and no E5M2
  *                                                     gate/up checkpoint)
  *   phase1_tiles/phase3_tiles [N+1 + tiles] int32     first tile of each block over its

@@ -410,7 +410,7 @@ static bool moe_fuse_bias(const moe_bwd_mxfp8_args* a) {
 // Phase 1 with its epilogue in one kernel (the conditions of mx::phase1_fusable,
 // which its launcher checks again): no dS in HBM, and no tile ranges.
 static bool moe_phase1_fused(const moe_bwd_mxfp8_args* a) {
-  return a->H % 128 == 0 && a->H <= 2048 && a->I <= 512 && !a->gate_act_checkpoint_T &&
+  return mx::phase1_fuses_sizes(a->H, a->I, a->N, a->block_size) && !a->gate_act_checkpoint_T &&
          !a->intermediate_checkpoint_T && !a->scaled_intermediate_checkpoint_T &&
          (!a->gate_up_checkpoint_codes || a->fmt_checkpoint == MXFP8_E4M3);
 }

@@ -40,15 +40,18 @@ TileRangeJob phase1_ranges(const Phase1Args& p) {
 
 // Where Phase 1 runs with its epilogue in the same kernel (phase1_fused_kernel):
 // H % 128 == 0 (the ring loop), no caller checkpoints, H <= 2048 (128 x 128
-// tiles, two workgroups per CU) and I <= 512.  Measured against the two
+// tiles, two workgroups per CU), I <= 512 and at least 256 tiles.  Measured against the two
 // kernels (Phase 1 + epilogue): 6% faster with I = 256 (H = 1536, B = 128),
 // even with I = 1408 (H = 2048), and 7% / 17% slower on H = 4096, I = 14336 at
 // 128 x 128 / 256 x 256 tiles: the epilogue's loads and stores do not overlap
 // the other workgroup's MFMAs, and the product itself needs both workgroups
 // to hide its latency, so the element-wise work adds to the product's time.
+// Fewer tiles than the 256 CUs take the two kernels: the epilogue's chunks are
+// smaller than a tile and keep more CUs busy (whole backward, 14 tiles: 45.4 us
+// against 48.6; 126 tiles: 117.5 against 121; 188 tiles: even).
 // An E5M2 checkpoint takes the two kernels (the fused one is built for bf16 and E4M3 checkpoints).
 bool phase1_fusable(const Phase1Args& p) {
-  return p.H % 128 == 0 && p.H <= 2048 && p.I <= 512 && !p.ga_ckpt && !p.in_ckpt && !p.sc_ckpt &&
+  return phase1_fuses_sizes(p.H, p.I, p.N, p.B) && !p.ga_ckpt && !p.in_ckpt && !p.sc_ckpt &&
          (!p.ck8_codes || p.ck8_fmt == kE4M3);
 }
 

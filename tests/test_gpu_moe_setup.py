@@ -106,3 +106,47 @@ def test_tile_ranges(H, I, B, E, N):
     wide = 2 * I % 128 == 0 and 2 * I >= 1024 and B >= 256 and H >= 256
     want = _ranges(ext, 256 if wide else 128, -(-H // 256), 2 * I * H >= 2 ** 25, B)
     assert np.array_equal(i32("phase3_tiles", len(want)), want)
+
+
+@pytest.mark.parametrize("act8", [False, True])
+@pytest.mark.parametrize("name", ["tiny", "fine_bias", "large_i", "geglu"])
+def test_blocks_of_padding_change_nothing(name, act8):
+    """A small layer takes Phase 1 and its epilogue apart, and Phases 3, 2 and 4 in one
+    launch; with 300 blocks, all but the first few padding, it takes Phase 1 with its
+    epilogue inside and the other phases apart.  The same bits.  db1 and db2 are atomic
+    fp32 sums: their order moves a term's rounding (2^-19 of the largest), and each of two
+    runs on each side may then round to the other bf16 neighbour, 4 * 2^-8 in all."""
+    cfg = {"tiny": S.TINY, "fine_bias": S.scaled(S.FINE, T=512, H=256, I=128, E=16, K=4, B=128),
+           "large_i": S.scaled(S.LARGE, T=256, H=384, I=160, E=4, K=2, B=256),
+           "geglu": S.scaled(S.TINY, T=300, H=128, I=320, E=5, K=2, B=128)}[name]
+    print("padding", name, act8, flush=True)
+    gp = gpu_problem(cfg)
+    n, N = gp["N"], 300
+    assert n < N <= 1024
+    t, E, H, I, B = gp["t"], cfg.E, cfg.H, cfg.I, cfg.B
+    gu_c, gu_s, d_c, d_s = gp["wq"]
+    act = mx.ACT_GEGLU if name == "geglu" else mx.ACT_SWIGLU
+
+    def run(blocks, accumulate=False):
+        pad = torch.full(((blocks - n) * B,), -1, dtype=torch.int32, device="cuda")
+        tpid = torch.cat([gp["tpid"], pad])
+        b2e = torch.cat([gp["b2e"], torch.arange(blocks - n, dtype=torch.int32, device="cuda") % E])
+        ckpt = torch.cat([t["ckpt"], torch.full((blocks - n, 2, I, B), torch.nan, dtype=torch.bfloat16, device="cuda")])
+        ck8 = mx.mxfp8_gated_act_fwd(ckpt, act, mx.E4M3, token_position_to_id=tpid, T=cfg.T)[1:] if act8 else None
+        op = mx.MoeBwd(t["hidden"], torch.from_numpy(gp["aff"]).cuda(), gu_c.view(E, H, 2, I), gu_s.view(E, H, 2, I // 32),
+                       d_c.view(E, I, H), d_s.view(E, I, H // 32), tpid, b2e, t["dy"], B, None if act8 else ckpt,
+                       down_proj_bias=t["b2"], affinity_on=cfg.affinity_on, gate_up_checkpoint=ck8, activation=act,
+                       accumulate=accumulate)
+        for _ in range(2):
+            op.run()
+        torch.cuda.synchronize()
+        return op.out
+
+    for accumulate in (False, True):
+        small, padded = run(n, accumulate), run(N, accumulate)
+        for k in ("dx", "daff", "dwgu", "dwd"):
+            assert torch.equal(small[k].view(torch.int16), padded[k].view(torch.int16)), k
+        if cfg.has_bias:
+            for k in ("db1", "db2"):
+                a, b = small[k].float(), padded[k].float()
+                assert ((a - b).abs() <= 2.0 ** -6 * b.abs() + 2.0 ** -19 * b.abs().max()).all(), k
