@@ -681,6 +681,12 @@ static int moe_run(const moe_bwd_mxfp8_args* a, void* ws, size_t ws_bytes, void*
   g4.M = I; g4.N = H; g4.out = a->down_proj_weight_grad; g4.ldo = H; g4.out_gstride = I * H;
   // the three products in one launch, for a whole backward of a small layer
   const bool joint = whole && !side && mx::moe_grads_fit(p3, g2, g4, int(E), device_cus(st));
+  mx::ScalesToPairs jobs[2];
+  int njobs = 0;
+  if (h_pairs) jobs[njobs++] = {a->down_scales, E, I, H, at(L.wd_scales_pairs)};
+  if (gu_pairs) jobs[njobs++] = {a->gate_up_scales, E, H, 2 * I, at(L.wgu_scales_pairs)};
+  // stage 1 and the inverse map's fill in one launch, for a whole backward
+  const bool prep = whole && mx::moe_prep_fits(T, H);
   int stage = -1;
 #define STEP(call, what) \
   if (stage >= lo && stage <= hi && (e = (call)) != hipSuccess) return hip_status(e, what);
@@ -690,22 +696,23 @@ static int moe_run(const moe_bwd_mxfp8_args* a, void* ws, size_t ws_bytes, void*
     STEP(mx::launch_fill_u32(db1_acc, E * 2 * I, 0u, st), "zero db1 accumulator");
     STEP(mx::launch_fill_u32(db2_acc, E * H, 0u, st), "zero db2 accumulator");
   }
+  if (prep)
+    STEP(mx::launch_moe_prep(a->output_hidden_states_grad, T, H, a->fmt_grad, at(L.dy_codes), at(L.dy_scales), jobs,
+                             njobs, slot_of, T * E, st),
+         "quantize dY, weight scales to pairs, inverse map");
   STEP(mx::launch_slot_setup(a->token_position_to_id, a->block_to_expert, a->expert_affinities_masked, T, E, N, B,
                              a->num_valid_tokens, slot_tok, slot_aff, slot_of, daff_slot, flag, boff, blist,
-                             ranges, nranges, st),
+                             ranges, nranges, prep, st),
        "slot setup");
   stage = 1;
   // S1: dY quantised along H per token row (Phase-1 operand, gathered by token later).
   // H % 128 == 0: Phase 1 streams the codes with pair-major scales (dY's written so,
   // W_down's re-laid); otherwise it reads their exact bf16 values.
-  STEP(mx::launch_quant_rows(a->output_hidden_states_grad, T, H, a->fmt_grad, at(L.dy_codes), at(L.dy_scales), st,
-                             h_pairs ? nullptr : reinterpret_cast<uint16_t*>(at(L.dy_deq)), h_pairs),
-       "quantize dY");
-  mx::ScalesToPairs jobs[2];
-  int njobs = 0;
-  if (h_pairs) jobs[njobs++] = {a->down_scales, E, I, H, at(L.wd_scales_pairs)};
-  if (gu_pairs) jobs[njobs++] = {a->gate_up_scales, E, H, 2 * I, at(L.wgu_scales_pairs)};
-  if (njobs) STEP(mx::launch_scales_to_pairs(jobs, njobs, st), "weight scales to pairs");
+  if (!prep)
+    STEP(mx::launch_quant_rows(a->output_hidden_states_grad, T, H, a->fmt_grad, at(L.dy_codes), at(L.dy_scales), st,
+                               h_pairs ? nullptr : reinterpret_cast<uint16_t*>(at(L.dy_deq)), h_pairs),
+         "quantize dY");
+  if (njobs && !prep) STEP(mx::launch_scales_to_pairs(jobs, njobs, st), "weight scales to pairs");
   if (!h_pairs)
     STEP(mx::launch_dequant_rows(a->down_codes, a->down_scales, E * I, H, a->fmt_weight,
                                  reinterpret_cast<uint16_t*>(at(L.wd_deq)), st),
@@ -775,12 +782,10 @@ static int moe_run(const moe_bwd_mxfp8_args* a, void* ws, size_t ws_bytes, void*
   if (side && stage >= lo && stage <= hi && (e = hipStreamWaitEvent(st, side->ev[2], 0)) != hipSuccess)
     return hip_status(e, "caller's stream after the gathers");
   const bool acc = a->accumulate != 0;
-  STEP(mx::launch_dx_reduce(dx_slot, slot_of, T, E, H, a->hidden_states_grad, a->expert_affinities_masked_grad, st, acc),
-       "dX per-token sums");
-  STEP(mx::launch_daff_scatter(daff_slot, reinterpret_cast<const float*>(at(L.daff_part)),
-                               I / 32 + (moe_fuse_bias(a) ? H / 128 : 0), slot_tok,
-                               a->block_to_expert, E, B, N, a->expert_affinities_masked_grad, st, acc),
-       "d(affinity) scatter");
+  STEP(mx::launch_finish(dx_slot, slot_of, T, E, H, a->hidden_states_grad, daff_slot,
+                         reinterpret_cast<const float*>(at(L.daff_part)), I / 32 + (moe_fuse_bias(a) ? H / 128 : 0),
+                         slot_tok, a->block_to_expert, B, N, a->expert_affinities_masked_grad, st, acc),
+       "dX per-token sums and d(affinity) scatter");
   if (a->has_bias) {
     STEP(mx::launch_f32_to_bf16(db1_acc, a->gate_and_up_proj_bias_grad, E * 2 * I, st, acc), "db1 to bf16");
     STEP(mx::launch_f32_to_bf16(db2_acc, a->down_proj_bias_grad, E * H, st, acc), "db2 to bf16");

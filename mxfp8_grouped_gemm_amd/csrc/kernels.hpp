@@ -61,6 +61,11 @@ struct ScalesToPairs {
   uint8_t* out;
 };
 hipError_t launch_scales_to_pairs(const ScalesToPairs* jobs, int n, hipStream_t st);
+// launch_quant_rows (pair-major scales), launch_scales_to_pairs and a fill of nfill
+// words with -1 in one launch, for small x (cols % 128 == 0)
+bool moe_prep_fits(int64_t rows, int64_t cols);
+hipError_t launch_moe_prep(const uint16_t* x, int64_t rows, int64_t cols, int fmt, uint8_t* codes, uint8_t* scales,
+                           const ScalesToPairs* jobs, int n, int32_t* fill, int64_t nfill, hipStream_t st);
 
 // gemm_dense.hip: C[m][n] = sum_k A[m][k] B[n][k] -> bf16 out[g][m][n].
 // A [M][lda] and B [N][ldb] fp8 codes, K-contiguous.  Scales pair-major
@@ -210,18 +215,15 @@ inline bool setup_makes_ranges(int64_t N, int64_t E) { return N <= kListMax && E
 hipError_t launch_slot_setup(const int32_t* tpid, const int32_t* b2e, const float* aff, int64_t T, int64_t E,
                              int64_t N, int64_t B, const int32_t* nvalid, int32_t* slot_tok, float* slot_aff,
                              int32_t* slot_of, float* daff_slot, int32_t* flag, int32_t* off, int32_t* list,
-                             const TileRangeJob* jobs, int njobs, hipStream_t st);
-// accumulate: each bf16 output becomes bf16(old + value) (else bf16(value), and
-// launch_dx_reduce zeroes daff [T*E] for the scatter that follows it)
-hipError_t launch_dx_reduce(const float* dx_slot, const int32_t* slot_of, int64_t T, int64_t E, int64_t H,
-                            uint16_t* dx, uint16_t* daff, hipStream_t st, bool accumulate = false);
+                             const TileRangeJob* jobs, int njobs, bool slot_of_filled, hipStream_t st);
+// accumulate: each bf16 output becomes bf16(old + value) (else bf16(value))
+hipError_t launch_finish(const float* dx_slot, const int32_t* slot_of, int64_t T, int64_t E, int64_t H, uint16_t* dx,
+                         const float* daff_slot, const float* daff_part, int64_t nparts, const int32_t* slot_tok,
+                         const int32_t* b2e, int64_t B, int64_t N, uint16_t* daff, hipStream_t st, bool accumulate);
 hipError_t launch_bias(const uint16_t* dy, const uint16_t* b2, const int32_t* slot_tok, const float* slot_aff,
                        const int32_t* b2e, const int32_t* flag, int64_t H, int64_t B, int64_t N, float* daff_slot,
                        float* db2_acc, hipStream_t st);
 hipError_t launch_f32_to_bf16(const float* src, uint16_t* dst, int64_t n, hipStream_t st, bool accumulate = false);
-hipError_t launch_daff_scatter(const float* daff_slot, const float* daff_part, int64_t nparts,
-                               const int32_t* slot_tok, const int32_t* b2e, int64_t E, int64_t B, int64_t N,
-                               uint16_t* daff, hipStream_t st, bool accumulate = false);
 
 // moe_phase1_*.hip (product, epilogue), moe_phase3.hip
 struct Phase1Args {

@@ -3,7 +3,10 @@
 // The three products only depend on the epilogue, so where all their tiles run
 // at once (a workgroup per CU) one launch takes as long as the longest of them:
 // the first n3 workgroups run Phase 3's tiles, then Phase 2's, then Phase 4's.  The
-// tiles are those of the separate kernels, to the bit.
+// tiles are those of the separate kernels, to the bit.  Measured at T = 256,
+// H = 128, I = 256, E = 4, top-2 (28 tiles of 2 to 8 ring stages, all latency): 8.8 us
+// against 8.4 + 5.2 + 5.2 in three launches.  With more tiles than CUs the
+// phases keep their own tile orders and shapes.
 #include "gemm_store.hpp"
 #include "moe_phase3.hpp"
 

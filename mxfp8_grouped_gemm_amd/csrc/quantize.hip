@@ -83,18 +83,19 @@ __device__ __forceinline__ void quant_rows_chunk(const uint4 v, int64_t c, uint2
   }
 }
 
+constexpr int64_t kSmallRows = int64_t(1) << 22;   // chunks of a small input
+constexpr int kSmallRowsU = 4;
+
 // U chunks per thread and pass, their loads issued together (U = 4 for small
 // inputs, where a thread per chunk leaves the kernel mostly workgroup start-up:
 // measured on [4096, 4096]).  nchunks is a multiple of 4, so a group's lanes
 // are all in range or all out.
 template <int FMT, bool DEQ, bool PAIRS, int U>
-__global__ void __launch_bounds__(256) quant_rows_kernel(const uint4* __restrict__ x,
-                                                          uint2* __restrict__ codes,
-                                                          uint8_t* __restrict__ scales,
-                                                          int64_t nchunks, uint4* __restrict__ deq,
-                                                          int64_t rows, int64_t gpr, int stage_major) {
-  const int64_t stride = int64_t(gridDim.x) * blockDim.x;
-  for (int64_t c0 = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; c0 < nchunks; c0 += U * stride) {
+__device__ __forceinline__ void quant_rows_part(const uint4* __restrict__ x, uint2* __restrict__ codes,
+                                                uint8_t* __restrict__ scales, int64_t nchunks, uint4* __restrict__ deq,
+                                                int64_t rows, int64_t gpr, int stage_major, unsigned wg, unsigned wgs) {
+  const int64_t stride = int64_t(wgs) * 256;
+  for (int64_t c0 = int64_t(wg) * 256 + threadIdx.x; c0 < nchunks; c0 += U * stride) {
     uint4 v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -107,6 +108,15 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const uint4* __restrict
       if (c < nchunks) quant_rows_chunk<FMT, DEQ, PAIRS>(v[u], c, codes, scales, deq, rows, gpr, stage_major);
     }
   }
+}
+
+template <int FMT, bool DEQ, bool PAIRS, int U>
+__global__ void __launch_bounds__(256) quant_rows_kernel(const uint4* __restrict__ x,
+                                                          uint2* __restrict__ codes,
+                                                          uint8_t* __restrict__ scales,
+                                                          int64_t nchunks, uint4* __restrict__ deq,
+                                                          int64_t rows, int64_t gpr, int stage_major) {
+  quant_rows_part<FMT, DEQ, PAIRS, U>(x, codes, scales, nchunks, deq, rows, gpr, stage_major, blockIdx.x, gridDim.x);
 }
 
 // codes [rows][cols] with scales along cols -> bf16; one thread per 16 codes.
@@ -464,10 +474,10 @@ struct PairsJob {
   unsigned gx, gy;      // workgroups along the words and the rows of a group
   unsigned first;       // the job's first workgroup
 };
-__global__ void __launch_bounds__(256) scales_to_pairs_kernel(PairsJob j0, PairsJob j1) {
+__device__ __forceinline__ void scales_to_pairs_tile(const PairsJob& j0, const PairsJob& j1, unsigned wg) {
   __shared__ uint32_t tile[32][65];
-  const PairsJob& j = blockIdx.x < j1.first ? j0 : j1;
-  const unsigned id = blockIdx.x - j.first, per = j.gx * j.gy;
+  const PairsJob& j = wg < j1.first ? j0 : j1;
+  const unsigned id = wg - j.first, per = j.gx * j.gy;
   const unsigned g = id / per, yx = id - g * per, y = yx / j.gx, x = yx - y * j.gx;
   const int64_t rows = j.rows, kp = j.kp, p0 = int64_t(x) * 32, r0 = int64_t(y) * 64;
   const uint32_t* src = j.in + g * rows * kp;
@@ -485,6 +495,36 @@ __global__ void __launch_bounds__(256) scales_to_pairs_kernel(PairsJob j0, Pairs
   }
 }
 
+__global__ void __launch_bounds__(256) scales_to_pairs_kernel(PairsJob j0, PairsJob j1) {
+  scales_to_pairs_tile(j0, j1, blockIdx.x);
+}
+
+// What the MoE backward makes from its inputs alone, in one launch: dY along H
+// (the first nq workgroups; codes row-major, scales pair-major), the weights' scales re-laid (ns) and
+// a fill with -1.  Each is a few microseconds of launch and latency in a small
+// layer (together, at T = 256, H = 128, E = 4: 4.0 us instead of 4.0 + 3.6 + 1.8);
+// a dY of more than kSmallRows chunks takes the separate kernels, whose time is
+// their traffic.
+template <int FMT>
+__global__ void __launch_bounds__(256) moe_prep_kernel(const uint4* __restrict__ x, uint2* __restrict__ codes,
+                                                       uint8_t* __restrict__ scales, int64_t nchunks, int64_t rows,
+                                                       int64_t gpr, unsigned nq, PairsJob j0, PairsJob j1, unsigned ns,
+                                                       int32_t* __restrict__ fill, int64_t nfill) {
+  const unsigned wg = blockIdx.x;
+  if (wg < nq) {
+    quant_rows_part<FMT, false, true, kSmallRowsU>(x, codes, scales, nchunks, nullptr, rows, gpr, 0, wg, nq);
+  } else if (wg < nq + ns) {
+    scales_to_pairs_tile(j0, j1, wg - nq);
+  } else {
+    const int64_t i = (int64_t(wg - nq - ns) * 256 + threadIdx.x) * 4;
+    if (i + 4 <= nfill) {
+      *reinterpret_cast<int4*>(fill + i) = int4{-1, -1, -1, -1};
+    } else {
+      for (int64_t k = i; k < nfill; ++k) fill[k] = -1;
+    }
+  }
+}
+
 // ---------------------------------------------------------------------------
 // host launchers
 template <int FMT, int U>
@@ -498,10 +538,10 @@ static void rows_dispatch(int blocks, hipStream_t st, const uint4* xs, uint2* cs
 template <int FMT>
 static void rows_dispatch(int64_t nchunks, hipStream_t st, const uint4* xs, uint2* cs, uint8_t* scales, uint4* ds,
                           int64_t rows, int64_t gpr, bool pairs, int sm) {
-  const bool small = nchunks <= (int64_t(1) << 22);
+  const bool small = nchunks <= kSmallRows;
   const int64_t want = small ? (nchunks + 1023) / 1024 : (nchunks + 255) / 256;
   const int blocks = int(want < 65536 ? want : 65536);
-  if (small) rows_dispatch<FMT, 4>(blocks, st, xs, cs, scales, nchunks, ds, rows, gpr, pairs, sm);
+  if (small) rows_dispatch<FMT, kSmallRowsU>(blocks, st, xs, cs, scales, nchunks, ds, rows, gpr, pairs, sm);
   else rows_dispatch<FMT, 1>(blocks, st, xs, cs, scales, nchunks, ds, rows, gpr, pairs, sm);
 }
 
@@ -520,9 +560,8 @@ hipError_t launch_quant_rows(const uint16_t* x, int64_t rows, int64_t cols, int 
   return hipGetLastError();
 }
 
-hipError_t launch_scales_to_pairs(const ScalesToPairs* jobs, int n, hipStream_t st) {
-  PairsJob j[2] = {};
-  int64_t total = 0;
+static hipError_t pairs_plan(const ScalesToPairs* jobs, int n, PairsJob (&j)[2], int64_t& total) {
+  total = 0;
   for (int i = 0; i < 2; ++i) {
     j[i].first = unsigned(total);
     if (i >= n) continue;
@@ -540,9 +579,36 @@ hipError_t launch_scales_to_pairs(const ScalesToPairs* jobs, int n, hipStream_t 
     total += gx * gy * q.groups;
   }
   if (total > INT32_MAX) return hipErrorInvalidValue;
-  if (total == 0) return hipSuccess;
   if (n < 2) j[1].first = unsigned(total);
+  return hipSuccess;
+}
+hipError_t launch_scales_to_pairs(const ScalesToPairs* jobs, int n, hipStream_t st) {
+  PairsJob j[2] = {};
+  int64_t total;
+  const hipError_t err = pairs_plan(jobs, n, j, total);
+  if (err != hipSuccess || total == 0) return err;
   scales_to_pairs_kernel<<<unsigned(total), 256, 0, st>>>(j[0], j[1]);
+  return hipGetLastError();
+}
+
+bool moe_prep_fits(int64_t rows, int64_t cols) { return cols % 128 == 0 && rows * cols / 8 <= kSmallRows; }
+hipError_t launch_moe_prep(const uint16_t* x, int64_t rows, int64_t cols, int fmt, uint8_t* codes, uint8_t* scales,
+                           const ScalesToPairs* jobs, int n, int32_t* fill, int64_t nfill, hipStream_t st) {
+  if (!moe_prep_fits(rows, cols)) return hipErrorInvalidValue;
+  PairsJob j[2] = {};
+  int64_t ns;
+  const hipError_t err = pairs_plan(jobs, n, j, ns);
+  if (err != hipSuccess) return err;
+  const int64_t nchunks = rows * cols / 8, nq = (nchunks + 1023) / 1024, grid = nq + ns + (nfill + 1023) / 1024;
+  if (grid > INT32_MAX) return hipErrorInvalidValue;
+  if (grid == 0) return hipSuccess;
+  auto go = [&](auto f) {
+    moe_prep_kernel<f()><<<unsigned(grid), 256, 0, st>>>(reinterpret_cast<const uint4*>(x), reinterpret_cast<uint2*>(codes),
+                                                         scales, nchunks, rows, cols / 32, unsigned(nq), j[0], j[1],
+                                                         unsigned(ns), fill, nfill);
+  };
+  if (fmt == kE4M3) go(std::integral_constant<int, kE4M3>{});
+  else go(std::integral_constant<int, kE5M2>{});
   return hipGetLastError();
 }
 
