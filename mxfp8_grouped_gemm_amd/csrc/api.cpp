@@ -687,6 +687,12 @@ static int moe_run(const moe_bwd_mxfp8_args* a, void* ws, size_t ws_bytes, void*
   if (gu_pairs) jobs[njobs++] = {a->gate_up_scales, E, H, 2 * I, at(L.wgu_scales_pairs)};
   // stage 1 and the inverse map's fill in one launch, for a whole backward
   const bool prep = whole && mx::moe_prep_fits(T, H);
+  // X and dY gathered in one launch where neither carries more (no fused bias
+  // reductions, no a*dY checkpoint), and the block lists beside them
+  const bool xy = !a->down_proj_act_checkpoint && !moe_fuse_bias(a) && mx::quant_tok_xy_fits(T, H, P);
+  const bool lists_later = whole && !side && xy && p3.ranges_done && mx::quant_tok_xy_lists(H, P, N, E);
+  mx::BlockLists lists{a->block_to_expert, flag, int(N), int(E), boff, blist, {}, nranges};
+  for (int i = 0; i < nranges; ++i) lists.jobs[i] = ranges[i];
   int stage = -1;
 #define STEP(call, what) \
   if (stage >= lo && stage <= hi && (e = (call)) != hipSuccess) return hip_status(e, what);
@@ -702,7 +708,7 @@ static int moe_run(const moe_bwd_mxfp8_args* a, void* ws, size_t ws_bytes, void*
          "quantize dY, weight scales to pairs, inverse map");
   STEP(mx::launch_slot_setup(a->token_position_to_id, a->block_to_expert, a->expert_affinities_masked, T, E, N, B,
                              a->num_valid_tokens, slot_tok, slot_aff, slot_of, daff_slot, flag, boff, blist,
-                             ranges, nranges, prep, st),
+                             ranges, nranges, prep, lists_later, st),
        "slot setup");
   stage = 1;
   // S1: dY quantised along H per token row (Phase-1 operand, gathered by token later).
@@ -721,11 +727,11 @@ static int moe_run(const moe_bwd_mxfp8_args* a, void* ws, size_t ws_bytes, void*
   STEP(order(side ? &side->ev[0] : nullptr, st, s2), "second stream after the set-up");
   // token-axis operands of Phases 2 and 4: X, a*dY (on H) or dY (on I); the intermediate
   // operand comes out of the Phase-1 epilogue
-  // (one launch where neither carries more: no fused bias reductions, no a*dY checkpoint)
-  if (!a->down_proj_act_checkpoint && !moe_fuse_bias(a) && mx::quant_tok_xy_fits(T, H, P)) {
+  if (xy) {
     STEP(mx::launch_quant_tok_xy(a->hidden_states, a->output_hidden_states_grad, T, H, slot_tok,
                                  a->affinity_on == 0 ? slot_aff : nullptr, P, a->fmt_act, a->fmt_grad,
-                                 at(L.x_tok_codes), at(L.x_tok_scales), at(L.gy_tok_codes), at(L.gy_tok_scales), s2),
+                                 at(L.x_tok_codes), at(L.x_tok_scales), at(L.gy_tok_codes), at(L.gy_tok_scales), s2,
+                                 lists_later ? &lists : nullptr),
          "gather-quantize X and dY");
   } else {
     STEP(mx::launch_quant_tok(a->hidden_states, T, H, slot_tok, nullptr, P, a->fmt_act, at(L.x_tok_codes),

@@ -40,14 +40,6 @@ hipError_t launch_quant_tok(const uint16_t* x, int64_t src_rows, int64_t cols, c
                             const float* rowscale, int64_t rows, int fmt, uint8_t* codes_t,
                             uint8_t* scales_t, hipStream_t st, bool pairs = false, bool self_rows = false,
                             const TokBias* bias = nullptr, bool stage_major = false);
-// the MoE backward's two gathers, X and dY (times rowscale, or null), by the same
-// index in one launch, codes stage-major and scales pair-major; for short gathers
-// from sources under 2 GiB, rows % 128 == 0
-bool quant_tok_xy_fits(int64_t src_rows, int64_t cols, int64_t rows);
-hipError_t launch_quant_tok_xy(const uint16_t* x, const uint16_t* dy, int64_t src_rows, int64_t cols,
-                               const int32_t* idx, const float* rowscale, int64_t rows, int fmt_x, int fmt_y,
-                               uint8_t* x_codes, uint8_t* x_scales, uint8_t* y_codes, uint8_t* y_scales,
-                               hipStream_t st);
 // prequant.hip: an operand quantised along its rows (codes [R][C], scales
 // [R/32][C]) into the GEMM layout: codes [C][R]; scales pair-major
 // [R/128][C][4] (pairs) or row-major [C][R/32]
@@ -215,7 +207,29 @@ inline bool setup_makes_ranges(int64_t N, int64_t E) { return N <= kListMax && E
 hipError_t launch_slot_setup(const int32_t* tpid, const int32_t* b2e, const float* aff, int64_t T, int64_t E,
                              int64_t N, int64_t B, const int32_t* nvalid, int32_t* slot_tok, float* slot_aff,
                              int32_t* slot_of, float* daff_slot, int32_t* flag, int32_t* off, int32_t* list,
-                             const TileRangeJob* jobs, int njobs, bool slot_of_filled, hipStream_t st);
+                             const TileRangeJob* jobs, int njobs, bool slot_of_filled, bool lists_later,
+                             hipStream_t st);
+// the block lists of up to kSmallLists blocks and experts, where launch_quant_tok_xy
+// makes them beside its tiles (lists_later above)
+constexpr int kSmallLists = 256;
+struct BlockLists {
+  const int32_t* b2e;
+  const int32_t* flag;
+  int N, E;
+  int32_t* off;
+  int32_t* list;
+  TileRangeJob jobs[2];
+  int njobs;
+};
+// the MoE backward's two gathers, X and dY (times rowscale, or null), by the same
+// index in one launch, codes stage-major and scales pair-major; for short gathers
+// from sources under 2 GiB, rows % 128 == 0
+bool quant_tok_xy_fits(int64_t src_rows, int64_t cols, int64_t rows);
+bool quant_tok_xy_lists(int64_t cols, int64_t rows, int64_t N, int64_t E);   // with lists too
+hipError_t launch_quant_tok_xy(const uint16_t* x, const uint16_t* dy, int64_t src_rows, int64_t cols,
+                               const int32_t* idx, const float* rowscale, int64_t rows, int fmt_x, int fmt_y,
+                               uint8_t* x_codes, uint8_t* x_scales, uint8_t* y_codes, uint8_t* y_scales,
+                               hipStream_t st, const BlockLists* lists = nullptr);
 // accumulate: each bf16 output becomes bf16(old + value) (else bf16(value))
 hipError_t launch_finish(const float* dx_slot, const int32_t* slot_of, int64_t T, int64_t E, int64_t H, uint16_t* dx,
                          const float* daff_slot, const float* daff_part, int64_t nparts, const int32_t* slot_tok,

@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "kernels.hpp"
+#include "moe_lists.hpp"
 #include "moe_tiles.hpp"
 #include "mx_device.hpp"
 #include "swiglu.hpp"
@@ -362,52 +363,7 @@ __global__ void __launch_bounds__(256) slot_block_kernel(const int32_t* __restri
   if (threadIdx.x == 0) flag[blockIdx.x] = max(max(red[0], red[1]), max(red[2], red[3]));
 }
 
-// Per-expert lists of occupied blocks in ascending order, for up to 1024 blocks
-// and experts: one workgroup, a thread per block.  The counts by LDS atomics,
-// the offsets by a scan over the experts, and a block's place in its list by
-// counting the blocks before it with its expert (N / 4 reads of four at a
-// time, the same address in every lane).
-// eb: LDS for an occupied block's expert, else -1 (16-byte aligned); cnt, wsum: LDS
-__device__ __forceinline__ void expert_lists(const int32_t* __restrict__ b2e, const int32_t* __restrict__ flag, int N,
-                                             int E, int32_t* __restrict__ off, int32_t* __restrict__ list, int32_t* eb,
-                                             int32_t* cnt, int32_t* wsum) {
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  int e = -1;
-  if (t < N && flag[t] != 0) e = b2e[t];
-  if (e < 0 || e >= E) e = -1;
-  eb[t] = e;
-  cnt[t] = 0;
-  __syncthreads();
-  if (e >= 0) atomicAdd(&cnt[e], 1);
-  __syncthreads();
-  const int c = cnt[t];
-  int x = c;
-  for (int o = 1; o < 64; o <<= 1) {
-    const int y = __shfl_up(x, o, 64);
-    if (lane >= o) x += y;
-  }
-  if (lane == 63) wsum[wave] = x;
-  __syncthreads();
-  int before = 0;
-  for (int w = 0; w < wave; ++w) before += wsum[w];
-  const int pos = before + x - c;   // expert t's first entry
-  cnt[t] = pos;
-  if (t < E) off[t] = pos;
-  if (t == E - 1) off[E] = pos + c;
-  __syncthreads();
-  if (e >= 0) {
-    int rank = 0;
-    const int4* q = reinterpret_cast<const int4*>(eb);
-#pragma unroll 4
-    for (int b = 0; b < N; b += 4) {
-      const int4 v = q[b >> 2];
-      rank += (v.x == e && b < t) + (v.y == e && b + 1 < t) + (v.z == e && b + 2 < t) + (v.w == e && b + 3 < t);
-    }
-    list[cnt[e] + rank] = t;
-  }
-}
-
-// The same for more blocks or experts: counts (one
+// The expert lists (moe_lists.hpp) of more than kListMax blocks or experts: counts (one
 // workgroup per expert, coalesced scans of the blocks), offsets (one
 // workgroup), then each expert's list in block order (one workgroup each).
 __global__ void __launch_bounds__(256) expert_count_kernel(const int32_t* __restrict__ b2e,
@@ -512,58 +468,10 @@ __global__ void __launch_bounds__(256) tile_ranges_kernel(const int32_t* __restr
   }
 }
 
-static int full_tiles(const TileRangeJob& j) { return (j.blk + j.W - 1) / j.W * j.other; }   // of a block all live
 
 hipError_t launch_tile_ranges(const int32_t* ext, int64_t N, const TileRangeJob& j, hipStream_t st) {
   tile_ranges_kernel<<<1, 256, 0, st>>>(ext, int(N), j.W, j.other, j.start, j.cut, j.conc, j.npairs, j.rr, full_tiles(j));
   return hipGetLastError();
-}
-
-// tile_ranges_kernel's results for up to kListMax blocks, a thread each
-__device__ __forceinline__ void tile_ranges_of(const int32_t* __restrict__ ext, int N, const TileRangeJob& j, int cmax,
-                                               int32_t* wfull, int32_t* wpart) {
-  const int b = threadIdx.x, lane = b & 63, wave = b >> 6;
-  const int c = b < N ? (ext[b] + j.W - 1) / j.W * j.other : 0;
-  const bool full = j.rr && c == cmax;
-  int xf = full ? c : 0, xp = full ? 0 : c;
-  for (int o = 1; o < 64; o <<= 1) {
-    const int yf = __shfl_up(xf, o, 64), yp = __shfl_up(xp, o, 64);
-    if (lane >= o) {
-      xf += yf;
-      xp += yp;
-    }
-  }
-  if (lane == 63) {
-    wfull[wave] = xf;
-    wpart[wave] = xp;
-  }
-  __syncthreads();
-  int bf = 0, bp = 0, tf = 0, tp = 0;
-  for (int w = 0; w < kListMax / 64; ++w) {
-    bf += w < wave ? wfull[w] : 0;
-    bp += w < wave ? wpart[w] : 0;
-    tf += wfull[w];
-    tp += wpart[w];
-  }
-  const int total = tf + tp;
-  const int t0 = full ? bf + xf - c : tf + bp + xp - c;   // partly filled blocks after the full ones
-  if (b < N) {
-    j.start[b] = t0;
-    int32_t* map = j.start + N + 1;
-    for (int t = t0; t < t0 + c; ++t) map[t] = b;
-  }
-  if (b == 0) {
-    j.start[N] = total;
-    if (j.cut) {   // the tail cut of each XCD
-      int base = 0;
-      for (int x = 0; x < 8; ++x) {
-        TailCut k = tail_cut_one(total, x, j.rr, j.conc, j.npairs);
-        k.base = base;
-        base += k.tail * (k.S - 1);
-        j.cut[x] = k;
-      }
-    }
-  }
 }
 
 // The expert lists (workgroup 0) and the tile ranges of up to two GEMMs (1, 2).
@@ -574,21 +482,23 @@ __global__ void __launch_bounds__(kListMax) block_lists_kernel(const int32_t* __
   __shared__ __attribute__((aligned(16))) int32_t eb[kListMax];
   __shared__ int32_t cnt[kListMax];
   __shared__ int32_t wsum[kListMax / 64];
-  if (blockIdx.x == 0) expert_lists(b2e, flag, N, E, off, list, eb, cnt, wsum);
-  else if (blockIdx.x == 1) tile_ranges_of(flag, N, j0, cmax0, eb, cnt);
-  else tile_ranges_of(flag, N, j1, cmax1, eb, cnt);
+  if (blockIdx.x == 0) expert_lists<kListMax>(b2e, flag, N, E, off, list, eb, cnt, wsum);
+  else if (blockIdx.x == 1) tile_ranges_of<kListMax>(flag, N, j0, cmax0, eb, cnt);
+  else tile_ranges_of<kListMax>(flag, N, j1, cmax1, eb, cnt);
 }
 
 hipError_t launch_slot_setup(const int32_t* tpid, const int32_t* b2e, const float* aff, int64_t T, int64_t E,
                              int64_t N, int64_t B, const int32_t* nvalid, int32_t* slot_tok, float* slot_aff,
                              int32_t* slot_of, float* daff_slot, int32_t* flag, int32_t* off, int32_t* list,
-                             const TileRangeJob* jobs, int njobs, bool slot_of_filled, hipStream_t st) {
+                             const TileRangeJob* jobs, int njobs, bool slot_of_filled, bool lists_later,
+                             hipStream_t st) {
   if (!slot_of_filled) {
     hipError_t err = launch_fill_u32(reinterpret_cast<uint32_t*>(slot_of), T * E, 0xffffffffu, st);
     if (err != hipSuccess) return err;
   }
   slot_block_kernel<<<unsigned(N), 256, 0, st>>>(tpid, b2e, aff, T, E, B, nvalid, slot_tok, slot_aff, slot_of, daff_slot,
                                                  flag);
+  if (lists_later) return hipGetLastError();
   if (setup_makes_ranges(N, E)) {
     TileRangeJob j[2] = {};
     int cmax[2] = {};

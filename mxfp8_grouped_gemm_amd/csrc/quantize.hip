@@ -18,6 +18,7 @@
 
 #include "gemm_v2.hpp"
 #include "kernels.hpp"
+#include "moe_lists.hpp"
 #include "mx_device.hpp"
 
 namespace mx {
@@ -381,7 +382,9 @@ __global__ void __launch_bounds__(256) quant_tok_kernel(const uint16_t* __restri
 }
 
 // X (blockIdx.z 0) and dY (1, with the affinities where ROWSCALE) gathered in
-// one launch, both pair-major and stage-major.
+// one launch, both pair-major and stage-major.  Planes 2 to 4, where the launch has them:
+// their first workgroups make the block lists, which nothing here reads (tiny: 2.8 us of a
+// launch of their own saved).
 template <int FX, int FY, bool ROWSCALE>
 __global__ void __launch_bounds__(256) quant_tok_xy_kernel(const uint16_t* __restrict__ x,
                                                            const uint16_t* __restrict__ dy, int64_t src_rows,
@@ -389,7 +392,21 @@ __global__ void __launch_bounds__(256) quant_tok_xy_kernel(const uint16_t* __res
                                                            const float* __restrict__ rowscale, int64_t rows,
                                                            uint8_t* __restrict__ x_codes, uint8_t* __restrict__ x_scales,
                                                            uint8_t* __restrict__ y_codes,
-                                                           uint8_t* __restrict__ y_scales) {
+                                                           uint8_t* __restrict__ y_scales, BlockLists lists, int cmax0,
+                                                           int cmax1) {
+  if (blockIdx.z >= 2) {
+    __shared__ __attribute__((aligned(16))) int32_t eb[kSmallLists];
+    __shared__ int32_t cnt[kSmallLists];
+    __shared__ int32_t wsum[kSmallLists / 64];
+    if (blockIdx.x || blockIdx.y) return;
+    if (blockIdx.z == 2)
+      expert_lists<kSmallLists>(lists.b2e, lists.flag, lists.N, lists.E, lists.off, lists.list, eb, cnt, wsum);
+    else if (blockIdx.z == 3)
+      tile_ranges_of<kSmallLists>(lists.flag, lists.N, lists.jobs[0], cmax0, eb, cnt);
+    else
+      tile_ranges_of<kSmallLists>(lists.flag, lists.N, lists.jobs[1], cmax1, eb, cnt);
+    return;
+  }
   if (blockIdx.z == 0)
     quant_tok_tile<FX, true, false, true, true, false>(x, src_rows, cols, idx, nullptr, rows, x_codes, x_scales, 0,
                                                        TokBias{}, 1);
@@ -712,20 +729,29 @@ bool quant_tok_xy_fits(int64_t src_rows, int64_t cols, int64_t rows) {
   const int64_t tiles = (cols + kTokCols - 1) / kTokCols * ((rows + kTokRows - 1) / kTokRows);
   return tiles <= 2048 && src_rows * cols * 2 < int64_t(v2::kOOB) && rows <= int64_t(INT32_MAX) && rows % 128 == 0;
 }
+// The lists' planes have as many workgroups as a gather's, all but one of them empty.
+bool quant_tok_xy_lists(int64_t cols, int64_t rows, int64_t N, int64_t E) {
+  const int64_t tiles = (cols + kTokCols - 1) / kTokCols * ((rows + kTokRows - 1) / kTokRows);
+  return tiles <= 256 && N <= kSmallLists && E <= kSmallLists;
+}
 hipError_t launch_quant_tok_xy(const uint16_t* x, const uint16_t* dy, int64_t src_rows, int64_t cols,
                                const int32_t* idx, const float* rowscale, int64_t rows, int fmt_x, int fmt_y,
                                uint8_t* x_codes, uint8_t* x_scales, uint8_t* y_codes, uint8_t* y_scales,
-                               hipStream_t st) {
-  if (rows == 0 || cols == 0) return hipSuccess;
+                               hipStream_t st, const BlockLists* lists) {
+  if (rows == 0 || cols == 0) return lists ? hipErrorInvalidValue : hipSuccess;
   if (!quant_tok_xy_fits(src_rows, cols, rows)) return hipErrorInvalidValue;
-  const dim3 grid(unsigned((cols + kTokCols - 1) / kTokCols), unsigned((rows + kTokRows - 1) / kTokRows), 2);
+  if (lists && !quant_tok_xy_lists(cols, rows, lists->N, lists->E)) return hipErrorInvalidValue;
+  const BlockLists l = lists ? *lists : BlockLists{};
+  const int cmax0 = l.njobs > 0 ? full_tiles(l.jobs[0]) : 0, cmax1 = l.njobs > 1 ? full_tiles(l.jobs[1]) : 0;
+  const dim3 grid(unsigned((cols + kTokCols - 1) / kTokCols), unsigned((rows + kTokRows - 1) / kTokRows),
+                  unsigned(2 + (lists ? 1 + l.njobs : 0)));
   auto go = [&](auto fx, auto fy) {
     if (rowscale)
       quant_tok_xy_kernel<fx(), fy(), true><<<grid, 256, 0, st>>>(x, dy, src_rows, cols, idx, rowscale, rows, x_codes,
-                                                                  x_scales, y_codes, y_scales);
+                                                                  x_scales, y_codes, y_scales, l, cmax0, cmax1);
     else
       quant_tok_xy_kernel<fx(), fy(), false><<<grid, 256, 0, st>>>(x, dy, src_rows, cols, idx, rowscale, rows, x_codes,
-                                                                   x_scales, y_codes, y_scales);
+                                                                   x_scales, y_codes, y_scales, l, cmax0, cmax1);
   };
   using E4 = std::integral_constant<int, kE4M3>;
   using E5 = std::integral_constant<int, kE5M2>;
