@@ -885,7 +885,7 @@ int moe_router_fwd(int mode, int64_t T, int64_t E, int64_t K, const void* logits
 
 // The workspace's regions, each 256-byte aligned; fills the record pointers of p where base is given.
 static size_t balance_regions(int64_t T, int64_t E, int64_t S, uint8_t* base, mx::BalanceArgs* p) {
-  const int64_t chunk = mx::balance_chunk_tokens(T, E);
+  const int64_t chunk = mx::balance_chunk_tokens(T, E, S);
   const int64_t recs = (T + chunk - 1) / chunk + S;
   size_t o = 0;
   auto put = [&](auto*& field, int64_t n) {

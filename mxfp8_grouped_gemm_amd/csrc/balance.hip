@@ -452,22 +452,29 @@ __global__ void __launch_bounds__(kBwdThreads) balance_bwd_kernel(BalanceArgs p)
 }
 
 // Tokens of one chunk: a round of the workgroup's rows, or as many as keep to
-// kChunks chunks.
-int64_t balance_chunk_tokens(int64_t T, int64_t E) {
+// kChunks chunks; fewer where several sequences would fall into one chunk, as
+// each costs its workgroup about 1.5 us of reduction: a sequence's mean length,
+// but no less than 4 tokens and no more than 2 kChunks chunks (1000 tokens of 8
+// experts in 64 sequences: 60 -> 18 us).
+int64_t balance_chunk_tokens(int64_t T, int64_t E, int64_t S) {
   const int64_t r = chunk_threads(E > 512 ? 16 : 8) / rows::lanes(E);
   const int64_t c = (T + kChunks - 1) / kChunks;
-  return c <= r ? r : (c + r - 1) / r * r;
+  const int64_t most = c <= r ? r : (c + r - 1) / r * r;
+  const int64_t least = (T + 2 * kChunks - 1) / (2 * kChunks);
+  int64_t few = (T + S - 1) / S;   // the mean
+  few = few > least ? few : least;
+  few = few > 4 ? few : 4;
+  return few < most ? few : most;
 }
 
-// One workgroup for everything, in one launch, where the tokens make one round of
-// its rows anyhow (up to 64 sequences), or two in few sequences: measured with
-// 60 experts, 64 tokens: 4.7 us against 9.5 in one sequence, 19.6 against 24.2
-// in 16; 128 tokens: 6.2 against 9.5, and 9.4 against 12.6 in 4.  Past that the
-// chunks of the two launches run side by side (256 tokens in 16 sequences:
-// 23.9 us in one workgroup, 15.0 in two launches).
+// One workgroup for everything, in one launch, where the tokens make at most two
+// rounds of its rows, in few sequences (each is a reduction of its own): measured with
+// 8 experts and 300 tokens 5.9 us against 8.1 in one sequence, 11.0 against 13.0
+// in 4, 17.6 against 16.1 in 8; 60 experts and 128 tokens 5.1 against 9.1, 8.9 against 11.1 in 4
+// and 14.1 against 11.9 in 8.
 static bool balance_one(const BalanceArgs& p) {
   const int64_t round = chunk_threads(p.E > 512 ? 16 : 8) / rows::lanes(p.E);
-  return (p.T <= round && p.S <= 64) || (p.T <= 2 * round && p.S <= 4);
+  return p.T <= 2 * round && p.S <= 4;
 }
 
 hipError_t launch_balance_fwd(const BalanceArgs& p, hipStream_t st) {

@@ -155,7 +155,7 @@ struct BalanceArgs {
   float* term_z;              // [S]
   unsigned* done;
 };
-int64_t balance_chunk_tokens(int64_t T, int64_t E);
+int64_t balance_chunk_tokens(int64_t T, int64_t E, int64_t S);
 hipError_t launch_balance_fwd(const BalanceArgs& p, hipStream_t st);
 hipError_t launch_balance_bwd(const BalanceArgs& p, hipStream_t st);
 

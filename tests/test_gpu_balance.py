@@ -186,7 +186,7 @@ def test_in_a_graph_with_a_shared_workspace():
 
 @pytest.mark.parametrize("E", [8, 60, 128, 700])
 def test_both_sides_of_the_one_workgroup_rule(E):
-    """One round of a workgroup's rows in up to 64 sequences, or two in up to four,
+    """Up to two rounds of a workgroup's rows in up to four sequences
     take one launch: sizes just inside and past the limits, against the oracle."""
     threads, lanes = (256, 64) if E > 512 else (512, max(1, 2 ** int(np.ceil(np.log2(E / 8)))))
     edge = threads // lanes
