@@ -558,8 +558,10 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, balance_coef:
         ptrs = (_tensor(loss, torch.float32, (2,), dev, "loss"), _tensor(counts, torch.int32, (S, E), dev, "counts"),
                 _tensor(num, torch.int32, (S + 2,), dev, "num_tokens"))
     if workspace is None:
-        size = _balance_workspace_size(T, E, S)
-        ws = _empty(size, dtype=torch.uint8, device=dev).data_ptr() if size else None   # 0: refused below
+        size, ws = _balance_workspace_size(T, E, S), None   # 0: refused below
+        if size:   # the name holds it until the kernels are enqueued
+            workspace = _empty(size, dtype=torch.uint8, device=dev)
+            ws = workspace.data_ptr()
     else:
         size = workspace.numel()
         ws = _tensor(workspace, torch.uint8, workspace.shape, dev, "workspace")
