@@ -7,6 +7,10 @@
 
 namespace mx {
 
+// Workgroups of 256 threads that one launch takes: the runtime runs a grid's
+// threads modulo 2^32, without an error.
+constexpr int64_t kMaxGrid256 = (int64_t(1) << 24) - 1;
+
 // quantize.hip
 // Scale layouts: row-major [rows][K/32], or pair-major [K/128][rows][4] (pairs
 // = true) for operands of the ring GEMM loop; see gemm_v3.hpp.

@@ -617,7 +617,8 @@ hipError_t launch_f32_to_bf16(const float* src, uint16_t* dst, int64_t n, hipStr
 
 // The finalisation's two halves in one launch (tiny: 4.2 us instead of 4.0 +
 // 3.3): the first T workgroups sum the tokens' dX rows, the others gather
-// d(affinity) of 64 slots each (they write other pairs than the first).
+// d(affinity) of 64 slots each (they write other pairs than the first).  More
+// workgroups than one launch takes (kMaxGrid256) go in several.
 //
 // dX[t] = sum over t's routed slots, in expert order, of the slot's Phase-3 row
 // (fp32), rounded to bf16; a token without slots gets zeros.  One workgroup
@@ -639,6 +640,7 @@ struct FinishArgs {
   const int32_t* b2e;
   int64_t B, P;
   uint16_t* daff;
+  int64_t first;   // this launch's first workgroup
 };
 template <bool ACC>
 __device__ __forceinline__ void dx_reduce(const FinishArgs& p, int64_t t) {
@@ -718,7 +720,7 @@ __device__ __forceinline__ void daff_scatter(const FinishArgs& p, int64_t wg) {
 
 template <bool ACC>
 __global__ void __launch_bounds__(256) finish_kernel(FinishArgs p) {
-  const int64_t wg = blockIdx.x;
+  const int64_t wg = p.first + blockIdx.x;
   if (wg < p.T) dx_reduce<ACC>(p, wg);
   else daff_scatter<ACC>(p, wg - p.T);
 }
@@ -727,11 +729,12 @@ hipError_t launch_finish(const float* dx_slot, const int32_t* slot_of, int64_t T
                          const float* daff_slot, const float* daff_part, int64_t nparts, const int32_t* slot_tok,
                          const int32_t* b2e, int64_t B, int64_t N, uint16_t* daff, hipStream_t st, bool accumulate) {
   const int64_t P = N * B, grid = T + (P + 63) / 64;
-  if (grid <= 0) return hipSuccess;
-  if (grid > INT32_MAX) return hipErrorInvalidValue;
-  const FinishArgs p{dx_slot, slot_of, T, E, H, dx, daff_slot, daff_part, nparts, slot_tok, b2e, B, P, daff};
-  if (accumulate) finish_kernel<true><<<unsigned(grid), 256, 0, st>>>(p);   // pairs without a slot keep their value
-  else finish_kernel<false><<<unsigned(grid), 256, 0, st>>>(p);
+  FinishArgs p{dx_slot, slot_of, T, E, H, dx, daff_slot, daff_part, nparts, slot_tok, b2e, B, P, daff, 0};
+  for (; p.first < grid; p.first += kMaxGrid256) {
+    const unsigned n = unsigned(grid - p.first < kMaxGrid256 ? grid - p.first : kMaxGrid256);
+    if (accumulate) finish_kernel<true><<<n, 256, 0, st>>>(p);   // pairs without a slot keep their value
+    else finish_kernel<false><<<n, 256, 0, st>>>(p);
+  }
   return hipGetLastError();
 }
 

@@ -595,7 +595,7 @@ static hipError_t pairs_plan(const ScalesToPairs* jobs, int n, PairsJob (&j)[2],
     j[i].gy = unsigned(gy);
     total += gx * gy * q.groups;
   }
-  if (total > INT32_MAX) return hipErrorInvalidValue;
+  if (total > kMaxGrid256) return hipErrorInvalidValue;
   if (n < 2) j[1].first = unsigned(total);
   return hipSuccess;
 }
@@ -617,7 +617,7 @@ hipError_t launch_moe_prep(const uint16_t* x, int64_t rows, int64_t cols, int fm
   const hipError_t err = pairs_plan(jobs, n, j, ns);
   if (err != hipSuccess) return err;
   const int64_t nchunks = rows * cols / 8, nq = (nchunks + 1023) / 1024, grid = nq + ns + (nfill + 1023) / 1024;
-  if (grid > INT32_MAX) return hipErrorInvalidValue;
+  if (grid > kMaxGrid256) return hipErrorInvalidValue;
   if (grid == 0) return hipSuccess;
   auto go = [&](auto f) {
     moe_prep_kernel<f()><<<unsigned(grid), 256, 0, st>>>(reinterpret_cast<const uint4*>(x), reinterpret_cast<uint2*>(codes),
