@@ -114,6 +114,7 @@ struct RouterArgs {
   const float* dscores;       // [T,K] upstream score gradients, or null when
   const uint16_t* daff;       // [T,E] bf16 affinity gradient is read at idx instead
   float* dlogits;             // [T,E] output
+  int64_t t0;                 // first token of a launch (set by the launcher)
 };
 hipError_t launch_router_bwd(const RouterArgs& p, hipStream_t st);
 

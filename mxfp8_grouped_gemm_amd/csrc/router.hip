@@ -49,7 +49,7 @@ __device__ __forceinline__ float seg_sum(float v) {
 template <int L, int EPL, int MODE, bool RENORM, bool DAFF>
 __global__ void __launch_bounds__(kRouterThreads) router_bwd_kernel(RouterArgs p) {
   const int lane = threadIdx.x % L;
-  const int64_t t = int64_t(blockIdx.x) * (kRouterThreads / L) + threadIdx.x / L;
+  const int64_t t = p.t0 + int64_t(blockIdx.x) * (kRouterThreads / L) + threadIdx.x / L;
   if (t >= p.T) return;   // whole segments leave together, so the butterflies stay in step
   const int E = int(p.E), K = int(p.K);
   const int32_t* idx = p.idx + t * K;
@@ -157,17 +157,19 @@ static void router_go(const RouterArgs& p, unsigned grid, hipStream_t st) {
 }
 
 template <int L, int EPL>
-static void router_mode(const RouterArgs& p, hipStream_t st) {
-  const int64_t rows_per_wg = kRouterThreads / L;
-  const unsigned grid = unsigned((p.T + rows_per_wg - 1) / rows_per_wg);
-  if (p.mode == kRouterSoftmaxOverTopk) router_go<L, EPL, kRouterSoftmaxOverTopk>(p, grid, st);
-  else if (p.mode == kRouterTopkOverSoftmax) router_go<L, EPL, kRouterTopkOverSoftmax>(p, grid, st);
-  else router_go<L, EPL, kRouterTopk>(p, grid, st);
+static void router_mode(RouterArgs p, hipStream_t st) {
+  constexpr int64_t rows_per_wg = kRouterThreads / L;
+  for (p.t0 = 0; p.t0 < p.T; p.t0 += kMaxGrid256 * rows_per_wg) {   // one launch for fewer than 2^24 workgroups
+    const int64_t wgs = (p.T - p.t0 + rows_per_wg - 1) / rows_per_wg;
+    const unsigned grid = unsigned(wgs < kMaxGrid256 ? wgs : kMaxGrid256);
+    if (p.mode == kRouterSoftmaxOverTopk) router_go<L, EPL, kRouterSoftmaxOverTopk>(p, grid, st);
+    else if (p.mode == kRouterTopkOverSoftmax) router_go<L, EPL, kRouterTopkOverSoftmax>(p, grid, st);
+    else router_go<L, EPL, kRouterTopk>(p, grid, st);
+  }
 }
 
 hipError_t launch_router_bwd(const RouterArgs& p, hipStream_t st) {
   if (p.T <= 0) return hipSuccess;
-  if ((p.T + 3) / 4 > int64_t(INT32_MAX)) return hipErrorInvalidValue;
   // L = E/8 rounded up to a power of two, kept in [8, 64]; EPL = columns per lane
   if (p.E <= 8) router_mode<8, 1>(p, st);
   else if (p.E <= 16) router_mode<8, 2>(p, st);

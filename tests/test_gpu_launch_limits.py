@@ -47,3 +47,18 @@ def test_finalisation_past_2_32_threads():
         torch.cuda.synchronize()
         for k, rows in (("dx", out["dx"][a:b]), ("daff", out["daff"][a:b])):
             assert torch.equal(part[k].view(torch.int16), rows.view(torch.int16)), (k, a)
+
+
+def test_router_backward_past_2_32_threads():
+    """8 lanes a token: 2^29 tokens and some.  Top-1 of one expert: d(logit) = d(score), 0 without a selection."""
+    T = 2 ** 29 + 1000
+    print("router backward", T, flush=True)
+    idx = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    idx[3::5] = -1
+    g = torch.empty(T, 1, device="cuda")
+    g.uniform_(1, 2)
+    out = torch.full((T, 1), torch.nan, device="cuda")
+    mx.moe_router_bwd(mx.ROUTER_TOPK, idx, dscores=g, num_experts=1, out=out)
+    torch.cuda.synchronize()
+    g[3::5] = 0
+    assert torch.equal(out, g)
