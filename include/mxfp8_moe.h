@@ -532,7 +532,7 @@ int moe_router_fwd(int mode, int64_t T, int64_t E, int64_t K, const void* logits
  *   T, E, K, S     tokens, experts, selections a token, sequences;
  *                  1 <= K <= min(E, 32), S >= 1.
  *   logits         [T,E] fp32 or bf16 (logits_type); arithmetic is fp32, the
- *                  losses' last sums fp64.
+ *                  squares of lse and the losses' last sums fp64.
  *   topk_idx       [T,K] int32 (forward only).
  *   token_mask     [T] bytes, or NULL.
  *   seq_starts     [S+1] int32 in device memory: sequence s is the tokens

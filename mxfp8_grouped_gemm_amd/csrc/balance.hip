@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(chunk_threads(EPL)) balance_chunk_kernel(Balan
   constexpr int IDS = (kRouterMaxK + L - 1) / L;   // ids of one lane, K <= 32
   __shared__ float lp[W][L * EPL];
   __shared__ int hist[L * EPL];
-  __shared__ float lz[W];
+  __shared__ double lz[W];
   __shared__ int ln[W];
   const int lane = threadIdx.x % L, slot = threadIdx.x / L, wave = threadIdx.x >> 6;
   const int E = int(p.E), K = int(p.K);
@@ -166,7 +166,9 @@ __global__ void __launch_bounds__(chunk_threads(EPL)) balance_chunk_kernel(Balan
   float acc[EPL];
 #pragma unroll
   for (int j = 0; j < EPL; ++j) acc[j] = 0.f;
-  float z2 = 0.f, n = 0.f;   // n: whole numbers, at most a chunk's tokens
+  // lse^2 in fp64: the square of a token whose logits are all the type's lowest value passes fp32
+  double z2 = 0.;
+  float n = 0.f;   // whole numbers, at most a chunk's tokens
   for (int e = threadIdx.x; e < E; e += THREADS) hist[e] = 0;
   SeqCursor q(p, ALL ? -1 : c0);
   __syncthreads();
@@ -182,9 +184,10 @@ __global__ void __launch_bounds__(chunk_threads(EPL)) balance_chunk_kernel(Balan
     z2 = seg::sum<64>(z2);
     n = seg::sum<64>(n);
     if ((threadIdx.x & 63) == 0) { lz[wave] = z2; ln[wave] = int(n); }
-    z2 = n = 0.f;
+    z2 = 0.;
+    n = 0.f;
     __syncthreads();
-    float zs = 0.f;
+    double zs = 0.;
     int ns = 0;
 #pragma unroll
     for (int w = 0; w < W; ++w) { zs += lz[w]; ns += ln[w]; }
@@ -238,7 +241,7 @@ __global__ void __launch_bounds__(chunk_threads(EPL)) balance_chunk_kernel(Balan
 #pragma unroll
         for (int j = 0; j < EPL; ++j) acc[j] += x[j];
         if (lane == 0) {
-          z2 += lse * lse;
+          z2 += double(lse) * double(lse);
           n += 1.f;
         }
 #pragma unroll
@@ -283,7 +286,8 @@ __device__ __forceinline__ T published(const T* p) {
 __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(BalanceArgs p) {
   constexpr int Q = kSumThreads / kTile, W = kSumThreads / 64;
   static_assert(kTile == 32, "two record groups a wave");
-  __shared__ float sp[W][kTile], sz[W];
+  __shared__ float sp[W][kTile];
+  __shared__ double sz[W];
   __shared__ int sc[W][kTile], sn[W];
   __shared__ bool last;
   const bool only = gridDim.x * gridDim.y == 1;
@@ -302,7 +306,7 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(BalanceArgs p)
     }
   }
   int n = 0;
-  float z = 0.f;
+  double z = 0.;
   for (int64_t k = f + tid; k <= l; k += kSumThreads) {
     n += p.part_n[k + s];
     z += p.part_z[k + s];
@@ -321,7 +325,8 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(BalanceArgs p)
   __syncthreads();
   if (tid < kTile) {
     n = 0;
-    z = v = 0.f;
+    z = 0.;
+    v = 0.f;
     c = 0;
 #pragma unroll
     for (int i = 0; i < W; ++i) {

@@ -154,10 +154,10 @@ struct BalanceArgs {
   int64_t chunk;              // tokens
   float* part_p;              // [chunks+S][E]
   int32_t* part_c;            // [chunks+S][E]
-  float* part_z;              // [chunks+S]
+  double* part_z;             // [chunks+S]
   int32_t* part_n;            // [chunks+S]
   double* term;               // [S][ceil(E/32)]
-  float* term_z;              // [S]
+  double* term_z;             // [S]
   unsigned* done;
 };
 int64_t balance_chunk_tokens(int64_t T, int64_t E, int64_t S);

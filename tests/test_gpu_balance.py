@@ -257,3 +257,23 @@ def test_two_streams_at_once():
         _check(*probs[i], (0.1, 0.1), None, outs[i][0], None)
         for o in outs[i][1:]:
             assert all(torch.equal(a, b) for a, b in zip(o, outs[i][0]))
+
+
+@pytest.mark.parametrize("T,E,S", [(100, 8, 1), (3000, 60, 7), (5000, 128, 1), (40, 700, 3)])
+def test_rows_at_the_lowest_value(T, E, S):
+    """Tokens whose logits are all the type's lowest value (a mask put in by hand): their
+    lse^2, 1.2e77, passes fp32.  Without a z loss its value is 0, with a coefficient that
+    brings the mean back into range the mean itself; probabilities stay uniform."""
+    z, idx, mask, seq = _problem(T, E, 3, S, torch.float32, 3 * T, closed=0)
+    for value, zc in ((torch.finfo(torch.float32).min, 0.0), (-1e20, 0.002), (-1e25, 2.0 ** -50)):
+        z[::7] = value
+        kw = dict(token_mask=_dev(mask), seq_starts=_dev(seq))
+        got = mx.moe_balance_loss(_dev(z), _dev(idx), 0.02, zc, **kw)
+        d = mx.moe_balance_loss_bwd(_dev(z), got[1], got[2], 3, 0.02, zc, **kw)
+        _check(z, idx, mask, seq, (0.02, zc), None, got, d)
+        assert torch.isfinite(got[0]).all() and torch.isfinite(d).all()
+    assert 1e30 < got[0][1]
+    low = z.to(torch.bfloat16)
+    low[::7] = torch.finfo(torch.bfloat16).min
+    loss = mx.moe_balance_loss(_dev(low), _dev(idx), 0.02, **kw)[0].tolist()
+    assert loss[1] == 0 and 0 < loss[0] < 1
