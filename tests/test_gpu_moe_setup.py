@@ -150,3 +150,35 @@ def test_blocks_of_padding_change_nothing(name, act8):
             for k in ("db1", "db2"):
                 a, b = small[k].float(), padded[k].float()
                 assert ((a - b).abs() <= 2.0 ** -6 * b.abs() + 2.0 ** -19 * b.abs().max()).all(), k
+
+
+@pytest.mark.parametrize("H,I,B,E,N,beside", [(128, 256, 128, 4, None, True), (256, 512, 512, 3, None, True),
+                                              (2048, 256, 128, 5, 30, False), (128, 96, 1024, 2, 31, True),
+                                              (128, 64, 128, 257, None, False)])
+def test_tile_ranges_of_layers_too_small_to_fuse(H, I, B, E, N, beside):
+    """H % 128 == 0, H <= 2048 and I <= 512 with fewer than 256 Phase-1 tiles: Phase 1 runs
+    apart, on ranges made beside the gathers (up to 256 of their tiles, blocks and
+    experts) or by the set-up's own kernel."""
+    T = 300 if E > 256 else 900
+    cfg = S.scaled(S.TINY, T=T, H=H, I=I, E=E, K=1 if E > 256 else 2, B=B)
+    print("ranges", H, I, B, E, N, flush=True)
+    gp = gpu_problem(cfg, N=N)
+    N = gp["N"]
+    tiles1 = -(-I // 128) * -(-B // 128) * N
+    assert (H // 128 * N * B // 128 <= 256 and E <= 256) == beside and N <= 1024
+    op = _bound(gp, gp["tpid"], gp["b2e"])
+    L = op.layout
+    if E <= 256:
+        assert tiles1 < 256 and L["phase1_ds"] < L["phase1_tiles"] < L["phase3_tiles"]
+    op.workspace.fill_(0x77)
+    op.run()
+    torch.cuda.synchronize()
+    ws = op.workspace.cpu().numpy()
+    i32 = lambda name, n: ws[L[name]:L[name] + 4 * n].view(np.int32)
+    ext = i32("block_flag", N).astype(np.int64)
+    if tiles1 < 256:
+        want = _ranges(ext, 128, -(-I // 128), False, B)
+        assert np.array_equal(i32("phase1_tiles", len(want)), want)
+    wide = 2 * I % 128 == 0 and 2 * I >= 1024 and B >= 256 and H >= 256
+    want = _ranges(ext, 256 if wide else 128, -(-H // 256), False, B)
+    assert np.array_equal(i32("phase3_tiles", len(want)), want)
