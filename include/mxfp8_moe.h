@@ -316,7 +316,12 @@ typedef struct {
    * bytes a gate/up pair instead of 4.  The backward works on the values they
    * stand for: the same results as with a bf16 checkpoint holding those values.
    * Padding slots' codes, and the scales of groups of padding alone, are
-   * ignored.  Not together with the [N,I,B] checkpoints above (UNSUPPORTED). */
+   * ignored.  Not together with the [N,I,B] checkpoints above (UNSUPPORTED).
+   * It saves memory first: the epilogue reads fewer bytes but decodes, so it is
+   * faster where it is bound by them (H = 4096, I = 14336: 7%) and slower where
+   * by its arithmetic (H = 2048, I = 1408: 3%; the whole backward within 1% of
+   * bf16 on both), and E5M2 takes the separate kernels where E4M3 and bf16 run
+   * Phase 1 with its epilogue in one (see phase1_ds; 2% of the backward).       */
   const uint8_t* gate_up_checkpoint_codes;
   const uint8_t* gate_up_checkpoint_scales;
   int fmt_checkpoint;   /* MXFP8_E4M3 or MXFP8_E5M2; read with gate_up_checkpoint_codes only */
@@ -385,7 +390,9 @@ typedef struct {
       expert_block_list, slot_token, slot_affinity, block_flag, total;
 } moe_bwd_mxfp8_workspace_layout;
 
-/* Host.  Fills *layout for the shapes in *args (pointers are not read).
+/* Host.  Fills *layout for the shapes in *args.  No pointer is followed, but which
+ * optional checkpoints are given (not NULL), fmt_checkpoint and has_bias shape it:
+ * query with the arguments of the call.
  * Returns MXFP8_OK or INVALID_ARG. */
 int moe_bwd_mxfp8_workspace_query(const moe_bwd_mxfp8_args* args,
                                   moe_bwd_mxfp8_workspace_layout* layout);
@@ -463,7 +470,10 @@ int moe_bwd_mxfp8_stage(const moe_bwd_mxfp8_args* args, void* workspace, size_t 
  *                read at the selected experts: exactly one of the two.
  *   renorm       0 or 1; non-zero only with MXFP8_ROUTER_TOPK_OVER_SOFTMAX.
  *   dlogits      [T,E] fp32 output, every entry written.
- * A row whose entries are all outside [0,E) gets zeros, whatever its logits hold.
+ * A row whose entries are all outside [0,E) gets zeros, whatever its logits hold;
+ * in any other row of MXFP8_ROUTER_TOPK_OVER_SOFTMAX a NaN among the logits makes the
+ * gradient NaN, also where moe_router_fwd took it for a closed expert (-inf closes
+ * one without that).
  * Arithmetic is fp32 (exp through the device math library).
  * Errors: INVALID_ARG for an unknown mode, a shape outside the bounds above,
  * renorm with another mode, both or neither of dscores/daff, a NULL pointer
@@ -491,9 +501,10 @@ int moe_router_bwd(int mode, int64_t T, int64_t E, int64_t K, const int32_t* top
  *   and moe_router_bwd) and score 0.
  *   Scores: MXFP8_ROUTER_SOFTMAX_OVER_TOPK  softmax over the selected logits;
  *     MXFP8_ROUTER_TOPK_OVER_SOFTMAX  the softmax over all E logits at the
- *     selected ones, divided by their sum with renorm; MXFP8_ROUTER_TOPK  the
- *     logits themselves.  A logit of +inf, or a NaN where the softmax is over
- *     all E logits, makes its token's scores NaN.
+ *     selected ones, divided by their sum with renorm (in which the sum over all
+ *     E cancels: computed over the selection); MXFP8_ROUTER_TOPK  the
+ *     logits themselves.  A logit of +inf makes its token's softmax scores NaN, a
+ *     closed NaN those of the softmax over all E logits without renorm.
  * Arguments:
  *   T, E, K      tokens, experts, selections; 1 <= K <= min(E, 32), E <= 4096.
  *   logits       [T,E] fp32 or bf16 (logits_type); arithmetic is fp32.
@@ -595,7 +606,12 @@ int moe_balance_loss_bwd(const moe_balance_args* args, void* stream);
  *   backward: with g, u the values of codes and scales and d = dinter
  *             [rows, cols] bf16:  dgate_up[r,0,c] = d u act'(g),
  *             dgate_up[r,1,c] = d act(g), each rounded once to bf16.
- * activation: MXFP8_ACT_SWIGLU or MXFP8_ACT_GEGLU (as in moe_bwd_mxfp8).
+ * activation: MXFP8_ACT_SWIGLU or MXFP8_ACT_GEGLU, the functions of moe_bwd_mxfp8.
+ * Both are evaluated in fp32, here and there, but GeGLU's normal CDF by another
+ * method: a fitted polynomial here (within 2e-6 of the value for |g| < 4, 8e-6 in
+ * the tail at g = -13), the device library's erfc there.  bf16 roundings of the two
+ * may then fall on neighbours where a value lies on a border.  SiLU of a gate below
+ * -87.3 is taken as 0 in both (its value is under 2^-119).
  * A dense FFN's gate/up product is rows = tokens, cols = I.  The MoE layer's
  * gate_up_proj_act_checkpoint_T [N,2,I,B] is rows = N, cols = I * B, whose
  * groups of 32 are then 32 consecutive slots, and the codes and scales are

@@ -297,7 +297,8 @@ hipError_t launch_phase1_epi(const Phase1Args& p, int fmt_grad, hipStream_t st);
 // Phase 1 and its epilogue in one kernel, where phase1_fusable: the same outputs
 // as launch_phase1 followed by launch_phase1_epi, without dS in HBM
 bool phase1_fusable(const Phase1Args& p);
-// the part of its rule that concerns the sizes (moe_phase1_128.hip)
+// the part of its rule that concerns the sizes (moe_phase1_128.hip).  256 tiles on any
+// device: the workspace's layout follows the rule and must not depend on the device's CUs.
 inline bool phase1_fuses_sizes(int64_t H, int64_t I, int64_t N, int64_t B) {
   return H % 128 == 0 && H <= 2048 && I <= 512 && ((I + 127) / 128) * ((B + 127) / 128) * N >= 256;
 }

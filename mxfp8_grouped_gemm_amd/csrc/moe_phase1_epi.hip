@@ -1,7 +1,7 @@
 // moe_phase1_epi.hip -- the stand-alone Phase-1 epilogue kernel: the SwiGLU (or
 // GeGLU) backward on the product dS that Phase 1 left in HBM (the arithmetic is
-// in moe_phase1_epi.hpp).  Taken where the fused Phase-1 kernel is not: caller
-// checkpoints, H not a multiple of 128.
+// in moe_phase1_epi.hpp).  Taken where the fused Phase-1 kernel is not
+// (phase1_fusable): other sizes, few tiles, [N,I,B] checkpoints, an E5M2 checkpoint.
 #include "moe_phase1_epi.hpp"
 
 namespace mx {

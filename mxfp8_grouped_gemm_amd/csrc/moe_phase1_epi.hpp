@@ -147,8 +147,8 @@ typedef unsigned short epi_us2 __attribute__((ext_vector_type(2)));
 // the two scale bytes of row i0 + l % 32 for the group its own slot is in, and
 // row k's reach its 32 lanes by one swizzle.  v_cvt_scalef32_f32_fp8 / _bf8
 // multiply a code by the power of two whose E8M0 byte is the exponent field of
-// their scale operand and ignore the other bits (byte 0 is 2^-127; checked for
-// every code and scale), so the word gate << 23 | up is the gate's operand as
+// their scale operand and ignore the other bits (byte 0 is 2^-127; a GPU test holds
+// every code at every scale byte from 0 to 254), so the word gate << 23 | up is the gate's operand as
 // it stands, and shifted by 23 the up's: 4 instructions a row, one more than the
 // bf16 checkpoint's unpacking.  A code times its scale is exact in fp32, and is
 // the value a bf16 checkpoint of the dequantised tensor holds: the two

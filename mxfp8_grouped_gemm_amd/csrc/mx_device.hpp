@@ -197,7 +197,9 @@ __device__ __forceinline__ uint32_t encode_bf16x4(uint32_t p01, uint32_t p23, fl
 // A wave that has called this (the FP16_OVFL bit of its mode register, which
 // also governs the fp8 conversions) gets saturation from the converters
 // themselves: encode_bf16x4 then needs no clamped inputs.  Checked on the GPU
-// like the above: every bf16 pattern x every scale the group rule can produce.
+// like the above, every bf16 pattern x every scale the group rule can produce; GPU
+// tests hold the epilogue's codes to the definition for every pattern in groups at its
+// own scale, and for groups past the largest value at scales across the range.
 __device__ __forceinline__ void saturate_fp8_conversions() {
 #if defined(__HIP_DEVICE_COMPILE__)
   __builtin_amdgcn_s_setreg(1 | 23 << 6, 1);   // hwreg(MODE, bit 23, 1 bit)

@@ -19,8 +19,12 @@ namespace rows {
 // result (results under 2^-126 may be 0).
 __device__ __forceinline__ float exp_fast(float d) { return __builtin_amdgcn_exp2f(d * 1.4426950408889634f); }
 
-// log(s) through v_log_f32, 1 / s through v_rcp_f32: within about an ulp, s in [1, 4096]
+// log(s) through v_log_f32, for sums of exponentials (s in [1, 4096]): v_log_f32 is
+// within about an ulp, and so is the product
 __device__ __forceinline__ float log_fast(float s) { return __builtin_amdgcn_logf(s) * 0.6931471805599453f; }
+// 1 / s through v_rcp_f32, within about an ulp of any s whose reciprocal is a normal
+// number: sums of exponentials, and balance.hip's counts (tokens, sequences times
+// selections: whole numbers up to 2^31, rounded to fp32)
 __device__ __forceinline__ float rcp_fast(float s) { return __builtin_amdgcn_rcpf(s); }
 
 __device__ __forceinline__ float value(float v) { return v; }
