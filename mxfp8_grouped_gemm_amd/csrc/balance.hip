@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(chunk_threads(EPL)) balance_chunk_kernel(Balan
       acc[j] = 0.f;
       if ((threadIdx.x & 63) < L) lp[wave][rows::column<L>(lane, j)] = v;
     }
-    z2 = seg::sum<64>(z2);
+    z2 = seg::across<L>(z2);   // the rows' first lanes hold it
     n = seg::sum<64>(n);
     if ((threadIdx.x & 63) == 0) { lz[wave] = z2; ln[wave] = int(n); }
     z2 = 0.;

@@ -43,25 +43,6 @@ __device__ __forceinline__ float sum(float v) {
     return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
   }));
 }
-// the two words of a double move the same way
-template <int L>
-__device__ __forceinline__ double sum(double v) {
-  static_assert(L >= 1 && L <= 64 && (L & (L - 1)) == 0, "a power of two");
-#if defined(__HIP_DEVICE_COMPILE__)
-  auto add = [&](auto move) { v += __hiloint2double(int(move(__double2hiint(v))), int(move(__double2loint(v)))); };
-  if constexpr (L > 1) add([](int x) { return dpp<kXor1>(x); });
-  if constexpr (L > 2) add([](int x) { return dpp<kXor2>(x); });
-  if constexpr (L > 4) add([](int x) { return dpp<kHalfMirror>(x); });
-  if constexpr (L > 8) add([](int x) { return dpp<kMirror>(x); });
-  auto swap = [&](auto rows) {
-    const auto hi = rows(__double2hiint(v)), lo = rows(__double2loint(v));
-    v = __hiloint2double(int(hi[0]), int(lo[0])) + __hiloint2double(int(hi[1]), int(lo[1]));
-  };
-  if constexpr (L > 16) swap([](int x) { return __builtin_amdgcn_permlane16_swap(x, x, false, false); });
-  if constexpr (L > 32) swap([](int x) { return __builtin_amdgcn_permlane32_swap(x, x, false, false); });
-#endif
-  return v;
-}
 template <int L>
 __device__ __forceinline__ float max(float v) {   // NaN only where every value is NaN
   return __uint_as_float(reduce<L>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
@@ -98,6 +79,24 @@ __device__ __forceinline__ float across(float v) {
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
     v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
   }
+#endif
+  return v;
+}
+// the two words of a double move the same way
+template <int L>
+__device__ __forceinline__ double across(double v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  auto add = [&](auto move) { v += __hiloint2double(int(move(__double2hiint(v))), int(move(__double2loint(v)))); };
+  if constexpr (L <= 1) add([](int x) { return dpp<kXor1>(x); });
+  if constexpr (L <= 2) add([](int x) { return dpp<kXor2>(x); });
+  if constexpr (L <= 8) add([](int x) { return dpp<kRor8>(x); });
+  if constexpr (L <= 4) add([](int x) { return dpp<kRor4>(x); });
+  auto swap = [&](auto rows) {
+    const auto hi = rows(__double2hiint(v)), lo = rows(__double2loint(v));
+    v = __hiloint2double(int(hi[0]), int(lo[0])) + __hiloint2double(int(hi[1]), int(lo[1]));
+  };
+  if constexpr (L <= 16) swap([](int x) { return __builtin_amdgcn_permlane16_swap(x, x, false, false); });
+  if constexpr (L <= 32) swap([](int x) { return __builtin_amdgcn_permlane32_swap(x, x, false, false); });
 #endif
   return v;
 }
