@@ -22,10 +22,10 @@
 // atomics, the same bits on every run.
 // HBM-bound by its bytes: E logits and K ids a token; backward E logits read, E
 // gradients written (rows in registers, router_rows.hpp).  T = 32768, E = 128,
-// K = 8, 16 sequences: chunks 8.7 us (17.8 MB), sums 6.8 us (latency: records,
-// one atomic, the last workgroup's terms), gradient 9.8 us (33.6 MB, 3.4 TB/s;
+// K = 8, 16 sequences: chunks 8.4 us (17.8 MB), sums 7.2 us (latency: records,
+// one atomic, the last workgroup's terms), gradient 9.2 us (33.6 MB, 3.7 TB/s;
 // an elementwise pass over as many bytes takes 6.4 us).  T = 16384, E = 8: 5.7
-// and 3.1 us (one workgroup, which needs no one else's terms), all of it latency.
+// and 3.7 us (one workgroup, which needs no one else's terms), all of it latency.
 #include "kernels.hpp"
 #include "router_rows.hpp"
 
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(kBwdThreads) balance_bwd_kernel(BalanceArgs p)
 // kChunks chunks; fewer where several sequences would fall into one chunk, as
 // each costs its workgroup about 1.5 us of reduction: a sequence's mean length,
 // but no less than 4 tokens and no more than 2 kChunks chunks (1000 tokens of 8
-// experts in 64 sequences: 60 -> 18 us).
+// experts in 64 sequences: 60 -> 14 us).
 int64_t balance_chunk_tokens(int64_t T, int64_t E, int64_t S) {
   const int64_t r = chunk_threads(E > 512 ? 16 : 8) / rows::lanes(E);
   const int64_t c = (T + kChunks - 1) / kChunks;
