@@ -640,6 +640,128 @@ int mxfp8_gated_act_fwd(const mxfp8_gated_act_args* args, const uint16_t* gate_u
 int mxfp8_gated_act_bwd(const mxfp8_gated_act_args* args, const uint16_t* dinter, const uint8_t* codes,
                         const uint8_t* scales, uint16_t* dgate_up, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * mxfp8_quantize_transposed -- a batch of matrices quantised along their rows'
+ * axis, written with that axis contiguous (what a product contracting over it
+ * reads), one pass:
+ *   x      [batch, rows, cols] bf16; groups of 32 along rows (rows % 32 == 0).
+ *   codes  [batch, cols, rows] u8, scales [batch, cols, rows/32] E8M0 bytes.
+ * The MoE layer's weights for moe_fwd_mxfp8: gate/up [E,H,2,I] as [E, H, 2I]
+ * gives [E,2,I,H], down [E,I,H] gives [E,H,I].  An empty x is not an error.
+ * Errors: INVALID_ARG for a negative size, rows % 32 != 0, a bad fmt, a NULL
+ * pointer, or x / codes not 16-byte aligned; UNSUPPORTED for more than 2^24 - 1
+ * tiles of 128 x 128; HIP if the launch fails. */
+int mxfp8_quantize_transposed(const uint16_t* x, int64_t batch, int64_t rows, int64_t cols, int fmt, uint8_t* codes,
+                              uint8_t* scales, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * dropout_add_fwd / dropout_add_bwd -- dropout whose mask is never stored:
+ *   forward:  y[r,c] = residual[r,c] + (keep(r * cols + c) ? scale * x[r,c] : 0)
+ *   backward: y[r,c] = keep(r * cols + c) ? scale * x[r,c] : 0, x the gradient
+ *             of the forward's y (the residual's gradient is that gradient)
+ * computed in fp32 and rounded once.  n = round(65536 p) and scale = 65536 /
+ * (65536 - n): the probability that is applied is n / 65536, and the expectation
+ * is kept for it.  keep(i): 16 bits of Philox4x32-10 (Salmon, Moraes, Dror,
+ * Shaw, "Parallel random numbers: as easy as 1, 2, 3", 2011) are at least n: half
+ * i % 2 (0: the low one) of output word (i % 8) / 2 at counter words (i / 8 low,
+ * high, offset low, high), key words (seed low, high).  So a mask depends on seed,
+ * offset and element alone, not on type, strides or launch.  A dropped element
+ * gives 0 whatever it holds.
+ *   rng    [2] int64 in device memory: seed, offset (read when the kernel runs,
+ *          so a captured call takes what they hold at each replay); may be NULL
+ *          where n == 0.  A program moves the offset on by one per mask.
+ *   ldx, ldr, ldy: elements from a row to the next (>= cols).  residual may be
+ *          NULL (and must be in the backward).  y may be x or residual, with the
+ *          same leading dimension; other overlaps give unspecified results.
+ *   type   MXFP8_TYPE_F32 or MXFP8_TYPE_BF16, of all three tensors.
+ * An empty tensor is not an error.
+ * Errors: INVALID_ARG for a negative size, an unknown type, p outside [0, 1] or
+ * NaN, a leading dimension below cols (or rows beyond 2^40 elements), a NULL pointer,
+ * a residual in the backward, or a tensor not 16-byte (rng: 8-byte) aligned;
+ * UNSUPPORTED for rows * cols above 2^34; HIP if the launch fails. */
+typedef struct {
+  int64_t rows, cols;
+  int64_t ldx, ldr, ldy;
+  int type;
+  double p;
+  const int64_t* rng;
+  const void* x;
+  const void* residual;
+  void* y;
+} dropout_add_args;
+int dropout_add_fwd(const dropout_add_args* args, void* stream);
+int dropout_add_bwd(const dropout_add_args* args, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_fwd_mxfp8 -- the forward of the MoE layer whose backward is moe_bwd_mxfp8:
+ * the routed gated feed-forward block.  With Q = MXFP8 E4M3, for every slot p of
+ * block b that holds token t, e = block_to_expert[b], a the affinity of (t, e):
+ *   g = Q(x_t) Wg[e]^T + b1[e][0],  u = Q(x_t) Wu[e]^T + b1[e][1]   (groups along H)
+ *   s = act(g) u, times a with the affinity on I
+ *   y_t = residual_t + drop( sum over t's slots, by ascending expert, of
+ *         a (Q(s) Wd[e]^T + b2[e]) )   (groups along I; without a, on I)
+ * Products and sums are fp32 (on the scaled fp8 MFMA), g and u are not rounded
+ * before s, and y is rounded once.  A token without a slot gets its residual, or 0.
+ * E = 1 with every token in a slot is a dense gated FFN.
+ * Arguments (moe_fwd_mxfp8_args; [T], [N], ... and the block lists as for
+ * moe_bwd_mxfp8):
+ *   hidden_states [T,H] bf16; expert_affinities_masked [T*E] fp32.
+ *   gate_up_codes [E,2,I,H] E4M3, gate_up_scales [E,2,I,H/32]: the weights
+ *       quantised along H; down_codes [E,H,I], down_scales [E,H,I/32]: along I
+ *       (mxfp8_quantize_transposed writes both from the layer's weights; the
+ *       backward contracts over other axes and has its own).
+ *   gate_up_proj_bias [E,2,I] bf16, down_proj_bias [E,H] bf16: either may be NULL.
+ *   num_valid_tokens: as for moe_bwd_mxfp8 (NULL: T); tokens from there on are
+ *       in no slot.
+ *   affinity_on 0 (H) or 1 (I, without biases); activation: the functions of
+ *       mxfp8_gated_act_fwd.
+ *   output_hidden_states [T,H] bf16: y.  It may be `residual`, but no other input.
+ *   The checkpoint for the backward, one of the two or neither (NULL):
+ *     gate_up_proj_act_checkpoint_T [N,2,I,B] bf16: g and u, rounded;
+ *     gate_up_checkpoint_codes [N,2,I,B] / _scales [N,2,I,B/32], format
+ *       fmt_checkpoint: the same quantised, groups of 32 along the slots.
+ *     Every element is written; slots without a token hold 0.
+ *   residual [T,H] bf16 or NULL.  dropout_p, dropout_rng: drop(v) is
+ *     dropout_add_fwd's rule over the [T,H] elements (0 and NULL: none); its
+ *     backward is dropout_add_bwd on y's gradient.
+ * Workspace: moe_fwd_mxfp8_workspace_size(args) bytes (0 on invalid shapes),
+ * 256-byte aligned; nothing in it outlives the call.  Only sizes shape it.
+ * Sums run in an order that the sizes and the block lists give: the results are
+ * the same bits on every run.  Device-side preconditions as for moe_bwd_mxfp8.
+ * Non-finite values: a group of X or s holding one has unspecified codes, and the
+ * token's row of y is unspecified; other tokens' are not affected.
+ * Errors: INVALID_ARG (shapes, null required pointers, alignment, formats, both
+ * checkpoints or half of one, dropout_p outside [0, 1], affinity_on or activation
+ * outside {0,1}), UNSUPPORTED (block_size outside the set, a bias with the affinity
+ * on I, sizes beyond 32-bit indexing: T * E, T * H, 2 * H * I or N * B * I / 32 above
+ * 2^31 - 1, N * B above 2^24, I above 2^22, or more tiles than one launch takes),
+ * WORKSPACE, HIP. */
+typedef struct {
+  int64_t T, H, I, E, N, block_size;
+  const uint16_t* hidden_states;
+  const float* expert_affinities_masked;
+  const uint8_t* gate_up_codes;
+  const uint8_t* gate_up_scales;
+  const uint8_t* down_codes;
+  const uint8_t* down_scales;
+  const int32_t* token_position_to_id;
+  const int32_t* block_to_expert;
+  const uint16_t* gate_up_proj_bias;
+  const uint16_t* down_proj_bias;
+  const int32_t* num_valid_tokens;
+  int affinity_on, activation;
+  uint16_t* output_hidden_states;
+  uint16_t* gate_up_proj_act_checkpoint_T;
+  uint8_t* gate_up_checkpoint_codes;
+  uint8_t* gate_up_checkpoint_scales;
+  int fmt_checkpoint;
+  const uint16_t* residual;
+  double dropout_p;
+  const int64_t* dropout_rng;
+} moe_fwd_mxfp8_args;
+size_t moe_fwd_mxfp8_workspace_size(const moe_fwd_mxfp8_args* args);
+int moe_fwd_mxfp8(const moe_fwd_mxfp8_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -89,6 +89,22 @@ class GatedActArgs(C.Structure):
                 ("token_position_to_id", _p), ("period", _i64), ("T", _i64)]
 
 
+class DropoutAddArgs(C.Structure):
+    _fields_ = [("rows", _i64), ("cols", _i64), ("ldx", _i64), ("ldr", _i64), ("ldy", _i64), ("type", C.c_int),
+                ("p", C.c_double), ("rng", _p), ("x", _p), ("residual", _p), ("y", _p)]
+
+
+class MoeFwdArgs(C.Structure):
+    _fields_ = [("T", _i64), ("H", _i64), ("I", _i64), ("E", _i64), ("N", _i64), ("block_size", _i64),
+                ("hidden_states", _p), ("expert_affinities_masked", _p), ("gate_up_codes", _p),
+                ("gate_up_scales", _p), ("down_codes", _p), ("down_scales", _p), ("token_position_to_id", _p),
+                ("block_to_expert", _p), ("gate_up_proj_bias", _p), ("down_proj_bias", _p), ("num_valid_tokens", _p),
+                ("affinity_on", C.c_int), ("activation", C.c_int), ("output_hidden_states", _p),
+                ("gate_up_proj_act_checkpoint_T", _p), ("gate_up_checkpoint_codes", _p),
+                ("gate_up_checkpoint_scales", _p), ("fmt_checkpoint", C.c_int), ("residual", _p),
+                ("dropout_p", C.c_double), ("dropout_rng", _p)]
+
+
 def _declare(L):
     L.mxfp8_last_error.restype = C.c_char_p
     L.mxfp8_version.restype = C.c_char_p
@@ -117,6 +133,11 @@ def _declare(L):
         ("moe_balance_loss_bwd", C.c_int, [C.POINTER(BalanceArgs), _p]),
         ("mxfp8_gated_act_fwd", C.c_int, [C.POINTER(GatedActArgs), _p, _p, _p, _p, _p]),
         ("mxfp8_gated_act_bwd", C.c_int, [C.POINTER(GatedActArgs), _p, _p, _p, _p, _p]),
+        ("mxfp8_quantize_transposed", C.c_int, [_p, _i64, _i64, _i64, C.c_int, _p, _p, _p]),
+        ("dropout_add_fwd", C.c_int, [C.POINTER(DropoutAddArgs), _p]),
+        ("dropout_add_bwd", C.c_int, [C.POINTER(DropoutAddArgs), _p]),
+        ("moe_fwd_mxfp8_workspace_size", C.c_size_t, [C.POINTER(MoeFwdArgs)]),
+        ("moe_fwd_mxfp8", C.c_int, [C.POINTER(MoeFwdArgs), _p, C.c_size_t, _p]),
     ):
         if hasattr(L, name):
             f = getattr(L, name)
@@ -658,3 +679,162 @@ def mxfp8_gated_act_bwd(dinter: torch.Tensor, codes: torch.Tensor, scales: torch
         d = _tensor(out, torch.bfloat16, shape, dev, "out")
     _call(dev, "mxfp8_gated_act_bwd", C.byref(a), *ptrs, d)
     return out
+
+
+# ----------------------------------------------------------------------------- weights for the forward
+def mxfp8_quantize_transposed(x: torch.Tensor, fmt: int = E4M3, out=None):
+    """x [batch, rows, cols] (or [rows, cols]) bf16, quantised along rows and transposed (include/mxfp8_moe.h:
+    mxfp8_quantize_transposed) -> (codes uint8 [batch, cols, rows], scales uint8 [batch, cols, rows/32]).
+
+    moe_fwd_mxfp8's weights: w_gate_up [E, H, 2, I] as ``w.view(E, H, 2 * I)``, whose codes are [E, 2, I, H], and
+    w_down [E, I, H].  out: optional (codes, scales) to write into."""
+    if x.dim() not in (2, 3):
+        raise ValueError("mxfp8_quantize_transposed: x must be [batch, rows, cols] or [rows, cols]")
+    rows, cols = x.shape[-2:]
+    if rows % 32:
+        raise ValueError(f"mxfp8_quantize_transposed: rows must be a multiple of 32 (got {rows})")
+    dev = x.device
+    src = _dev(x, torch.bfloat16, "x")
+    cshape, sshape = (*x.shape[:-2], cols, rows), (*x.shape[:-2], cols, rows // 32)
+    if out is None:
+        codes, scales = out = _empty(cshape, dtype=torch.uint8, device=dev), _empty(sshape, dtype=torch.uint8, device=dev)
+        ptrs = codes.data_ptr(), scales.data_ptr()
+    else:
+        codes, scales = out
+        ptrs = _tensor(codes, torch.uint8, cshape, dev, "codes"), _tensor(scales, torch.uint8, sshape, dev, "scales")
+    _call(dev, "mxfp8_quantize_transposed", src, x.shape[0] if x.dim() == 3 else 1, rows, cols, fmt, *ptrs)
+    return out
+
+
+# ----------------------------------------------------------------------------- dropout
+def _rows_of(t: torch.Tensor, dtype, shape, device, name):
+    """(address, leading dimension) of a [rows, cols] tensor whose rows are contiguous."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a device tensor")
+    if t.device != device:
+        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
+    if t.dim() == 2 and t.shape[1] > 0 and t.shape[0] > 1:
+        if (t.stride(1) != 1 and t.shape[1] > 1) or t.stride(0) < t.shape[1]:
+            raise ValueError(f"{name}: rows must be contiguous and not overlap (strides {t.stride()})")
+        return t.data_ptr(), t.stride(0)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t.data_ptr(), t.shape[-1] if t.dim() else 1
+
+
+def _rng(rng: Optional[torch.Tensor], device, name):
+    return _tensor(rng, torch.int64, (2,), device, name)
+
+
+def _dropout(name, x, p, rng, residual, out):
+    dev, shape, dtype = x.device, x.shape, x.dtype
+    if dtype is torch.bfloat16:
+        typ = 1
+    elif dtype is torch.float32:
+        typ = 0
+    else:
+        raise TypeError(f"{name}: x must be float32 or bfloat16, got {dtype}")
+    xp, ldx = _rows_of(x, dtype, shape, dev, "x")
+    cols = shape[-1] if len(shape) else 1
+    rows = 1
+    for n in shape[:-1]:
+        rows *= n
+    rp, ldr = (None, cols) if residual is None else _rows_of(residual, dtype, shape, dev, "residual")
+    if out is None:
+        out = _empty(shape, dtype=dtype, device=dev)
+        yp, ldy = out.data_ptr(), cols
+    else:
+        yp, ldy = _rows_of(out, dtype, shape, dev, "out")
+    a = DropoutAddArgs(rows, cols, ldx, ldr, ldy, typ, p, _rng(rng, dev, "rng"), xp, rp, yp)
+    _call(dev, name, C.byref(a))
+    return out
+
+
+def dropout_add(x: torch.Tensor, p: float, rng: Optional[torch.Tensor], residual: Optional[torch.Tensor] = None,
+                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """residual + dropout(x) (include/mxfp8_moe.h: dropout_add_fwd); the mask is a function of rng and is not stored.
+
+    x [..., cols] fp32 or bf16, contiguous, or [rows, cols] with contiguous rows at any stride; residual and out
+    likewise, out may be either of them.  rng [2] int64 on the device: seed and offset (None where p rounds to 0)."""
+    return _dropout("dropout_add_fwd", x, p, rng, residual, out)
+
+
+def dropout_add_bwd(grad: torch.Tensor, p: float, rng: Optional[torch.Tensor],
+                    out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """x's gradient of dropout_add from its result's (include/mxfp8_moe.h: dropout_add_bwd), with the forward's p and
+    rng; the residual's gradient is `grad` itself."""
+    return _dropout("dropout_add_bwd", grad, p, rng, None, out)
+
+
+# ----------------------------------------------------------------------------- MoE forward
+class MoeFwd:
+    """One MoE forward problem bound to device tensors (include/mxfp8_moe.h: moe_fwd_mxfp8).
+
+    Allocates the outputs and the workspace once; ``run()`` enqueues the whole forward on the current stream and
+    returns dict(out=[T, H] bf16, checkpoint=None, the bf16 [N, 2, I, B] tensor, or (codes, scales)): MoeBwd's
+    ``gate_up_proj_act_checkpoint_T`` or ``gate_up_checkpoint``.  checkpoint: None, "bf16" or "mxfp8"."""
+
+    def __init__(self, hidden_states, expert_affinities_masked, gate_up_codes, gate_up_scales, down_codes, down_scales,
+                 token_position_to_id, block_to_expert, block_size, gate_up_bias=None, down_bias=None, affinity_on=0,
+                 activation=ACT_SWIGLU, checkpoint=None, fmt_checkpoint=E4M3, residual=None, dropout_p=0.0,
+                 dropout_rng=None, num_valid_tokens=None, workspace=None, out=None):
+        if hidden_states.dim() != 2 or gate_up_codes.dim() != 4:
+            raise ValueError("moe_fwd_mxfp8: hidden_states must be [T, H] and gate_up_codes [E, 2, I, H]")
+        T, H = hidden_states.shape
+        E, _, I, _ = gate_up_codes.shape
+        N, B = block_to_expert.numel(), block_size
+        dev = hidden_states.device
+        bf16, u8 = torch.bfloat16, torch.uint8
+        if checkpoint not in (None, "bf16", "mxfp8"):
+            raise ValueError(f"moe_fwd_mxfp8: checkpoint must be None, 'bf16' or 'mxfp8', got {checkpoint!r}")
+        x = _dev(hidden_states, bf16, "hidden_states")
+        ins = (_tensor(expert_affinities_masked.view(-1) if expert_affinities_masked.is_contiguous()
+                       else expert_affinities_masked, torch.float32, (T * E,), dev, "expert_affinities_masked"),
+               _tensor(gate_up_codes, u8, (E, 2, I, H), dev, "gate_up_codes"),
+               _tensor(gate_up_scales, u8, (E, 2, I, H // 32), dev, "gate_up_scales"),
+               _tensor(down_codes, u8, (E, H, I), dev, "down_codes"),
+               _tensor(down_scales, u8, (E, H, I // 32), dev, "down_scales"),
+               _tensor(token_position_to_id, torch.int32, (N * B,), dev, "token_position_to_id"),
+               _tensor(block_to_expert, torch.int32, block_to_expert.shape, dev, "block_to_expert"),
+               _tensor(gate_up_bias, bf16, (E, 2, I), dev, "gate_up_bias"),
+               _tensor(down_bias, bf16, (E, H), dev, "down_bias"),
+               _tensor(num_valid_tokens, torch.int32, (1,), dev, "num_valid_tokens"))
+        res, rng = _tensor(residual, bf16, (T, H), dev, "residual"), _rng(dropout_rng, dev, "dropout_rng")
+        self.args = MoeFwdArgs(T, H, I, E, N, B, x, *ins, affinity_on, activation)
+        a = self.args
+        a.fmt_checkpoint, a.residual, a.dropout_p, a.dropout_rng = fmt_checkpoint, res, dropout_p, rng
+        size = lib().moe_fwd_mxfp8_workspace_size(C.byref(a))
+        if not size:   # refused before anything is enqueued, with its status and reason
+            _check(lib().moe_fwd_mxfp8(C.byref(a), None, 0, None), "moe_fwd_mxfp8")
+        if workspace is None:
+            workspace = _empty(size, dtype=u8, device=dev)
+        else:
+            _tensor(workspace, u8, workspace.shape, dev, "workspace")
+        if out is None:
+            out = _empty((T, H), dtype=bf16, device=dev)
+        a.output_hidden_states = _tensor(out, bf16, (T, H), dev, "out")
+        ck = None
+        if checkpoint == "bf16":
+            ck = _empty((N, 2, I, B), dtype=bf16, device=dev)
+            a.gate_up_proj_act_checkpoint_T = ck.data_ptr()
+        elif checkpoint == "mxfp8":
+            ck = (_empty((N, 2, I, B), dtype=u8, device=dev), _empty((N, 2, I, B // 32), dtype=u8, device=dev))
+            a.gate_up_checkpoint_codes, a.gate_up_checkpoint_scales = ck[0].data_ptr(), ck[1].data_ptr()
+        self.out = dict(out=out, checkpoint=ck)
+        self.workspace, self.device = workspace, dev
+        self.keep = (hidden_states, expert_affinities_masked, gate_up_codes, gate_up_scales, down_codes, down_scales,
+                     token_position_to_id, block_to_expert, gate_up_bias, down_bias, residual, dropout_rng,
+                     num_valid_tokens)
+
+    def run(self):
+        _call(self.device, "moe_fwd_mxfp8", C.byref(self.args), self.workspace.data_ptr(), self.workspace.numel())
+        return self.out
+
+
+def moe_fwd_mxfp8(*args, **kw):
+    """Functional form: builds a MoeFwd and runs it once; returns its dict."""
+    return MoeFwd(*args, **kw).run()

@@ -22,7 +22,8 @@ FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Wall", "-Wno-
          "-I", os.path.join(ROOT, "include"), "-I", CSRC]
 SOURCES = ["api.cpp", "quantize.hip", "gemm_dense.hip", "moe_aux.hip", "moe_phase1_256.hip", "moe_phase1_256x128.hip",
            "moe_phase1_128.hip", "moe_phase1_epi.hip", "moe_phase3.hip", "moe_grads.hip", "router.hip", "prequant.hip",
-           "router_fwd.hip", "balance.hip", "gated_act.hip"]
+           "router_fwd.hip", "balance.hip", "gated_act.hip", "api_fwd.cpp", "dropout.hip", "quantize_t.hip", "moe_fwd.hip",
+           "moe_fwd_gate_up_256.hip", "moe_fwd_gate_up_256x128.hip", "moe_fwd_gate_up_generic.hip"]
 
 
 def _compile(src: str, verbose: bool) -> str:

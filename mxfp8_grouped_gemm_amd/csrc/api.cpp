@@ -11,11 +11,12 @@
 #include <string>
 
 #include "../../include/mxfp8_moe.h"
+#include "api_util.hpp"
 #include "kernels.hpp"
 
-namespace {
+namespace mx_api {
 
-thread_local std::string g_last_error;
+static thread_local std::string g_last_error;
 
 int fail(int code, const char* fmt, ...) {
   char buf[512];
@@ -37,10 +38,26 @@ int hip_status(hipError_t e, const char* what) {
   return ok();
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool valid_fmt(int f) { return f == MXFP8_E4M3 || f == MXFP8_E5M2; }
 
-}  // namespace
+int device_cus(hipStream_t st) {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> cache[kMaxDevices];
+  int device = -1;
+  if ((st ? hipStreamGetDevice(st, &device) : hipGetDevice(&device)) != hipSuccess || device < 0 ||
+      device >= kMaxDevices)
+    return 0;
+  int c = cache[device].load(std::memory_order_relaxed);
+  if (c <= 0) {
+    if (hipDeviceGetAttribute(&c, hipDeviceAttributeMultiprocessorCount, device) != hipSuccess || c <= 0) return 0;
+    cache[device].store(c, std::memory_order_relaxed);
+  }
+  return c;
+}
+
+}  // namespace mx_api
+
+using namespace mx_api;
 
 extern "C" {
 
@@ -63,8 +80,6 @@ int mxfp8_quantize(const uint16_t* x, int64_t rows, int64_t cols, int axis, int 
   if (axis == 1) return hip_status(mx::launch_quant_rows(x, rows, cols, fmt, codes, scales, st), "quant_rows");
   return hip_status(mx::launch_quant_cols(x, rows, cols, fmt, codes, scales, st), "quant_cols");
 }
-
-static size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 
 /* Dense workspace: four quantised operands, codes then scales, 256-aligned. */
 static void dense_regions(int64_t M, int64_t N, int64_t K, size_t off[8], size_t* total) {
@@ -379,26 +394,6 @@ static SideStream* side_stream(int device) {
   }
   return x.ok ? &x : nullptr;
 }
-// CUs of the device that `st` runs on (0 if unknown), looked up once per device.
-static int device_cus(hipStream_t st) {
-  constexpr int kMaxDevices = 64;
-  static std::atomic<int> cache[kMaxDevices];
-  int device = -1;
-  if ((st ? hipStreamGetDevice(st, &device) : hipGetDevice(&device)) != hipSuccess || device < 0 ||
-      device >= kMaxDevices)
-    return 0;
-  int c = cache[device].load(std::memory_order_relaxed);
-  if (c <= 0) {
-    if (hipDeviceGetAttribute(&c, hipDeviceAttributeMultiprocessorCount, device) != hipSuccess || c <= 0) return 0;
-    cache[device].store(c, std::memory_order_relaxed);
-  }
-  return c;
-}
-// An expert weight operand at least this large (8x one XCD's 4 MB L2) is shared
-// by all XCDs through the infinity cache: its GEMM hands tiles out round robin
-// (moe_tiles.hpp).
-constexpr int64_t kRoundRobinWeightBytes = int64_t(32) << 20;
-
 // The bias reductions ride on the gather of dY rows (one read of each row)
 // when H is a multiple of 128 and those rows are gathered, i.e. no a*dY
 // checkpoint replaces them, and dY is under 2 GiB (that gather then reads it

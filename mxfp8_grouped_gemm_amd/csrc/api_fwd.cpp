@@ -1,0 +1,239 @@
+// api_fwd.cpp -- the C ABI of the MoE forward, its few-token form, dropout and
+// the transposed quantiser (include/mxfp8_moe.h): argument validation,
+// workspace carving and the launch sequence on the caller's stream.
+#include <climits>
+#include <cmath>
+
+#include "../../include/mxfp8_moe.h"
+#include "api_util.hpp"
+#include "kernels.hpp"
+
+using namespace mx_api;
+
+// The rule of a dropout probability: false unless 0 <= p <= 1.
+static bool dropout_rule(double p, const int64_t* rng, mx::DropoutRule& r) {
+  if (!(p >= 0. && p <= 1.)) return false;
+  r.thr = uint32_t(std::floor(p * 65536. + 0.5));
+  r.scale = r.thr < 65536 ? float(65536. / (65536. - r.thr)) : 0.f;
+  r.rng = rng;
+  return true;
+}
+
+extern "C" {
+
+int mxfp8_quantize_transposed(const uint16_t* x, int64_t batch, int64_t rows, int64_t cols, int fmt, uint8_t* codes,
+                              uint8_t* scales, void* stream) {
+  const char* me = "mxfp8_quantize_transposed";
+  if (batch < 0 || rows < 0 || cols < 0) return fail(MXFP8_ERR_INVALID_ARG, "%s: negative shape", me);
+  if (!valid_fmt(fmt)) return fail(MXFP8_ERR_INVALID_ARG, "%s: fmt %d is not E4M3/E5M2", me, fmt);
+  if (rows % 32) return fail(MXFP8_ERR_INVALID_ARG, "%s: rows %% 32 != 0", me);
+  if (batch == 0 || rows == 0 || cols == 0) return ok();
+  if (!x || !codes || !scales) return fail(MXFP8_ERR_INVALID_ARG, "%s: null pointer", me);
+  if (!aligned16(x) || !aligned16(codes))
+    return fail(MXFP8_ERR_INVALID_ARG, "%s: x and codes must be 16-byte aligned", me);
+  if (mx::quantize_t_grid(batch, rows, cols) > mx::kMaxGrid256)
+    return fail(MXFP8_ERR_UNSUPPORTED, "%s: more than %lld tiles of 128 x 128", me, (long long)mx::kMaxGrid256);
+  return hip_status(mx::launch_quantize_t(x, batch, rows, cols, fmt, codes, scales, static_cast<hipStream_t>(stream)),
+                    me);
+}
+
+/* ---- dropout ------------------------------------------------------------- */
+
+static int dropout_run(const char* me, const dropout_add_args* a, bool backward, void* stream) {
+  if (!a) return fail(MXFP8_ERR_INVALID_ARG, "%s: null args", me);
+  if (a->rows < 0 || a->cols < 0) return fail(MXFP8_ERR_INVALID_ARG, "%s: negative shape", me);
+  if (a->type != MXFP8_TYPE_F32 && a->type != MXFP8_TYPE_BF16)
+    return fail(MXFP8_ERR_INVALID_ARG, "%s: type %d is not F32/BF16", me, a->type);
+  mx::DropoutArgs d{};
+  if (!dropout_rule(a->p, a->rng, d.rule))
+    return fail(MXFP8_ERR_INVALID_ARG, "%s: p must be in [0, 1] (got %g)", me, a->p);
+  if (backward && a->residual) return fail(MXFP8_ERR_INVALID_ARG, "%s: the backward takes no residual", me);
+  if (a->rows == 0 || a->cols == 0) return ok();
+  if (a->rows > (int64_t(1) << 34) / a->cols) return fail(MXFP8_ERR_UNSUPPORTED, "%s: rows * cols beyond 2^34", me);
+  const int64_t lds[3] = {a->ldx, a->ldy, a->residual ? a->ldr : a->cols};
+  for (int64_t ld : lds)
+    if (ld < a->cols || ld > (int64_t(1) << 40) / a->rows)
+      return fail(MXFP8_ERR_INVALID_ARG, "%s: a leading dimension is below cols or reaches past 2^40 elements", me);
+  if (!a->x || !a->y || (d.rule.thr && !a->rng)) return fail(MXFP8_ERR_INVALID_ARG, "%s: null pointer", me);
+  const void* al[3] = {a->x, a->residual, a->y};
+  for (const void* q : al)
+    if (!aligned16(q)) return fail(MXFP8_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", me);
+  if (reinterpret_cast<uintptr_t>(a->rng) & 7u) return fail(MXFP8_ERR_INVALID_ARG, "%s: rng must be 8-byte aligned", me);
+  d.x = a->x; d.residual = a->residual; d.y = a->y;
+  d.rows = a->rows; d.cols = a->cols;
+  d.ldx = a->ldx; d.ldr = a->residual ? a->ldr : a->cols; d.ldy = a->ldy;
+  d.bf16 = a->type == MXFP8_TYPE_BF16;
+  return hip_status(mx::launch_dropout(d, static_cast<hipStream_t>(stream)), me);
+}
+
+int dropout_add_fwd(const dropout_add_args* a, void* stream) { return dropout_run("dropout_add_fwd", a, false, stream); }
+int dropout_add_bwd(const dropout_add_args* a, void* stream) { return dropout_run("dropout_add_bwd", a, true, stream); }
+
+/* ---- MoE forward --------------------------------------------------------- */
+
+namespace {
+struct FwdLayout {
+  size_t x_codes, x_scales, wgu_pairs, wd_pairs, inter_codes, inter_scales, rows, parts, tiles1, tiles2, slot_of,
+      slot_tok, slot_aff, flag, total;
+};
+}  // namespace
+
+static void fwd_layout(const moe_fwd_mxfp8_args* a, FwdLayout* L) {
+  const int64_t T = a->T, H = a->H, I = a->I, E = a->E, N = a->N, B = a->block_size, P = N * B;
+  size_t o = 0;
+  auto put = [&](size_t& field, int64_t bytes) {
+    field = o;
+    o = up256(o + size_t(bytes));
+  };
+  put(L->x_codes, T * H);
+  put(L->x_scales, T * H / 32);
+  put(L->wgu_pairs, H % 128 == 0 ? E * 2 * I * (H / 32) : 0);
+  put(L->wd_pairs, I % 128 == 0 ? E * H * (I / 32) : 0);
+  put(L->inter_codes, P * I);
+  put(L->inter_scales, P * I / 32);
+  put(L->rows, P * H * 4);
+  mx::Phase3Args q{};
+  q.H = H; q.I = I / 2; q.N = N; q.B = B;
+  put(L->parts, mx::phase3_parts_bytes(q));
+  // tile starts [N+1], then the tile -> block map over every tile a block can have at the smallest tile
+  put(L->tiles1, (N + 1 + N * ((I + 63) / 64) * ((B + 127) / 128)) * 4);
+  put(L->tiles2, (N + 1 + N * ((B + 127) / 128) * ((H + 127) / 128)) * 4);
+  put(L->slot_of, T * E * 4);
+  put(L->slot_tok, P * 4);
+  put(L->slot_aff, P * 4);
+  put(L->flag, N * 4);
+  L->total = o;
+}
+
+static int fwd_check_shapes(const moe_fwd_mxfp8_args* a) {
+  const char* me = "moe_fwd_mxfp8";
+  if (!a) return fail(MXFP8_ERR_INVALID_ARG, "%s: null args", me);
+  const int64_t T = a->T, H = a->H, I = a->I, E = a->E, N = a->N, B = a->block_size;
+  if (T <= 0 || H <= 0 || I <= 0 || E <= 0 || N <= 0 || B <= 0)
+    return fail(MXFP8_ERR_INVALID_ARG, "%s: sizes must be positive", me);
+  if (H % 32 || I % 32)
+    return fail(MXFP8_ERR_INVALID_ARG, "%s: H and I must be multiples of 32 (got %lld, %lld)", me, (long long)H,
+                (long long)I);
+  if (B != 128 && B != 256 && B != 512 && B != 1024)
+    return fail(MXFP8_ERR_UNSUPPORTED, "%s: block_size %lld not in {128,256,512,1024}", me, (long long)B);
+  // X's code rows, an expert's weight rows and the slots' scales are read through one buffer each, at 32-bit offsets
+  if (N > INT32_MAX / B || T > INT32_MAX / E || T > INT32_MAX / H || I > INT32_MAX / 2 / H ||
+      N * B > (int64_t(1) << 24) || 2 * I > (int64_t(1) << 23) || N * B > INT32_MAX / (I / 32))
+    return fail(MXFP8_ERR_UNSUPPORTED, "%s: sizes beyond 32-bit indexing", me);
+  // one launch of each product and of the checkpoint's rows
+  if (N * ((I + 63) / 64) * (B / 128) > mx::kMaxGrid256 || N * ((H + 127) / 128) * (B / 128) > mx::kMaxGrid256 - 512 ||
+      N * ((2 * I + 15) / 16) > mx::kMaxGrid256 || T > mx::kMaxGrid256)
+    return fail(MXFP8_ERR_UNSUPPORTED, "%s: more tiles than one launch takes", me);
+  return MXFP8_OK;
+}
+
+size_t moe_fwd_mxfp8_workspace_size(const moe_fwd_mxfp8_args* a) {
+  if (fwd_check_shapes(a)) return 0;
+  FwdLayout L;
+  fwd_layout(a, &L);
+  return L.total;
+}
+
+int moe_fwd_mxfp8(const moe_fwd_mxfp8_args* a, void* ws, size_t ws_bytes, void* stream) {
+  const char* me = "moe_fwd_mxfp8";
+  int rc = fwd_check_shapes(a);
+  if (rc) return rc;
+  if (a->affinity_on != 0 && a->affinity_on != 1)
+    return fail(MXFP8_ERR_INVALID_ARG, "%s: affinity_on must be 0 (H) or 1 (I)", me);
+  if (a->activation != MXFP8_ACT_SWIGLU && a->activation != MXFP8_ACT_GEGLU)
+    return fail(MXFP8_ERR_INVALID_ARG, "%s: activation must be 0 (SwiGLU) or 1 (GeGLU)", me);
+  if (a->affinity_on == 1 && (a->gate_up_proj_bias || a->down_proj_bias))
+    return fail(MXFP8_ERR_UNSUPPORTED, "%s: a bias with the affinity on I is not supported", me);
+  mx::DropoutRule drop{};
+  if (!dropout_rule(a->dropout_p, a->dropout_rng, drop))
+    return fail(MXFP8_ERR_INVALID_ARG, "%s: dropout_p must be in [0, 1] (got %g)", me, a->dropout_p);
+  const void* req[] = {a->hidden_states, a->expert_affinities_masked, a->gate_up_codes, a->gate_up_scales,
+                       a->down_codes, a->down_scales, a->token_position_to_id, a->block_to_expert,
+                       a->output_hidden_states};
+  for (const void* q : req)
+    if (!q) return fail(MXFP8_ERR_INVALID_ARG, "%s: a required pointer is null", me);
+  if (drop.thr && !a->dropout_rng) return fail(MXFP8_ERR_INVALID_ARG, "%s: dropout needs dropout_rng", me);
+  const void* opt[] = {a->gate_up_proj_bias, a->down_proj_bias, a->gate_up_proj_act_checkpoint_T,
+                       a->gate_up_checkpoint_codes, a->gate_up_checkpoint_scales, a->residual};
+  for (const void* q : req)
+    if (!aligned16(q)) return fail(MXFP8_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", me);
+  for (const void* q : opt)
+    if (!aligned16(q)) return fail(MXFP8_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", me);
+  if (!a->gate_up_checkpoint_codes != !a->gate_up_checkpoint_scales)
+    return fail(MXFP8_ERR_INVALID_ARG, "%s: gate_up_checkpoint_codes and _scales go together", me);
+  if (a->gate_up_checkpoint_codes && a->gate_up_proj_act_checkpoint_T)
+    return fail(MXFP8_ERR_INVALID_ARG, "%s: one gate/up checkpoint, in bf16 or in MXFP8, not both", me);
+  if (a->gate_up_checkpoint_codes && !valid_fmt(a->fmt_checkpoint))
+    return fail(MXFP8_ERR_INVALID_ARG, "%s: fmt_checkpoint must be E4M3 (0) or E5M2 (1)", me);
+  if ((reinterpret_cast<uintptr_t>(a->num_valid_tokens) & 3u) || (reinterpret_cast<uintptr_t>(a->dropout_rng) & 7u))
+    return fail(MXFP8_ERR_INVALID_ARG, "%s: num_valid_tokens must be 4-byte and dropout_rng 8-byte aligned", me);
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u))
+    return fail(MXFP8_ERR_INVALID_ARG, "%s: workspace must be non-null and 256-byte aligned", me);
+  FwdLayout L;
+  fwd_layout(a, &L);
+  if (ws_bytes < L.total) return fail(MXFP8_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", me, ws_bytes, L.total);
+
+  const int64_t T = a->T, H = a->H, I = a->I, E = a->E, N = a->N, B = a->block_size;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  auto at = [&](size_t off) { return w + off; };
+  auto ints = [&](size_t off) { return reinterpret_cast<int32_t*>(w + off); };
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  hipError_t e;
+  const bool hp = H % 128 == 0, ip = I % 128 == 0;   // the ring loops, pair-major scales
+  float* slot_aff = reinterpret_cast<float*>(at(L.slot_aff));
+
+  mx::MoeFwdArgs g{};
+  g.T = T; g.H = H; g.I = I; g.E = E; g.N = N; g.B = B;
+  g.x_codes = at(L.x_codes); g.x_scales = at(L.x_scales);
+  g.w_codes = a->gate_up_codes; g.w_scales = hp ? at(L.wgu_pairs) : a->gate_up_scales;
+  g.b1 = a->gate_up_proj_bias;
+  g.slot_tok = ints(L.slot_tok); g.slot_aff = slot_aff; g.b2e = a->block_to_expert; g.flag = ints(L.flag);
+  g.tile_start = ints(L.tiles1);
+  g.inter_codes = at(L.inter_codes); g.inter_scales = at(L.inter_scales); g.inter_pairs = ip;
+  g.ckpt = a->gate_up_proj_act_checkpoint_T;
+  g.ck8_codes = a->gate_up_checkpoint_codes; g.ck8_scales = a->gate_up_checkpoint_scales; g.ck8_fmt = a->fmt_checkpoint;
+  g.geglu = a->activation == MXFP8_ACT_GEGLU; g.on_i = a->affinity_on;
+  g.rr_tiles = 2 * I * H >= kRoundRobinWeightBytes;
+  // the down projection: Phase 3's product with a contraction of I
+  mx::Phase3Args d{};
+  d.dgu_row_codes = g.inter_codes; d.dgu_row_scales = g.inter_scales;
+  d.wgu_codes = a->down_codes; d.wgu_scales = ip ? at(L.wd_pairs) : a->down_scales;
+  d.slot_tok = g.slot_tok; d.b2e = a->block_to_expert; d.flag = g.flag; d.tile_start = ints(L.tiles2);
+  d.H = H; d.I = I / 2; d.N = N; d.B = B; d.dx_slot = reinterpret_cast<float*>(at(L.rows));
+  d.conc = device_cus(st);
+  d.parts = mx::phase3_parts_bytes(d) > 0 ? at(L.parts) : nullptr;
+  d.rr_tiles = H * I >= kRoundRobinWeightBytes;
+  d.ranges_done = 1;
+
+  mx::ScalesToPairs jobs[2];
+  int njobs = 0;
+  if (hp) jobs[njobs++] = {a->gate_up_scales, E, 2 * I, H, at(L.wgu_pairs)};
+  if (ip) jobs[njobs++] = {a->down_scales, E, H, I, at(L.wd_pairs)};
+#define STEP(call, what) \
+  if ((e = (call)) != hipSuccess) return hip_status(e, what);
+  // X along H (per token: the gather by slot does not cross a row), the scales' layout, the inverse map's fill
+  const bool prep = mx::moe_prep_fits(T, H);
+  if (prep) {
+    STEP(mx::launch_moe_prep(a->hidden_states, T, H, MXFP8_E4M3, at(L.x_codes), at(L.x_scales), jobs, njobs,
+                             ints(L.slot_of), T * E, st),
+         "quantize X, weight scales to pairs, inverse map");
+  } else {
+    STEP(mx::launch_quant_rows(a->hidden_states, T, H, MXFP8_E4M3, at(L.x_codes), at(L.x_scales), st, nullptr, hp),
+         "quantize X");
+    if (njobs) STEP(mx::launch_scales_to_pairs(jobs, njobs, st), "weight scales to pairs");
+  }
+  STEP(mx::launch_fwd_setup(a->token_position_to_id, a->block_to_expert, a->expert_affinities_masked, T, E, N, B,
+                            a->num_valid_tokens, ints(L.slot_tok), slot_aff, ints(L.slot_of), ints(L.flag),
+                            mx::fwd_gate_up_ranges(g), mx::phase3_ranges(d), prep, st),
+       "slot setup");
+  STEP(mx::launch_fwd_gate_up(g, st), "gate/up projections and activation");
+  if (g.ckpt || g.ck8_codes) STEP(mx::launch_fwd_dead_ckpt(g, st), "checkpoint's dead tiles");
+  STEP(mx::launch_phase3(d, MXFP8_E4M3, MXFP8_E4M3, st), "down projection");
+  const mx::MoeCombineArgs c{d.dx_slot, ints(L.slot_of), a->affinity_on == 0 ? slot_aff : nullptr, a->down_proj_bias,
+                             a->residual, a->output_hidden_states, T, E, H, drop};
+  STEP(mx::launch_fwd_combine(c, st), "sum of the tokens' slots");
+#undef STEP
+  return ok();
+}
+
+}  // extern "C"

@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "philox.hpp"
+
 namespace mx {
 
 // Workgroups of 256 threads that one launch takes: the runtime runs a grid's
@@ -339,5 +341,65 @@ hipError_t launch_moe_grads(Phase3Args p3, GemmStoreArgs g2, GemmStoreArgs g4, i
 int64_t phase3_max_tiles(const Phase3Args& p);
 // bytes of the parts buffer (H, I, N, B set)
 int64_t phase3_parts_bytes(const Phase3Args& p);
+
+// dropout.hip, quantize_t.hip, moe_fwd*.hip -- the forward of the MoE layer and its neighbours
+struct DropoutArgs {
+  const void* x;
+  const void* residual;       // or null
+  void* y;
+  int64_t rows, cols, ldx, ldr, ldy;   // leading dimensions in elements
+  int bf16;                   // bf16 (else fp32)
+  DropoutRule rule;
+};
+hipError_t launch_dropout(const DropoutArgs& p, hipStream_t st);
+// x [G][R][C] -> codes [G][C][R], scales [G][C][R/32] (R % 32 == 0)
+int64_t quantize_t_grid(int64_t G, int64_t R, int64_t C);   // above kMaxGrid256: more than one launch takes
+hipError_t launch_quantize_t(const uint16_t* x, int64_t G, int64_t R, int64_t C, int fmt, uint8_t* codes,
+                             uint8_t* scales, hipStream_t st);
+
+struct MoeFwdArgs {
+  int64_t T, H, I, E, N, B;
+  // scales pair-major where H % 128 == 0 (w: per expert), else row-major
+  const uint8_t* x_codes;       // [T][H]
+  const uint8_t* x_scales;
+  const uint8_t* w_codes;       // [E][2I][H]
+  const uint8_t* w_scales;
+  const uint16_t* b1;           // [E][2][I] bf16, or null
+  const int32_t* slot_tok;      // [P]
+  const float* slot_aff;        // [P]
+  const int32_t* b2e;           // [N]
+  const int32_t* flag;          // [N]: the block's extent
+  int32_t* tile_start;          // tile ranges (moe_tiles.hpp)
+  uint8_t* inter_codes;         // inter_pairs: stage-major, P rows over I, scales pair-major [I/128][P][4];
+  uint8_t* inter_scales;        // else row-major
+  int inter_pairs;              // I % 128 == 0
+  uint16_t* ckpt;               // [N][2][I][B] bf16, or null and
+  uint8_t* ck8_codes;           // [N][2][I][B], [N][2][I][B/32] (or null: no checkpoint)
+  uint8_t* ck8_scales;
+  int ck8_fmt;
+  int geglu, on_i;
+  int rr_tiles;
+  int tiles_m;                  // set by the launcher
+};
+TileRangeJob fwd_gate_up_ranges(const MoeFwdArgs& p);
+hipError_t launch_fwd_gate_up(const MoeFwdArgs& p, hipStream_t st);
+hipError_t launch_fwd_dead_ckpt(const MoeFwdArgs& p, hipStream_t st);
+// slot_tok, slot_aff, slot_of (filled with -1 before, unless told so) and the blocks' extents, then the tile
+// ranges of the two products
+hipError_t launch_fwd_setup(const int32_t* tpid, const int32_t* b2e, const float* aff, int64_t T, int64_t E, int64_t N,
+                            int64_t B, const int32_t* nvalid, int32_t* slot_tok, float* slot_aff, int32_t* slot_of,
+                            int32_t* flag, const TileRangeJob& j0, const TileRangeJob& j1, bool slot_of_filled,
+                            hipStream_t st);
+struct MoeCombineArgs {
+  const float* rows;            // [P][H]
+  const int32_t* slot_of;       // [T][E]
+  const float* slot_aff;        // [P], or null: 1
+  const uint16_t* b2;           // [E][H] bf16, or null
+  const uint16_t* residual;     // [T][H] bf16, or null
+  uint16_t* out;                // [T][H]
+  int64_t T, E, H;
+  DropoutRule drop;
+};
+hipError_t launch_fwd_combine(const MoeCombineArgs& p, hipStream_t st);
 
 }  // namespace mx

@@ -1,0 +1,231 @@
+// moe_fwd_gate_up.hpp -- the MoE forward's first product: both projections of
+// the routed gated feed-forward block, its activation and the product of the
+// two in one kernel.  The template and its launcher; the tile shapes are
+// instantiated in moe_fwd_gate_up_*.hip so they compile in parallel.
+//
+// Per block b of expert e (tile rows = gate and up rows, tile columns = block
+// slot p, contraction over H, on the scaled fp8 MFMA):
+//   g[i][p] = sum_h deq(Wg)[i][h] deq(Q(x_tok))[h] + b1[0][i],  u likewise
+//   s = act(g) u (times the slot's affinity with the affinity on I), fp32
+//   s -> MXFP8 E4M3, groups of 32 along i: the down projection's operand
+//   g, u -> the checkpoint that moe_bwd_mxfp8 reads, [N][2][I][B]: bf16, or
+//           MXFP8 codes and scales of the bf16 values, groups of 32 along the
+//           slots (one rounding more than from fp32, so that the 8-bit
+//           checkpoint is the bf16 one, quantised)
+// s is rounded once, to its code: from the fp32 sums, not the bf16 checkpoint.
+// The scaled MFMA's own rounding (about 6e-6 of a result's size) moves one code
+// in some thousands to its neighbour.
+//
+// A tile of BM rows holds BM / 2 gate rows and the same BM / 2 up rows, as
+// fragments of 32 in turn: a lane's accumulators then hold gate and up of the
+// same 16 (i, p), 16 of a group's 32 i with the lane's other half holding the
+// rest, so activation, product and group maxima stay in registers.  The tile
+// columns are the slots, whose X code rows are gathered by token.
+#pragma once
+#include "gemm_v2.hpp"
+#include "gemm_v3.hpp"
+#include "gemm_v4.hpp"
+#include "kernels.hpp"
+#include "moe_tiles.hpp"
+#include "mx_device.hpp"
+#include "swiglu.hpp"
+
+namespace mx {
+
+using v2::v16f;
+
+// Tile row r -> row of the expert's [2I] weight rows (gate, then up), or -1
+// past I.  i0: the tile's first i.
+template <int BM>
+__device__ __forceinline__ int64_t fwd_weight_row(int r, int64_t i0, int64_t I) {
+  const int w = r / (BM / 2), f = (r % (BM / 2)) / 32;
+  const int64_t i = i0 + w * (BM / 4) + (f >> 1) * 32 + (r & 31);
+  return i < I ? (f & 1) * I + i : -1;
+}
+
+template <int BM, int BN>
+constexpr int fwd_ring_smem() {
+  return BM == 256 && BN == 256 ? v4::smem_bytes(BM, BN) : v3::smem_bytes(BM, BN);
+}
+
+// One fragment pair's checkpoint (32 rows i x 32 slots, words gate | up << 16)
+// through LDS, turned so that a lane holds 8 consecutive slots of a row:
+// 4 lanes then store 64 consecutive bytes (bf16) or 32 (codes).  A row's 32
+// slots are a group of the 8-bit checkpoint: 4 lanes share its maximum.
+constexpr int kCkPitch = 36;   // words a row; 16-byte reads
+constexpr int kCkWaveBytes = 32 * kCkPitch * 4;
+template <int CK>   // 1: bf16, 2 + format: MXFP8
+__device__ __forceinline__ void fwd_store_ckpt(const MoeFwdArgs& p, int b, int64_t i, int64_t s, const uint32_t* lds) {
+  const int lane = threadIdx.x & 63, c = lane & 3;
+#pragma unroll
+  for (int it = 0; it < 2; ++it) {
+    const int r = 16 * it + (lane >> 2);
+    const uint4 a = *reinterpret_cast<const uint4*>(lds + r * kCkPitch + 8 * c);
+    const uint4 d = *reinterpret_cast<const uint4*>(lds + r * kCkPitch + 8 * c + 4);
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, d.x, d.y, d.z, d.w};
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+      uint32_t v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = part ? hi_halves(w[2 * k], w[2 * k + 1]) : lo_halves(w[2 * k], w[2 * k + 1]);
+      const int64_t row = (int64_t(b) * 2 + part) * p.I + i + r;
+      if constexpr (CK == 1) {
+        store_nt(p.ckpt + row * p.B + s + 8 * c, make_uint4(v[0], v[1], v[2], v[3]));
+      } else {
+        constexpr int F = CK - 2;
+        uint32_t m = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m = absmax_bf16x2(m, v[k]);
+        m = max(m & 0xffffu, m >> 16);
+        m = max(m, uint32_t(__shfl_xor(int(m), 1, 64)));
+        m = max(m, uint32_t(__shfl_xor(int(m), 2, 64)));
+        const int X = scale_exp<F>(m << 16);
+        const uint32_t lim = bf16_limit<F>(X) * 0x10001u;
+        const float sc = cvt_scale(X);
+        const uint32_t lo = encode_bf16x4<F>(clamp_bf16x2(v[0], lim), clamp_bf16x2(v[1], lim), sc);
+        const uint32_t hi = encode_bf16x4<F>(clamp_bf16x2(v[2], lim), clamp_bf16x2(v[3], lim), sc);
+        *reinterpret_cast<uint2*>(p.ck8_codes + row * p.B + s + 8 * c) = make_uint2(lo, hi);
+        if (c == 0) p.ck8_scales[row * (p.B / 32) + s / 32] = uint8_t(X + 127);
+      }
+    }
+  }
+}
+
+template <int BM, int BN, bool GENERIC, bool GEGLU, int CK>
+__global__ void __launch_bounds__(v2::kThreads) fwd_gate_up_kernel(MoeFwdArgs p) {
+  constexpr int SMEM = GENERIC ? 2 * (BM + BN) * v2::BK : fwd_ring_smem<BM, BN>();
+  static_assert(SMEM >= 4 * kCkWaveBytes, "the checkpoint's staging fits the ring");
+  __shared__ __attribute__((aligned(16))) uint8_t smem[SMEM];
+  constexpr int FM = BM / 64, FN = BN / 64;
+  BlockTiles bt;
+  if (!block_tile(p.tile_start, p.flag, BN, int(p.N), blockIdx.x, p.rr_tiles, bt)) return;
+  const int b = bt.b;
+  int tm, tn;
+  v2::grouped_tile<8>(bt.local, p.tiles_m, bt.slots, tm, tn);
+  const int64_t i0 = int64_t(tm) * (BM / 2), n0 = int64_t(tn) * BN;
+  const int64_t sbase = int64_t(b) * p.B, e = p.b2e[b];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, h = lane >> 5, r = lane & 31;
+  const int wm = wave >> 1, wn = wave & 1;
+  const int32_t* st = p.slot_tok + sbase;
+  const int64_t B_ = p.B, I_ = p.I;
+  auto tok_of = [&](int q) -> int64_t { const int64_t s = n0 + q; return s < B_ ? int64_t(st[s]) : -1; };
+  auto row_of = [&](int q) -> int64_t { return fwd_weight_row<BM>(q, i0, I_); };
+  const uint8_t* wc = p.w_codes + e * 2 * p.I * p.H;
+  const uint8_t* ws = p.w_scales + e * 2 * p.I * (p.H / 32);
+  v16f acc[FM][FN];
+  if constexpr (GENERIC) {
+    v2::Operand<BM, FM> A;
+    v2::Operand<BN, FN> B;
+    v2::setup_gather(A, wc, ws, 2 * p.I, p.H, p.H / 32, wm * (BM / 2), row_of);
+    v2::setup_gather(B, p.x_codes, p.x_scales, p.T, p.H, p.H / 32, wn * (BN / 2), tok_of);
+    v2::mainloop<BM, BN, v2::kFp8, kE4M3, kE4M3, true>(A, B, int((p.H + v2::BK - 1) / v2::BK), v2::KMapPlain{p.H}, smem,
+                                                       acc);
+  } else {
+    v3::ScaleDma<BM, BN> sd;
+    v3::setup_scales_map(sd, ws, 2 * p.I, 2 * p.I * (p.H / 32), row_of, p.x_scales, p.T, p.T * (p.H / 32), tok_of);
+    if constexpr (BM == 256 && BN == 256) {
+      v4::Op<BM> A;
+      v4::Op<BN> B;
+      v4::setup_gather(A, wc, 2 * p.I, p.H, row_of);
+      v4::setup_gather(B, p.x_codes, p.T, p.H, tok_of);
+      v4::mainloop<BM, BN, v3::kFp8, kE4M3, kE4M3>(A, B, &sd, int(p.H / v4::PK), v4::KMapPlain{}, smem, acc);
+    } else {
+      v3::Op<BM> A;
+      v3::Op<BN> B;
+      v3::setup_gather(A, wc, 2 * p.I, p.H, row_of);
+      v3::setup_gather(B, p.x_codes, p.T, p.H, tok_of);
+      v3::mainloop<BM, BN, v3::kFp8, kE4M3, kE4M3>(A, B, &sd, int(p.H / v3::SK), v3::KMapPlain{}, smem, acc);
+    }
+  }
+  if constexpr (CK != 0) __syncthreads();   // every wave is done with the ring: its bytes stage the checkpoint
+  uint32_t* stage = reinterpret_cast<uint32_t*>(smem + wave * kCkWaveBytes);
+  const int64_t P = p.N * p.B;
+  // this lane's slots
+  bool ok[FN];
+  float aff[FN];
+#pragma unroll
+  for (int j = 0; j < FN; ++j) {
+    const int64_t s = sbase + n0 + wn * (BN / 2) + 32 * j + r;   // BN divides B: inside the block
+    ok[j] = p.slot_tok[s] >= 0;
+    aff[j] = p.on_i ? p.slot_aff[s] : 1.f;
+  }
+  v2::static_for<FM / 2>([&](auto Q) {
+    const int64_t i = i0 + wm * (BM / 4) + 32 * int(Q);   // the group's first i; I % 32 == 0: all of it or nothing
+    if (i < p.I) {
+      float bg[16], bu[16];
+      if (p.b1) {
+        const uint16_t* row = p.b1 + e * 2 * p.I + i + 4 * h;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const uint2 g = *reinterpret_cast<const uint2*>(row + 8 * t);
+          const uint2 u = *reinterpret_cast<const uint2*>(row + p.I + 8 * t);
+          bg[4 * t] = lo_bf16(g.x); bg[4 * t + 1] = hi_bf16(g.x); bg[4 * t + 2] = lo_bf16(g.y); bg[4 * t + 3] = hi_bf16(g.y);
+          bu[4 * t] = lo_bf16(u.x); bu[4 * t + 1] = hi_bf16(u.x); bu[4 * t + 2] = lo_bf16(u.y); bu[4 * t + 3] = hi_bf16(u.y);
+        }
+      } else {
+#pragma unroll
+        for (int t = 0; t < 16; ++t) bg[t] = bu[t] = 0.f;
+      }
+      v2::static_for<FN>([&](auto J) {
+        const int64_t s = n0 + wn * (BN / 2) + 32 * int(J);   // the fragment's first slot
+        float v[16];
+        uint32_t m = 0;
+        v2::static_for<16>([&](auto K) {
+          constexpr int k = K;
+          const float g = ok[J] ? acc[2 * int(Q)][J][k] + bg[k] : 0.f;
+          const float u = ok[J] ? acc[2 * int(Q) + 1][J][k] + bu[k] : 0.f;
+          v[k] = gate_act<GEGLU>(g) * u * aff[J];
+          m = max(m, abs_bits(v[k]));
+          if constexpr (CK != 0) stage[(8 * (k >> 2) + 4 * h + (k & 3)) * kCkPitch + r] = bf16x2_pack(g, u);
+        });
+#if defined(__HIP_DEVICE_COMPILE__)
+        {
+          const auto x = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+          m = max(uint32_t(x[0]), uint32_t(x[1]));
+        }
+        const int X = scale_exp<kE4M3>(m);
+        const float inv = inv_scale(X);
+        uint32_t w[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) w[t] = encode4<kE4M3>(v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3], inv);
+        // word t of half h: rows 8t + 4h .. + 3.  Half 0 takes rows 0..15, half 1 rows 16..31.
+        const auto x = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+        const auto y = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+        const int64_t slot = sbase + s + r, at = i + 16 * h;
+        uint8_t* dst = p.inter_codes + (p.inter_pairs ? stage_major_off(slot, at, P, p.I) : slot * p.I + at);
+        *reinterpret_cast<uint4*>(dst) = make_uint4(x[0], x[1], y[0], y[1]);
+        if (h == 0)
+          p.inter_scales[p.inter_pairs ? ((i >> 7) * P + slot) * 4 + (i >> 5 & 3) : slot * (p.I / 32) + (i >> 5)] =
+              uint8_t(X + 127);
+#endif
+        if constexpr (CK != 0) {
+          __builtin_amdgcn_wave_barrier();   // the wave's own LDS operations run in order
+          fwd_store_ckpt<CK>(p, b, i, s, stage);
+          __builtin_amdgcn_wave_barrier();
+        }
+      });
+    }
+  });
+}
+
+// ---------------------------------------------------------------------------
+template <int BM, int BN, bool G>
+hipError_t fwd_gate_up_launch(MoeFwdArgs p, hipStream_t st) {
+  p.tiles_m = int((p.I + BM / 2 - 1) / (BM / 2));
+  const int64_t blocks = (int64_t(p.tiles_m) * (p.B / BN) * p.N + 7) & ~int64_t(7);   // every tile, rounded to 8
+  if (blocks > kMaxGrid256) return hipErrorInvalidValue;
+  auto go = [&](auto geglu, auto ck) {
+    fwd_gate_up_kernel<BM, BN, G, geglu(), ck()><<<unsigned(blocks), v2::kThreads, 0, st>>>(p);
+  };
+  auto kind = [&](auto geglu) {
+    if (p.ckpt) go(geglu, std::integral_constant<int, 1>{});
+    else if (!p.ck8_codes) go(geglu, std::integral_constant<int, 0>{});
+    else if (p.ck8_fmt == kE4M3) go(geglu, std::integral_constant<int, 2 + kE4M3>{});
+    else go(geglu, std::integral_constant<int, 2 + kE5M2>{});
+  };
+  if (p.geglu) kind(std::true_type{});
+  else kind(std::false_type{});
+  return hipGetLastError();
+}
+
+}  // namespace mx

@@ -1,0 +1,88 @@
+// quantize_t.hip -- MXFP8 quantisation of a batch of matrices along their rows,
+// written transposed: x [G][R][C] bf16 -> codes [G][C][R], scales [G][C][R/32],
+// so that the quantised axis (the one a product contracts over) is contiguous.
+//
+// Bound by memory: 2 bytes read and 1.03 written an element.  A workgroup takes
+// 128 rows x 128 columns; wave w rows 32w .. 32w + 31 (one group), lane l the
+// columns 2l and 2l + 1, so each of its 32 loads is 256 consecutive bytes of a
+// row and a lane holds two whole groups in registers.
+#include <type_traits>
+
+#include "kernels.hpp"
+#include "mx_device.hpp"
+
+namespace mx {
+
+namespace {
+constexpr int kT = 128;   // tile: rows and columns
+
+// PAIRED: C even, so a lane's two columns are one aligned word.
+template <int FMT, bool PAIRED>
+__global__ void __launch_bounds__(256) quantize_t_kernel(const uint16_t* __restrict__ x, int64_t R, int64_t C,
+                                                         int tiles_r, int tiles_c, uint8_t* __restrict__ codes,
+                                                         uint8_t* __restrict__ scales) {
+  const int tc = blockIdx.x % tiles_c, rest = blockIdx.x / tiles_c, tr = rest % tiles_r;
+  const int64_t m = rest / tiles_r;
+  const int lane = threadIdx.x & 63;
+  const int64_t r0 = int64_t(tr) * kT + 32 * (threadIdx.x >> 6), c = int64_t(tc) * kT + 2 * lane;
+  if (r0 >= R || c >= C) return;
+  const bool two = c + 1 < C;
+  const uint16_t* src = x + (m * R + r0) * C + c;
+  uint32_t w[32], am = 0;
+#pragma unroll
+  for (int r = 0; r < 32; ++r) {
+    if constexpr (PAIRED) w[r] = *reinterpret_cast<const uint32_t*>(src + r * C);
+    else w[r] = uint32_t(src[r * C]) | (two ? uint32_t(src[r * C + 1]) << 16 : 0u);
+  }
+#pragma unroll
+  for (int r = 0; r < 32; ++r) am = absmax_bf16x2(am, w[r]);
+  const int X0 = scale_exp<FMT>(am << 16), X1 = scale_exp<FMT>(am & 0xffff0000u);
+  const uint32_t lim = bf16_limit<FMT>(X0) | (bf16_limit<FMT>(X1) << 16);
+  const float s0 = cvt_scale(X0), s1 = cvt_scale(X1);
+  uint32_t p0[8], p1[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const uint32_t a = clamp_bf16x2(w[4 * q], lim), b = clamp_bf16x2(w[4 * q + 1], lim);
+    const uint32_t d = clamp_bf16x2(w[4 * q + 2], lim), e = clamp_bf16x2(w[4 * q + 3], lim);
+    p0[q] = encode_bf16x4<FMT>(lo_halves(a, b), lo_halves(d, e), s0);
+    p1[q] = encode_bf16x4<FMT>(hi_halves(a, b), hi_halves(d, e), s1);
+  }
+  const int64_t row = m * C + c;   // of the result
+  uint4* dst = reinterpret_cast<uint4*>(codes + row * R + r0);
+  dst[0] = make_uint4(p0[0], p0[1], p0[2], p0[3]);
+  dst[1] = make_uint4(p0[4], p0[5], p0[6], p0[7]);
+  scales[row * (R / 32) + r0 / 32] = uint8_t(X0 + 127);
+  if (two) {
+    dst = reinterpret_cast<uint4*>(codes + (row + 1) * R + r0);
+    dst[0] = make_uint4(p1[0], p1[1], p1[2], p1[3]);
+    dst[1] = make_uint4(p1[4], p1[5], p1[6], p1[7]);
+    scales[(row + 1) * (R / 32) + r0 / 32] = uint8_t(X1 + 127);
+  }
+}
+}  // namespace
+
+int64_t quantize_t_grid(int64_t G, int64_t R, int64_t C) {
+  const int64_t tr = (R + kT - 1) / kT, tc = (C + kT - 1) / kT;
+  if (tr > kMaxGrid256 || tc > kMaxGrid256 || tr * tc > kMaxGrid256 || G > kMaxGrid256) return kMaxGrid256 + 1;
+  return G * tr * tc;
+}
+
+hipError_t launch_quantize_t(const uint16_t* x, int64_t G, int64_t R, int64_t C, int fmt, uint8_t* codes,
+                             uint8_t* scales, hipStream_t st) {
+  const int64_t grid = quantize_t_grid(G, R, C);
+  if (grid == 0) return hipSuccess;
+  if (grid > kMaxGrid256) return hipErrorInvalidValue;
+  const int tr = int((R + kT - 1) / kT), tc = int((C + kT - 1) / kT);
+  auto go = [&](auto f, auto paired) {
+    quantize_t_kernel<f(), paired()><<<unsigned(grid), 256, 0, st>>>(x, R, C, tr, tc, codes, scales);
+  };
+  auto kind = [&](auto f) {
+    if (C % 2 == 0) go(f, std::true_type{});
+    else go(f, std::false_type{});
+  };
+  if (fmt == kE4M3) kind(std::integral_constant<int, kE4M3>{});
+  else kind(std::integral_constant<int, kE5M2>{});
+  return hipGetLastError();
+}
+
+}  // namespace mx

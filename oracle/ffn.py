@@ -1,0 +1,167 @@
+"""The MoE forward and its neighbours in numpy, 64 bits: the definitions that the GPU tests hold the kernels to, and
+the bounds that follow from how a kernel may round.
+
+moe_fwd returns, next to y, how far a kernel's y may be off: its products go through the scaled fp8 MFMA, whose error was
+measured against exact sums (at most 2.4e-5 of the sum of the products' magnitudes), and a value s near a border between
+two E4M3 codes (or a group's largest magnitude near a power of two) may then take the other one."""
+from __future__ import annotations
+
+import numpy as np
+
+E4M3, E5M2 = 0, 1
+_EMAX = (8, 15)
+_MAX = (448.0, 57344.0)
+_MBITS = (3, 2)
+_EMIN = (-6, -14)
+MFMA_ERR = 2.4e-5     # of the sum of |products|
+
+
+def code_values(codes, fmt=E4M3):
+    """The values of fp8 codes (float64)."""
+    c = np.asarray(codes, np.int64)
+    m, bias = _MBITS[fmt], (7, 15)[fmt]
+    e, f = (c & 0x7F) >> m, c & ((1 << m) - 1)
+    v = np.where(e == 0, f * 2.0 ** (1 - bias - m), (1 + f / 2.0 ** m) * 2.0 ** (e - bias))
+    return np.where(c & 0x80, -v, v)
+
+
+def mx_values(codes, scales, fmt=E4M3):
+    """codes [..., n] with E8M0 scale bytes [..., n/32] -> float64."""
+    s = np.exp2(np.asarray(scales, np.float64) - 127)
+    v = code_values(codes, fmt)
+    return (v.reshape(*s.shape, 32) * s[..., None]).reshape(v.shape)
+
+
+def scale_exp(amax, fmt=E4M3):
+    """X of a group whose largest magnitude is amax."""
+    _, e = np.frexp(amax)
+    return np.clip(np.where(amax > 0, e - 1 - _EMAX[fmt], -127), -127, 127).astype(np.int64)
+
+
+def mx_round(v, X, fmt=E4M3):
+    """v through the code of scale 2^X (arrays of one shape), as a value."""
+    y = np.ldexp(np.asarray(v, np.float64), -X)
+    _, e = np.frexp(y)
+    q = np.exp2(np.maximum(e - 1, _EMIN[fmt]) - float(_MBITS[fmt]))
+    return np.ldexp(np.clip(np.rint(y / q) * q, -_MAX[fmt], _MAX[fmt]), X)
+
+
+def mx_requant(v, fmt=E4M3):
+    """v [..., n] through MXFP8 and back, groups of 32 along the last axis; and the X of each group."""
+    g = v.reshape(*v.shape[:-1], v.shape[-1] // 32, 32)
+    X = scale_exp(np.abs(g).max(-1), fmt)
+    return mx_round(g, np.broadcast_to(X[..., None], g.shape), fmt).reshape(v.shape), X
+
+
+def mx_requant_bounds(v, d, fmt=E4M3):
+    """mx_requant(v) and how far the result may be off when v may be off by d: the other side's code, or scale."""
+    g, e = (a.reshape(*a.shape[:-1], a.shape[-1] // 32, 32) for a in (v, d))
+    base, _ = mx_requant(v, fmt)
+    base = base.reshape(g.shape)
+    off = np.zeros_like(g)
+    top = np.abs(g)
+    for amax in ((np.maximum(top - e, 0)).max(-1), (top + e).max(-1)):
+        X = np.broadcast_to(scale_exp(amax, fmt)[..., None], g.shape)
+        for w in (g - e, g, g + e):
+            off = np.maximum(off, np.abs(mx_round(w, X, fmt) - base))
+    return base.reshape(v.shape), off.reshape(v.shape)
+
+
+def bf16_round(v):
+    """float64 -> the nearest bf16 value (ties to even), as float64; normal range."""
+    v = np.asarray(v, np.float64)
+    _, e = np.frexp(v)
+    q = np.exp2(np.maximum(e - 1, -126) - 7.0)
+    return np.rint(v / q) * q
+
+
+def act(g, geglu):
+    from scipy.special import ndtr
+    g = np.asarray(g, np.float64)
+    if geglu:
+        return g * ndtr(g)
+    return g / (1 + np.exp(-np.clip(g, -700, 700)))
+
+
+def expert(xq, wgu, wd, b1, b2, a, geglu, on_i):
+    """One expert on rows xq [n, H]: wgu [2, I, H], wd [H, I], b1 [2, I], b2 [H] or None, a [n] ->
+    (gu [n, 2, I], its bound, y [n, H], its bound)."""
+    n, H = xq.shape
+    I = wd.shape[1]
+    w = wgu.reshape(2 * I, H)
+    gu = (xq @ w.T).reshape(n, 2, I)
+    err = MFMA_ERR + (H / 64 + 1) * 2.0 ** -24           # the MFMAs, and the additions into the accumulator
+    dgu = (np.abs(xq) @ np.abs(w).T).reshape(n, 2, I) * err
+    if b1 is not None:
+        gu = gu + b1
+        dgu = dgu + np.abs(gu) * 2.0 ** -24
+    g, u, dg, du = gu[:, 0], gu[:, 1], dgu[:, 0], dgu[:, 1]
+    h = act(g, geglu)
+    s = h * u
+    # |act'| <= 1.13 (both); the activation's own evaluation within 1e-5
+    ds = 1.13 * dg * (np.abs(u) + du) + np.abs(h) * du + 1e-5 * np.abs(s)
+    if on_i:
+        s, ds = s * a[:, None], ds * np.abs(a[:, None]) + np.abs(s * a[:, None]) * 2.0 ** -24
+    sq, dsq = mx_requant_bounds(s, ds)
+    y = sq @ wd.T
+    dy = dsq @ np.abs(wd).T + (np.abs(sq) + dsq) @ np.abs(wd).T * (MFMA_ERR + (I / 64 + 1) * 2.0 ** -24)
+    if b2 is not None:
+        y = y + b2
+        dy = dy + np.abs(y) * 2.0 ** -24
+    if not on_i:
+        y, dy = y * a[:, None], dy * np.abs(a[:, None])
+    return gu, dgu, y, dy + np.abs(y) * 2.0 ** -23
+
+
+def moe_fwd(x, pairs, wgu, wd, b1=None, b2=None, geglu=False, on_i=False, residual=None, keep=None, scale=1.0):
+    """x [T, H] (values); pairs {expert: (tokens, affinities)}; wgu [E, 2, I, H], wd [E, H, I] (values) ->
+    (y [T, H], its bound before the output's rounding, {expert: (gu [n, 2, I], its bound)}).  keep [T, H]: the dropout
+    mask, whose kept elements are scaled."""
+    xq, _ = mx_requant(np.asarray(x, np.float64))
+    y, dy = np.zeros_like(xq), np.zeros_like(xq)
+    gus = {}
+    for e, (t, a) in sorted(pairs.items()):
+        t, a = np.asarray(t, np.int64), np.asarray(a, np.float64)
+        gu, dgu, z, dz = expert(xq[t], wgu[e], wd[e], None if b1 is None else b1[e], None if b2 is None else b2[e], a,
+                                geglu, on_i)
+        gus[e] = (gu, dgu)
+        np.add.at(y, t, z)
+        np.add.at(dy, t, dz + np.abs(z) * 2.0 ** -23)    # the sum over a token's slots
+    if keep is not None:
+        y, dy = np.where(keep, y * scale, 0.0), np.where(keep, dy * scale, 0.0)
+    dy = dy + np.abs(y) * 2.0 ** -23
+    if residual is not None:
+        y = y + residual
+    return y, dy + np.abs(y) * 2.0 ** -23, gus
+
+
+# ----------------------------------------------------------------------------- dropout
+def philox_words(counters, offset, seed):
+    """Philox4x32-10: uint64 counters [n] (the low two words), offset (the high two), seed (the key) -> [n, 4] words."""
+    M = (0xD2511F53, 0xCD9E8D57)
+    W = (0x9E3779B9, 0xBB67AE85)
+    m32, sh = np.uint64(0xFFFFFFFF), np.uint64(32)
+    c = np.asarray(counters, np.uint64)
+    x = [c & m32, c >> sh, np.full_like(c, offset & 0xFFFFFFFF), np.full_like(c, offset >> 32 & 0xFFFFFFFF)]
+    k = [seed & 0xFFFFFFFF, seed >> 32 & 0xFFFFFFFF]
+    for _ in range(10):
+        p0, p1 = x[0] * np.uint64(M[0]), x[2] * np.uint64(M[1])
+        x = [(p1 >> sh) ^ x[1] ^ np.uint64(k[0]), p1 & m32, (p0 >> sh) ^ x[3] ^ np.uint64(k[1]), p0 & m32]
+        k = [(k[0] + W[0]) & 0xFFFFFFFF, (k[1] + W[1]) & 0xFFFFFFFF]
+    return np.stack(x, -1).astype(np.uint32)
+
+
+def dropout_threshold(p):
+    return int(np.floor(p * 65536 + 0.5))
+
+
+def dropout_keep(n, p, seed, offset):
+    """The mask of n elements (bool)."""
+    w = philox_words(np.arange((n + 7) // 8, dtype=np.uint64), offset, seed)
+    bits = np.stack([w & 0xFFFF, w >> 16], -1).reshape(-1)[:n]
+    return bits >= dropout_threshold(p)
+
+
+def dropout_scale(p):
+    t = dropout_threshold(p)
+    return 65536.0 / (65536 - t) if t < 65536 else 0.0

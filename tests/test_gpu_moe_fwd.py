@@ -1,0 +1,213 @@
+"""moe_fwd_mxfp8 on the GPU against the layer in 64 bits (oracle/ffn.py, whose bounds the tolerances are)."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from ffn_common import HALF, Problem, bf16_values, check_rows
+from oracle import ffn
+
+pytestmark = pytest.mark.gpu
+
+CASES = {
+    # both ring loops' tiles: 256 x 256, 256 x 128, 128 x 128 (I < 128); contractions of one 128-byte pair on
+    "ring_256": dict(T=700, H=256, I=384, E=3, K=2, B=512, residual=True),
+    "ring_256x128": dict(T=300, H=128, I=256, E=4, K=2, B=128, bias=True),
+    "ring_128": dict(T=300, H=384, I=96, E=4, K=1, B=256, on_i=True),
+    # H, I or both not a multiple of 128
+    "ragged_H": dict(T=260, H=160, I=128, E=2, K=2, B=256, geglu=True, bias=True),
+    "ragged_I": dict(T=200, H=128, I=160, E=3, K=2, B=128, geglu=True, on_i=True, residual=True),
+    "ragged_both": dict(T=330, H=608, I=352, E=3, K=3, B=256, bias=True, p=0.2, residual=True, dropped=0.2),
+    "smallest": dict(T=1, H=32, I=32, E=1, K=1, B=128, bias=True, residual=True),
+    "one_token_many_experts": dict(T=1, H=128, I=128, E=70, K=8, B=128, p=0.5),
+    # a contraction long enough for cut tiles, and a wide row
+    "long_I": dict(T=150, H=256, I=4224, E=2, K=1, B=256, on_i=True),
+    "wide_H": dict(T=140, H=2304, I=128, E=2, K=2, B=128, bias=True, p=0.1, dropped=0.5),
+    # large values: the activation's flat parts
+    "large_values": dict(T=200, H=128, I=128, E=2, K=1, B=128, sigma=40.0),
+    "large_values_geglu": dict(T=200, H=128, I=128, E=2, K=1, B=128, sigma=40.0, geglu=True),
+}
+
+
+def _run(p, checkpoint=None, **more):
+    import mxfp8_grouped_gemm_amd as mx
+    pos, kw = p.on()
+    r = mx.moe_fwd_mxfp8(*pos, **{**kw, **more}, checkpoint=checkpoint)
+    torch.cuda.synchronize()
+    return r
+
+
+def _gate_up(p, gus):
+    """gu and its bound in the checkpoint's layout [N, 2, I, B], zeros in the slots of no token."""
+    ck, d = np.zeros((2, p.N, 2, p.I, p.B))
+    seen = {}
+    for b, e in enumerate(p.b2e):
+        n = int((p.tpid[b * p.B:(b + 1) * p.B] >= 0).sum())
+        k = seen.get(e, 0)
+        if n:
+            for dst, src in ((ck, gus[e][0]), (d, gus[e][1])):
+                dst[b, :, :, :n] = src[k:k + n].transpose(1, 2, 0)
+        seen[e] = k + n
+    return ck, d
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_forward(name):
+    p = Problem(**CASES[name], seed=sum(map(ord, name)))
+    y, dy, gus = p.exact()
+    r = _run(p, "bf16")
+    check_rows(r["out"], y, dy, name)
+    ck, d = _gate_up(p, gus)
+    got = bf16_values(r["checkpoint"])
+    assert (np.abs(got - ck) <= d + (np.abs(ck) + d) * HALF).all()
+    assert not got[(p.tpid < 0).reshape(p.N, 1, 1, p.B).repeat(2, 1).repeat(p.I, 2)].any()
+    # without a checkpoint, and again: the same bits
+    assert torch.equal(_run(p)["out"], r["out"])
+    # the 8-bit checkpoint is the bf16 one, quantised
+    for fmt in (oracle.E4M3, oracle.E5M2):
+        r8 = _run(p, "mxfp8", fmt_checkpoint=fmt)
+        bits = r["checkpoint"].cpu().view(torch.int16).numpy().view(np.uint16)
+        codes, scales = oracle.quantize(bits.reshape(-1, p.B), 1, fmt)
+        assert np.array_equal(r8["checkpoint"][0].cpu().numpy().reshape(codes.shape), codes)
+        assert np.array_equal(r8["checkpoint"][1].cpu().numpy().reshape(scales.shape), scales)
+        assert torch.equal(r8["out"], r["out"])
+
+
+def test_many_blocks():
+    """More blocks than the set-up's one-workgroup lists take, most of them empty, and more than one round of tiles."""
+    p = Problem(T=600, H=128, I=64, E=40, K=4, B=128, seed=5)
+    pad = 1100 - p.N
+    p.tpid = np.concatenate([p.tpid, np.full(pad * p.B, -1, np.int32)])
+    p.b2e = np.concatenate([p.b2e, np.full(pad, 39, np.int32)])
+    p.N = 1100
+    y, dy, _ = p.exact()
+    check_rows(_run(p, "mxfp8")["out"], y, dy)
+
+
+def test_valid_tokens_and_foreign_blocks():
+    """Tokens from num_valid_tokens on are in no slot; blocks of an expert outside [0, E) are skipped."""
+    p = Problem(T=200, H=128, I=128, E=3, K=2, B=128, residual=True, seed=6)
+    n = torch.tensor([150], dtype=torch.int32, device="cuda")
+    p.b2e[-1] = 7
+    p.tpid[-p.B:-p.B + 5] = np.arange(5)
+    for e, (t, a) in p.pairs.items():
+        p.pairs[e] = (t[t < 150], a[t < 150])
+    y, dy, _ = p.exact()
+    out = _run(p, num_valid_tokens=n)["out"]
+    check_rows(out, y, dy)
+    assert torch.equal(out[150:].cpu(), p.residual[150:])
+
+
+def test_in_place_residual_and_padding_garbage():
+    """out may be the residual; rows of hidden_states that no slot reads may hold anything."""
+    import mxfp8_grouped_gemm_amd as mx
+    p = Problem(T=130, H=256, I=128, E=2, K=1, B=128, residual=True, dropped=0.4, seed=8)
+    y, dy, _ = p.exact()
+    unused = np.nonzero((p.idx < 0).all(1))[0]
+    pos, kw = p.on()
+    pos[0][torch.from_numpy(unused).cuda()] = float("nan")
+    res = kw["residual"]
+    mx.moe_fwd_mxfp8(*pos, **kw, out=res)
+    torch.cuda.synchronize()
+    check_rows(res, y, dy)
+
+
+def test_nan_stays_in_its_row():
+    """A NaN in one token's row reaches no other token."""
+    p = Problem(T=140, H=128, I=128, E=2, K=2, B=128, seed=9)
+    clean = _run(p)["out"]
+    p.x[77, 5] = float("nan")
+    out = _run(p)["out"]
+    rows = torch.arange(140) != 77
+    assert torch.equal(out[rows.cuda()], clean[rows.cuda()])
+
+
+def test_dense_block():
+    """One expert that every token is routed to: a dense gated FFN."""
+    p = Problem(T=300, H=256, I=256, E=1, K=1, B=256, idx=np.zeros((300, 1), np.int32), seed=10)
+    p.aff[:] = 1.0
+    p.pairs = {0: (np.arange(300), np.ones(300))}
+    y, dy, _ = p.exact()
+    check_rows(_run(p)["out"], y, dy)
+
+
+def test_two_streams_and_a_graph():
+    """Calls on another stream; a captured call replayed on changed inputs, another dropout offset among them, with eager
+    work in between."""
+    import mxfp8_grouped_gemm_amd as mx
+    p = Problem(T=300, H=256, I=256, E=4, K=2, B=128, residual=True, p=0.3, seed=11)
+    pos, kw = p.on()
+    eager = mx.MoeFwd(*pos, **kw, checkpoint="mxfp8")
+    want = eager.run()["out"].clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    op = mx.MoeFwd(*pos, **kw, checkpoint="mxfp8")
+    with torch.cuda.stream(s):
+        got = op.run()["out"].clone()
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        op.run()
+    x0 = pos[0].clone()
+    for k in range(4):
+        pos[0].copy_(x0 * (1 + k))
+        kw["dropout_rng"][1] = 1000 + k
+        want = {n: v for n, v in eager.run().items()}
+        op.out["out"].zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(op.out["out"], want["out"])
+        assert torch.equal(op.out["checkpoint"][0], want["checkpoint"][0])
+        assert torch.equal(op.out["checkpoint"][1], want["checkpoint"][1])
+
+
+@pytest.mark.parametrize("checkpoint", ["bf16", "mxfp8"])
+def test_forward_and_backward(checkpoint):
+    """A layer's forward and backward as a training step makes them: weights quantised for both, the forward's checkpoint
+    into the backward, the gradient through the residual's dropout.  The backward from the forward's checkpoint gives the
+    oracle's gradients for the same checkpoint."""
+    import mxfp8_grouped_gemm_amd as mx
+    from helpers import assert_parity, bf, parity_stats
+    from moe_gpu_common import host
+    p = Problem(T=256, H=128, I=256, E=4, K=2, B=128, residual=True, p=0.25, seed=12)
+    dev = "cuda"
+    x, wgu, wd = p.x.to(dev), p.w_gate_up.to(dev), p.w_down.to(dev)
+    topk = torch.from_numpy(p.idx).to(dev)
+    tpid, b2e = mx.moe_build_blocks(topk, p.E, p.B)
+    aff = torch.from_numpy(p.aff.reshape(-1)).to(dev)
+    rng = torch.tensor(p.seed_offset, dtype=torch.int64, device=dev)
+    gu_c, gu_s = mx.mxfp8_quantize_transposed(wgu.view(p.E, p.H, 2 * p.I))
+    d_c, d_s = mx.mxfp8_quantize_transposed(wd)
+    assert np.array_equal(gu_c.cpu().numpy().reshape(p.q[0].shape), p.q[0]) and np.array_equal(d_s.cpu().numpy(), p.q[3])
+    f = mx.moe_fwd_mxfp8(x, aff, gu_c.view(p.E, 2, p.I, p.H), gu_s.view(p.E, 2, p.I, p.H // 32), d_c, d_s, tpid, b2e, p.B,
+                         checkpoint=checkpoint, residual=p.residual.to(dev), dropout_p=p.p, dropout_rng=rng)
+    y, dy, _ = p.exact()
+    check_rows(f["out"], y, dy)
+    dout = torch.randn(p.T, p.H, device=dev, generator=torch.Generator(dev).manual_seed(1)).to(torch.bfloat16)
+    dlayer = mx.dropout_add_bwd(dout, p.p, rng)
+    bgu_c, bgu_s = mx.mxfp8_quantize(wgu.view(-1, p.I))
+    bd_c, bd_s = mx.mxfp8_quantize(wd.view(-1, p.H))
+    E, H, I = p.E, p.H, p.I
+    ck = f["checkpoint"]
+    kw = dict(gate_up_checkpoint=ck) if checkpoint == "mxfp8" else {}
+    g = mx.moe_bwd_mxfp8(x, aff, bgu_c.view(E, H, 2, I), bgu_s.view(E, H, 2, I // 32), bd_c.view(E, I, H),
+                         bd_s.view(E, I, H // 32), tpid, b2e, dlayer, p.B, ck if checkpoint == "bf16" else None, **kw)
+    torch.cuda.synchronize()
+    keep = ffn.dropout_keep(p.T * H, p.p, *p.seed_offset).reshape(p.T, H)
+    want = np.where(keep, bf16_values(dout) * ffn.dropout_scale(p.p), 0.0)
+    assert (np.abs(bf16_values(dlayer) - want) <= np.abs(want) * (HALF + 2.0 ** -23)).all()
+    if checkpoint == "mxfp8":
+        v = ffn.mx_values(ck[0].cpu().numpy(), ck[1].cpu().numpy())
+        ck = torch.from_numpy(v.astype(np.float32)).to(torch.bfloat16)    # exact: 4 significant bits
+    N = b2e.numel()
+    prob = oracle.MoeProblem(T=p.T, H=H, I=I, E=E, N=N, B=p.B, hidden=host(x), aff=host(aff).reshape(-1),
+                             wgu_codes=bgu_c.cpu().numpy().reshape(E, H, 2, I),
+                             wgu_scales=bgu_s.cpu().numpy().reshape(E, H, 2, I // 32),
+                             wd_codes=bd_c.cpu().numpy().reshape(E, I, H), wd_scales=bd_s.cpu().numpy().reshape(E, I, H // 32),
+                             tpid=tpid.cpu().numpy(), b2e=b2e.cpu().numpy(), dy=host(dlayer), ckpt=host(ck), b2=None,
+                             affinity_on=0, has_bias=0, nthreads=0)
+    ref = oracle.moe_bwd(prob)
+    for k, rows, experts in (("dx", p.T, None), ("daff", None, None), ("dwgu", None, E), ("dwd", None, E)):
+        assert_parity(k, parity_stats(bf(host(g[k])), bf(ref[k]), rows=rows, experts=experts))
