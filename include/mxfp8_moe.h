@@ -762,6 +762,45 @@ typedef struct {
 size_t moe_fwd_mxfp8_workspace_size(const moe_fwd_mxfp8_args* args);
 int moe_fwd_mxfp8(const moe_fwd_mxfp8_args* args, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * moe_tokens_fwd_mxfp8 -- the layer of moe_fwd_mxfp8 for few tokens (decoding),
+ * straight from moe_router_fwd's selections: no block lists, no checkpoint, no
+ * dropout, and T * K may be below E.
+ *   y_t = residual_t + sum over k, in order, of the expert topk_idx[t][k]'s share
+ *         with affinity topk_scores[t][k]; ids outside [0,E) are dropped.  An id
+ *         that a token holds twice counts twice.
+ * Roundings as in moe_fwd_mxfp8.
+ * Arguments (moe_tokens_fwd_mxfp8_args):
+ *   T <= MOE_TOKENS_FWD_MAX_TOKENS, 1 <= K <= MXFP8_ROUTER_MAX_K.
+ *   hidden_states [T,H] bf16; topk_idx [T,K] int32, topk_scores [T,K] fp32.
+ *   Weights, biases, affinity_on, activation, residual, output_hidden_states: as
+ *   for moe_fwd_mxfp8.
+ * Workspace: moe_tokens_fwd_mxfp8_workspace_size(args) bytes (0 on invalid
+ * shapes), 256-byte aligned; nothing in it outlives the call.
+ * T == 0 is not an error: nothing is enqueued.  The same bits on every run.
+ * Errors: INVALID_ARG (shapes, K above the bound, null required pointers,
+ * alignment, affinity_on or activation outside {0,1}), UNSUPPORTED (more tokens,
+ * a bias with the affinity on I, 2 * H * I or T * K * I above 2^31 - 1, H or I
+ * above 2^22), WORKSPACE, HIP. */
+#define MOE_TOKENS_FWD_MAX_TOKENS 256
+typedef struct {
+  int64_t T, H, I, E, K;
+  const uint16_t* hidden_states;
+  const int32_t* topk_idx;
+  const float* topk_scores;
+  const uint8_t* gate_up_codes;
+  const uint8_t* gate_up_scales;
+  const uint8_t* down_codes;
+  const uint8_t* down_scales;
+  const uint16_t* gate_up_proj_bias;
+  const uint16_t* down_proj_bias;
+  int affinity_on, activation;
+  const uint16_t* residual;
+  uint16_t* output_hidden_states;
+} moe_tokens_fwd_mxfp8_args;
+size_t moe_tokens_fwd_mxfp8_workspace_size(const moe_tokens_fwd_mxfp8_args* args);
+int moe_tokens_fwd_mxfp8(const moe_tokens_fwd_mxfp8_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

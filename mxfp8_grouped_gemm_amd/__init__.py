@@ -105,6 +105,13 @@ class MoeFwdArgs(C.Structure):
                 ("dropout_p", C.c_double), ("dropout_rng", _p)]
 
 
+class MoeTokensFwdArgs(C.Structure):
+    _fields_ = [("T", _i64), ("H", _i64), ("I", _i64), ("E", _i64), ("K", _i64), ("hidden_states", _p),
+                ("topk_idx", _p), ("topk_scores", _p), ("gate_up_codes", _p), ("gate_up_scales", _p),
+                ("down_codes", _p), ("down_scales", _p), ("gate_up_proj_bias", _p), ("down_proj_bias", _p),
+                ("affinity_on", C.c_int), ("activation", C.c_int), ("residual", _p), ("output_hidden_states", _p)]
+
+
 def _declare(L):
     L.mxfp8_last_error.restype = C.c_char_p
     L.mxfp8_version.restype = C.c_char_p
@@ -138,6 +145,8 @@ def _declare(L):
         ("dropout_add_bwd", C.c_int, [C.POINTER(DropoutAddArgs), _p]),
         ("moe_fwd_mxfp8_workspace_size", C.c_size_t, [C.POINTER(MoeFwdArgs)]),
         ("moe_fwd_mxfp8", C.c_int, [C.POINTER(MoeFwdArgs), _p, C.c_size_t, _p]),
+        ("moe_tokens_fwd_mxfp8_workspace_size", C.c_size_t, [C.POINTER(MoeTokensFwdArgs)]),
+        ("moe_tokens_fwd_mxfp8", C.c_int, [C.POINTER(MoeTokensFwdArgs), _p, C.c_size_t, _p]),
     ):
         if hasattr(L, name):
             f = getattr(L, name)
@@ -838,3 +847,53 @@ class MoeFwd:
 def moe_fwd_mxfp8(*args, **kw):
     """Functional form: builds a MoeFwd and runs it once; returns its dict."""
     return MoeFwd(*args, **kw).run()
+
+
+@lru_cache(maxsize=256)
+def _tokens_workspace_size(T, H, I, E, K):
+    a = MoeTokensFwdArgs(T, H, I, E, K)
+    size = lib().moe_tokens_fwd_mxfp8_workspace_size(C.byref(a))
+    if not size and T:   # refused before anything is enqueued, with its status and reason
+        _check(lib().moe_tokens_fwd_mxfp8(C.byref(a), None, 0, None), "moe_tokens_fwd_mxfp8")
+    return size
+
+
+def moe_tokens_fwd_mxfp8(hidden_states: torch.Tensor, topk_idx: torch.Tensor, topk_scores: torch.Tensor,
+                         gate_up_codes: torch.Tensor, gate_up_scales: torch.Tensor, down_codes: torch.Tensor,
+                         down_scales: torch.Tensor, gate_up_bias: Optional[torch.Tensor] = None,
+                         down_bias: Optional[torch.Tensor] = None, affinity_on: int = 0, activation: int = ACT_SWIGLU,
+                         residual: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                         out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The MoE layer's forward for up to 256 tokens, from the router's selections (include/mxfp8_moe.h:
+    moe_tokens_fwd_mxfp8): hidden_states [T, H] bf16, topk_idx [T, K] int32 and topk_scores [T, K] fp32 as
+    moe_router_fwd returns them, weights as for moe_fwd_mxfp8 -> [T, H] bf16."""
+    if hidden_states.dim() != 2 or topk_idx.dim() != 2 or gate_up_codes.dim() != 4:
+        raise ValueError("moe_tokens_fwd_mxfp8: hidden_states must be [T, H], topk_idx [T, K], gate_up_codes [E, 2, I, H]")
+    T, H = hidden_states.shape
+    K = topk_idx.shape[1]
+    E, _, I, _ = gate_up_codes.shape
+    dev = hidden_states.device
+    bf16, u8 = torch.bfloat16, torch.uint8
+    a = MoeTokensFwdArgs(T, H, I, E, K, _dev(hidden_states, bf16, "hidden_states"),
+                         _tensor(topk_idx, torch.int32, (T, K), dev, "topk_idx"),
+                         _tensor(topk_scores, torch.float32, (T, K), dev, "topk_scores"),
+                         _tensor(gate_up_codes, u8, (E, 2, I, H), dev, "gate_up_codes"),
+                         _tensor(gate_up_scales, u8, (E, 2, I, H // 32), dev, "gate_up_scales"),
+                         _tensor(down_codes, u8, (E, H, I), dev, "down_codes"),
+                         _tensor(down_scales, u8, (E, H, I // 32), dev, "down_scales"),
+                         _tensor(gate_up_bias, bf16, (E, 2, I), dev, "gate_up_bias"),
+                         _tensor(down_bias, bf16, (E, H), dev, "down_bias"), affinity_on, activation,
+                         _tensor(residual, bf16, (T, H), dev, "residual"))
+    if workspace is None:
+        size = _tokens_workspace_size(T, H, I, E, K)
+        workspace = _empty(size, dtype=u8, device=dev)   # the name holds it until the kernels are enqueued
+    else:
+        size = workspace.numel()
+        _tensor(workspace, u8, workspace.shape, dev, "workspace")
+    if out is None:
+        out = _empty((T, H), dtype=bf16, device=dev)
+        a.output_hidden_states = out.data_ptr()
+    else:
+        a.output_hidden_states = _tensor(out, bf16, (T, H), dev, "out")
+    _call(dev, "moe_tokens_fwd_mxfp8", C.byref(a), workspace.data_ptr(), size)
+    return out

@@ -236,4 +236,94 @@ int moe_fwd_mxfp8(const moe_fwd_mxfp8_args* a, void* ws, size_t ws_bytes, void* 
   return ok();
 }
 
+/* ---- MoE forward of few tokens ------------------------------------------- */
+
+namespace {
+struct TokLayout {
+  size_t x_codes, x_scales, s_codes, s_scales, rows, total;
+};
+}  // namespace
+
+static int tokens_check_shapes(const moe_tokens_fwd_mxfp8_args* a) {
+  const char* me = "moe_tokens_fwd_mxfp8";
+  if (!a) return fail(MXFP8_ERR_INVALID_ARG, "%s: null args", me);
+  const int64_t T = a->T, H = a->H, I = a->I, E = a->E, K = a->K;
+  if (T < 0 || H <= 0 || I <= 0 || E <= 0 || K <= 0) return fail(MXFP8_ERR_INVALID_ARG, "%s: sizes must be positive", me);
+  if (H % 32 || I % 32)
+    return fail(MXFP8_ERR_INVALID_ARG, "%s: H and I must be multiples of 32 (got %lld, %lld)", me, (long long)H,
+                (long long)I);
+  if (K > MXFP8_ROUTER_MAX_K) return fail(MXFP8_ERR_INVALID_ARG, "%s: K above %d", me, MXFP8_ROUTER_MAX_K);
+  if (T > MOE_TOKENS_FWD_MAX_TOKENS)
+    return fail(MXFP8_ERR_UNSUPPORTED, "%s: more than %d tokens (moe_fwd_mxfp8 takes any number, over block lists)", me,
+                MOE_TOKENS_FWD_MAX_TOKENS);
+  // an expert's weight rows are read through one buffer, at 32-bit offsets
+  if (I > INT32_MAX / 2 / H || H > (int64_t(1) << 22) || I > (int64_t(1) << 22) || E > (int64_t(1) << 31) ||
+      T * K * I > INT32_MAX)
+    return fail(MXFP8_ERR_UNSUPPORTED, "%s: sizes beyond 32-bit indexing", me);
+  return MXFP8_OK;
+}
+
+static void tokens_layout(const moe_tokens_fwd_mxfp8_args* a, TokLayout* L) {
+  const int64_t T = a->T, H = a->H, I = a->I, M = T * a->K;
+  size_t o = 0;
+  auto put = [&](size_t& field, int64_t bytes) {
+    field = o;
+    o = up256(o + size_t(bytes));
+  };
+  put(L->x_codes, T * H);
+  put(L->x_scales, T * H / 32);
+  put(L->s_codes, M * I);
+  put(L->s_scales, M * I / 32);
+  put(L->rows, (M ? mx::tokens_splits(T, H, I, a->E, a->K) : 0) * M * H * 4);
+  L->total = o;
+}
+
+size_t moe_tokens_fwd_mxfp8_workspace_size(const moe_tokens_fwd_mxfp8_args* a) {
+  if (tokens_check_shapes(a)) return 0;
+  TokLayout L;
+  tokens_layout(a, &L);
+  return L.total;
+}
+
+int moe_tokens_fwd_mxfp8(const moe_tokens_fwd_mxfp8_args* a, void* ws, size_t ws_bytes, void* stream) {
+  const char* me = "moe_tokens_fwd_mxfp8";
+  int rc = tokens_check_shapes(a);
+  if (rc) return rc;
+  if (a->affinity_on != 0 && a->affinity_on != 1)
+    return fail(MXFP8_ERR_INVALID_ARG, "%s: affinity_on must be 0 (H) or 1 (I)", me);
+  if (a->activation != MXFP8_ACT_SWIGLU && a->activation != MXFP8_ACT_GEGLU)
+    return fail(MXFP8_ERR_INVALID_ARG, "%s: activation must be 0 (SwiGLU) or 1 (GeGLU)", me);
+  if (a->affinity_on == 1 && (a->gate_up_proj_bias || a->down_proj_bias))
+    return fail(MXFP8_ERR_UNSUPPORTED, "%s: a bias with the affinity on I is not supported", me);
+  if (a->T == 0) return ok();
+  const void* req[] = {a->hidden_states, a->topk_idx, a->topk_scores, a->gate_up_codes, a->gate_up_scales,
+                       a->down_codes, a->down_scales, a->output_hidden_states};
+  const void* opt[] = {a->gate_up_proj_bias, a->down_proj_bias, a->residual};
+  for (const void* q : req)
+    if (!q) return fail(MXFP8_ERR_INVALID_ARG, "%s: a required pointer is null", me);
+  for (const void* q : req)
+    if (!aligned16(q)) return fail(MXFP8_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", me);
+  for (const void* q : opt)
+    if (!aligned16(q)) return fail(MXFP8_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", me);
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u))
+    return fail(MXFP8_ERR_INVALID_ARG, "%s: workspace must be non-null and 256-byte aligned", me);
+  TokLayout L;
+  tokens_layout(a, &L);
+  if (ws_bytes < L.total) return fail(MXFP8_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", me, ws_bytes, L.total);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  mx::MoeTokensArgs p{};
+  p.T = a->T; p.H = a->H; p.I = a->I; p.E = a->E; p.K = a->K;
+  p.idx = a->topk_idx; p.scores = a->topk_scores;
+  p.x_codes = w + L.x_codes; p.x_scales = w + L.x_scales;
+  p.w_codes = a->gate_up_codes; p.w_scales = a->gate_up_scales;
+  p.wd_codes = a->down_codes; p.wd_scales = a->down_scales;
+  p.b1 = a->gate_up_proj_bias; p.b2 = a->down_proj_bias;
+  p.s_codes = w + L.s_codes; p.s_scales = w + L.s_scales;
+  p.rows = reinterpret_cast<float*>(w + L.rows);
+  p.residual = a->residual; p.out = a->output_hidden_states;
+  p.geglu = a->activation == MXFP8_ACT_GEGLU; p.on_i = a->affinity_on;
+  p.splits = int(mx::tokens_splits(a->T, a->H, a->I, a->E, a->K));
+  return hip_status(mx::launch_moe_tokens(p, a->hidden_states, static_cast<hipStream_t>(stream)), me);
+}
+
 }  // extern "C"

@@ -402,4 +402,29 @@ struct MoeCombineArgs {
 };
 hipError_t launch_fwd_combine(const MoeCombineArgs& p, hipStream_t st);
 
+// moe_tokens.hip -- the same layer for few tokens
+struct MoeTokensArgs {
+  int64_t T, H, I, E, K;
+  const int32_t* idx;           // [T][K]
+  const float* scores;          // [T][K]
+  uint8_t* x_codes;             // [T][H], scales [T][H/32]
+  uint8_t* x_scales;
+  const uint8_t* w_codes;       // [E][2I][H], scales [E][2I][H/32]
+  const uint8_t* w_scales;
+  const uint8_t* wd_codes;      // [E][H][I], scales [E][H][I/32]
+  const uint8_t* wd_scales;
+  const uint16_t* b1;           // or null
+  const uint16_t* b2;
+  uint8_t* s_codes;             // [T K][I], scales [T K][I/32]
+  uint8_t* s_scales;
+  float* rows;                  // [splits][T K][H]
+  const uint16_t* residual;     // or null
+  uint16_t* out;                // [T][H]
+  int geglu, on_i;
+  int splits;                   // tokens_splits
+  int by_pair;                  // set by the launcher
+};
+int64_t tokens_splits(int64_t T, int64_t H, int64_t I, int64_t E, int64_t K);
+hipError_t launch_moe_tokens(MoeTokensArgs p, const uint16_t* x, hipStream_t st);
+
 }  // namespace mx

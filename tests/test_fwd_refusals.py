@@ -13,7 +13,8 @@ F = 0x10000
 ODD = 0x10004
 
 
-@pytest.mark.parametrize("cls,ctype", [("DropoutAddArgs", "dropout_add_args"), ("MoeFwdArgs", "moe_fwd_mxfp8_args")])
+@pytest.mark.parametrize("cls,ctype", [("DropoutAddArgs", "dropout_add_args"), ("MoeFwdArgs", "moe_fwd_mxfp8_args"),
+                                       ("MoeTokensFwdArgs", "moe_tokens_fwd_mxfp8_args")])
 def test_binding_structs_match_the_header(cls, ctype, tmp_path):
     _structs_match(cls, ctype, tmp_path)
 
@@ -96,6 +97,40 @@ def test_moe_fwd_refusals():
     assert L.moe_fwd_mxfp8(None, F, 1 << 60, None) == 1 and L.moe_fwd_mxfp8_workspace_size(None) == 0
 
 
+def _tok(**kw):
+    a = mx.MoeTokensFwdArgs(8, 128, 256, 4, 2, *([F] * 7), None, None, 0, 0, None, F)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+def test_moe_tokens_fwd_refusals():
+    L = mx.lib()
+    need = L.moe_tokens_fwd_mxfp8_workspace_size(C.byref(_tok()))
+    assert need > 0 and need % 256 == 0
+
+    def run(ws=F, nbytes=1 << 60, **kw):
+        return L.moe_tokens_fwd_mxfp8(C.byref(_tok(**kw)), ws, nbytes, None)
+
+    for bad in (dict(T=-1), dict(H=0), dict(I=-32), dict(E=0), dict(K=0), dict(K=33), dict(H=48), dict(I=40)):
+        assert run(**bad) == 1, bad
+        assert L.moe_tokens_fwd_mxfp8_workspace_size(C.byref(_tok(**bad))) == 0
+    for large in (dict(T=257), dict(H=2 ** 20, I=2 ** 10), dict(H=2 ** 23, I=32), dict(I=2 ** 23, H=32), dict(E=2 ** 40),
+                  dict(T=256, K=32, I=2 ** 18, H=32)):
+        assert run(**large) == 2, large
+        assert L.moe_tokens_fwd_mxfp8_workspace_size(C.byref(_tok(**large))) == 0
+    for name in ("hidden_states", "topk_idx", "topk_scores", "gate_up_codes", "gate_up_scales", "down_codes", "down_scales",
+                 "output_hidden_states"):
+        assert run(**{name: None}) == 1 and run(**{name: ODD}) == 1, name
+    for bad in (dict(gate_up_proj_bias=ODD), dict(down_proj_bias=ODD), dict(residual=ODD), dict(affinity_on=2),
+                dict(activation=-1), dict(ws=None), dict(ws=0x10010)):
+        assert run(**bad) == 1, bad
+    assert run(affinity_on=1, gate_up_proj_bias=F) == 2 and run(affinity_on=1, down_proj_bias=F) == 2
+    assert run(nbytes=need - 1) == 3 and "workspace" in mx.last_error()
+    assert run(T=0, hidden_states=None, topk_idx=None, ws=None) == 0
+    assert L.moe_tokens_fwd_mxfp8(None, F, 1 << 60, None) == 1 and L.moe_tokens_fwd_mxfp8_workspace_size(None) == 0
+
+
 def test_bindings_check_their_tensors():
     z = torch.zeros(4, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="device tensor"):
@@ -116,3 +151,7 @@ def test_bindings_check_their_tensors():
         mx.moe_fwd_mxfp8(z, None, w, None, None, None, None, i, 128, checkpoint="fp8")
     with pytest.raises(ValueError, match="device tensor"):
         mx.moe_fwd_mxfp8(z, None, w, None, None, None, None, i, 128)
+    with pytest.raises(ValueError, match="topk_idx"):
+        mx.moe_tokens_fwd_mxfp8(z, i, None, w, None, None, None)
+    with pytest.raises(ValueError, match="device tensor"):
+        mx.moe_tokens_fwd_mxfp8(z, i.view(1, 1), None, w, None, None, None)

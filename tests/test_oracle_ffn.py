@@ -71,3 +71,12 @@ def test_one_pair_by_hand():
     z, _, _ = ffn.moe_fwd(x, {0: ([0], [0.5])}, np.stack([eye, eye])[None], eye[None], keep=keep, scale=2.0,
                           residual=np.ones((1, H)))
     assert z[0, 0] == 1.0 and z[0, 1] == pytest.approx(1 + 2 * y[0, 1])
+
+
+def test_product_rests_by_hand():
+    """Products below 2^(E - 13) of their 8 are cut off whole, others to a multiple; other groups keep their own unit."""
+    a, b = np.ones((1, 32)), np.zeros((2, 32))
+    b[0, 0], b[0, 1], b[0, 2] = 1.0, 2.0 ** -14, -1.5 * 2.0 ** -13      # unit 2^-13
+    b[0, 8] = 2.0 ** -14
+    b[1, :2] = 1.75 * 2.0 ** -10, 1.25
+    assert np.array_equal(ffn.product_rests(a, b), [[2.0 ** -14 + 0.5 * 2.0 ** -13, 0.0]])
