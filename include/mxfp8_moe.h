@@ -780,8 +780,8 @@ int moe_fwd_mxfp8(const moe_fwd_mxfp8_args* args, void* workspace, size_t worksp
  * T == 0 is not an error: nothing is enqueued.  The same bits on every run.
  * Errors: INVALID_ARG (shapes, K above the bound, null required pointers,
  * alignment, affinity_on or activation outside {0,1}), UNSUPPORTED (more tokens,
- * a bias with the affinity on I, 2 * H * I or T * K * I above 2^31 - 1, H or I
- * above 2^22), WORKSPACE, HIP. */
+ * more than MXFP8_ROUTER_MAX_EXPERTS experts, a bias with the affinity on I,
+ * 2 * H * I or T * K * I above 2^31 - 1, H or I above 2^22), WORKSPACE, HIP. */
 #define MOE_TOKENS_FWD_MAX_TOKENS 256
 typedef struct {
   int64_t T, H, I, E, K;

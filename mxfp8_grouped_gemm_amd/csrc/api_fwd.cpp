@@ -240,7 +240,7 @@ int moe_fwd_mxfp8(const moe_fwd_mxfp8_args* a, void* ws, size_t ws_bytes, void* 
 
 namespace {
 struct TokLayout {
-  size_t x_codes, x_scales, s_codes, s_scales, rows, total;
+  size_t x_codes, x_scales, units, list, done, s_codes, s_scales, rows, total;
 };
 }  // namespace
 
@@ -257,9 +257,10 @@ static int tokens_check_shapes(const moe_tokens_fwd_mxfp8_args* a) {
     return fail(MXFP8_ERR_UNSUPPORTED, "%s: more than %d tokens (moe_fwd_mxfp8 takes any number, over block lists)", me,
                 MOE_TOKENS_FWD_MAX_TOKENS);
   // an expert's weight rows are read through one buffer, at 32-bit offsets
-  if (I > INT32_MAX / 2 / H || H > (int64_t(1) << 22) || I > (int64_t(1) << 22) || E > (int64_t(1) << 31) ||
+  if (I > INT32_MAX / 2 / H || H > (int64_t(1) << 22) || I > (int64_t(1) << 22) || E > MXFP8_ROUTER_MAX_EXPERTS ||
       T * K * I > INT32_MAX)
-    return fail(MXFP8_ERR_UNSUPPORTED, "%s: sizes beyond 32-bit indexing", me);
+    return fail(MXFP8_ERR_UNSUPPORTED, "%s: more than %d experts, or sizes beyond 32-bit indexing", me,
+                MXFP8_ROUTER_MAX_EXPERTS);
   return MXFP8_OK;
 }
 
@@ -270,8 +271,12 @@ static void tokens_layout(const moe_tokens_fwd_mxfp8_args* a, TokLayout* L) {
     field = o;
     o = up256(o + size_t(bytes));
   };
-  put(L->x_codes, T * H);
-  put(L->x_scales, T * H / 32);
+  const bool few = mx::tokens_few(T);
+  put(L->x_codes, few ? 0 : T * H);
+  put(L->x_scales, few ? 0 : T * H / 32);
+  put(L->units, few ? 0 : (1 + 3 * mx::tokens_units(T, a->E, a->K)) * 4);
+  put(L->list, few ? 0 : M * 4);
+  put(L->done, few ? (H + 63) / 64 * 4 : 0);
   put(L->s_codes, M * I);
   put(L->s_scales, M * I / 32);
   put(L->rows, (M ? mx::tokens_splits(T, H, I, a->E, a->K) : 0) * M * H * 4);
@@ -314,7 +319,10 @@ int moe_tokens_fwd_mxfp8(const moe_tokens_fwd_mxfp8_args* a, void* ws, size_t ws
   mx::MoeTokensArgs p{};
   p.T = a->T; p.H = a->H; p.I = a->I; p.E = a->E; p.K = a->K;
   p.idx = a->topk_idx; p.scores = a->topk_scores;
+  p.x = a->hidden_states;
   p.x_codes = w + L.x_codes; p.x_scales = w + L.x_scales;
+  p.units = reinterpret_cast<int32_t*>(w + L.units); p.list = reinterpret_cast<int32_t*>(w + L.list);
+  p.done = reinterpret_cast<unsigned*>(w + L.done);
   p.w_codes = a->gate_up_codes; p.w_scales = a->gate_up_scales;
   p.wd_codes = a->down_codes; p.wd_scales = a->down_scales;
   p.b1 = a->gate_up_proj_bias; p.b2 = a->down_proj_bias;
@@ -323,7 +331,7 @@ int moe_tokens_fwd_mxfp8(const moe_tokens_fwd_mxfp8_args* a, void* ws, size_t ws
   p.residual = a->residual; p.out = a->output_hidden_states;
   p.geglu = a->activation == MXFP8_ACT_GEGLU; p.on_i = a->affinity_on;
   p.splits = int(mx::tokens_splits(a->T, a->H, a->I, a->E, a->K));
-  return hip_status(mx::launch_moe_tokens(p, a->hidden_states, static_cast<hipStream_t>(stream)), me);
+  return hip_status(mx::launch_moe_tokens(p, static_cast<hipStream_t>(stream)), me);
 }
 
 }  // extern "C"

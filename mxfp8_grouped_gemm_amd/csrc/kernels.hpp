@@ -407,8 +407,13 @@ struct MoeTokensArgs {
   int64_t T, H, I, E, K;
   const int32_t* idx;           // [T][K]
   const float* scores;          // [T][K]
+  const uint16_t* x;            // [T][H] bf16
+  // more than a few tokens (launch_tok_prep): X quantised, and the pairs t K + k by expert
   uint8_t* x_codes;             // [T][H], scales [T][H/32]
   uint8_t* x_scales;
+  int32_t* units;               // how many units; each one's expert, first entry of the list, entries [nunits][3]
+  int32_t* list;                // [T K]
+  unsigned* done;               // a few tokens: workgroups that have finished, per tile of 64 columns of H
   const uint8_t* w_codes;       // [E][2I][H], scales [E][2I][H/32]
   const uint8_t* w_scales;
   const uint8_t* wd_codes;      // [E][H][I], scales [E][H][I/32]
@@ -422,9 +427,13 @@ struct MoeTokensArgs {
   uint16_t* out;                // [T][H]
   int geglu, on_i;
   int splits;                   // tokens_splits
-  int by_pair;                  // set by the launcher
+  int nunits, by_pair;          // set by the launcher: units at most; a few tokens: pairs stand for experts
 };
 int64_t tokens_splits(int64_t T, int64_t H, int64_t I, int64_t E, int64_t K);
-hipError_t launch_moe_tokens(MoeTokensArgs p, const uint16_t* x, hipStream_t st);
+int64_t tokens_units(int64_t T, int64_t E, int64_t K);   // nunits
+bool tokens_few(int64_t T);                              // no prep: no codes of X, no lists
+hipError_t launch_moe_tokens(MoeTokensArgs p, hipStream_t st);
+// quantize.hip: X quantised along H, and the pairs listed by expert (E <= 4096), in units of up to ncol
+hipError_t launch_tok_prep(const MoeTokensArgs& p, int ncol, hipStream_t st);
 
 }  // namespace mx

@@ -542,6 +542,69 @@ __global__ void __launch_bounds__(256) moe_prep_kernel(const uint4* __restrict__
   }
 }
 
+// The few-token forward's preparation: workgroup 0 lists the pairs t K + k by
+// expert, each expert's in units of up to ncol (a histogram, a scan over the
+// experts that counts units too, and the entries placed in any order: pairs are
+// columns of a product, and a column's values do not depend on where it stands),
+// the others quantise X.
+constexpr int kTokExperts = 4096;
+__global__ void __launch_bounds__(256) tok_prep_kernel(const uint4* __restrict__ x, uint2* __restrict__ codes,
+                                                       uint8_t* __restrict__ scales, int64_t nchunks, int64_t rows,
+                                                       int64_t gpr, const int32_t* __restrict__ idx, int M, int E,
+                                                       int ncol, int32_t* __restrict__ units,
+                                                       int32_t* __restrict__ list) {
+  __shared__ int cnt[kTokExperts];
+  __shared__ int wsum[4];
+  if (blockIdx.x != 0) {
+    quant_rows_part<kE4M3, false, false, kSmallRowsU>(x, codes, scales, nchunks, nullptr, rows, gpr, 0, blockIdx.x - 1,
+                                                      gridDim.x - 1);
+    return;
+  }
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  for (int e = t; e < E; e += 256) cnt[e] = 0;
+  __syncthreads();
+#pragma unroll 4
+  for (int j = t; j < M; j += 256) {
+    const int e = idx[j];
+    if (e >= 0 && e < E) atomicAdd(&cnt[e], 1);
+  }
+  __syncthreads();
+  // a thread's run of experts: its pairs (below 2^14) and units (below 2^14), in one word
+  const int per = (E + 255) / 256, e0 = t * per, e1 = e0 + per < E ? e0 + per : E;
+  int mine = 0;
+  for (int e = e0; e < e1; ++e) mine += (cnt[e] << 16) + (cnt[e] + ncol - 1) / ncol;
+  int sum = mine;
+  for (int o = 1; o < 64; o <<= 1) {
+    const int y = __shfl_up(sum, o, 64);
+    if (lane >= o) sum += y;
+  }
+  if (lane == 63) wsum[wave] = sum;
+  __syncthreads();
+  int before = sum - mine, total = 0;
+  for (int w = 0; w < 4; ++w) {
+    before += w < wave ? wsum[w] : 0;
+    total += wsum[w];
+  }
+  int pos = before >> 16, u = before & 0xffff;
+  for (int e = e0; e < e1; ++e) {
+    const int n = cnt[e];
+    for (int c = 0; c < n; c += ncol, ++u) {
+      units[1 + 3 * u] = e;
+      units[2 + 3 * u] = pos + c;
+      units[3 + 3 * u] = n - c < ncol ? n - c : ncol;
+    }
+    cnt[e] = pos;
+    pos += n;
+  }
+  if (t == 0) units[0] = total & 0xffff;
+  __syncthreads();
+#pragma unroll 4
+  for (int j = t; j < M; j += 256) {
+    const int e = idx[j];
+    if (e >= 0 && e < E) list[atomicAdd(&cnt[e], 1)] = j;
+  }
+}
+
 // ---------------------------------------------------------------------------
 // host launchers
 template <int FMT, int U>
@@ -574,6 +637,15 @@ hipError_t launch_quant_rows(const uint16_t* x, int64_t rows, int64_t cols, int 
   const int sm = stage_major ? 1 : 0;
   if (fmt == kE4M3) rows_dispatch<kE4M3>(nchunks, st, xs, cs, scales, ds, rows, cols / 32, pairs, sm);
   else rows_dispatch<kE5M2>(nchunks, st, xs, cs, scales, ds, rows, cols / 32, pairs, sm);
+  return hipGetLastError();
+}
+
+hipError_t launch_tok_prep(const MoeTokensArgs& p, int ncol, hipStream_t st) {
+  const int64_t nchunks = p.T * p.H / 8, nq = (nchunks + 1023) / 1024, M = p.T * p.K;
+  if (p.E > kTokExperts || M >= 1 << 14 || nq > 65535) return hipErrorInvalidValue;
+  tok_prep_kernel<<<unsigned(1 + nq), 256, 0, st>>>(reinterpret_cast<const uint4*>(p.x), reinterpret_cast<uint2*>(p.x_codes),
+                                                    p.x_scales, nchunks, p.T, p.H / 32, p.idx, int(M), int(p.E), ncol,
+                                                    p.units, p.list);
   return hipGetLastError();
 }
 

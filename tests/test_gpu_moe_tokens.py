@@ -22,6 +22,12 @@ CASES = {
     "ragged_dense": dict(T=100, H=96, I=224, E=3, K=2, on_i=True),
     "most": dict(T=256, H=128, I=128, E=24, K=8, bias=True, residual=True, dropped=0.3),
     "long_split": dict(T=3, H=128, I=8320, E=2, K=1, residual=True),
+    "four": dict(T=4, H=352, I=256, E=12, K=5, bias=True, residual=True),
+    "four_whole_tiles": dict(T=4, H=128, I=1088, E=40, K=32, residual=True),       # 1360 tiles of the gate/up product
+    "four_wide": dict(T=4, H=2144, I=160, E=32, K=32, bias=True),                  # 1088 of the down projection, a half one last
+    "five": dict(T=5, H=192, I=128, E=9, K=3, on_i=True),
+    "whole_tiles": dict(T=40, H=2208, I=1120, E=32, K=2, geglu=True),
+    "whole_tiles_64": dict(T=200, H=2112, I=96, E=32, K=3, residual=True, bias=True),
     "large_values": dict(T=20, H=128, I=128, E=2, K=1, sigma=40.0),
 }
 
