@@ -73,35 +73,41 @@ int dropout_add_bwd(const dropout_add_args* a, void* stream) { return dropout_ru
 
 namespace {
 struct FwdLayout {
-  size_t x_codes, x_scales, wgu_pairs, wd_pairs, inter_codes, inter_scales, rows, parts, tiles1, tiles2, slot_of,
-      slot_tok, slot_aff, flag, total;
+  size_t x_codes, x_scales, wgu_pairs, wd_pairs, inter_codes, inter_scales, rows, row_scale, parts, tiles1, dead, tiles2,
+      slot_of, slot_tok, slot_aff, flag, done, total;
 };
+int64_t up128(int64_t v) { return (v + 127) & ~int64_t(127); }
 }  // namespace
 
 static void fwd_layout(const moe_fwd_mxfp8_args* a, FwdLayout* L) {
   const int64_t T = a->T, H = a->H, I = a->I, E = a->E, N = a->N, B = a->block_size, P = N * B;
+  const int64_t Hp = up128(H), Ip = up128(I);
+  const bool f16 = mx::fwd_down_fits(I);
   size_t o = 0;
   auto put = [&](size_t& field, int64_t bytes) {
     field = o;
     o = up256(o + size_t(bytes));
   };
-  put(L->x_codes, T * H);
-  put(L->x_scales, T * H / 32);
-  put(L->wgu_pairs, H % 128 == 0 ? E * 2 * I * (H / 32) : 0);
-  put(L->wd_pairs, I % 128 == 0 ? E * H * (I / 32) : 0);
-  put(L->inter_codes, P * I);
-  put(L->inter_scales, P * I / 32);
-  put(L->rows, P * H * 4);
+  put(L->x_codes, T * Hp);
+  put(L->x_scales, T * (Hp / 32));
+  put(L->wgu_pairs, E * 2 * I * (Hp / 32));
+  put(L->wd_pairs, E * H * (Ip / 32));
+  put(L->inter_codes, P * Ip);
+  put(L->inter_scales, P * (Ip / 32));
+  put(L->rows, P * H * (f16 ? 2 : 4));
+  put(L->row_scale, f16 ? P * ((H + 127) / 128) * 4 : 0);
   mx::Phase3Args q{};
   q.H = H; q.I = I / 2; q.N = N; q.B = B;
-  put(L->parts, mx::phase3_parts_bytes(q));
+  put(L->parts, f16 ? 0 : mx::phase3_parts_bytes(q));
   // tile starts [N+1], then the tile -> block map over every tile a block can have at the smallest tile
-  put(L->tiles1, (N + 1 + N * ((I + 63) / 64) * ((B + 127) / 128)) * 4);
-  put(L->tiles2, (N + 1 + N * ((B + 127) / 128) * ((H + 127) / 128)) * 4);
+  put(L->tiles1, (N + 1 + N * (Ip / 64) * (B / 128)) * 4);
+  put(L->dead, N * 4);
+  put(L->tiles2, (N + 1 + N * (B / 128) * ((H + 127) / 128)) * 4);
   put(L->slot_of, T * E * 4);
   put(L->slot_tok, P * 4);
   put(L->slot_aff, P * 4);
   put(L->flag, N * 4);
+  put(L->done, 4);
   L->total = o;
 }
 
@@ -117,12 +123,15 @@ static int fwd_check_shapes(const moe_fwd_mxfp8_args* a) {
   if (B != 128 && B != 256 && B != 512 && B != 1024)
     return fail(MXFP8_ERR_UNSUPPORTED, "%s: block_size %lld not in {128,256,512,1024}", me, (long long)B);
   // X's code rows, an expert's weight rows and the slots' scales are read through one buffer each, at 32-bit offsets
-  if (N > INT32_MAX / B || T > INT32_MAX / E || T > INT32_MAX / H || I > INT32_MAX / 2 / H ||
-      N * B > (int64_t(1) << 24) || 2 * I > (int64_t(1) << 23) || N * B > INT32_MAX / (I / 32))
+  const int64_t big = int64_t(1) << 40;
+  if (T > big || H > big || I > big || E > big || N > big || N > INT32_MAX / B || T > INT32_MAX / E ||
+      T > INT32_MAX / up128(H) || I > INT32_MAX / 2 / up128(H) || up128(I) > INT32_MAX / H ||
+      N * B > (int64_t(1) << 24) || 2 * I > (int64_t(1) << 23) || N * B > INT32_MAX / (up128(I) / 32))
     return fail(MXFP8_ERR_UNSUPPORTED, "%s: sizes beyond 32-bit indexing", me);
-  // one launch of each product and of the checkpoint's rows
-  if (N * ((I + 63) / 64) * (B / 128) > mx::kMaxGrid256 || N * ((H + 127) / 128) * (B / 128) > mx::kMaxGrid256 - 512 ||
-      N * ((2 * I + 15) / 16) > mx::kMaxGrid256 || T > mx::kMaxGrid256)
+  // one launch of each product, of the weights' scales and of the tokens
+  if (N * (up128(I) / 64) * (B / 128) > mx::kMaxGrid256 - 8 || N * ((H + 127) / 128) * (B / 128) > mx::kMaxGrid256 - 512 ||
+      E > (int64_t(1) << 23) / ((2 * I + 63) / 64 * ((H + 4095) / 4096) + (H + 63) / 64 * ((I + 4095) / 4096)) ||
+      T > mx::kMaxGrid256)
     return fail(MXFP8_ERR_UNSUPPORTED, "%s: more tiles than one launch takes", me);
   return MXFP8_OK;
 }
@@ -179,58 +188,57 @@ int moe_fwd_mxfp8(const moe_fwd_mxfp8_args* a, void* ws, size_t ws_bytes, void* 
   auto ints = [&](size_t off) { return reinterpret_cast<int32_t*>(w + off); };
   hipStream_t st = static_cast<hipStream_t>(stream);
   hipError_t e;
-  const bool hp = H % 128 == 0, ip = I % 128 == 0;   // the ring loops, pair-major scales
+  const bool f16 = mx::fwd_down_fits(I);
   float* slot_aff = reinterpret_cast<float*>(at(L.slot_aff));
 
   mx::MoeFwdArgs g{};
   g.T = T; g.H = H; g.I = I; g.E = E; g.N = N; g.B = B;
+  g.Hp = up128(H); g.Ip = up128(I);
   g.x_codes = at(L.x_codes); g.x_scales = at(L.x_scales);
-  g.w_codes = a->gate_up_codes; g.w_scales = hp ? at(L.wgu_pairs) : a->gate_up_scales;
+  g.w_codes = a->gate_up_codes; g.w_scales = at(L.wgu_pairs);
   g.b1 = a->gate_up_proj_bias;
   g.slot_tok = ints(L.slot_tok); g.slot_aff = slot_aff; g.b2e = a->block_to_expert; g.flag = ints(L.flag);
   g.tile_start = ints(L.tiles1);
-  g.inter_codes = at(L.inter_codes); g.inter_scales = at(L.inter_scales); g.inter_pairs = ip;
+  g.inter_codes = at(L.inter_codes); g.inter_scales = at(L.inter_scales);
   g.ckpt = a->gate_up_proj_act_checkpoint_T;
   g.ck8_codes = a->gate_up_checkpoint_codes; g.ck8_scales = a->gate_up_checkpoint_scales; g.ck8_fmt = a->fmt_checkpoint;
+  g.dead = g.ckpt || g.ck8_codes ? ints(L.dead) : nullptr;
   g.geglu = a->activation == MXFP8_ACT_GEGLU; g.on_i = a->affinity_on;
   g.rr_tiles = 2 * I * H >= kRoundRobinWeightBytes;
-  // the down projection: Phase 3's product with a contraction of I
-  mx::Phase3Args d{};
-  d.dgu_row_codes = g.inter_codes; d.dgu_row_scales = g.inter_scales;
-  d.wgu_codes = a->down_codes; d.wgu_scales = ip ? at(L.wd_pairs) : a->down_scales;
-  d.slot_tok = g.slot_tok; d.b2e = a->block_to_expert; d.flag = g.flag; d.tile_start = ints(L.tiles2);
-  d.H = H; d.I = I / 2; d.N = N; d.B = B; d.dx_slot = reinterpret_cast<float*>(at(L.rows));
-  d.conc = device_cus(st);
-  d.parts = mx::phase3_parts_bytes(d) > 0 ? at(L.parts) : nullptr;
+  // the down projection: rows in scaled fp16, or Phase 3's product with a contraction of I
+  mx::MoeFwdDownArgs d{};
+  d.H = H; d.I = I; d.Ip = g.Ip; d.N = N; d.B = B;
+  d.inter_codes = g.inter_codes; d.inter_scales = g.inter_scales;
+  d.w_codes = a->down_codes; d.w_scales = at(L.wd_pairs);
+  d.b2e = a->block_to_expert; d.flag = g.flag; d.tile_start = ints(L.tiles2);
+  d.rows = reinterpret_cast<uint16_t*>(at(L.rows)); d.row_scale = reinterpret_cast<float*>(at(L.row_scale));
   d.rr_tiles = H * I >= kRoundRobinWeightBytes;
-  d.ranges_done = 1;
-
-  mx::ScalesToPairs jobs[2];
-  int njobs = 0;
-  if (hp) jobs[njobs++] = {a->gate_up_scales, E, 2 * I, H, at(L.wgu_pairs)};
-  if (ip) jobs[njobs++] = {a->down_scales, E, H, I, at(L.wd_pairs)};
+  mx::Phase3Args d3{};
+  d3.dgu_row_codes = g.inter_codes; d3.dgu_row_scales = g.inter_scales;
+  d3.wgu_codes = a->down_codes; d3.wgu_scales = d.w_scales;
+  d3.slot_tok = g.slot_tok; d3.b2e = a->block_to_expert; d3.flag = g.flag; d3.tile_start = d.tile_start;
+  d3.H = H; d3.I = I / 2; d3.N = N; d3.B = B; d3.dx_slot = reinterpret_cast<float*>(at(L.rows));
+  d3.conc = device_cus(st);
+  d3.parts = !f16 && mx::phase3_parts_bytes(d3) > 0 ? at(L.parts) : nullptr;
+  d3.rr_tiles = d.rr_tiles;
+  d3.ranges_done = 1;
 #define STEP(call, what) \
   if ((e = (call)) != hipSuccess) return hip_status(e, what);
-  // X along H (per token: the gather by slot does not cross a row), the scales' layout, the inverse map's fill
-  const bool prep = mx::moe_prep_fits(T, H);
-  if (prep) {
-    STEP(mx::launch_moe_prep(a->hidden_states, T, H, MXFP8_E4M3, at(L.x_codes), at(L.x_scales), jobs, njobs,
-                             ints(L.slot_of), T * E, st),
-         "quantize X, weight scales to pairs, inverse map");
-  } else {
-    STEP(mx::launch_quant_rows(a->hidden_states, T, H, MXFP8_E4M3, at(L.x_codes), at(L.x_scales), st, nullptr, hp),
-         "quantize X");
-    if (njobs) STEP(mx::launch_scales_to_pairs(jobs, njobs, st), "weight scales to pairs");
-  }
-  STEP(mx::launch_fwd_setup(a->token_position_to_id, a->block_to_expert, a->expert_affinities_masked, T, E, N, B,
-                            a->num_valid_tokens, ints(L.slot_tok), slot_aff, ints(L.slot_of), ints(L.flag),
-                            mx::fwd_gate_up_ranges(g), mx::phase3_ranges(d), prep, st),
-       "slot setup");
+  const mx::MoeFwdPrep prep{a->hidden_states, T, H, g.Hp, I, g.Ip, E, N, B, at(L.x_codes), at(L.x_scales),
+                            a->gate_up_scales, at(L.wgu_pairs), a->down_scales, at(L.wd_pairs), a->token_position_to_id,
+                            a->block_to_expert, a->expert_affinities_masked, a->num_valid_tokens, ints(L.slot_tok), slot_aff,
+                            ints(L.slot_of), ints(L.flag), reinterpret_cast<unsigned*>(at(L.done)),
+                            {mx::fwd_gate_up_ranges(g), f16 ? mx::fwd_down_ranges(d) : mx::phase3_ranges(d3)}};
+  STEP(mx::launch_fwd_prep(prep, st), "X, weight scales and slots");
   STEP(mx::launch_fwd_gate_up(g, st), "gate/up projections and activation");
-  if (g.ckpt || g.ck8_codes) STEP(mx::launch_fwd_dead_ckpt(g, st), "checkpoint's dead tiles");
-  STEP(mx::launch_phase3(d, MXFP8_E4M3, MXFP8_E4M3, st), "down projection");
-  const mx::MoeCombineArgs c{d.dx_slot, ints(L.slot_of), a->affinity_on == 0 ? slot_aff : nullptr, a->down_proj_bias,
-                             a->residual, a->output_hidden_states, T, E, H, drop};
+  if (f16) {
+    STEP(mx::launch_fwd_down(d, st), "down projection");
+  } else {
+    STEP(mx::launch_phase3(d3, MXFP8_E4M3, MXFP8_E4M3, st), "down projection");
+  }
+  const mx::MoeCombineArgs c{f16 ? nullptr : d3.dx_slot, f16 ? d.rows : nullptr, f16 ? d.row_scale : nullptr, ints(L.slot_of),
+                             a->affinity_on == 0 ? slot_aff : nullptr, a->down_proj_bias, a->residual,
+                             a->output_hidden_states, T, E, H, drop};
   STEP(mx::launch_fwd_combine(c, st), "sum of the tokens' slots");
 #undef STEP
   return ok();

@@ -205,6 +205,8 @@ struct TileRangeJob {
   int32_t* start;
   TailCut* cut;
   int conc, npairs, rr;
+  int32_t* dead = nullptr;   // [N] or null: where given, the tiles of no live slot follow the live ones in the map
+                             // (dead[b]: block b's first entry there, counted from the first live tile)
 };
 hipError_t launch_tile_ranges(const int32_t* ext, int64_t N, const TileRangeJob& job, hipStream_t st);
 // Up to kListMax blocks and experts, the set-up's last kernel makes the ranges
@@ -357,22 +359,25 @@ int64_t quantize_t_grid(int64_t G, int64_t R, int64_t C);   // above kMaxGrid256
 hipError_t launch_quantize_t(const uint16_t* x, int64_t G, int64_t R, int64_t C, int fmt, uint8_t* codes,
                              uint8_t* scales, hipStream_t st);
 
+// Contractions are padded to whole pairs of 128: Hp, Ip.  Operands that the
+// library writes hold zeros there, scales are pair-major, and the caller's weight
+// rows are read up to their end (gemm_v3.hpp, RAG).
 struct MoeFwdArgs {
   int64_t T, H, I, E, N, B;
-  // scales pair-major where H % 128 == 0 (w: per expert), else row-major
-  const uint8_t* x_codes;       // [T][H]
-  const uint8_t* x_scales;
+  int64_t Hp, Ip;
+  const uint8_t* x_codes;       // [T][Hp]
+  const uint8_t* x_scales;      // [Hp/128][T][4]
   const uint8_t* w_codes;       // [E][2I][H]
-  const uint8_t* w_scales;
+  const uint8_t* w_scales;      // [E][Hp/128][2I][4]
   const uint16_t* b1;           // [E][2][I] bf16, or null
   const int32_t* slot_tok;      // [P]
   const float* slot_aff;        // [P]
   const int32_t* b2e;           // [N]
   const int32_t* flag;          // [N]: the block's extent
-  int32_t* tile_start;          // tile ranges (moe_tiles.hpp)
-  uint8_t* inter_codes;         // inter_pairs: stage-major, P rows over I, scales pair-major [I/128][P][4];
-  uint8_t* inter_scales;        // else row-major
-  int inter_pairs;              // I % 128 == 0
+  int32_t* tile_start;          // tile ranges (moe_tiles.hpp), dead tiles behind the live ones
+  int32_t* dead;                // [N]: TileRangeJob.dead (with a checkpoint)
+  uint8_t* inter_codes;         // stage-major, P rows over Ip
+  uint8_t* inter_scales;        // [Ip/128][P][4]
   uint16_t* ckpt;               // [N][2][I][B] bf16, or null and
   uint8_t* ck8_codes;           // [N][2][I][B], [N][2][I][B/32] (or null: no checkpoint)
   uint8_t* ck8_scales;
@@ -383,15 +388,54 @@ struct MoeFwdArgs {
 };
 TileRangeJob fwd_gate_up_ranges(const MoeFwdArgs& p);
 hipError_t launch_fwd_gate_up(const MoeFwdArgs& p, hipStream_t st);
-hipError_t launch_fwd_dead_ckpt(const MoeFwdArgs& p, hipStream_t st);
-// slot_tok, slot_aff, slot_of (filled with -1 before, unless told so) and the blocks' extents, then the tile
-// ranges of the two products
-hipError_t launch_fwd_setup(const int32_t* tpid, const int32_t* b2e, const float* aff, int64_t T, int64_t E, int64_t N,
-                            int64_t B, const int32_t* nvalid, int32_t* slot_tok, float* slot_aff, int32_t* slot_of,
-                            int32_t* flag, const TileRangeJob& j0, const TileRangeJob& j1, bool slot_of_filled,
-                            hipStream_t st);
+
+// The down projection of short contractions, its rows in scaled fp16 (moe_fwd_down.hpp)
+struct MoeFwdDownArgs {
+  int64_t H, I, Ip, N, B;
+  const uint8_t* inter_codes;
+  const uint8_t* inter_scales;
+  const uint8_t* w_codes;       // [E][H][I]
+  const uint8_t* w_scales;      // [E][Ip/128][H][4]
+  const int32_t* b2e;
+  const int32_t* flag;
+  int32_t* tile_start;
+  uint16_t* rows;               // [P][H] fp16
+  float* row_scale;             // [P][ceil(H/128)]
+  int rr_tiles;
+  int tiles_n;                  // set by the launcher
+};
+bool fwd_down_fits(int64_t I);  // else launch_phase3
+TileRangeJob fwd_down_ranges(const MoeFwdDownArgs& p);
+hipError_t launch_fwd_down(const MoeFwdDownArgs& p, hipStream_t st);
+
+// What comes before the products: X along H, the weights' scales, the slots
+// (slot_tok, slot_aff, slot_of, the blocks' extents) and the two products' tile ranges
+struct MoeFwdPrep {
+  const uint16_t* x;
+  int64_t T, H, Hp, I, Ip, E, N, B;
+  uint8_t* x_codes;
+  uint8_t* x_scales;
+  const uint8_t* wgu_scales;    // [E][2I][H/32] -> [E][Hp/128][2I][4]
+  uint8_t* wgu_pairs;
+  const uint8_t* wd_scales;     // [E][H][I/32] -> [E][Ip/128][H][4]
+  uint8_t* wd_pairs;
+  const int32_t* tpid;
+  const int32_t* b2e;
+  const float* aff;
+  const int32_t* nvalid;
+  int32_t* slot_tok;
+  float* slot_aff;
+  int32_t* slot_of;
+  int32_t* flag;
+  unsigned* done;               // blocks set up so far (N <= kListMax)
+  TileRangeJob jobs[2];
+};
+hipError_t launch_fwd_prep(const MoeFwdPrep& p, hipStream_t st);
+
 struct MoeCombineArgs {
-  const float* rows;            // [P][H]
+  const float* rows;            // [P][H], or null and
+  const uint16_t* rows16;       // [P][H] fp16 times row_scale [P][ceil(H/128)]
+  const float* row_scale;
   const int32_t* slot_of;       // [T][E]
   const float* slot_aff;        // [P], or null: 1
   const uint16_t* b2;           // [E][H] bf16, or null

@@ -332,7 +332,7 @@ hipError_t launch_build_blocks(const int32_t* topk, int64_t T, int64_t K, int64_
 // above T means T) so is every token at or past it.  Then the block's extent:
 // one past its last routed slot (0: no routed slot, the block takes no part in
 // the GEMMs).  Slots at or past the extent are padding, so the GEMMs skip tiles
-// that start there.  One workgroup per block; daff_slot (where given) starts as zeros.
+// that start there.  One workgroup per block; daff_slot starts as zeros.
 __global__ void __launch_bounds__(256) slot_block_kernel(const int32_t* __restrict__ tpid,
                                                          const int32_t* __restrict__ b2e,
                                                          const float* __restrict__ aff, int64_t T, int64_t E, int64_t B,
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(256) slot_block_kernel(const int32_t* __restri
     const bool ok = t >= 0 && t < Tv && e >= 0 && e < E;
     slot_tok[s] = ok ? int32_t(t) : -1;
     slot_aff[s] = ok ? aff[t * E + e] : 0.f;
-    if (daff_slot) daff_slot[s] = 0.f;
+    daff_slot[s] = 0.f;
     if (ok) {
       slot_of[t * E + e] = int32_t(s);
       ext = int(p) + 1;   // p ascends per thread
@@ -417,9 +417,9 @@ __global__ void __launch_bounds__(256) expert_list_kernel(const int32_t* __restr
 // tile -> block map start[N + 1 + t] = b for every tile t of block b, so a
 // GEMM workgroup finds its block with one load instead of a binary search
 // (a dozen dependent loads before its first DMA).  One workgroup.
-__device__ __forceinline__ void tile_ranges_any(const int32_t* __restrict__ ext, int N, int W, int other,
-                                                int32_t* __restrict__ start, TailCut* __restrict__ cut, int conc,
-                                                int npairs, int rr, int cmax) {
+__global__ void __launch_bounds__(256) tile_ranges_kernel(const int32_t* __restrict__ ext, int N, int W, int other,
+                                                          int32_t* __restrict__ start, TailCut* __restrict__ cut,
+                                                          int conc, int npairs, int rr, int cmax) {
   // With rr, the blocks whose slot tiles are all live (cmax tiles) come first,
   // in block order, and the partly filled ones after them: every round of
   // tiles then covers whole blocks of one expert (moe_tiles.hpp).
@@ -468,11 +468,6 @@ __device__ __forceinline__ void tile_ranges_any(const int32_t* __restrict__ ext,
   }
 }
 
-__global__ void __launch_bounds__(256) tile_ranges_kernel(const int32_t* __restrict__ ext, int N, int W, int other,
-                                                          int32_t* __restrict__ start, TailCut* __restrict__ cut,
-                                                          int conc, int npairs, int rr, int cmax) {
-  tile_ranges_any(ext, N, W, other, start, cut, conc, npairs, rr, cmax);
-}
 
 hipError_t launch_tile_ranges(const int32_t* ext, int64_t N, const TileRangeJob& j, hipStream_t st) {
   tile_ranges_kernel<<<1, 256, 0, st>>>(ext, int(N), j.W, j.other, j.start, j.cut, j.conc, j.npairs, j.rr, full_tiles(j));
@@ -521,35 +516,6 @@ hipError_t launch_slot_setup(const int32_t* tpid, const int32_t* b2e, const floa
   expert_count_kernel<<<unsigned(E), 256, 0, st>>>(b2e, flag, int(N), off + 1);
   expert_offsets_kernel<<<1, 256, 0, st>>>(off + 1, int(E), off);
   expert_list_kernel<<<unsigned(E), 256, 0, st>>>(b2e, flag, int(N), off, list);
-  return hipGetLastError();
-}
-
-// The MoE forward's: no expert lists, the tile ranges of its two products.
-__global__ void __launch_bounds__(kListMax) fwd_ranges_kernel(const int32_t* __restrict__ flag, int N, TileRangeJob j0,
-                                                              TileRangeJob j1, int cmax0, int cmax1) {
-  __shared__ int32_t full[kListMax / 64], part[kListMax / 64];
-  if (blockIdx.x == 0) tile_ranges_of<kListMax>(flag, N, j0, cmax0, full, part);
-  else tile_ranges_of<kListMax>(flag, N, j1, cmax1, full, part);
-}
-__global__ void __launch_bounds__(256) fwd_ranges_large_kernel(const int32_t* __restrict__ flag, int N, TileRangeJob j0,
-                                                               TileRangeJob j1, int cmax0, int cmax1) {
-  const TileRangeJob j = blockIdx.x == 0 ? j0 : j1;
-  tile_ranges_any(flag, N, j.W, j.other, j.start, j.cut, j.conc, j.npairs, j.rr, blockIdx.x == 0 ? cmax0 : cmax1);
-}
-hipError_t launch_fwd_setup(const int32_t* tpid, const int32_t* b2e, const float* aff, int64_t T, int64_t E, int64_t N,
-                            int64_t B, const int32_t* nvalid, int32_t* slot_tok, float* slot_aff, int32_t* slot_of,
-                            int32_t* flag, const TileRangeJob& j0, const TileRangeJob& j1, bool slot_of_filled,
-                            hipStream_t st) {
-  if (!slot_of_filled) {
-    hipError_t err = launch_fill_u32(reinterpret_cast<uint32_t*>(slot_of), T * E, 0xffffffffu, st);
-    if (err != hipSuccess) return err;
-  }
-  slot_block_kernel<<<unsigned(N), 256, 0, st>>>(tpid, b2e, aff, T, E, B, nvalid, slot_tok, slot_aff, slot_of, nullptr,
-                                                 flag);
-  if (N <= kListMax)
-    fwd_ranges_kernel<<<2, kListMax, 0, st>>>(flag, int(N), j0, j1, full_tiles(j0), full_tiles(j1));
-  else
-    fwd_ranges_large_kernel<<<2, 256, 0, st>>>(flag, int(N), j0, j1, full_tiles(j0), full_tiles(j1));
   return hipGetLastError();
 }
 

@@ -1,72 +1,36 @@
 // moe_fwd.hip -- the MoE forward around its two products: the gate/up kernel at
-// 128 x 128 tiles and the tile-shape dispatch, the slots' set-up, the
-// checkpoint's dead tiles, and the sum over a token's slots.
-//
-// The down projection is Phase 3's kernel (moe_phase3.hip): rows = slots, the
-// contraction over I instead of 2I, each slot's fp32 row stored on its own.
+// 128 x 128 tiles and the tile-shape dispatch, and the sum over a token's slots.
 #include "moe_fwd_gate_up.hpp"
-#include "moe_lists.hpp"
 #include "philox.hpp"
 
 namespace mx {
 
-template hipError_t fwd_gate_up_launch<128, 128, false>(MoeFwdArgs, hipStream_t);
-extern template hipError_t fwd_gate_up_launch<128, 128, true>(MoeFwdArgs, hipStream_t);
-extern template hipError_t fwd_gate_up_launch<256, 256, false>(MoeFwdArgs, hipStream_t);
-extern template hipError_t fwd_gate_up_launch<256, 128, false>(MoeFwdArgs, hipStream_t);
+template hipError_t fwd_gate_up_launch<128, 128>(MoeFwdArgs, hipStream_t);
+extern template hipError_t fwd_gate_up_launch<256, 256>(MoeFwdArgs, hipStream_t);
+extern template hipError_t fwd_gate_up_launch<256, 128>(MoeFwdArgs, hipStream_t);
 
 namespace {
-struct Tile {
+struct Shape {
   int m, n;
 };
-Tile fwd_tile(const MoeFwdArgs& p) {
-  if (p.H % 128 != 0 || p.I < 128) return {128, 128};
-  return {256, p.B >= 256 ? 256 : 128};
+// 256 x 256 tiles from contractions and blocks that are long enough for them (H = 4096: 3.7 ms against 5.1
+// at 128 x 128; H = 2048: 288 us against 308); 128 x 128, two workgroups a CU, where a block has 128 slots
+// (H = 1536: 385 us against 420 at 256 x 128).
+Shape fwd_shape(const MoeFwdArgs& p) {
+  if (p.I < 128 || p.B < 256 || p.H < 1024) return {128, 128};
+  return {256, 256};
 }
 }  // namespace
 
 TileRangeJob fwd_gate_up_ranges(const MoeFwdArgs& p) {
-  const Tile t = fwd_tile(p);
-  return {t.n, int((p.I + t.m / 2 - 1) / (t.m / 2)), int(p.B), p.tile_start, nullptr, 0, 0, p.rr_tiles};
+  const Shape t = fwd_shape(p);
+  return {t.n, int(p.Ip / (t.m / 2)), int(p.B), p.tile_start, nullptr, 0, 0, p.rr_tiles, p.dead};
 }
 
 hipError_t launch_fwd_gate_up(const MoeFwdArgs& p, hipStream_t st) {
-  if (p.H % 128 != 0) return fwd_gate_up_launch<128, 128, true>(p, st);
-  const Tile t = fwd_tile(p);
-  if (t.m == 128) return fwd_gate_up_launch<128, 128, false>(p, st);
-  return t.n == 256 ? fwd_gate_up_launch<256, 256, false>(p, st) : fwd_gate_up_launch<256, 128, false>(p, st);
-}
-
-// ---------------------------------------------------------------------------
-// The checkpoint's slots behind a block's last live tile: zeros (and scale byte
-// 0, an all-zero group's).  One workgroup per 16 rows of a block.
-namespace {
-constexpr int kDeadRows = 16;
-__global__ void __launch_bounds__(256) fwd_dead_ckpt_kernel(MoeFwdArgs p, int W, int parts) {
-  const int b = blockIdx.x / parts, part = blockIdx.x % parts;
-  const int64_t s0 = int64_t((p.flag[b] + W - 1) / W) * W;   // the first slot of no live tile
-  if (s0 >= p.B) return;
-  const int64_t r0 = int64_t(part) * kDeadRows, rows = 2 * p.I - r0 < kDeadRows ? 2 * p.I - r0 : kDeadRows;
-  const int64_t base = int64_t(b) * 2 * p.I + r0;
-  const int per = int((p.B - s0) * (p.ckpt ? 2 : 1) / 16);   // 16-byte runs a row
-  for (int k = threadIdx.x; k < rows * per; k += 256) {
-    const int64_t row = base + k / per, c = k % per;
-    uint8_t* dst = p.ckpt ? reinterpret_cast<uint8_t*>(p.ckpt + row * p.B + s0) : p.ck8_codes + row * p.B + s0;
-    store_nt(dst + 16 * c, make_uint4(0u, 0u, 0u, 0u));
-  }
-  if (!p.ckpt) {
-    const int words = int((p.B - s0) / 128);   // of 4 scale bytes; W % 128 == 0
-    for (int k = threadIdx.x; k < rows * words; k += 256)
-      *reinterpret_cast<uint32_t*>(p.ck8_scales + (base + k / words) * (p.B / 32) + s0 / 32 + 4 * (k % words)) = 0u;
-  }
-}
-}  // namespace
-
-hipError_t launch_fwd_dead_ckpt(const MoeFwdArgs& p, hipStream_t st) {
-  const int64_t parts = (2 * p.I + kDeadRows - 1) / kDeadRows;
-  if (parts * p.N > kMaxGrid256) return hipErrorInvalidValue;
-  fwd_dead_ckpt_kernel<<<unsigned(parts * p.N), 256, 0, st>>>(p, fwd_tile(p).n, int(parts));
-  return hipGetLastError();
+  const Shape t = fwd_shape(p);
+  if (t.m == 128) return fwd_gate_up_launch<128, 128>(p, st);
+  return t.n == 256 ? fwd_gate_up_launch<256, 256>(p, st) : fwd_gate_up_launch<256, 128>(p, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -76,7 +40,8 @@ hipError_t launch_fwd_dead_ckpt(const MoeFwdArgs& p, hipStream_t st) {
 // the token's slots by itself, 64 experts a ballot, and a thread summing 8
 // columns: 16-byte stores, and one counter of the dropout mask.
 namespace {
-template <int TPT>
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+template <int TPT, bool F16>
 __global__ void __launch_bounds__(256) fwd_combine_kernel(MoeCombineArgs p) {
   const int64_t t = int64_t(blockIdx.x) * (256 / TPT) + threadIdx.x / TPT;
   if (t >= p.T) return;
@@ -92,8 +57,9 @@ __global__ void __launch_bounds__(256) fwd_combine_kernel(MoeCombineArgs p) {
       while (live) {
         // up to 4 slots at a time, their rows loaded before the first is added
         constexpr int U = 4;
-        float4 v[U][2];
-        float a[U];
+        float4 v[F16 ? 1 : U][2];
+        u32x4_t v16[F16 ? U : 1];
+        float a[U], sc[F16 ? U : 1];
         uint4 bias[U];
         int n = 0;
 #pragma unroll
@@ -105,10 +71,15 @@ __global__ void __launch_bounds__(256) fwd_combine_kernel(MoeCombineArgs p) {
             const int64_t s = __builtin_amdgcn_readlane(so, l);
             a[k] = p.slot_aff ? p.slot_aff[s] : 1.f;
             if (in) {
-              const f32x4_t* row = reinterpret_cast<const f32x4_t*>(p.rows + s * p.H + 8 * c);
-              const f32x4_t x = __builtin_nontemporal_load(row), y = __builtin_nontemporal_load(row + 1);
-              v[k][0] = make_float4(x[0], x[1], x[2], x[3]);
-              v[k][1] = make_float4(y[0], y[1], y[2], y[3]);
+              if constexpr (F16) {
+                v16[k] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p.rows16 + s * p.H + 8 * c));
+                sc[k] = p.row_scale[s * ((p.H + 127) / 128) + c / 16];
+              } else {
+                const f32x4_t* row = reinterpret_cast<const f32x4_t*>(p.rows + s * p.H + 8 * c);
+                const f32x4_t x = __builtin_nontemporal_load(row), y = __builtin_nontemporal_load(row + 1);
+                v[k][0] = make_float4(x[0], x[1], x[2], x[3]);
+                v[k][1] = make_float4(y[0], y[1], y[2], y[3]);
+              }
               if (p.b2) bias[k] = *reinterpret_cast<const uint4*>(p.b2 + (e0 + l) * p.H + 8 * c);
             }
             n = k + 1;
@@ -118,7 +89,19 @@ __global__ void __launch_bounds__(256) fwd_combine_kernel(MoeCombineArgs p) {
 #pragma unroll
         for (int k = 0; k < U; ++k) {
           if (k >= n) continue;
-          float x[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w, v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
+          float x[8];
+          if constexpr (F16) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t pair = v16[k][j];   // (a bit cast of the vector's element itself gives element 0)
+              const f16x2_t q = __builtin_bit_cast(f16x2_t, pair);
+              x[2 * j] = float(q[0]) * sc[k];
+              x[2 * j + 1] = float(q[1]) * sc[k];
+            }
+          } else {
+            x[0] = v[k][0].x; x[1] = v[k][0].y; x[2] = v[k][0].z; x[3] = v[k][0].w;
+            x[4] = v[k][1].x; x[5] = v[k][1].y; x[6] = v[k][1].z; x[7] = v[k][1].w;
+          }
           if (p.b2) {
             const uint32_t w[4] = {bias[k].x, bias[k].y, bias[k].z, bias[k].w};
 #pragma unroll
@@ -157,9 +140,13 @@ hipError_t launch_fwd_combine(const MoeCombineArgs& p, hipStream_t st) {
   const int tpt = p.H <= 512 ? 64 : p.H <= 1024 ? 128 : 256;   // 8 columns a thread
   const int64_t per = 256 / tpt, grid = (p.T + per - 1) / per;
   if (grid > kMaxGrid256) return hipErrorInvalidValue;
-  if (tpt == 64) fwd_combine_kernel<64><<<unsigned(grid), 256, 0, st>>>(p);
-  else if (tpt == 128) fwd_combine_kernel<128><<<unsigned(grid), 256, 0, st>>>(p);
-  else fwd_combine_kernel<256><<<unsigned(grid), 256, 0, st>>>(p);
+  auto go = [&](auto f16) {
+    if (tpt == 64) fwd_combine_kernel<64, f16()><<<unsigned(grid), 256, 0, st>>>(p);
+    else if (tpt == 128) fwd_combine_kernel<128, f16()><<<unsigned(grid), 256, 0, st>>>(p);
+    else fwd_combine_kernel<256, f16()><<<unsigned(grid), 256, 0, st>>>(p);
+  };
+  if (p.rows16) go(std::true_type{});
+  else go(std::false_type{});
   return hipGetLastError();
 }
 

@@ -20,7 +20,10 @@
 // fragments of 32 in turn: a lane's accumulators then hold gate and up of the
 // same 16 (i, p), 16 of a group's 32 i with the lane's other half holding the
 // rest, so activation, product and group maxima stay in registers.  The tile
-// columns are the slots, whose X code rows are gathered by token.
+// columns are the slots, whose X code rows are gathered by token.  Tiles cover
+// i up to Ip, the contraction of the down projection in whole pairs: groups from
+// I on get zeros.  Workgroups whose tile holds no routed slot write the
+// checkpoint's zeros there.
 #pragma once
 #include "gemm_v2.hpp"
 #include "gemm_v3.hpp"
@@ -43,9 +46,58 @@ __device__ __forceinline__ int64_t fwd_weight_row(int r, int64_t i0, int64_t I) 
   return i < I ? (f & 1) * I + i : -1;
 }
 
-template <int BM, int BN>
+// 256 x 256 tiles of aligned rows run the pair-slot ring, whose DMA moves whole
+// lines of row-major operands; the others the four-slot ring.
+template <int BM, int BN, bool RAG>
+constexpr bool kFwdPairRing = BM == 256 && BN == 256 && !RAG;
+template <int BM, int BN, bool RAG>
 constexpr int fwd_ring_smem() {
-  return BM == 256 && BN == 256 ? v4::smem_bytes(BM, BN) : v3::smem_bytes(BM, BN);
+  return kFwdPairRing<BM, BN, RAG> ? v4::smem_bytes(BM, BN) : v3::smem_bytes(BM, BN);
+}
+
+// This workgroup's tile: block b, slot tile tn, i tile tm; live: it holds a
+// routed slot.  false: nothing to do.
+struct FwdTile {
+  int b, tm, tn;
+  bool live;
+};
+template <int BN>
+__device__ __forceinline__ bool fwd_tile_of(const MoeFwdArgs& p, bool want_dead, FwdTile& t) {
+  const int N = int(p.N), wg = blockIdx.x;
+  const int total = p.tile_start[N], t8 = (total + 7) & ~7;
+  const int id = wg < t8 && !p.rr_tiles ? v2::xcd_remap(wg, t8) : wg;
+  t.live = id < total;
+  if (!t.live && (!want_dead || id >= N * p.tiles_m * int(p.B / BN))) return false;
+  t.b = p.tile_start[N + 1 + id];
+  const int slots = (p.flag[t.b] + BN - 1) / BN;
+  if (t.live) {
+    v2::grouped_tile<8>(id - p.tile_start[t.b], p.tiles_m, slots, t.tm, t.tn);
+  } else {
+    const int local = id - p.dead[t.b];
+    t.tn = slots + local / p.tiles_m;
+    t.tm = local % p.tiles_m;
+  }
+  return true;
+}
+
+// The checkpoint of a tile without routed slots: zeros (scale byte 0: an all-zero group's).
+template <int BM, int BN, int CK>
+__device__ __forceinline__ void fwd_zero_ckpt(const MoeFwdArgs& p, const FwdTile& t) {
+  const int64_t i0 = int64_t(t.tm) * (BM / 2), s0 = int64_t(t.tn) * BN;
+  const int rows = p.I - i0 < BM / 2 ? int(p.I - i0) : BM / 2;   // not positive: past I
+  constexpr int RUNS = BN * (CK == 1 ? 2 : 1) / 16;             // 16-byte runs a row
+  for (int part = 0; part < 2; ++part) {
+    const int64_t row0 = (int64_t(t.b) * 2 + part) * p.I + i0;
+    for (int k = threadIdx.x; k < rows * RUNS; k += v2::kThreads) {
+      const int64_t at = (row0 + k / RUNS) * p.B + s0;
+      uint8_t* dst = (CK == 1 ? reinterpret_cast<uint8_t*>(p.ckpt + at) : p.ck8_codes + at) + 16 * (k % RUNS);
+      store_nt(dst, make_uint4(0u, 0u, 0u, 0u));
+    }
+    if constexpr (CK != 1) {
+      for (int k = threadIdx.x; k < rows * (BN / 128); k += v2::kThreads)
+        *reinterpret_cast<uint32_t*>(p.ck8_scales + (row0 + k / (BN / 128)) * (p.B / 32) + s0 / 32 + 4 * (k % (BN / 128))) = 0u;
+    }
+  }
 }
 
 // One fragment pair's checkpoint (32 rows i x 32 slots, words gate | up << 16)
@@ -91,18 +143,20 @@ __device__ __forceinline__ void fwd_store_ckpt(const MoeFwdArgs& p, int b, int64
   }
 }
 
-template <int BM, int BN, bool GENERIC, bool GEGLU, int CK>
+template <int BM, int BN, bool RAG, bool GEGLU, int CK>
 __global__ void __launch_bounds__(v2::kThreads) fwd_gate_up_kernel(MoeFwdArgs p) {
-  constexpr int SMEM = GENERIC ? 2 * (BM + BN) * v2::BK : fwd_ring_smem<BM, BN>();
+  constexpr int SMEM = fwd_ring_smem<BM, BN, RAG>();
   static_assert(SMEM >= 4 * kCkWaveBytes, "the checkpoint's staging fits the ring");
   __shared__ __attribute__((aligned(16))) uint8_t smem[SMEM];
   constexpr int FM = BM / 64, FN = BN / 64;
-  BlockTiles bt;
-  if (!block_tile(p.tile_start, p.flag, BN, int(p.N), blockIdx.x, p.rr_tiles, bt)) return;
-  const int b = bt.b;
-  int tm, tn;
-  v2::grouped_tile<8>(bt.local, p.tiles_m, bt.slots, tm, tn);
-  const int64_t i0 = int64_t(tm) * (BM / 2), n0 = int64_t(tn) * BN;
+  FwdTile tile;
+  if (!fwd_tile_of<BN>(p, CK != 0, tile)) return;
+  if (CK != 0 && !tile.live) {
+    fwd_zero_ckpt<BM, BN, CK>(p, tile);
+    return;
+  }
+  const int b = tile.b;
+  const int64_t i0 = int64_t(tile.tm) * (BM / 2), n0 = int64_t(tile.tn) * BN;
   const int64_t sbase = int64_t(b) * p.B, e = p.b2e[b];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, h = lane >> 5, r = lane & 31;
   const int wm = wave >> 1, wn = wave & 1;
@@ -111,30 +165,24 @@ __global__ void __launch_bounds__(v2::kThreads) fwd_gate_up_kernel(MoeFwdArgs p)
   auto tok_of = [&](int q) -> int64_t { const int64_t s = n0 + q; return s < B_ ? int64_t(st[s]) : -1; };
   auto row_of = [&](int q) -> int64_t { return fwd_weight_row<BM>(q, i0, I_); };
   const uint8_t* wc = p.w_codes + e * 2 * p.I * p.H;
-  const uint8_t* ws = p.w_scales + e * 2 * p.I * (p.H / 32);
+  const uint8_t* ws = p.w_scales + e * 2 * p.I * (p.Hp / 32);
   v16f acc[FM][FN];
-  if constexpr (GENERIC) {
-    v2::Operand<BM, FM> A;
-    v2::Operand<BN, FN> B;
-    v2::setup_gather(A, wc, ws, 2 * p.I, p.H, p.H / 32, wm * (BM / 2), row_of);
-    v2::setup_gather(B, p.x_codes, p.x_scales, p.T, p.H, p.H / 32, wn * (BN / 2), tok_of);
-    v2::mainloop<BM, BN, v2::kFp8, kE4M3, kE4M3, true>(A, B, int((p.H + v2::BK - 1) / v2::BK), v2::KMapPlain{p.H}, smem,
-                                                       acc);
-  } else {
+  if (i0 < p.I) {   // else the tile lies between I and Ip: no products
     v3::ScaleDma<BM, BN> sd;
-    v3::setup_scales_map(sd, ws, 2 * p.I, 2 * p.I * (p.H / 32), row_of, p.x_scales, p.T, p.T * (p.H / 32), tok_of);
-    if constexpr (BM == 256 && BN == 256) {
+    v3::setup_scales_map(sd, ws, 2 * p.I, 2 * p.I * (p.Hp / 32), row_of, p.x_scales, p.T, p.T * (p.Hp / 32), tok_of);
+    if constexpr (kFwdPairRing<BM, BN, RAG>) {
       v4::Op<BM> A;
       v4::Op<BN> B;
       v4::setup_gather(A, wc, 2 * p.I, p.H, row_of);
-      v4::setup_gather(B, p.x_codes, p.T, p.H, tok_of);
-      v4::mainloop<BM, BN, v3::kFp8, kE4M3, kE4M3>(A, B, &sd, int(p.H / v4::PK), v4::KMapPlain{}, smem, acc);
+      v4::setup_gather(B, p.x_codes, p.T, p.Hp, tok_of);
+      v4::mainloop<BM, BN, v3::kFp8, kE4M3, kE4M3>(A, B, &sd, int(p.Hp / v4::PK), v4::KMapPlain{}, smem, acc);
     } else {
       v3::Op<BM> A;
       v3::Op<BN> B;
       v3::setup_gather(A, wc, 2 * p.I, p.H, row_of);
-      v3::setup_gather(B, p.x_codes, p.T, p.H, tok_of);
-      v3::mainloop<BM, BN, v3::kFp8, kE4M3, kE4M3>(A, B, &sd, int(p.H / v3::SK), v3::KMapPlain{}, smem, acc);
+      v3::setup_gather(B, p.x_codes, p.T, p.Hp, tok_of);
+      v3::mainloop<BM, BN, v3::kFp8, kE4M3, kE4M3, v3::KMapPlain, RAG ? 1 : 0>(A, B, &sd, int(p.Hp / v3::SK),
+                                                                              v3::KMapPlain{}, smem, acc, uint32_t(p.H));
     }
   }
   if constexpr (CK != 0) __syncthreads();   // every wave is done with the ring: its bytes stage the checkpoint
@@ -151,7 +199,14 @@ __global__ void __launch_bounds__(v2::kThreads) fwd_gate_up_kernel(MoeFwdArgs p)
   }
   v2::static_for<FM / 2>([&](auto Q) {
     const int64_t i = i0 + wm * (BM / 4) + 32 * int(Q);   // the group's first i; I % 32 == 0: all of it or nothing
-    if (i < p.I) {
+    if (i >= p.I) {   // up to Ip: zeros
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const int64_t slot = sbase + n0 + wn * (BN / 2) + 32 * j + r;
+        *reinterpret_cast<uint4*>(p.inter_codes + stage_major_off(slot, i + 16 * h, P, p.Ip)) = make_uint4(0u, 0u, 0u, 0u);
+        if (h == 0) p.inter_scales[((i >> 7) * P + slot) * 4 + (i >> 5 & 3)] = 0;
+      }
+    } else {
       float bg[16], bu[16];
       if (p.b1) {
         const uint16_t* row = p.b1 + e * 2 * p.I + i + 4 * h;
@@ -192,11 +247,8 @@ __global__ void __launch_bounds__(v2::kThreads) fwd_gate_up_kernel(MoeFwdArgs p)
         const auto x = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
         const auto y = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
         const int64_t slot = sbase + s + r, at = i + 16 * h;
-        uint8_t* dst = p.inter_codes + (p.inter_pairs ? stage_major_off(slot, at, P, p.I) : slot * p.I + at);
-        *reinterpret_cast<uint4*>(dst) = make_uint4(x[0], x[1], y[0], y[1]);
-        if (h == 0)
-          p.inter_scales[p.inter_pairs ? ((i >> 7) * P + slot) * 4 + (i >> 5 & 3) : slot * (p.I / 32) + (i >> 5)] =
-              uint8_t(X + 127);
+        *reinterpret_cast<uint4*>(p.inter_codes + stage_major_off(slot, at, P, p.Ip)) = make_uint4(x[0], x[1], y[0], y[1]);
+        if (h == 0) p.inter_scales[((i >> 7) * P + slot) * 4 + (i >> 5 & 3)] = uint8_t(X + 127);
 #endif
         if constexpr (CK != 0) {
           __builtin_amdgcn_wave_barrier();   // the wave's own LDS operations run in order
@@ -209,22 +261,26 @@ __global__ void __launch_bounds__(v2::kThreads) fwd_gate_up_kernel(MoeFwdArgs p)
 }
 
 // ---------------------------------------------------------------------------
-template <int BM, int BN, bool G>
+template <int BM, int BN>
 hipError_t fwd_gate_up_launch(MoeFwdArgs p, hipStream_t st) {
-  p.tiles_m = int((p.I + BM / 2 - 1) / (BM / 2));
+  p.tiles_m = int(p.Ip / (BM / 2));
   const int64_t blocks = (int64_t(p.tiles_m) * (p.B / BN) * p.N + 7) & ~int64_t(7);   // every tile, rounded to 8
   if (blocks > kMaxGrid256) return hipErrorInvalidValue;
-  auto go = [&](auto geglu, auto ck) {
-    fwd_gate_up_kernel<BM, BN, G, geglu(), ck()><<<unsigned(blocks), v2::kThreads, 0, st>>>(p);
+  auto go = [&](auto rag, auto geglu, auto ck) {
+    fwd_gate_up_kernel<BM, BN, rag(), geglu(), ck()><<<unsigned(blocks), v2::kThreads, 0, st>>>(p);
   };
-  auto kind = [&](auto geglu) {
-    if (p.ckpt) go(geglu, std::integral_constant<int, 1>{});
-    else if (!p.ck8_codes) go(geglu, std::integral_constant<int, 0>{});
-    else if (p.ck8_fmt == kE4M3) go(geglu, std::integral_constant<int, 2 + kE4M3>{});
-    else go(geglu, std::integral_constant<int, 2 + kE5M2>{});
+  auto kind = [&](auto rag, auto geglu) {
+    if (p.ckpt) go(rag, geglu, std::integral_constant<int, 1>{});
+    else if (!p.ck8_codes) go(rag, geglu, std::integral_constant<int, 0>{});
+    else if (p.ck8_fmt == kE4M3) go(rag, geglu, std::integral_constant<int, 2 + kE4M3>{});
+    else go(rag, geglu, std::integral_constant<int, 2 + kE5M2>{});
   };
-  if (p.geglu) kind(std::true_type{});
-  else kind(std::false_type{});
+  auto act = [&](auto rag) {
+    if (p.geglu) kind(rag, std::true_type{});
+    else kind(rag, std::false_type{});
+  };
+  if (p.H % 128) act(std::true_type{});
+  else act(std::false_type{});
   return hipGetLastError();
 }
 

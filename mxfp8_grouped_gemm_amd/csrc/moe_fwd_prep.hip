@@ -1,0 +1,281 @@
+// moe_fwd_prep.hip -- what the MoE forward makes before its two products.
+//
+//   fwd_prep_kernel   X along H to codes (rows padded to Hp with zeros, scales
+//                     pair-major), both weights' scales pair-major and padded,
+//                     and slot_of filled with -1; for a small layer one more
+//                     workgroup does the rest as well
+//   fwd_slots_kernel  a workgroup per block: its slots' tokens and affinities, the
+//                     inverse map and its extent; the last one to finish makes the
+//                     tile ranges of the two products (up to kListMax blocks)
+//   fwd_ranges_kernel the ranges of more blocks, a workgroup for each product
+// X is bound by memory; the rest is launches and latency (T = 256, E = 4: one
+// launch of 5 us where four of 2.5 to 4 us stood).
+#include "kernels.hpp"
+#include "moe_tiles.hpp"
+#include "mx_device.hpp"
+
+namespace mx {
+
+namespace {
+constexpr int kThreads = 256;
+constexpr int64_t kSmallSlots = 4096, kSmallPairs = 16384;   // a small layer: slots, T * E
+constexpr int kSmallBlocks = int(kSmallSlots / 128);
+
+bool small_layer(const MoeFwdPrep& p) { return p.N * p.B <= kSmallSlots && p.T * p.E <= kSmallPairs; }
+
+// ---------------------------------------------------------------------------
+// X: a thread takes 8 columns, 4 lanes a group of 32.
+__device__ __forceinline__ void quant_x(const MoeFwdPrep& p, unsigned wg, unsigned wgs) {
+  constexpr int U = 4;   // chunks of a thread, their loads issued together
+  const uint32_t per = uint32_t(p.Hp / 8), n = uint32_t(p.T) * per, stride = wgs * kThreads;   // T * Hp < 2^32
+  for (uint32_t c0 = wg * kThreads + threadIdx.x; c0 < n; c0 += U * stride) {
+    uint4 v[U];
+    uint32_t row[U], col[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t c = c0 + u * stride;
+      row[u] = c / per;
+      col[u] = (c - row[u] * per) * 8;
+      v[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (c < n && col[u] < p.H) v[u] = *reinterpret_cast<const uint4*>(p.x + int64_t(row[u]) * p.H + col[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+      uint32_t m = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) m = absmax_bf16x2(m, w[k]);
+      m = max(m & 0xffffu, m >> 16);
+      m = max(m, uint32_t(__shfl_xor(int(m), 1, 64)));   // n is a multiple of 16: a group's lanes stay together
+      m = max(m, uint32_t(__shfl_xor(int(m), 2, 64)));
+      const int X = scale_exp<kE4M3>(m << 16);
+      const uint32_t lim = bf16_limit<kE4M3>(X) * 0x10001u;
+      const float s = cvt_scale(X);
+      if (c0 + u * stride < n) {
+        const uint32_t lo = encode_bf16x4<kE4M3>(clamp_bf16x2(w[0], lim), clamp_bf16x2(w[1], lim), s);
+        const uint32_t hi = encode_bf16x4<kE4M3>(clamp_bf16x2(w[2], lim), clamp_bf16x2(w[3], lim), s);
+        *reinterpret_cast<uint2*>(p.x_codes + int64_t(row[u]) * p.Hp + col[u]) = make_uint2(lo, hi);
+        if ((col[u] & 31) == 0)
+          p.x_scales[((col[u] >> 7) * p.T + row[u]) * 4 + (col[u] >> 5 & 3)] = col[u] < p.H ? uint8_t(X + 127) : uint8_t(0);
+      }
+    }
+  }
+}
+
+// Weight scales [E][rows][G] -> [E][kp][rows][4], bytes from G on 0: a workgroup
+// turns 64 rows x 32 words through LDS.
+struct PairsJob {
+  const uint8_t* in;
+  uint32_t* out;
+  int64_t rows, G, kp;
+  unsigned gx, gy, n;   // workgroups: along the words, the rows, in all
+};
+PairsJob pairs_job(const uint8_t* in, uint8_t* out, int64_t E, int64_t rows, int64_t k) {
+  PairsJob j{in, reinterpret_cast<uint32_t*>(out), rows, k / 32, (k + 127) / 128, 0, 0, 0};
+  j.gx = unsigned((j.kp + 31) / 32);
+  j.gy = unsigned((rows + 63) / 64);
+  j.n = unsigned(E) * j.gx * j.gy;
+  return j;
+}
+__device__ __forceinline__ void scale_pairs(const PairsJob& j, unsigned id, uint32_t (*tile)[65]) {
+  const unsigned per = j.gx * j.gy, g = id / per, yx = id - g * per, y = yx / j.gx, x = yx - y * j.gx;
+  const int64_t p0 = int64_t(x) * 32, r0 = int64_t(y) * 64;
+  const uint8_t* src = j.in + g * j.rows * j.G;
+  uint32_t* dst = j.out + g * j.rows * j.kp;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int i = threadIdx.x + kThreads * k, r = i >> 5, q = i & 31;
+    if (r0 + r < j.rows && p0 + q < j.kp) {
+      const uint8_t* s = src + (r0 + r) * j.G + 4 * (p0 + q);
+      uint32_t w = 0;
+      if (j.G % 4 == 0) {
+        w = *reinterpret_cast<const uint32_t*>(s);
+      } else {
+        const int64_t left = j.G - 4 * (p0 + q);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) w |= b < left ? uint32_t(s[b]) << (8 * b) : 0u;
+      }
+      tile[q][r] = w;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int i = threadIdx.x + kThreads * k, q = i >> 6, r = i & 63;
+    if (r0 + r < j.rows && p0 + q < j.kp) dst[(p0 + q) * j.rows + r0 + r] = tile[q][r];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Tile ranges (moe_tiles.hpp) of up to any number of blocks by one workgroup of
+// TH threads; ext(b): block b's extent.  lds: TH / 64 words of 8 bytes.
+template <int TH, class Ext>
+__device__ __forceinline__ void make_ranges(const Ext& ext, int N, const TileRangeJob& j, uint64_t* lds) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, cmax = (j.blk + j.W - 1) / j.W * j.other;
+  auto tiles = [&](int b) { return (ext(b) + j.W - 1) / j.W * j.other; };
+  uint64_t carry = 0;   // tiles so far: of fully live blocks (with rr) in the high word, of the others in the low
+  for (int b0 = 0; b0 < N; b0 += TH) {
+    const int b = b0 + threadIdx.x, c = b < N ? tiles(b) : 0;
+    const bool full = j.rr && c == cmax;
+    const uint64_t mine = full ? uint64_t(c) << 32 : uint64_t(c);
+    uint64_t x = mine;
+    for (int o = 1; o < 64; o <<= 1) {
+      const uint64_t y = __shfl_up(static_cast<unsigned long long>(x), o, 64);
+      if (lane >= o) x += y;
+    }
+    if (lane == 63) lds[wave] = x;
+    __syncthreads();
+    uint64_t before = carry + x - mine;
+    for (int w = 0; w < TH / 64; ++w) {
+      const uint64_t s = lds[w];
+      before += w < wave ? s : 0;
+      carry += s;
+    }
+    __syncthreads();
+    if (b < N) {
+      j.start[b] = int32_t(full ? before >> 32 : before);   // among its kind, for now
+      if (j.dead) j.dead[b] = b * cmax - int32_t(before >> 32) - int32_t(before);
+    }
+  }
+  const int nfull = int(carry >> 32), total = nfull + int32_t(carry);
+  int32_t* map = j.start + N + 1;
+  for (int b = threadIdx.x; b < N; b += TH) {   // the thread's own entries
+    const int c = tiles(b), t0 = j.start[b] + (j.rr && c == cmax ? 0 : nfull);
+    j.start[b] = t0;
+    for (int t = t0; t < t0 + c; ++t) map[t] = b;
+    if (j.dead) {
+      const int d0 = j.dead[b] + total;
+      j.dead[b] = d0;
+      for (int t = d0; t < d0 + cmax - c; ++t) map[t] = b;
+    }
+  }
+  if (threadIdx.x == 0) {
+    j.start[N] = total;
+    if (j.cut) {   // the tail cut of each XCD
+      int base = 0;
+      for (int x = 0; x < 8; ++x) {
+        TailCut k = tail_cut_one(total, x, j.rr, j.conc, j.npairs);
+        k.base = base;
+        base += k.tail * (k.S - 1);
+        j.cut[x] = k;
+      }
+    }
+  }
+}
+
+// One slot: its token and affinity (padding: -1, 0), the inverse map.  Padding
+// is what holds no token below the count of valid ones, or lies in a block of no expert.
+__device__ __forceinline__ bool put_slot(const MoeFwdPrep& p, int64_t s, int64_t Tv, int64_t e) {
+  const int64_t t = p.tpid[s];
+  const bool ok = t >= 0 && t < Tv && e >= 0 && e < p.E;
+  p.slot_tok[s] = ok ? int32_t(t) : -1;
+  p.slot_aff[s] = ok ? p.aff[t * p.E + e] : 0.f;
+  if (ok) p.slot_of[t * p.E + e] = int32_t(s);
+  return ok;
+}
+__device__ __forceinline__ int64_t valid_tokens(const MoeFwdPrep& p) {
+  const int64_t n = p.nvalid ? int64_t(*p.nvalid) : p.T;
+  return n < 0 ? 0 : (n < p.T ? n : p.T);
+}
+
+__global__ void __launch_bounds__(kThreads) fwd_prep_kernel(MoeFwdPrep p, PairsJob j0, PairsJob j1, unsigned nq,
+                                                            unsigned nf, int small) {
+  __shared__ uint32_t tile[32][65];
+  __shared__ int ext[kSmallBlocks];
+  __shared__ uint64_t lds[kThreads / 64];
+  const unsigned wg = blockIdx.x;
+  if (small && wg == 0) {   // the whole set-up of the slots
+    for (int64_t k = threadIdx.x; k < p.T * p.E; k += kThreads) p.slot_of[k] = -1;
+    for (int b = threadIdx.x; b < p.N; b += kThreads) ext[b] = 0;
+    __syncthreads();
+    const int64_t Tv = valid_tokens(p);
+    const int P = int(p.N * p.B), B = int(p.B);
+#pragma unroll 4
+    for (int s = threadIdx.x; s < P; s += kThreads) {
+      const int b = s / B;
+      if (put_slot(p, s, Tv, p.b2e[b])) atomicMax(&ext[b], s - b * B + 1);
+    }
+    __syncthreads();
+    for (int b = threadIdx.x; b < p.N; b += kThreads) p.flag[b] = ext[b];
+    for (int k = 0; k < 2; ++k) make_ranges<kThreads>([&](int b) { return ext[b]; }, int(p.N), p.jobs[k], lds);
+    return;
+  }
+  unsigned id = wg - (small ? 1 : 0);
+  if (id == 0 && threadIdx.x == 0) *p.done = 0;   // read by the next launch only
+  if (id < nq) {
+    quant_x(p, id, nq);
+    return;
+  }
+  id -= nq;
+  if (id < j0.n) {
+    scale_pairs(j0, id, tile);
+    return;
+  }
+  id -= j0.n;
+  if (id < j1.n) {
+    scale_pairs(j1, id, tile);
+    return;
+  }
+  id -= j1.n;
+  const int64_t n = p.T * p.E, i = (int64_t(id) * kThreads + threadIdx.x) * 4;
+  if (i + 4 <= n) {
+    *reinterpret_cast<int4*>(p.slot_of + i) = int4{-1, -1, -1, -1};
+  } else {
+    for (int64_t k = i; k < n; ++k) p.slot_of[k] = -1;
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) fwd_slots_kernel(MoeFwdPrep p, int ranges) {
+  __shared__ int red[kThreads / 64];
+  __shared__ uint64_t lds[kThreads / 64];
+  __shared__ int last;
+  const int b = blockIdx.x;
+  const int64_t Tv = valid_tokens(p), e = p.b2e[b];
+  int ext = 0;
+  for (int s = threadIdx.x; s < p.B; s += kThreads)   // ascending per thread
+    if (put_slot(p, int64_t(b) * p.B + s, Tv, e)) ext = s + 1;
+  for (int o = 32; o > 0; o >>= 1) ext = max(ext, __shfl_xor(ext, o, 64));
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = ext;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    ext = max(max(red[0], red[1]), max(red[2], red[3]));
+    if (ranges) {   // published at agent scope: the last workgroup reads all of them
+      __hip_atomic_store(p.flag + b, ext, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      last = __hip_atomic_fetch_add(p.done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+    } else {
+      p.flag[b] = ext;
+    }
+  }
+  if (!ranges) return;
+  __syncthreads();
+  if (!last) return;
+  auto extent = [&](int q) { return __hip_atomic_load(p.flag + q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
+  for (int k = 0; k < 2; ++k) make_ranges<kThreads>(extent, int(p.N), p.jobs[k], lds);
+}
+
+constexpr int kRangeThreads = 1024;
+__global__ void __launch_bounds__(kRangeThreads) fwd_ranges_kernel(MoeFwdPrep p) {
+  __shared__ uint64_t lds[kRangeThreads / 64];
+  make_ranges<kRangeThreads>([&](int b) { return p.flag[b]; }, int(p.N), p.jobs[blockIdx.x], lds);
+}
+}  // namespace
+
+hipError_t launch_fwd_prep(const MoeFwdPrep& p, hipStream_t st) {
+  const bool small = small_layer(p);
+  const PairsJob j0 = pairs_job(p.wgu_scales, p.wgu_pairs, p.E, 2 * p.I, p.H);
+  const PairsJob j1 = pairs_job(p.wd_scales, p.wd_pairs, p.E, p.H, p.I);
+  const int64_t chunks = p.T * (p.Hp / 8), want = (chunks + 4 * kThreads - 1) / (4 * kThreads);
+  const int64_t nq = want < 65536 ? want : 65536, nf = small ? 0 : (p.T * p.E + 4 * kThreads - 1) / (4 * kThreads);
+  const int64_t ns = p.E * (int64_t(j0.gx) * j0.gy + int64_t(j1.gx) * j1.gy), grid = nq + ns + nf + (small ? 1 : 0);
+  if (grid > kMaxGrid256) return hipErrorInvalidValue;
+  fwd_prep_kernel<<<unsigned(grid), kThreads, 0, st>>>(p, j0, j1, unsigned(nq), unsigned(nf), small ? 1 : 0);
+  if (!small) {
+    const bool ranges = p.N <= kListMax;
+    fwd_slots_kernel<<<unsigned(p.N), kThreads, 0, st>>>(p, ranges ? 1 : 0);
+    if (!ranges) fwd_ranges_kernel<<<2, kRangeThreads, 0, st>>>(p);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace mx

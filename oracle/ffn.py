@@ -103,9 +103,10 @@ def product_rests(a, b):
     return out.cpu().numpy()
 
 
-def expert(xq, wgu, wd, b1, b2, a, geglu, on_i):
+def expert(xq, wgu, wd, b1, b2, a, geglu, on_i, f16=False):
     """One expert on rows xq [n, H]: wgu [2, I, H], wd [H, I], b1 [2, I], b2 [H] or None, a [n] ->
-    (gu [n, 2, I], its bound, y [n, H], its bound)."""
+    (gu [n, 2, I], its bound, y [n, H], its bound).  f16: the down projection's rows are kept in fp16 times a power of
+    two that puts a row's largest value in [2^14, 2^15)."""
     n, H = xq.shape
     I = wd.shape[1]
     w = wgu.reshape(2 * I, H)
@@ -128,6 +129,8 @@ def expert(xq, wgu, wd, b1, b2, a, geglu, on_i):
     # large for the other seven
     dy = 2 * (dsq @ np.abs(wd).T + product_rests(sq, wd))
     dy = dy + (np.abs(sq) + dsq) @ np.abs(wd).T * (8 * np.ceil(I / 64) + 8) * 2.0 ** -24
+    if f16:   # half a step of 11 bits, or of the smallest 2^-24 where the largest is 2^14 or more
+        dy = dy + (np.abs(y) + dy) * 2.0 ** -11 + np.abs(y).max(1, keepdims=True) * 2.0 ** -39
     if b2 is not None:
         y = y + b2
         dy = dy + np.abs(y) * 2.0 ** -24
@@ -136,7 +139,8 @@ def expert(xq, wgu, wd, b1, b2, a, geglu, on_i):
     return gu, dgu, y, dy + np.abs(y) * 2.0 ** -23
 
 
-def moe_fwd(x, pairs, wgu, wd, b1=None, b2=None, geglu=False, on_i=False, residual=None, keep=None, scale=1.0):
+def moe_fwd(x, pairs, wgu, wd, b1=None, b2=None, geglu=False, on_i=False, residual=None, keep=None, scale=1.0,
+            f16=False):
     """x [T, H] (values); pairs {expert: (tokens, affinities)}; wgu [E, 2, I, H], wd [E, H, I] (values) ->
     (y [T, H], its bound before the output's rounding, {expert: (gu [n, 2, I], its bound)}).  keep [T, H]: the dropout
     mask, whose kept elements are scaled."""
@@ -146,7 +150,7 @@ def moe_fwd(x, pairs, wgu, wd, b1=None, b2=None, geglu=False, on_i=False, residu
     for e, (t, a) in sorted(pairs.items()):
         t, a = np.asarray(t, np.int64), np.asarray(a, np.float64)
         gu, dgu, z, dz = expert(xq[t], wgu[e], wd[e], None if b1 is None else b1[e], None if b2 is None else b2[e], a,
-                                geglu, on_i)
+                                geglu, on_i, f16)
         gus[e] = (gu, dgu)
         np.add.at(y, t, z)
         np.add.at(dy, t, dz + np.abs(z) * 2.0 ** -23)    # the sum over a token's slots

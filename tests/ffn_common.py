@@ -63,13 +63,16 @@ class Problem:
             [*oracle.quantize(_bits(wgu), 1, oracle.E4M3), *oracle.quantize(_bits(wd), 1, oracle.E4M3)],
             [(E, 2, I, H), (E, 2, I, H // 32), (E, H, I), (E, H, I // 32)])]
 
-    def exact(self):
+    def exact(self, blocks=True):
+        """y, its bound and the gate/up values.  blocks: of the block form, which keeps the down projection's rows in scaled
+        fp16 up to a contraction of 4096 (moe_fwd_down.hip)."""
         wgu, wd = ffn.mx_values(self.q[0], self.q[1]), ffn.mx_values(self.q[2], self.q[3])
         v = {k: None if t is None else bf16_values(t) for k, t in
              dict(b1=self.b1, b2=self.b2, residual=self.residual).items()}
         keep = ffn.dropout_keep(self.T * self.H, self.p, *self.seed_offset).reshape(self.T, self.H) if self.p else None
         return ffn.moe_fwd(bf16_values(self.x), self.pairs, wgu, wd, geglu=self.geglu, on_i=self.on_i, keep=keep,
-                           scale=ffn.dropout_scale(self.p), **v)
+                           scale=ffn.dropout_scale(self.p),
+                           f16=blocks and (self.I < 4096 or self.I % 128 != 0), **v)
 
     def on(self, device="cuda"):
         """The arguments of moe_fwd_mxfp8 (positional, keywords) on a device."""

@@ -10,10 +10,17 @@ from oracle import ffn
 pytestmark = pytest.mark.gpu
 
 CASES = {
-    # both ring loops' tiles: 256 x 256, 256 x 128, 128 x 128 (I < 128); contractions of one 128-byte pair on
-    "ring_256": dict(T=700, H=256, I=384, E=3, K=2, B=512, residual=True),
-    "ring_256x128": dict(T=300, H=128, I=256, E=4, K=2, B=128, bias=True),
-    "ring_128": dict(T=300, H=384, I=96, E=4, K=1, B=256, on_i=True),
+    # the gate/up product's tiles: 256 x 256 on either ring, 128 x 128 (short H, I < 128, blocks of 128 slots)
+    "tiles_256": dict(T=700, H=1024, I=384, E=3, K=2, B=512, residual=True),
+    "tiles_256_ragged": dict(T=300, H=1056, I=192, E=2, K=1, B=256, bias=True),
+    "tiles_128": dict(T=300, H=128, I=256, E=4, K=2, B=128, bias=True),
+    "tiles_128_short_I": dict(T=300, H=384, I=96, E=4, K=1, B=256, on_i=True),
+    # the down projection's: 256 x 256, 128 x 256 (256 of them or more), aligned and not; 128 x 128 above
+    "down_256": dict(T=300, H=288, I=1024, E=2, K=1, B=256, residual=True),
+    "down_256_ragged": dict(T=300, H=288, I=1056, E=2, K=1, B=256),
+    "down_128x256": dict(T=120, H=2304, I=128, E=30, K=2, bias=True),
+    "down_128x256_ragged": dict(T=120, H=2336, I=160, E=30, K=2),
+    "down_long_ragged": dict(T=100, H=96, I=4128, E=1, K=1),
     # H, I or both not a multiple of 128
     "ragged_H": dict(T=260, H=160, I=128, E=2, K=2, B=256, geglu=True, bias=True),
     "ragged_I": dict(T=200, H=128, I=160, E=3, K=2, B=128, geglu=True, on_i=True, residual=True),
@@ -71,6 +78,32 @@ def test_forward(name):
         assert np.array_equal(r8["checkpoint"][0].cpu().numpy().reshape(codes.shape), codes)
         assert np.array_equal(r8["checkpoint"][1].cpu().numpy().reshape(scales.shape), scales)
         assert torch.equal(r8["out"], r["out"])
+
+
+@pytest.mark.parametrize("B", [128, 256, 512, 1024])
+def test_block_sizes(B):
+    """Partly filled and empty blocks of every size: what the checkpoint holds in tiles without a token."""
+    p = Problem(T=37, H=1024, I=160, E=3, K=2, B=B, seed=B)
+    y, dy, gus = p.exact()
+    r = _run(p, "bf16")
+    check_rows(r["out"], y, dy)
+    ck, d = _gate_up(p, gus)
+    assert (np.abs(bf16_values(r["checkpoint"]) - ck) <= d + (np.abs(ck) + d) * HALF).all()
+    codes, scales = _run(p, "mxfp8")["checkpoint"]
+    dead = torch.from_numpy((p.tpid < 0).reshape(p.N, 1, 1, B)).cuda()
+    assert not (codes.bool() & dead).any()
+    assert not (scales.bool() & dead.view(p.N, 1, 1, B // 32, 32).all(-1)).any()
+
+
+def test_rows_of_far_apart_sizes():
+    """A token whose output is 2^40 times another's in the same tile leaves that one as exact."""
+    p = Problem(T=128, H=128, I=64, E=1, K=1, B=128, idx=np.zeros((128, 1), np.int32), seed=21)
+    p.x[::2] *= 2.0 ** 20        # g and u alike: y by 2^40 (SiLU is the identity or 0 there)
+    y, dy, _ = p.exact()
+    out = _run(p)["out"]
+    check_rows(out, y, dy)
+    rel = np.abs(bf16_values(out) - y)[1::2].max() / np.abs(y[1::2]).max()
+    assert rel < 2.0 ** -7
 
 
 def test_many_blocks():
