@@ -88,14 +88,15 @@ static void fwd_layout(const moe_fwd_mxfp8_args* a, FwdLayout* L) {
     field = o;
     o = up256(o + size_t(bytes));
   };
-  put(L->x_codes, T * Hp);
-  put(L->x_scales, T * (Hp / 32));
+  const int64_t xr = mx::fwd_x_by_slot(H, a->I, a->N, a->block_size) ? P : T;
+  put(L->x_codes, xr * Hp);
+  put(L->x_scales, xr * (Hp / 32));
   put(L->wgu_pairs, E * 2 * I * (Hp / 32));
   put(L->wd_pairs, E * H * (Ip / 32));
   put(L->inter_codes, P * Ip);
   put(L->inter_scales, P * (Ip / 32));
   put(L->rows, P * H * (f16 ? 2 : 4));
-  put(L->row_scale, f16 ? P * ((H + 127) / 128) * 4 : 0);
+  put(L->row_scale, f16 ? P * ((H + 63) / 64) * 4 : 0);
   mx::Phase3Args q{};
   q.H = H; q.I = I / 2; q.N = N; q.B = B;
   put(L->parts, f16 ? 0 : mx::phase3_parts_bytes(q));
@@ -195,6 +196,7 @@ int moe_fwd_mxfp8(const moe_fwd_mxfp8_args* a, void* ws, size_t ws_bytes, void* 
   g.T = T; g.H = H; g.I = I; g.E = E; g.N = N; g.B = B;
   g.Hp = up128(H); g.Ip = up128(I);
   g.x_codes = at(L.x_codes); g.x_scales = at(L.x_scales);
+  g.x_by_slot = mx::fwd_x_by_slot(H, I, N, B);
   g.w_codes = a->gate_up_codes; g.w_scales = at(L.wgu_pairs);
   g.b1 = a->gate_up_proj_bias;
   g.slot_tok = ints(L.slot_tok); g.slot_aff = slot_aff; g.b2e = a->block_to_expert; g.flag = ints(L.flag);
@@ -227,7 +229,7 @@ int moe_fwd_mxfp8(const moe_fwd_mxfp8_args* a, void* ws, size_t ws_bytes, void* 
   const mx::MoeFwdPrep prep{a->hidden_states, T, H, g.Hp, I, g.Ip, E, N, B, at(L.x_codes), at(L.x_scales),
                             a->gate_up_scales, at(L.wgu_pairs), a->down_scales, at(L.wd_pairs), a->token_position_to_id,
                             a->block_to_expert, a->expert_affinities_masked, a->num_valid_tokens, ints(L.slot_tok), slot_aff,
-                            ints(L.slot_of), ints(L.flag), reinterpret_cast<unsigned*>(at(L.done)),
+                            ints(L.slot_of), ints(L.flag), reinterpret_cast<unsigned*>(at(L.done)), g.x_by_slot,
                             {mx::fwd_gate_up_ranges(g), f16 ? mx::fwd_down_ranges(d) : mx::phase3_ranges(d3)}};
   STEP(mx::launch_fwd_prep(prep, st), "X, weight scales and slots");
   STEP(mx::launch_fwd_gate_up(g, st), "gate/up projections and activation");

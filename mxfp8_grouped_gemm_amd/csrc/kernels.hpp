@@ -365,8 +365,9 @@ hipError_t launch_quantize_t(const uint16_t* x, int64_t G, int64_t R, int64_t C,
 struct MoeFwdArgs {
   int64_t T, H, I, E, N, B;
   int64_t Hp, Ip;
-  const uint8_t* x_codes;       // [T][Hp]
-  const uint8_t* x_scales;      // [Hp/128][T][4]
+  const uint8_t* x_codes;       // [T][Hp], or by slot: stage-major [P][Hp]
+  const uint8_t* x_scales;      // [Hp/128][T or P][4]
+  int x_by_slot;                // fwd_x_by_slot
   const uint8_t* w_codes;       // [E][2I][H]
   const uint8_t* w_scales;      // [E][Hp/128][2I][4]
   const uint16_t* b1;           // [E][2][I] bf16, or null
@@ -386,6 +387,7 @@ struct MoeFwdArgs {
   int rr_tiles;
   int tiles_m;                  // set by the launcher
 };
+bool fwd_x_by_slot(int64_t H, int64_t I, int64_t N, int64_t B);   // X quantised into the slots' order
 TileRangeJob fwd_gate_up_ranges(const MoeFwdArgs& p);
 hipError_t launch_fwd_gate_up(const MoeFwdArgs& p, hipStream_t st);
 
@@ -400,9 +402,9 @@ struct MoeFwdDownArgs {
   const int32_t* flag;
   int32_t* tile_start;
   uint16_t* rows;               // [P][H] fp16
-  float* row_scale;             // [P][ceil(H/128)]
+  float* row_scale;             // [P][ceil(H/64)]
   int rr_tiles;
-  int tiles_n;                  // set by the launcher
+  int tiles_m;                  // set by the launcher
 };
 bool fwd_down_fits(int64_t I);  // else launch_phase3
 TileRangeJob fwd_down_ranges(const MoeFwdDownArgs& p);
@@ -428,13 +430,14 @@ struct MoeFwdPrep {
   int32_t* slot_of;
   int32_t* flag;
   unsigned* done;               // blocks set up so far (N <= kListMax)
+  int x_by_slot;                // as MoeFwdArgs
   TileRangeJob jobs[2];
 };
 hipError_t launch_fwd_prep(const MoeFwdPrep& p, hipStream_t st);
 
 struct MoeCombineArgs {
   const float* rows;            // [P][H], or null and
-  const uint16_t* rows16;       // [P][H] fp16 times row_scale [P][ceil(H/128)]
+  const uint16_t* rows16;       // [P][H] fp16 times row_scale [P][ceil(H/64)]
   const float* row_scale;
   const int32_t* slot_of;       // [T][E]
   const float* slot_aff;        // [P], or null: 1

@@ -7,30 +7,28 @@ namespace mx {
 
 template hipError_t fwd_gate_up_launch<128, 128>(MoeFwdArgs, hipStream_t);
 extern template hipError_t fwd_gate_up_launch<256, 256>(MoeFwdArgs, hipStream_t);
-extern template hipError_t fwd_gate_up_launch<256, 128>(MoeFwdArgs, hipStream_t);
 
 namespace {
-struct Shape {
-  int m, n;
-};
-// 256 x 256 tiles from contractions and blocks that are long enough for them (H = 4096: 3.7 ms against 5.1
-// at 128 x 128; H = 2048: 288 us against 308); 128 x 128, two workgroups a CU, where a block has 128 slots
-// (H = 1536: 385 us against 420 at 256 x 128).
-Shape fwd_shape(const MoeFwdArgs& p) {
-  if (p.I < 128 || p.B < 256 || p.H < 1024) return {128, 128};
-  return {256, 256};
-}
+// The tile's side: 256 from contractions and blocks that are long enough for one workgroup a CU
+// (H = 4096: 3.6 ms against 5.1 at 128; H = 2048: 290 us against 308), else 128, two workgroups a CU
+// (blocks of 128 slots, H = 1536: 390 us against 420 at 256 x 128).
+int fwd_side(int64_t H, int64_t I, int64_t B) { return I < 128 || B < 256 || H < 1024 ? 128 : 256; }
 }  // namespace
 
+// Every slot's X row by itself and stage-major costs the preparation 0.25 ns a KB of it and spares each 256-row
+// tile's reads half lines: H = 4096, I = 14336, 40k slots: preparation 62 -> 98 us, products 3.65 -> 3.44 ms;
+// H = 2048, I = 1408: 20 -> 43 us for 290 -> 287.
+bool fwd_x_by_slot(int64_t H, int64_t I, int64_t N, int64_t B) {
+  return I >= 4096 && fwd_side(H, I, B) == 256 && (H + 127) / 128 * 4 <= (int64_t(1) << 30) / (N * B);   // one launch, 32-bit offsets
+}
+
 TileRangeJob fwd_gate_up_ranges(const MoeFwdArgs& p) {
-  const Shape t = fwd_shape(p);
-  return {t.n, int(p.Ip / (t.m / 2)), int(p.B), p.tile_start, nullptr, 0, 0, p.rr_tiles, p.dead};
+  const int side = fwd_side(p.H, p.I, p.B);
+  return {side, int(p.Ip / (side / 2)), int(p.B), p.tile_start, nullptr, 0, 0, p.rr_tiles, p.dead};
 }
 
 hipError_t launch_fwd_gate_up(const MoeFwdArgs& p, hipStream_t st) {
-  const Shape t = fwd_shape(p);
-  if (t.m == 128) return fwd_gate_up_launch<128, 128>(p, st);
-  return t.n == 256 ? fwd_gate_up_launch<256, 256>(p, st) : fwd_gate_up_launch<256, 128>(p, st);
+  return fwd_side(p.H, p.I, p.B) == 128 ? fwd_gate_up_launch<128, 128>(p, st) : fwd_gate_up_launch<256, 256>(p, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -73,7 +71,7 @@ __global__ void __launch_bounds__(256) fwd_combine_kernel(MoeCombineArgs p) {
             if (in) {
               if constexpr (F16) {
                 v16[k] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p.rows16 + s * p.H + 8 * c));
-                sc[k] = p.row_scale[s * ((p.H + 127) / 128) + c / 16];
+                sc[k] = p.row_scale[s * ((p.H + 63) / 64) + c / 8];
               } else {
                 const f32x4_t* row = reinterpret_cast<const f32x4_t*>(p.rows + s * p.H + 8 * c);
                 const f32x4_t x = __builtin_nontemporal_load(row), y = __builtin_nontemporal_load(row + 1);

@@ -27,7 +27,6 @@
 #pragma once
 #include "gemm_v2.hpp"
 #include "gemm_v3.hpp"
-#include "gemm_v4.hpp"
 #include "kernels.hpp"
 #include "moe_tiles.hpp"
 #include "mx_device.hpp"
@@ -44,15 +43,6 @@ __device__ __forceinline__ int64_t fwd_weight_row(int r, int64_t i0, int64_t I) 
   const int w = r / (BM / 2), f = (r % (BM / 2)) / 32;
   const int64_t i = i0 + w * (BM / 4) + (f >> 1) * 32 + (r & 31);
   return i < I ? (f & 1) * I + i : -1;
-}
-
-// 256 x 256 tiles of aligned rows run the pair-slot ring, whose DMA moves whole
-// lines of row-major operands; the others the four-slot ring.
-template <int BM, int BN, bool RAG>
-constexpr bool kFwdPairRing = BM == 256 && BN == 256 && !RAG;
-template <int BM, int BN, bool RAG>
-constexpr int fwd_ring_smem() {
-  return kFwdPairRing<BM, BN, RAG> ? v4::smem_bytes(BM, BN) : v3::smem_bytes(BM, BN);
 }
 
 // This workgroup's tile: block b, slot tile tn, i tile tm; live: it holds a
@@ -132,10 +122,8 @@ __device__ __forceinline__ void fwd_store_ckpt(const MoeFwdArgs& p, int b, int64
         m = max(m, uint32_t(__shfl_xor(int(m), 1, 64)));
         m = max(m, uint32_t(__shfl_xor(int(m), 2, 64)));
         const int X = scale_exp<F>(m << 16);
-        const uint32_t lim = bf16_limit<F>(X) * 0x10001u;
         const float sc = cvt_scale(X);
-        const uint32_t lo = encode_bf16x4<F>(clamp_bf16x2(v[0], lim), clamp_bf16x2(v[1], lim), sc);
-        const uint32_t hi = encode_bf16x4<F>(clamp_bf16x2(v[2], lim), clamp_bf16x2(v[3], lim), sc);
+        const uint32_t lo = encode_bf16x4<F>(v[0], v[1], sc), hi = encode_bf16x4<F>(v[2], v[3], sc);   // they saturate
         *reinterpret_cast<uint2*>(p.ck8_codes + row * p.B + s + 8 * c) = make_uint2(lo, hi);
         if (c == 0) p.ck8_scales[row * (p.B / 32) + s / 32] = uint8_t(X + 127);
       }
@@ -145,7 +133,7 @@ __device__ __forceinline__ void fwd_store_ckpt(const MoeFwdArgs& p, int b, int64
 
 template <int BM, int BN, bool RAG, bool GEGLU, int CK>
 __global__ void __launch_bounds__(v2::kThreads) fwd_gate_up_kernel(MoeFwdArgs p) {
-  constexpr int SMEM = fwd_ring_smem<BM, BN, RAG>();
+  constexpr int SMEM = v3::smem_bytes(BM, BN);
   static_assert(SMEM >= 4 * kCkWaveBytes, "the checkpoint's staging fits the ring");
   __shared__ __attribute__((aligned(16))) uint8_t smem[SMEM];
   constexpr int FM = BM / 64, FN = BN / 64;
@@ -157,7 +145,7 @@ __global__ void __launch_bounds__(v2::kThreads) fwd_gate_up_kernel(MoeFwdArgs p)
   }
   const int b = tile.b;
   const int64_t i0 = int64_t(tile.tm) * (BM / 2), n0 = int64_t(tile.tn) * BN;
-  const int64_t sbase = int64_t(b) * p.B, e = p.b2e[b];
+  const int64_t sbase = int64_t(b) * p.B, e = p.b2e[b], P = p.N * p.B;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, h = lane >> 5, r = lane & 31;
   const int wm = wave >> 1, wn = wave & 1;
   const int32_t* st = p.slot_tok + sbase;
@@ -169,26 +157,23 @@ __global__ void __launch_bounds__(v2::kThreads) fwd_gate_up_kernel(MoeFwdArgs p)
   v16f acc[FM][FN];
   if (i0 < p.I) {   // else the tile lies between I and Ip: no products
     v3::ScaleDma<BM, BN> sd;
-    v3::setup_scales_map(sd, ws, 2 * p.I, 2 * p.I * (p.Hp / 32), row_of, p.x_scales, p.T, p.T * (p.Hp / 32), tok_of);
-    if constexpr (kFwdPairRing<BM, BN, RAG>) {
-      v4::Op<BM> A;
-      v4::Op<BN> B;
-      v4::setup_gather(A, wc, 2 * p.I, p.H, row_of);
-      v4::setup_gather(B, p.x_codes, p.T, p.Hp, tok_of);
-      v4::mainloop<BM, BN, v3::kFp8, kE4M3, kE4M3>(A, B, &sd, int(p.Hp / v4::PK), v4::KMapPlain{}, smem, acc);
-    } else {
-      v3::Op<BM> A;
-      v3::Op<BN> B;
-      v3::setup_gather(A, wc, 2 * p.I, p.H, row_of);
-      v3::setup_gather(B, p.x_codes, p.T, p.Hp, tok_of);
-      v3::mainloop<BM, BN, v3::kFp8, kE4M3, kE4M3, v3::KMapPlain, RAG ? 1 : 0>(A, B, &sd, int(p.Hp / v3::SK),
-                                                                              v3::KMapPlain{}, smem, acc, uint32_t(p.H));
-    }
+    const int64_t xr = p.x_by_slot ? P : p.T;
+    v3::setup_scales_map(sd, ws, 2 * p.I, 2 * p.I * (p.Hp / 32), row_of, p.x_scales, xr, xr * (p.Hp / 32),
+                         [&](int q) -> int64_t { return p.x_by_slot ? (q < BN ? sbase + n0 + q : -1) : tok_of(q); });
+    // the four-slot ring, also for these row-major operands (256 x 256: 3.6 ms against 3.9 on the pair-slot
+    // ring at H = 4096, 287 us against 332 at H = 2048)
+    v3::Op<BM> A;
+    v3::Op<BN> B;
+    v3::setup_gather(A, wc, 2 * p.I, p.H, row_of);
+    if (p.x_by_slot) v3::setup_rows_sm(B, p.x_codes, sbase + n0, sbase + p.B, P, p.Hp);
+    else v3::setup_gather(B, p.x_codes, p.T, p.Hp, tok_of);
+    v3::mainloop<BM, BN, v3::kFp8, kE4M3, kE4M3, v3::KMapPlain, RAG ? 1 : 0>(A, B, &sd, int(p.Hp / v3::SK),
+                                                                            v3::KMapPlain{}, smem, acc, uint32_t(p.H));
   }
   if constexpr (CK != 0) __syncthreads();   // every wave is done with the ring: its bytes stage the checkpoint
   uint32_t* stage = reinterpret_cast<uint32_t*>(smem + wave * kCkWaveBytes);
-  const int64_t P = p.N * p.B;
-  // this lane's slots
+  saturate_fp8_conversions();
+  // this lane's slots.  A slot without a token has X rows of zeros, so g = u = 0 without a bias.
   bool ok[FN];
   float aff[FN];
 #pragma unroll
@@ -207,19 +192,21 @@ __global__ void __launch_bounds__(v2::kThreads) fwd_gate_up_kernel(MoeFwdArgs p)
         if (h == 0) p.inter_scales[((i >> 7) * P + slot) * 4 + (i >> 5 & 3)] = 0;
       }
     } else {
-      float bg[16], bu[16];
       if (p.b1) {
         const uint16_t* row = p.b1 + e * 2 * p.I + i + 4 * h;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const uint2 g = *reinterpret_cast<const uint2*>(row + 8 * t);
-          const uint2 u = *reinterpret_cast<const uint2*>(row + p.I + 8 * t);
-          bg[4 * t] = lo_bf16(g.x); bg[4 * t + 1] = hi_bf16(g.x); bg[4 * t + 2] = lo_bf16(g.y); bg[4 * t + 3] = hi_bf16(g.y);
-          bu[4 * t] = lo_bf16(u.x); bu[4 * t + 1] = hi_bf16(u.x); bu[4 * t + 2] = lo_bf16(u.y); bu[4 * t + 3] = hi_bf16(u.y);
-        }
-      } else {
-#pragma unroll
-        for (int t = 0; t < 16; ++t) bg[t] = bu[t] = 0.f;
+        v2::static_for<4>([&](auto K) {
+          const uint2 g = *reinterpret_cast<const uint2*>(row + 8 * int(K));
+          const uint2 u = *reinterpret_cast<const uint2*>(row + p.I + 8 * int(K));
+          const float bg[4] = {lo_bf16(g.x), hi_bf16(g.x), lo_bf16(g.y), hi_bf16(g.y)};
+          const float bu[4] = {lo_bf16(u.x), hi_bf16(u.x), lo_bf16(u.y), hi_bf16(u.y)};
+          v2::static_for<FN>([&](auto J) {
+            v2::static_for<4>([&](auto D) {
+              constexpr int k = 4 * int(K) + int(D);
+              acc[2 * int(Q)][J][k] = ok[J] ? acc[2 * int(Q)][J][k] + bg[int(D)] : 0.f;
+              acc[2 * int(Q) + 1][J][k] = ok[J] ? acc[2 * int(Q) + 1][J][k] + bu[int(D)] : 0.f;
+            });
+          });
+        });
       }
       v2::static_for<FN>([&](auto J) {
         const int64_t s = n0 + wn * (BN / 2) + 32 * int(J);   // the fragment's first slot
@@ -227,22 +214,26 @@ __global__ void __launch_bounds__(v2::kThreads) fwd_gate_up_kernel(MoeFwdArgs p)
         uint32_t m = 0;
         v2::static_for<16>([&](auto K) {
           constexpr int k = K;
-          const float g = ok[J] ? acc[2 * int(Q)][J][k] + bg[k] : 0.f;
-          const float u = ok[J] ? acc[2 * int(Q) + 1][J][k] + bu[k] : 0.f;
-          v[k] = gate_act<GEGLU>(g) * u * aff[J];
-          m = max(m, abs_bits(v[k]));
+          const float g = acc[2 * int(Q)][J][k], u = acc[2 * int(Q) + 1][J][k];
+          v[k] = gate_act<GEGLU>(g) * u;
           if constexpr (CK != 0) stage[(8 * (k >> 2) + 4 * h + (k & 3)) * kCkPitch + r] = bf16x2_pack(g, u);
         });
+        if (p.on_i) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) v[k] *= aff[J];
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) m = max(m, abs_bits(v[k]));
 #if defined(__HIP_DEVICE_COMPILE__)
         {
           const auto x = __builtin_amdgcn_permlane32_swap(m, m, false, false);
           m = max(uint32_t(x[0]), uint32_t(x[1]));
         }
         const int X = scale_exp<kE4M3>(m);
-        const float inv = inv_scale(X);
+        const float sc = cvt_scale(X);
         uint32_t w[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) w[t] = encode4<kE4M3>(v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3], inv);
+        for (int t = 0; t < 4; ++t) w[t] = encode_f32x4(v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3], sc);
         // word t of half h: rows 8t + 4h .. + 3.  Half 0 takes rows 0..15, half 1 rows 16..31.
         const auto x = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
         const auto y = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);

@@ -25,6 +25,21 @@ bool small_layer(const MoeFwdPrep& p) { return p.N * p.B <= kSmallSlots && p.T *
 
 // ---------------------------------------------------------------------------
 // X: a thread takes 8 columns, 4 lanes a group of 32.
+// The codes of a lane's 8 columns (its group's other lanes beside it) and their scale.
+__device__ __forceinline__ uint2 quant_x8(const uint4& v, int& X) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) m = absmax_bf16x2(m, w[k]);
+  m = max(m & 0xffffu, m >> 16);
+  m = max(m, uint32_t(__shfl_xor(int(m), 1, 64)));
+  m = max(m, uint32_t(__shfl_xor(int(m), 2, 64)));
+  X = scale_exp<kE4M3>(m << 16);
+  const uint32_t lim = bf16_limit<kE4M3>(X) * 0x10001u;
+  const float s = cvt_scale(X);
+  return make_uint2(encode_bf16x4<kE4M3>(clamp_bf16x2(w[0], lim), clamp_bf16x2(w[1], lim), s),
+                    encode_bf16x4<kE4M3>(clamp_bf16x2(w[2], lim), clamp_bf16x2(w[3], lim), s));
+}
 __device__ __forceinline__ void quant_x(const MoeFwdPrep& p, unsigned wg, unsigned wgs) {
   constexpr int U = 4;   // chunks of a thread, their loads issued together
   const uint32_t per = uint32_t(p.Hp / 8), n = uint32_t(p.T) * per, stride = wgs * kThreads;   // T * Hp < 2^32
@@ -41,23 +56,44 @@ __device__ __forceinline__ void quant_x(const MoeFwdPrep& p, unsigned wg, unsign
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-      uint32_t m = 0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) m = absmax_bf16x2(m, w[k]);
-      m = max(m & 0xffffu, m >> 16);
-      m = max(m, uint32_t(__shfl_xor(int(m), 1, 64)));   // n is a multiple of 16: a group's lanes stay together
-      m = max(m, uint32_t(__shfl_xor(int(m), 2, 64)));
-      const int X = scale_exp<kE4M3>(m << 16);
-      const uint32_t lim = bf16_limit<kE4M3>(X) * 0x10001u;
-      const float s = cvt_scale(X);
+      int X;
+      const uint2 q = quant_x8(v[u], X);   // n is a multiple of 16: a group's lanes stay together
       if (c0 + u * stride < n) {
-        const uint32_t lo = encode_bf16x4<kE4M3>(clamp_bf16x2(w[0], lim), clamp_bf16x2(w[1], lim), s);
-        const uint32_t hi = encode_bf16x4<kE4M3>(clamp_bf16x2(w[2], lim), clamp_bf16x2(w[3], lim), s);
-        *reinterpret_cast<uint2*>(p.x_codes + int64_t(row[u]) * p.Hp + col[u]) = make_uint2(lo, hi);
+        *reinterpret_cast<uint2*>(p.x_codes + int64_t(row[u]) * p.Hp + col[u]) = q;
         if ((col[u] & 31) == 0)
           p.x_scales[((col[u] >> 7) * p.T + row[u]) * 4 + (col[u] >> 5 & 3)] = col[u] < p.H ? uint8_t(X + 127) : uint8_t(0);
       }
+    }
+  }
+}
+
+__device__ __forceinline__ int64_t valid_tokens(const MoeFwdPrep& p) {
+  const int64_t n = p.nvalid ? int64_t(*p.nvalid) : p.T;
+  return n < 0 ? 0 : (n < p.T ? n : p.T);
+}
+
+// X as slots: each slot's token's row again, codes stage-major over the P slots (zeros in padding).  A
+// workgroup takes 32 slots x 256 columns, 2 KB of consecutive codes at a time.
+__device__ __forceinline__ void quant_slots(const MoeFwdPrep& p, unsigned id) {
+  constexpr int U = 4;
+  const unsigned per = unsigned((p.Hp + 255) / 256), g = id / per;
+  const int64_t P = p.N * p.B, slot = int64_t(g) * 32 + threadIdx.x / 8, e = p.b2e[slot / p.B], t = p.tpid[slot];
+  const bool ok = t >= 0 && t < valid_tokens(p) && e >= 0 && e < p.E;
+  const int64_t col0 = int64_t(id - g * per) * 256 + (threadIdx.x & 7) * 8;
+  uint4 v[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t c = col0 + 64 * u;
+    v[u] = ok && c < p.H ? *reinterpret_cast<const uint4*>(p.x + t * p.H + c) : make_uint4(0u, 0u, 0u, 0u);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t c = col0 + 64 * u;
+    int X;
+    const uint2 q = quant_x8(v[u], X);
+    if (c < p.Hp) {   // Hp % 128 == 0
+      *reinterpret_cast<uint2*>(p.x_codes + stage_major_off(slot, c, P, p.Hp)) = q;
+      if ((c & 31) == 0) p.x_scales[((c >> 7) * P + slot) * 4 + (c >> 5 & 3)] = c < p.H ? uint8_t(X + 127) : uint8_t(0);
     }
   }
 }
@@ -107,82 +143,118 @@ __device__ __forceinline__ void scale_pairs(const PairsJob& j, unsigned id, uint
 }
 
 // ---------------------------------------------------------------------------
-// Tile ranges (moe_tiles.hpp) of up to any number of blocks by one workgroup of
-// TH threads; ext(b): block b's extent.  lds: TH / 64 words of 8 bytes.
+// Tile ranges (moe_tiles.hpp) of any number of blocks by one workgroup of TH
+// threads; ext(b): block b's extent.  One pass over the blocks for the totals,
+// one for the starts and the map: TH blocks at a time, a block's map entries
+// by as many lanes as it has tiles, from starts held in LDS (one thread a block
+// for 78 blocks of 224 tiles took 12 us more).
+template <int TH>
+struct RangeLds {
+  uint64_t wave[TH / 64];
+  int32_t c[TH], start[TH], dead[TH];
+};
 template <int TH, class Ext>
-__device__ __forceinline__ void make_ranges(const Ext& ext, int N, const TileRangeJob& j, uint64_t* lds) {
+__device__ __forceinline__ void make_ranges(const Ext& ext, int N, const TileRangeJob& j, RangeLds<TH>& lds) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, cmax = (j.blk + j.W - 1) / j.W * j.other;
-  auto tiles = [&](int b) { return (ext(b) + j.W - 1) / j.W * j.other; };
-  uint64_t carry = 0;   // tiles so far: of fully live blocks (with rr) in the high word, of the others in the low
+  // tiles of fully live blocks (with rr) in the high word, of the others in the low
+  auto word = [&](int c) { return j.rr && c == cmax ? uint64_t(c) << 32 : uint64_t(c); };
+  auto sum_waves = [&](uint64_t x, uint64_t& before) {   // x: lane 63's is the wave's; returns the sum, before: of earlier waves
+    __syncthreads();
+    if (lane == 63) lds.wave[wave] = x;
+    __syncthreads();
+    uint64_t all = 0;
+    before = 0;
+    for (int w = 0; w < TH / 64; ++w) {
+      const uint64_t s = lds.wave[w];
+      before += w < wave ? s : 0;
+      all += s;
+    }
+    return all;
+  };
+  uint64_t mine = 0, before;
+  for (int b = threadIdx.x; b < N; b += TH) mine += word((ext(b) + j.W - 1) / j.W * j.other);
+  for (int o = 32; o > 0; o >>= 1) mine += __shfl_xor(static_cast<unsigned long long>(mine), o, 64);
+  const uint64_t sum = sum_waves(mine, before);
+  const int nfull = int(sum >> 32), total = nfull + int32_t(sum);
+  int32_t* map = j.start + N + 1;
+  uint64_t carry = 0;   // of earlier blocks
   for (int b0 = 0; b0 < N; b0 += TH) {
-    const int b = b0 + threadIdx.x, c = b < N ? tiles(b) : 0;
-    const bool full = j.rr && c == cmax;
-    const uint64_t mine = full ? uint64_t(c) << 32 : uint64_t(c);
-    uint64_t x = mine;
+    const int b = b0 + threadIdx.x, c = b < N ? (ext(b) + j.W - 1) / j.W * j.other : 0;
+    uint64_t x = word(c);
     for (int o = 1; o < 64; o <<= 1) {
       const uint64_t y = __shfl_up(static_cast<unsigned long long>(x), o, 64);
       if (lane >= o) x += y;
     }
-    if (lane == 63) lds[wave] = x;
-    __syncthreads();
-    uint64_t before = carry + x - mine;
-    for (int w = 0; w < TH / 64; ++w) {
-      const uint64_t s = lds[w];
-      before += w < wave ? s : 0;
-      carry += s;
-    }
-    __syncthreads();
+    const uint64_t chunk = sum_waves(x, before);
+    before += carry + x - word(c);
+    carry += chunk;
+    const int32_t start = j.rr && c == cmax ? int32_t(before >> 32) : nfull + int32_t(before);
+    const int32_t dead = total + b * cmax - int32_t(before >> 32) - int32_t(before);
+    lds.c[threadIdx.x] = c;
+    lds.start[threadIdx.x] = start;
+    lds.dead[threadIdx.x] = dead;
     if (b < N) {
-      j.start[b] = int32_t(full ? before >> 32 : before);   // among its kind, for now
-      if (j.dead) j.dead[b] = b * cmax - int32_t(before >> 32) - int32_t(before);
+      j.start[b] = start;
+      if (j.dead) j.dead[b] = dead;
+    }
+    __syncthreads();
+    const int L = cmax > 16 ? 64 : cmax > 4 ? 16 : 4, nb = min(TH, N - b0);
+    for (int k = threadIdx.x / L; k < nb; k += TH / L) {
+      const int cc = lds.c[k], s = lds.start[k], d = lds.dead[k] - cc;
+      for (int t = threadIdx.x % L; t < (j.dead ? cmax : cc); t += L) map[t < cc ? s + t : d + t] = b0 + k;
     }
   }
-  const int nfull = int(carry >> 32), total = nfull + int32_t(carry);
-  int32_t* map = j.start + N + 1;
-  for (int b = threadIdx.x; b < N; b += TH) {   // the thread's own entries
-    const int c = tiles(b), t0 = j.start[b] + (j.rr && c == cmax ? 0 : nfull);
-    j.start[b] = t0;
-    for (int t = t0; t < t0 + c; ++t) map[t] = b;
-    if (j.dead) {
-      const int d0 = j.dead[b] + total;
-      j.dead[b] = d0;
-      for (int t = d0; t < d0 + cmax - c; ++t) map[t] = b;
+  if (threadIdx.x == 0) j.start[N] = total;
+  if (j.cut && threadIdx.x < 8) {   // the tail cut of each XCD
+    TailCut k = tail_cut_one(total, int(threadIdx.x), j.rr, j.conc, j.npairs);
+    const int mineb = k.tail * (k.S - 1);
+    int base = mineb;
+    for (int o = 1; o < 8; o <<= 1) {
+      const int y = __shfl_up(base, o, 8);
+      if (int(threadIdx.x) >= o) base += y;
     }
-  }
-  if (threadIdx.x == 0) {
-    j.start[N] = total;
-    if (j.cut) {   // the tail cut of each XCD
-      int base = 0;
-      for (int x = 0; x < 8; ++x) {
-        TailCut k = tail_cut_one(total, x, j.rr, j.conc, j.npairs);
-        k.base = base;
-        base += k.tail * (k.S - 1);
-        j.cut[x] = k;
-      }
-    }
+    k.base = base - mineb;
+    j.cut[threadIdx.x] = k;
   }
 }
 
-// One slot: its token and affinity (padding: -1, 0), the inverse map.  Padding
-// is what holds no token below the count of valid ones, or lies in a block of no expert.
-__device__ __forceinline__ bool put_slot(const MoeFwdPrep& p, int64_t s, int64_t Tv, int64_t e) {
-  const int64_t t = p.tpid[s];
-  const bool ok = t >= 0 && t < Tv && e >= 0 && e < p.E;
-  p.slot_tok[s] = ok ? int32_t(t) : -1;
-  p.slot_aff[s] = ok ? p.aff[t * p.E + e] : 0.f;
-  if (ok) p.slot_of[t * p.E + e] = int32_t(s);
-  return ok;
+// Four slots s + k step below end (in a block of expert(s)): tokens and
+// affinities (padding: -1, 0), the inverse map; routed(s) for each that has a token.
+// Padding is what holds no token below the count of valid ones, or lies in a block
+// of no expert.  The four's loads are issued together.
+template <class Expert, class Routed>
+__device__ __forceinline__ void put_slots(const MoeFwdPrep& p, int64_t s0, int64_t step, int64_t end, int64_t Tv,
+                                          const Expert& expert, const Routed& routed) {
+  int64_t t[4], e[4];
+  float a[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int64_t s = s0 + k * step;
+    t[k] = s < end ? int64_t(p.tpid[s]) : -1;
+    e[k] = s < end ? expert(s) : -1;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (t[k] >= Tv || e[k] < 0 || e[k] >= p.E) t[k] = -1;
+    a[k] = t[k] >= 0 ? p.aff[t[k] * p.E + e[k]] : 0.f;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int64_t s = s0 + k * step;
+    if (s >= end) continue;
+    p.slot_tok[s] = t[k] >= 0 ? int32_t(t[k]) : -1;
+    p.slot_aff[s] = a[k];
+    if (t[k] >= 0) {
+      p.slot_of[t[k] * p.E + e[k]] = int32_t(s);
+      routed(s);
+    }
+  }
 }
-__device__ __forceinline__ int64_t valid_tokens(const MoeFwdPrep& p) {
-  const int64_t n = p.nvalid ? int64_t(*p.nvalid) : p.T;
-  return n < 0 ? 0 : (n < p.T ? n : p.T);
-}
-
 __global__ void __launch_bounds__(kThreads) fwd_prep_kernel(MoeFwdPrep p, PairsJob j0, PairsJob j1, unsigned nq,
                                                             unsigned nf, int small) {
   __shared__ uint32_t tile[32][65];
   __shared__ int ext[kSmallBlocks];
-  __shared__ uint64_t lds[kThreads / 64];
+  __shared__ RangeLds<kThreads> lds;
   const unsigned wg = blockIdx.x;
   if (small && wg == 0) {   // the whole set-up of the slots
     for (int64_t k = threadIdx.x; k < p.T * p.E; k += kThreads) p.slot_of[k] = -1;
@@ -190,11 +262,9 @@ __global__ void __launch_bounds__(kThreads) fwd_prep_kernel(MoeFwdPrep p, PairsJ
     __syncthreads();
     const int64_t Tv = valid_tokens(p);
     const int P = int(p.N * p.B), B = int(p.B);
-#pragma unroll 4
-    for (int s = threadIdx.x; s < P; s += kThreads) {
-      const int b = s / B;
-      if (put_slot(p, s, Tv, p.b2e[b])) atomicMax(&ext[b], s - b * B + 1);
-    }
+    for (int s = threadIdx.x; s < P; s += 4 * kThreads)
+      put_slots(p, s, kThreads, P, Tv, [&](int64_t q) { return int64_t(p.b2e[int(q) / B]); },
+                [&](int64_t q) { atomicMax(&ext[int(q) / B], int(q) % B + 1); });
     __syncthreads();
     for (int b = threadIdx.x; b < p.N; b += kThreads) p.flag[b] = ext[b];
     for (int k = 0; k < 2; ++k) make_ranges<kThreads>([&](int b) { return ext[b]; }, int(p.N), p.jobs[k], lds);
@@ -203,6 +273,7 @@ __global__ void __launch_bounds__(kThreads) fwd_prep_kernel(MoeFwdPrep p, PairsJ
   unsigned id = wg - (small ? 1 : 0);
   if (id == 0 && threadIdx.x == 0) *p.done = 0;   // read by the next launch only
   if (id < nq) {
+    if (p.x_by_slot) return quant_slots(p, id);
     quant_x(p, id, nq);
     return;
   }
@@ -226,14 +297,15 @@ __global__ void __launch_bounds__(kThreads) fwd_prep_kernel(MoeFwdPrep p, PairsJ
 }
 
 __global__ void __launch_bounds__(kThreads) fwd_slots_kernel(MoeFwdPrep p, int ranges) {
-  __shared__ int red[kThreads / 64];
-  __shared__ uint64_t lds[kThreads / 64];
+  __shared__ int red[kThreads / 64], exts[kListMax];
+  __shared__ RangeLds<kThreads> lds;
   __shared__ int last;
   const int b = blockIdx.x;
   const int64_t Tv = valid_tokens(p), e = p.b2e[b];
   int ext = 0;
-  for (int s = threadIdx.x; s < p.B; s += kThreads)   // ascending per thread
-    if (put_slot(p, int64_t(b) * p.B + s, Tv, e)) ext = s + 1;
+  const int64_t first = int64_t(b) * p.B;
+  for (int64_t s = first + threadIdx.x; s < first + p.B; s += 4 * kThreads)   // ascending per thread
+    put_slots(p, s, kThreads, first + p.B, Tv, [&](int64_t) { return e; }, [&](int64_t q) { ext = int(q - first) + 1; });
   for (int o = 32; o > 0; o >>= 1) ext = max(ext, __shfl_xor(ext, o, 64));
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = ext;
   __syncthreads();
@@ -250,13 +322,15 @@ __global__ void __launch_bounds__(kThreads) fwd_slots_kernel(MoeFwdPrep p, int r
   if (!ranges) return;
   __syncthreads();
   if (!last) return;
-  auto extent = [&](int q) { return __hip_atomic_load(p.flag + q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
-  for (int k = 0; k < 2; ++k) make_ranges<kThreads>(extent, int(p.N), p.jobs[k], lds);
+  for (int q = threadIdx.x; q < p.N; q += kThreads)   // N <= kListMax
+    exts[q] = __hip_atomic_load(p.flag + q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  for (int k = 0; k < 2; ++k) make_ranges<kThreads>([&](int q) { return exts[q]; }, int(p.N), p.jobs[k], lds);
 }
 
 constexpr int kRangeThreads = 1024;
 __global__ void __launch_bounds__(kRangeThreads) fwd_ranges_kernel(MoeFwdPrep p) {
-  __shared__ uint64_t lds[kRangeThreads / 64];
+  __shared__ RangeLds<kRangeThreads> lds;
   make_ranges<kRangeThreads>([&](int b) { return p.flag[b]; }, int(p.N), p.jobs[blockIdx.x], lds);
 }
 }  // namespace
@@ -266,7 +340,7 @@ hipError_t launch_fwd_prep(const MoeFwdPrep& p, hipStream_t st) {
   const PairsJob j0 = pairs_job(p.wgu_scales, p.wgu_pairs, p.E, 2 * p.I, p.H);
   const PairsJob j1 = pairs_job(p.wd_scales, p.wd_pairs, p.E, p.H, p.I);
   const int64_t chunks = p.T * (p.Hp / 8), want = (chunks + 4 * kThreads - 1) / (4 * kThreads);
-  const int64_t nq = want < 65536 ? want : 65536, nf = small ? 0 : (p.T * p.E + 4 * kThreads - 1) / (4 * kThreads);
+  const int64_t nq = p.x_by_slot ? p.N * p.B / 32 * ((p.Hp + 255) / 256) : want < 65536 ? want : 65536, nf = small ? 0 : (p.T * p.E + 4 * kThreads - 1) / (4 * kThreads);
   const int64_t ns = p.E * (int64_t(j0.gx) * j0.gy + int64_t(j1.gx) * j1.gy), grid = nq + ns + nf + (small ? 1 : 0);
   if (grid > kMaxGrid256) return hipErrorInvalidValue;
   fwd_prep_kernel<<<unsigned(grid), kThreads, 0, st>>>(p, j0, j1, unsigned(nq), unsigned(nf), small ? 1 : 0);

@@ -205,6 +205,17 @@ __device__ __forceinline__ void saturate_fp8_conversions() {
   __builtin_amdgcn_s_setreg(1 | 23 << 6, 1);   // hwreg(MODE, bit 23, 1 bit)
 #endif
 }
+// Four codes of fp32 values with scale 2^X (s = cvt_scale(X)) in a wave that has
+// called saturate_fp8_conversions: v_cvt_scalef32_pk_fp8_f32 divides, rounds to
+// nearest-even and saturates.  Equal to encode4 on 2^30 values (every binade below a
+// group's largest, ties among them) at the scales that the group rule gives them.
+__device__ __forceinline__ uint32_t encode_f32x4(float v0, float v1, float v2, float v3, float s) {
+  typedef short s16x2 __attribute__((ext_vector_type(2)));
+  s16x2 r = {0, 0};
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, v0, v1, s, false);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, v2, v3, s, true);
+  return __builtin_bit_cast(uint32_t, r);
+}
 // low / high halves of two words, packed (a's in the low half)
 __device__ __forceinline__ uint32_t lo_halves(uint32_t a, uint32_t b) { return (a & 0xffffu) | (b << 16); }
 __device__ __forceinline__ uint32_t hi_halves(uint32_t a, uint32_t b) { return (a >> 16) | (b & 0xffff0000u); }
