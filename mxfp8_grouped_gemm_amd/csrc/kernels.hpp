@@ -404,11 +404,13 @@ struct MoeFwdDownArgs {
   uint16_t* rows;               // [P][H] fp16
   float* row_scale;             // [P][ceil(H/64)]
   int rr_tiles;
-  int tiles_m;                  // set by the launcher
+  int tiles_m, tiles_wg;        // set by the launcher
 };
 bool fwd_down_fits(int64_t I);  // else launch_phase3
 TileRangeJob fwd_down_ranges(const MoeFwdDownArgs& p);
 hipError_t launch_fwd_down(const MoeFwdDownArgs& p, hipStream_t st);
+TileRangeJob fwd_down_short_ranges(const MoeFwdDownArgs& p);   // I <= 256
+hipError_t launch_fwd_down_short(MoeFwdDownArgs p, hipStream_t st);
 
 // What comes before the products: X along H, the weights' scales, the slots
 // (slot_tok, slot_aff, slot_of, the blocks' extents) and the two products' tile ranges

@@ -74,19 +74,16 @@ __global__ void __launch_bounds__(v2::kThreads) fwd_down_kernel(MoeFwdDownArgs p
         m = max(uint32_t(x[0]), uint32_t(x[1]));
       }
 #endif
-      // biased exponent of the largest, at least 15 so that both scales are normal numbers
-      const uint32_t ex = max(m >> 23, 15u);
-      const float mul = __uint_as_float((268u - ex) << 23);   // 2^(141 - ex): the largest in [2^14, 2^15)
-      if (h == 0) scales[slot * NS + wm * (NS / 2) + int(RUN)] = __uint_as_float((ex - 14u) << 23);
+      float mul, scale;
+      f16_row_scale(m, mul, scale);
+      if (h == 0) scales[slot * NS + wm * (NS / 2) + int(RUN)] = scale;
       v2::static_for<2>([&](auto F) {
         constexpr int fi = 2 * int(RUN) + int(F);
         v2::static_for<4>([&](auto K) {
           constexpr int q = 4 * int(K);
-          typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-          const f16x2 lo = {_Float16(acc[fi][FJ][q] * mul), _Float16(acc[fi][FJ][q + 1] * mul)};
-          const f16x2 hi = {_Float16(acc[fi][FJ][q + 2] * mul), _Float16(acc[fi][FJ][q + 3] * mul)};
+          const v16f& c = acc[fi][FJ];
           *reinterpret_cast<uint2*>(dst + (32 * fi + 8 * int(K)) * 2) =
-              make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
+              make_uint2(f16x2_pack(c[q] * mul, c[q + 1] * mul), f16x2_pack(c[q + 2] * mul, c[q + 3] * mul));
         });
       });
     });
@@ -137,11 +134,13 @@ hipError_t go(MoeFwdDownArgs p, hipStream_t st) {
 bool fwd_down_fits(int64_t I) { return I < 4096 || I % 128 != 0; }
 
 TileRangeJob fwd_down_ranges(const MoeFwdDownArgs& p) {
+  if (p.Ip <= 256) return fwd_down_short_ranges(p);
   const Shape t = down_shape(p);
   return {t.n, int((p.H + t.m - 1) / t.m), int(p.B), p.tile_start, nullptr, 0, 0, p.rr_tiles};
 }
 
 hipError_t launch_fwd_down(const MoeFwdDownArgs& p, hipStream_t st) {
+  if (p.Ip <= 256) return launch_fwd_down_short(p, st);
   return down_shape(p).m == 256 ? go<256, 256>(p, st) : go<128, 128>(p, st);
 }
 

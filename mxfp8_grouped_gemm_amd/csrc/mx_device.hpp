@@ -216,6 +216,19 @@ __device__ __forceinline__ uint32_t encode_f32x4(float v0, float v1, float v2, f
   r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, v2, v3, s, true);
   return __builtin_bit_cast(uint32_t, r);
 }
+// Rows in fp16 times a power of two: from the bits of the largest magnitude, the factor that brings it into
+// [2^14, 2^15) and the scale that undoes it (biased exponent at least 15: both are normal numbers).
+__device__ __forceinline__ void f16_row_scale(uint32_t max_bits, float& mul, float& scale) {
+  const uint32_t ex = max(max_bits >> 23, 15u);
+  mul = __uint_as_float((268u - ex) << 23);   // 2^(141 - ex)
+  scale = __uint_as_float((ex - 14u) << 23);
+}
+__device__ __forceinline__ uint32_t f16x2_pack(float a, float b) {
+  typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+  const f16x2 v = {_Float16(a), _Float16(b)};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
 // low / high halves of two words, packed (a's in the low half)
 __device__ __forceinline__ uint32_t lo_halves(uint32_t a, uint32_t b) { return (a & 0xffffu) | (b << 16); }
 __device__ __forceinline__ uint32_t hi_halves(uint32_t a, uint32_t b) { return (a >> 16) | (b & 0xffff0000u); }

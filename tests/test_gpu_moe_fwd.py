@@ -117,6 +117,31 @@ def test_many_blocks():
     check_rows(_run(p, "mxfp8")["out"], y, dy)
 
 
+@pytest.mark.parametrize("I", [64, 160, 256])
+def test_short_contractions_over_many_tiles(I):
+    """Enough blocks that a workgroup of the short down projection goes through several tiles of H, the last one partial."""
+    p = Problem(T=300, H=2080, I=I, E=3, K=2, B=128, bias=I == 64, dropped=0.1, seed=40 + I)
+    pad = 512 - p.N
+    p.tpid = np.concatenate([p.tpid, np.full(pad * p.B, -1, np.int32)])
+    p.b2e = np.concatenate([p.b2e, np.full(pad, 2, np.int32)])
+    p.N = 512
+    y, dy, _ = p.exact()
+    check_rows(_run(p)["out"], y, dy)
+
+
+@pytest.mark.parametrize("H,I,B", [(1056, 4096, 256), (1024, 4128, 512)])
+def test_long_intermediate(H, I, B):
+    """X quantised slot by slot; with rows of fp32 and of fp16, a ragged H and a ragged I."""
+    p = Problem(T=330, H=H, I=I, E=2, K=1, B=B, dropped=0.1, residual=True, bias=B == 512, seed=I)
+    y, dy, gus = p.exact()
+    got = _run(p, "bf16")
+    check_rows(got["out"], y, dy)
+    ck, d = _gate_up(p, gus)
+    gu = bf16_values(got["checkpoint"])
+    assert (np.abs(gu - ck) <= d + (np.abs(ck) + d) * HALF).all()
+    assert not gu[(p.tpid < 0).reshape(p.N, 1, 1, p.B).repeat(2, 1).repeat(p.I, 2)].any()
+
+
 def test_valid_tokens_and_foreign_blocks():
     """Tokens from num_valid_tokens on are in no slot; blocks of an expert outside [0, E) are skipped."""
     p = Problem(T=200, H=128, I=128, E=3, K=2, B=128, residual=True, seed=6)
