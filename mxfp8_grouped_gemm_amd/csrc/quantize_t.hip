@@ -5,7 +5,10 @@
 // Bound by memory: 2 bytes read and 1.03 written an element.  A workgroup takes
 // 128 rows x 128 columns; wave w rows 32w .. 32w + 31 (one group), lane l the
 // columns 2l and 2l + 1, so each of its 32 loads is 256 consecutive bytes of a
-// row and a lane holds two whole groups in registers.
+// row and a lane holds two whole groups in registers.  The codes go through LDS,
+// where 8 lanes then write a column's 128 bytes at once.  16 matrices of 2048 x 2816:
+// 56 us, 5.0 TB/s (a copy of 1 GiB runs at 5.1); 76 us with each lane storing its own
+// 32-byte pieces.
 #include <type_traits>
 
 #include "kernels.hpp"
@@ -14,7 +17,8 @@
 namespace mx {
 
 namespace {
-constexpr int kT = 128;   // tile: rows and columns
+constexpr int kT = 128;        // tile: rows and columns
+constexpr int kPitch = kT + 16;   // LDS bytes of a column's codes
 
 // PAIRED: C even, so a lane's two columns are one aligned word.
 template <int FMT, bool PAIRED>
@@ -25,14 +29,19 @@ __global__ void __launch_bounds__(256) quantize_t_kernel(const uint16_t* __restr
   const int64_t m = rest / tiles_r;
   const int lane = threadIdx.x & 63;
   const int64_t r0 = int64_t(tr) * kT + 32 * (threadIdx.x >> 6), c = int64_t(tc) * kT + 2 * lane;
-  if (r0 >= R || c >= C) return;
-  const bool two = c + 1 < C;
+  __shared__ __attribute__((aligned(16))) uint8_t tile[kT * kPitch];
+  __shared__ uint32_t tile_scales[kT];
+  const bool in = r0 < R && c < C, two = c + 1 < C;
   const uint16_t* src = x + (m * R + r0) * C + c;
   uint32_t w[32], am = 0;
 #pragma unroll
   for (int r = 0; r < 32; ++r) {
-    if constexpr (PAIRED) w[r] = *reinterpret_cast<const uint32_t*>(src + r * C);
-    else w[r] = uint32_t(src[r * C]) | (two ? uint32_t(src[r * C + 1]) << 16 : 0u);
+    w[r] = 0;
+    if constexpr (PAIRED) {
+      if (in) w[r] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(src + r * C));
+    } else {
+      if (in) w[r] = uint32_t(src[r * C]) | (two ? uint32_t(src[r * C + 1]) << 16 : 0u);
+    }
   }
 #pragma unroll
   for (int r = 0; r < 32; ++r) am = absmax_bf16x2(am, w[r]);
@@ -47,16 +56,37 @@ __global__ void __launch_bounds__(256) quantize_t_kernel(const uint16_t* __restr
     p0[q] = encode_bf16x4<FMT>(lo_halves(a, b), lo_halves(d, e), s0);
     p1[q] = encode_bf16x4<FMT>(hi_halves(a, b), hi_halves(d, e), s1);
   }
-  const int64_t row = m * C + c;   // of the result
-  uint4* dst = reinterpret_cast<uint4*>(codes + row * R + r0);
+  const int wave = threadIdx.x >> 6;
+  uint4* dst = reinterpret_cast<uint4*>(tile + 2 * lane * kPitch + 32 * wave);
   dst[0] = make_uint4(p0[0], p0[1], p0[2], p0[3]);
   dst[1] = make_uint4(p0[4], p0[5], p0[6], p0[7]);
-  scales[row * (R / 32) + r0 / 32] = uint8_t(X0 + 127);
-  if (two) {
-    dst = reinterpret_cast<uint4*>(codes + (row + 1) * R + r0);
-    dst[0] = make_uint4(p1[0], p1[1], p1[2], p1[3]);
-    dst[1] = make_uint4(p1[4], p1[5], p1[6], p1[7]);
-    scales[(row + 1) * (R / 32) + r0 / 32] = uint8_t(X1 + 127);
+  dst += kPitch / 16;
+  dst[0] = make_uint4(p1[0], p1[1], p1[2], p1[3]);
+  dst[1] = make_uint4(p1[4], p1[5], p1[6], p1[7]);
+  uint8_t* sc = reinterpret_cast<uint8_t*>(tile_scales + 2 * lane) + wave;
+  sc[0] = uint8_t(X0 + 127);
+  sc[4] = uint8_t(X1 + 127);
+  __syncthreads();
+  const int64_t c0 = int64_t(tc) * kT, row0 = m * C + c0, first = int64_t(tr) * kT;   // of the result
+  const int q = threadIdx.x & 7;
+  if (first + 16 * q < R) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int col = 32 * k + (threadIdx.x >> 3);
+      if (c0 + col < C)
+        store_nt(codes + (row0 + col) * R + first + 16 * q, *reinterpret_cast<const uint4*>(tile + col * kPitch + 16 * q));
+    }
+  }
+  if (threadIdx.x < kT && c0 + threadIdx.x < C) {
+    const uint32_t v = tile_scales[threadIdx.x];
+    uint8_t* to = scales + (row0 + threadIdx.x) * (R / 32) + first / 32;
+    if (R % 128 == 0 && (reinterpret_cast<uintptr_t>(scales) & 3) == 0) {   // scales: of any alignment
+      *reinterpret_cast<uint32_t*>(to) = v;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (first + 32 * k < R) to[k] = uint8_t(v >> (8 * k));
+    }
   }
 }
 }  // namespace

@@ -39,3 +39,15 @@ def test_past_32_bits():
     one = mx.mxfp8_quantize_transposed(x[-1].contiguous())
     assert torch.equal(c[-1], one[0]) and torch.equal(s[-1], one[1])
     assert not c[-1, :-1].any() and not c[:-1].any() and int(s[-1, -1, -1]) == 127 + 5 - 8
+
+
+@pytest.mark.parametrize("shift", [1, 2, 4])
+def test_scales_of_any_alignment(shift):
+    import mxfp8_grouped_gemm_amd as mx
+    x = torch.randn(2, 256, 70, device="cuda").to(torch.bfloat16)
+    want = mx.mxfp8_quantize_transposed(x)
+    buf = torch.full((2 * 70 * 8 + 16,), 77, dtype=torch.uint8, device="cuda")
+    s = buf[shift:shift + 2 * 70 * 8].view(2, 70, 8)
+    c, _ = mx.mxfp8_quantize_transposed(x, out=(torch.empty_like(want[0]), s))
+    assert torch.equal(c, want[0]) and torch.equal(s, want[1])
+    assert (buf[:shift] == 77).all() and (buf[shift + 2 * 70 * 8:] == 77).all()
