@@ -23,7 +23,7 @@ FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Wall", "-Wno-
 SOURCES = ["api.cpp", "quantize.hip", "gemm_dense.hip", "moe_aux.hip", "moe_phase1_256.hip", "moe_phase1_256x128.hip",
            "moe_phase1_128.hip", "moe_phase1_epi.hip", "moe_phase3.hip", "moe_grads.hip", "router.hip", "prequant.hip",
            "router_fwd.hip", "balance.hip", "gated_act.hip", "api_fwd.cpp", "dropout.hip", "quantize_t.hip", "moe_fwd.hip",
-           "moe_fwd_gate_up_256.hip", "moe_fwd_down.hip", "moe_fwd_down_short.hip", "moe_fwd_prep.hip",
+           "moe_fwd_gate_up_256.hip", "moe_fwd_gate_up_exact.hip", "moe_fwd_down.hip", "moe_fwd_down_short.hip", "moe_fwd_prep.hip",
            "moe_tokens.hip"]
 
 

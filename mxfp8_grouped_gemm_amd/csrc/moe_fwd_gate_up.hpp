@@ -13,8 +13,13 @@
 //           slots (one rounding more than from fp32, so that the 8-bit
 //           checkpoint is the bf16 one, quantised)
 // s is rounded once, to its code: from the fp32 sums, not the bf16 checkpoint.
-// The scaled MFMA's own rounding (about 6e-6 of a result's size) moves one code
-// in some thousands to its neighbour.
+// The scaled MFMA truncates small products (some 5e-5 of a result's size in all),
+// which moves 0.16% of the codes to a neighbour, and once in some ten thousand
+// groups the scale: y is then 0.0020 off the formula (norm of the difference over
+// y's) where its own rounding to bf16 is 0.0017.  Where there are few tiles
+// (fwd_few_tiles), a call of few groups could meet such a one to its whole extent,
+// and its time goes by latency: there the products are the codes' exact bf16 values
+// on the bf16 MFMA (kFp8Bf16), at half the rate.
 //
 // A tile of BM rows holds BM / 2 gate rows and the same BM / 2 up rows, as
 // fragments of 32 in turn: a lane's accumulators then hold gate and up of the
@@ -131,7 +136,7 @@ __device__ __forceinline__ void fwd_store_ckpt(const MoeFwdArgs& p, int b, int64
   }
 }
 
-template <int BM, int BN, bool RAG, bool GEGLU, int CK>
+template <int BM, int BN, int ELEM, bool RAG, bool GEGLU, int CK>
 __global__ void __launch_bounds__(v2::kThreads) fwd_gate_up_kernel(MoeFwdArgs p) {
   constexpr int SMEM = v3::smem_bytes(BM, BN);
   static_assert(SMEM >= 4 * kCkWaveBytes, "the checkpoint's staging fits the ring");
@@ -167,7 +172,7 @@ __global__ void __launch_bounds__(v2::kThreads) fwd_gate_up_kernel(MoeFwdArgs p)
     v3::setup_gather(A, wc, 2 * p.I, p.H, row_of);
     if (p.x_by_slot) v3::setup_rows_sm(B, p.x_codes, sbase + n0, sbase + p.B, P, p.Hp);
     else v3::setup_gather(B, p.x_codes, p.T, p.Hp, tok_of);
-    v3::mainloop<BM, BN, v3::kFp8, kE4M3, kE4M3, v3::KMapPlain, RAG ? 1 : 0>(A, B, &sd, int(p.Hp / v3::SK),
+    v3::mainloop<BM, BN, ELEM, kE4M3, kE4M3, v3::KMapPlain, RAG ? 1 : 0>(A, B, &sd, int(p.Hp / v3::SK),
                                                                             v3::KMapPlain{}, smem, acc, uint32_t(p.H));
   }
   if constexpr (CK != 0) __syncthreads();   // every wave is done with the ring: its bytes stage the checkpoint
@@ -252,13 +257,13 @@ __global__ void __launch_bounds__(v2::kThreads) fwd_gate_up_kernel(MoeFwdArgs p)
 }
 
 // ---------------------------------------------------------------------------
-template <int BM, int BN>
+template <int BM, int BN, int ELEM>
 hipError_t fwd_gate_up_launch(MoeFwdArgs p, hipStream_t st) {
   p.tiles_m = int(p.Ip / (BM / 2));
   const int64_t blocks = (int64_t(p.tiles_m) * (p.B / BN) * p.N + 7) & ~int64_t(7);   // every tile, rounded to 8
   if (blocks > kMaxGrid256) return hipErrorInvalidValue;
   auto go = [&](auto rag, auto geglu, auto ck) {
-    fwd_gate_up_kernel<BM, BN, rag(), geglu(), ck()><<<unsigned(blocks), v2::kThreads, 0, st>>>(p);
+    fwd_gate_up_kernel<BM, BN, ELEM, rag(), geglu(), ck()><<<unsigned(blocks), v2::kThreads, 0, st>>>(p);
   };
   auto kind = [&](auto rag, auto geglu) {
     if (p.ckpt) go(rag, geglu, std::integral_constant<int, 1>{});

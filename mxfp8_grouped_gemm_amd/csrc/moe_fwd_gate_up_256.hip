@@ -3,6 +3,6 @@
 
 namespace mx {
 
-template hipError_t fwd_gate_up_launch<256, 256>(MoeFwdArgs, hipStream_t);
+template hipError_t fwd_gate_up_launch<256, 256, v3::kFp8>(MoeFwdArgs, hipStream_t);
 
 }  // namespace mx

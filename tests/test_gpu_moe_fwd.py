@@ -129,17 +129,41 @@ def test_short_contractions_over_many_tiles(I):
     check_rows(_run(p)["out"], y, dy)
 
 
-@pytest.mark.parametrize("H,I,B", [(1056, 4096, 256), (1024, 4128, 512)])
-def test_long_intermediate(H, I, B):
-    """X quantised slot by slot; with rows of fp32 and of fp16, a ragged H and a ragged I."""
-    p = Problem(T=330, H=H, I=I, E=2, K=1, B=B, dropped=0.1, residual=True, bias=B == 512, seed=I)
+# name: the problem and how many blocks its list is padded to, those behind of no token
+PADDED = {
+    # 256 x 256 tiles, whole and ragged contractions
+    "tiles_256": (dict(T=300, H=1024, I=384, E=3, K=2, B=256, dropped=0.1, bias=True), 60),
+    "tiles_256_ragged": (dict(T=300, H=1056, I=416, E=3, K=2, B=512, dropped=0.1, geglu=True), 40),
+    # X quantised slot by slot; rows of fp32 and of fp16
+    "by_slot": (dict(T=330, H=1056, I=4096, E=2, K=1, B=256, dropped=0.1, residual=True), 12),
+    "by_slot_f16": (dict(T=330, H=1024, I=4128, E=2, K=1, B=512, dropped=0.1, bias=True), 9),
+    # the scaled MFMA at 128 x 128
+    "tiles_128": (dict(T=300, H=768, I=160, E=5, K=2, B=128, on_i=True), 200),
+}
+
+
+@pytest.mark.parametrize("name", PADDED)
+def test_padded_block_list(name):
+    """Lists as long as a fixed capacity needs: more tiles than one round of the CUs, most of no token."""
+    args, N = PADDED[name]
+    p = Problem(**args, seed=sum(map(ord, name)))
+    assert p.N <= N
+    p.tpid = np.concatenate([p.tpid, np.full((N - p.N) * p.B, -1, np.int32)])
+    p.b2e = np.concatenate([p.b2e, np.full(N - p.N, p.E - 1, np.int32)])
+    p.N = N
     y, dy, gus = p.exact()
-    got = _run(p, "bf16")
-    check_rows(got["out"], y, dy)
+    r = _run(p, "bf16")
+    check_rows(r["out"], y, dy, name)
     ck, d = _gate_up(p, gus)
-    gu = bf16_values(got["checkpoint"])
+    gu = bf16_values(r["checkpoint"])
     assert (np.abs(gu - ck) <= d + (np.abs(ck) + d) * HALF).all()
     assert not gu[(p.tpid < 0).reshape(p.N, 1, 1, p.B).repeat(2, 1).repeat(p.I, 2)].any()
+    bits = r["checkpoint"].cpu().view(torch.int16).numpy().view(np.uint16)
+    codes, scales = oracle.quantize(bits.reshape(-1, p.B), 1, oracle.E4M3)
+    r8 = _run(p, "mxfp8")
+    assert torch.equal(r8["out"], r["out"])
+    assert np.array_equal(r8["checkpoint"][0].cpu().numpy().reshape(codes.shape), codes)
+    assert np.array_equal(r8["checkpoint"][1].cpu().numpy().reshape(scales.shape), scales)
 
 
 def test_valid_tokens_and_foreign_blocks():
