@@ -134,8 +134,13 @@ __device__ __forceinline__ uint32_t tok_quantise(const uint4 (&v)[2], uint4& cod
 // ntiles tiles.  w, ws: the expert's codes and scales, rows of K bytes (wrows of
 // them); row(q), q < 64: tile 0's source rows; tile t's lie t * trows further
 // down.  x, xs: the columns' codes and scales, or bf16 rows (BF16X), col(q): source
-// row or -1.  done(t, acc) takes a tile's sums.
-template <int NCOL, bool GENERIC, bool BF16X>
+// row or -1.  done(t, acc) takes a tile's sums.  EXACT: on the bf16 MFMA, from the
+// codes' exact values: the gate/up sums are rounded to codes again, and the scaled
+// MFMA's truncation of small products would move some of those to a neighbour, once
+// in some ten thousand groups a scale, which a call of a few hundred groups shows in
+// full (y 0.0047 off the formula where its rounding to bf16 is 0.0017).  The stream
+// of weights hides the difference.
+template <int NCOL, bool GENERIC, bool BF16X, bool EXACT>
 struct TokLoop {
   static constexpr int FN = NCOL <= 32 ? 1 : 2;
   static constexpr int XB = BF16X ? 2 : 1;                                     // bytes an element of the columns
@@ -301,16 +306,23 @@ struct TokLoop {
 #pragma unroll
             for (int c = 0; c < 2; ++c) sb[0] |= tok_quantise(xv[P][c], fb[P][0][c]) << (8 * (2 * P + c));
         }
-#pragma unroll
-        for (int f = 0; f < 2; ++f)
-#pragma unroll
-          for (int j = 0; j < FN; ++j)
-            acc[f][j] = v3::mma<kE4M3, kE4M3, 0>(fa[0][f], fb[0][j], acc[f][j], int(sa[f] >> (8 * h)), int(sb[j] >> (8 * h)));
-#pragma unroll
-        for (int f = 0; f < 2; ++f)
-#pragma unroll
-          for (int j = 0; j < FN; ++j)
-            acc[f][j] = v3::mma<kE4M3, kE4M3, 2>(fa[1][f], fb[1][j], acc[f][j], int(sa[f] >> (8 * h)), int(sb[j] >> (8 * h)));
+        v2::static_for<2>([&](auto P) {
+          v2::static_for<2>([&](auto F) {
+            v2::static_for<FN>([&](auto J) {
+              if constexpr (EXACT) {
+                using R = v3::Ring<128, 128, v3::kFp8Bf16, kE4M3, kE4M3, v3::KMapPlain>;
+                v2::static_for<4>([&](auto C) {   // 16 columns each
+                  acc[F][J] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(R::template step_operand<kE4M3, P, C>(fa[P][F], sa[F]),
+                                                                      R::template step_operand<kE4M3, P, C>(fb[P][J], sb[J]),
+                                                                      acc[F][J], 0, 0, 0);
+                });
+              } else {
+                acc[F][J] = v3::mma<kE4M3, kE4M3, 2 * int(P)>(fa[P][F], fb[P][J], acc[F][J], int(sa[F] >> (8 * h)),
+                                                              int(sb[J] >> (8 * h)));
+              }
+            });
+          });
+        });
       }
       done(t, acc);
     }
@@ -349,7 +361,7 @@ __device__ __forceinline__ float published(const float* p) {
 template <int NCOL, bool GENERIC, int KS>
 __global__ void __launch_bounds__(64 * kWaves) tok_gate_up_kernel(MoeTokensArgs p) {
   constexpr bool FEW = NCOL == kFewTokens;
-  using Loop = TokLoop<NCOL, GENERIC, FEW>;
+  using Loop = TokLoop<NCOL, GENERIC, FEW, true>;
   using L = TokLds<NCOL, FEW>;
   constexpr int FN = Loop::FN;
   __shared__ __attribute__((aligned(16))) uint8_t smem[L::BYTES];
@@ -481,7 +493,7 @@ __global__ void __launch_bounds__(64 * kWaves) tok_gate_up_kernel(MoeTokensArgs 
 template <int NCOL, bool GENERIC, int KS>
 __global__ void __launch_bounds__(64 * kWaves) tok_down_kernel(MoeTokensArgs p) {
   constexpr bool FEW = NCOL == kFewTokens, LAST = FEW && KS == 4;
-  using Loop = TokLoop<(NCOL < 8 ? 8 : NCOL), GENERIC, false>;
+  using Loop = TokLoop<(NCOL < 8 ? 8 : NCOL), GENERIC, false, false>;
   using L = TokLds<(NCOL < 8 ? 8 : NCOL), false>;
   constexpr int FN = Loop::FN;
   __shared__ __attribute__((aligned(16))) uint8_t smem[L::BYTES];
