@@ -7,8 +7,10 @@
 // columns 2l and 2l + 1, so each of its 32 loads is 256 consecutive bytes of a
 // row and a lane holds two whole groups in registers.  The codes go through LDS,
 // where 8 lanes then write a column's 128 bytes at once.  16 matrices of 2048 x 2816:
-// 56 us, 5.0 TB/s (a copy of 1 GiB runs at 5.1); 76 us with each lane storing its own
-// 32-byte pieces.
+// 48 us, 5.8 TB/s (a copy of 1 GiB runs at 5.1); 77 us with each lane storing its own
+// 32-byte pieces.  Loads and stores go through the caches: nontemporal loads cost rows
+// that start inside a line a quarter (1184 x 2116: 41 -> 52 us) and the others a tenth,
+// nontemporal stores 3 us of the 48.
 #include <type_traits>
 
 #include "kernels.hpp"
@@ -35,13 +37,36 @@ __global__ void __launch_bounds__(256) quantize_t_kernel(const uint16_t* __restr
   const uint16_t* src = x + (m * R + r0) * C + c;
   uint32_t w[32], am = 0;
 #pragma unroll
-  for (int r = 0; r < 32; ++r) {
-    w[r] = 0;
-    if constexpr (PAIRED) {
-      if (in) w[r] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(src + r * C));
-    } else {
-      if (in) w[r] = uint32_t(src[r * C]) | (two ? uint32_t(src[r * C + 1]) << 16 : 0u);
+  for (int r = 0; r < 32; ++r) w[r] = 0;
+  if constexpr (PAIRED) {
+    if (in) {
+#pragma unroll
+      for (int r = 0; r < 32; ++r) w[r] = *reinterpret_cast<const uint32_t*>(src + r * C);
     }
+  } else if (int64_t(blockIdx.x) + 1 < gridDim.x) {
+    // odd C: every other row's pairs straddle two words, the second of which is the next lane's first
+    // (22 matrices of 1184 x 2115: 47 us, 75 with 2-byte loads).  A word may reach past the tile, not past x:
+    // the last tile takes the other way.
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(x);
+    if (r0 < R) {   // whole waves
+      uint32_t tail[32];
+#pragma unroll
+      for (int r = 0; r < 32; ++r) {
+        const int64_t at = (m * R + r0 + r) * C + (c < C ? c : C - 1);
+        w[r] = words[at >> 1];
+        tail[r] = lane == 63 && (at & 1) && two ? words[(at >> 1) + 1] : 0u;
+      }
+#pragma unroll
+      for (int r = 0; r < 32; ++r) {
+        const uint32_t next = uint32_t(__builtin_amdgcn_update_dpp(int(tail[r]), int(w[r]), 0x130, 0xf, 0xf, false));
+        const bool odd = ((m * R + r0 + r) * C & 1) != 0;   // c is even
+        w[r] = odd ? (w[r] >> 16) | (next << 16) : w[r];
+        w[r] = two ? w[r] : c < C ? w[r] & 0xffffu : 0u;
+      }
+    }
+  } else if (in) {
+#pragma unroll
+    for (int r = 0; r < 32; ++r) w[r] = uint32_t(src[r * C]) | (two ? uint32_t(src[r * C + 1]) << 16 : 0u);
   }
 #pragma unroll
   for (int r = 0; r < 32; ++r) am = absmax_bf16x2(am, w[r]);
@@ -74,7 +99,7 @@ __global__ void __launch_bounds__(256) quantize_t_kernel(const uint16_t* __restr
     for (int k = 0; k < 4; ++k) {
       const int col = 32 * k + (threadIdx.x >> 3);
       if (c0 + col < C)
-        store_nt(codes + (row0 + col) * R + first + 16 * q, *reinterpret_cast<const uint4*>(tile + col * kPitch + 16 * q));
+        *reinterpret_cast<uint4*>(codes + (row0 + col) * R + first + 16 * q) = *reinterpret_cast<const uint4*>(tile + col * kPitch + 16 * q);
     }
   }
   if (threadIdx.x < kT && c0 + threadIdx.x < C) {

@@ -9,8 +9,8 @@ pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("fmt", [oracle.E4M3, oracle.E5M2])
-@pytest.mark.parametrize("G,R,C", [(1, 32, 1), (1, 32, 2), (3, 96, 77), (2, 128, 128), (1, 160, 129), (5, 64, 1000), (2, 608, 130),
-                                   (1, 4096, 34), (40, 32, 64)])
+@pytest.mark.parametrize("G,R,C", [(1, 32, 1), (1, 32, 2), (3, 96, 77), (2, 128, 128), (1, 160, 129), (5, 64, 1000), (2, 608, 130), (3, 160, 255),
+                                   (1, 4096, 34), (40, 32, 64), (1, 64, 385), (2, 32, 127)])
 def test_codes_and_scales(G, R, C, fmt):
     import mxfp8_grouped_gemm_amd as mx
     r = np.random.default_rng(G * R + C)
