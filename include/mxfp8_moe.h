@@ -700,9 +700,13 @@ int dropout_add_bwd(const dropout_add_args* args, void* stream);
  *   s = act(g) u, times a with the affinity on I
  *   y_t = residual_t + drop( sum over t's slots, by ascending expert, of
  *         a (Q(s) Wd[e]^T + b2[e]) )   (groups along I; without a, on I)
- * Products and sums are fp32 (on the scaled fp8 MFMA), g and u are not rounded
- * before s, and y is rounded once.  A token without a slot gets its residual, or 0.
- * E = 1 with every token in a slot is a dense gated FFN.
+ * Products are summed in fp32 (on the scaled fp8 MFMA, which truncates products far
+ * below the largest of their eight; for g and u of few slots on the bf16 MFMA, from
+ * the codes' exact values), g and u are not rounded before s, and y is rounded once.
+ * In between, a slot's share of y is kept in fp32, or, with I below 4096 or no
+ * multiple of 128, in fp16 times a power of two per 64 columns (off by at most 2^-12
+ * of itself).  A token without a slot gets its residual, or 0.  E = 1 with every token
+ * in a slot is a dense gated FFN.
  * Arguments (moe_fwd_mxfp8_args; [T], [N], ... and the block lists as for
  * moe_bwd_mxfp8):
  *   hidden_states [T,H] bf16; expert_affinities_masked [T*E] fp32.
@@ -726,15 +730,20 @@ int dropout_add_bwd(const dropout_add_args* args, void* stream);
  *     backward is dropout_add_bwd on y's gradient.
  * Workspace: moe_fwd_mxfp8_workspace_size(args) bytes (0 on invalid shapes),
  * 256-byte aligned; nothing in it outlives the call.  Only sizes shape it.
- * Sums run in an order that the sizes and the block lists give: the results are
- * the same bits on every run.  Device-side preconditions as for moe_bwd_mxfp8.
+ * Sums run in an order, and the kernels are chosen, by the sizes and the block
+ * lists: the results are the same bits on every run.  Device-side preconditions as
+ * for moe_bwd_mxfp8.
  * Non-finite values: a group of X or s holding one has unspecified codes, and the
- * token's row of y is unspecified; other tokens' are not affected.
+ * token's row of y is unspecified; other tokens' are not affected (but a group of 32
+ * slots of an 8-bit checkpoint that holds one is unspecified).  The weights' codes
+ * and scales are finite.
  * Errors: INVALID_ARG (shapes, null required pointers, alignment, formats, both
  * checkpoints or half of one, dropout_p outside [0, 1], affinity_on or activation
  * outside {0,1}), UNSUPPORTED (block_size outside the set, a bias with the affinity
- * on I, sizes beyond 32-bit indexing: T * E, T * H, 2 * H * I or N * B * I / 32 above
- * 2^31 - 1, N * B above 2^24, I above 2^22, or more tiles than one launch takes),
+ * on I, sizes beyond 32-bit indexing: T * E, T * H', 2 * H' * I, H * I' or N * B * I' / 32
+ * above 2^31 - 1 (H', I': rounded up to 128), N * B above 2^24, I above 2^22, or more
+ * tiles, tokens or groups of weight scales than one launch takes: T above 2^24 - 1, E
+ * above 2^23 over the tiles of 64 rows x 4096 columns of an expert's weights),
  * WORKSPACE, HIP. */
 typedef struct {
   int64_t T, H, I, E, N, block_size;
@@ -769,7 +778,8 @@ int moe_fwd_mxfp8(const moe_fwd_mxfp8_args* args, void* workspace, size_t worksp
  *   y_t = residual_t + sum over k, in order, of the expert topk_idx[t][k]'s share
  *         with affinity topk_scores[t][k]; ids outside [0,E) are dropped.  An id
  *         that a token holds twice counts twice.
- * Roundings as in moe_fwd_mxfp8.
+ * g and u are summed on the bf16 MFMA from the codes' exact values, the down
+ * projection on the scaled fp8 MFMA, all in fp32; otherwise rounded as in moe_fwd_mxfp8.
  * Arguments (moe_tokens_fwd_mxfp8_args):
  *   T <= MOE_TOKENS_FWD_MAX_TOKENS, 1 <= K <= MXFP8_ROUTER_MAX_K.
  *   hidden_states [T,H] bf16; topk_idx [T,K] int32, topk_scores [T,K] fp32.

@@ -45,7 +45,9 @@ hipError_t launch_fwd_gate_up(const MoeFwdArgs& p, hipStream_t st) {
 // a (row + b2) ), fp32, rounded once; with the affinity on I the rows carry it
 // already.  A team of TPT threads per token (whole waves), each wave finding
 // the token's slots by itself, 64 experts a ballot, and a thread summing 8
-// columns: 16-byte stores, and one counter of the dropout mask.
+// columns: 16-byte stores, and one counter of the dropout mask.  Bound by the
+// rows' bytes: 262144 of H = 1536 in fp16, 906 MB with the result, 181 us, 5.0 TB/s
+// (eight slots at a time, more registers, 196).
 namespace {
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 template <int TPT, bool F16>

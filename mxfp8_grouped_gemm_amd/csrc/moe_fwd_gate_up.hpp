@@ -25,10 +25,18 @@
 // fragments of 32 in turn: a lane's accumulators then hold gate and up of the
 // same 16 (i, p), 16 of a group's 32 i with the lane's other half holding the
 // rest, so activation, product and group maxima stay in registers.  The tile
-// columns are the slots, whose X code rows are gathered by token.  Tiles cover
+// columns are the slots, whose X code rows are gathered by token (or lie in the slots'
+// order, fwd_x_by_slot).  Tiles cover
 // i up to Ip, the contraction of the down projection in whole pairs: groups from
 // I on get zeros.  Workgroups whose tile holds no routed slot write the
 // checkpoint's zeros there.
+//
+// Measured (256 x 256 tiles but the last): 32768 slots, H = 4096, I = 14336, 3.5 ms,
+// 2.2 PFLOP/s; H = 2048, I = 1408, 8-bit checkpoint, 285 us, 1.33 PFLOP/s; 262144 slots,
+// H = 1536, I = 256, bf16 checkpoint, 400 us, 1.03 PFLOP/s.  Without their stages (two of
+// them only) these take 0.7 ms, 129 and 179 us: what bounds the short contractions is the
+// start of a tile (its block, expert, tokens, first loads: a chain of latencies) and its
+// epilogue, which one workgroup a CU does not overlap.
 #pragma once
 #include "gemm_v2.hpp"
 #include "gemm_v3.hpp"

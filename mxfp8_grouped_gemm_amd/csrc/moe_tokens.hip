@@ -18,6 +18,10 @@
 // the down projection adds up the splits and selections: two launches.  More
 // tokens: a launch before that lists the pairs by expert and quantises X, and
 // one after that adds up.
+// Measured: T = 1, two experts of H = 4096, I = 14336: 51 + 26 us, 4.7 TB/s of weights;
+// T = 200 over 128 experts of H = 1536, I = 256: 5 + 37 + 21 + 7 us, 2.7 TB/s in the
+// products, where each workgroup's 393 KB leave no time to hide the chain before its
+// first load (5 us) or its epilogue; T = 1, eight of those: 9.3 + 9.6 us, all latency.
 #include <type_traits>
 
 #include "gemm_v4.hpp"
