@@ -293,3 +293,51 @@ def test_forward_and_backward(checkpoint):
     ref = oracle.moe_bwd(prob)
     for k, rows, experts in (("dx", p.T, None), ("daff", None, None), ("dwgu", None, E), ("dwd", None, E)):
         assert_parity(k, parity_stats(bf(host(g[k])), bf(ref[k]), rows=rows, experts=experts))
+
+
+def test_rows_past_32_bits():
+    """2^20 slots whose rows take more than 2^32 bytes: 512 tokens 256 times over, all the same, the first against the oracle."""
+    import mxfp8_grouped_gemm_amd as mx
+    p = Problem(T=512, H=2080, I=32, E=8, K=8, B=1024, seed=21)
+    pos, kw = p.on()
+    n = 256
+    T = n * p.T
+    x, aff = pos[0].repeat(n, 1), pos[1].view(p.T, p.E).repeat(n, 1)
+    tpid = torch.arange(T, dtype=torch.int32, device="cuda").repeat(p.E)
+    b2e = torch.arange(p.E, dtype=torch.int32, device="cuda").repeat_interleave(T // p.B)
+    assert tpid.numel() * p.H * 2 > 1 << 32
+    y = mx.moe_fwd_mxfp8(x, aff.view(-1), *pos[2:6], tpid, b2e, p.B)["out"].view(n, p.T, p.H)
+    assert (y == y[:1]).all()
+    want, dy, _ = p.exact()
+    check_rows(y[0], want, dy)
+
+
+def test_weights_past_32_bits():
+    """An expert whose weights lie behind the 2^32nd byte gives what it gives alone, with block lists and for few tokens."""
+    import mxfp8_grouped_gemm_amd as mx
+    E, H, I, B, T = 38, 4096, 14336, 128, 96
+    g = torch.Generator("cuda").manual_seed(3)
+
+    def codes(*shape):   # E4M3 of magnitude 0.5 to 0.94
+        c = torch.randint(0x30, 0x38, shape, generator=g, device="cuda", dtype=torch.uint8)
+        return c | (torch.randint(0, 2, shape, generator=g, device="cuda", dtype=torch.uint8) << 7)
+    wgu, wd = codes(E, 2, I, H), codes(E, H, I)
+    assert wgu[:-1].numel() > 1 << 32
+    sgu = torch.full((E, 2, I, H // 32), 127 - 5, dtype=torch.uint8, device="cuda")
+    sd = torch.full((E, H, I // 32), 127 - 6, dtype=torch.uint8, device="cuda")
+    x = torch.randn(T, H, generator=g, device="cuda").to(torch.bfloat16)
+    tpid = torch.full((B,), -1, dtype=torch.int32, device="cuda")
+    tpid[:T] = torch.arange(T, device="cuda")
+    aff = torch.zeros(T, E, device="cuda")
+    aff[:, -1] = 0.75
+    many = mx.moe_fwd_mxfp8(x, aff.view(-1), wgu, sgu, wd, sd, tpid, torch.full((1,), E - 1, dtype=torch.int32, device="cuda"), B)
+    last = [t[-1:].contiguous() for t in (wgu, sgu, wd, sd)]
+    one = mx.moe_fwd_mxfp8(x, aff[:, -1].contiguous(), *last, tpid, torch.zeros(1, dtype=torch.int32, device="cuda"), B)
+    assert many["out"].float().norm() > 0 and torch.equal(many["out"], one["out"])
+    for n in (1, 3, 9, T):
+        ids = torch.full((n, 1), E - 1, dtype=torch.int32, device="cuda")
+        a = torch.full((n, 1), 0.75, device="cuda")
+        y = mx.moe_tokens_fwd_mxfp8(x[:n], ids, a, wgu, sgu, wd, sd)
+        z = mx.moe_tokens_fwd_mxfp8(x[:n], torch.zeros_like(ids), a, *last)
+        # E chooses how many columns a workgroup takes, not how a column is summed, up to the split of the contraction
+        assert y.float().norm() > 0 and (y.double() - z.double()).norm() <= 2 ** -8 * z.double().norm()
