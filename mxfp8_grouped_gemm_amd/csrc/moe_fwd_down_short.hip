@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(v2::kThreads, 2) fwd_down_short_kernel(MoeFwdD
       });
     });
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the next rows (and the last tile's stores, a tile old)
-    __builtin_amdgcn_wave_barrier();   // the staging is the wave's own: its LDS operations run in order
+    wave_lds_order();   // the staging is the wave's own
     const int c = lane & 7;
     if (m0 + 8 * c < p.H) {   // H % 32 == 0
       uint16_t* dst = p.rows + (s0 + wn * 64 + (lane >> 3)) * p.H + m0 + 8 * c;

@@ -255,9 +255,9 @@ __global__ void __launch_bounds__(v2::kThreads) fwd_gate_up_kernel(MoeFwdArgs p)
         if (h == 0) p.inter_scales[((i >> 7) * P + slot) * 4 + (i >> 5 & 3)] = uint8_t(X + 127);
 #endif
         if constexpr (CK != 0) {
-          __builtin_amdgcn_wave_barrier();   // the wave's own LDS operations run in order
+          wave_lds_order();
           fwd_store_ckpt<CK>(p, b, i, s, stage);
-          __builtin_amdgcn_wave_barrier();
+          wave_lds_order();
         }
       });
     }

@@ -9,7 +9,7 @@
 //                     tile ranges of the two products (up to kListMax blocks)
 //   fwd_ranges_kernel the ranges of more blocks, a workgroup for each product
 // X is bound by memory (32768 x 1536: 42 us with 151 MB of weights' scales, 3.6 TB/s);
-// the rest is launches and latency (T = 256, E = 4: one launch of 7 us where four of
+// the rest is launches and latency (T = 256, E = 4: one launch of 5 us where four of
 // 2.5 to 4 us stood).
 #include "kernels.hpp"
 #include "moe_tiles.hpp"
@@ -19,10 +19,12 @@ namespace mx {
 
 namespace {
 constexpr int kThreads = 256;
-constexpr int64_t kSmallSlots = 4096, kSmallPairs = 16384;   // a small layer: slots, T * E
-constexpr int kSmallBlocks = int(kSmallSlots / 128);
+// A small layer (slots, T * E): one workgroup of kSmallThreads sets up its slots beside the others.  T = 1500, 23
+// blocks of 256: 10.0 us (15.6 with 256 threads), where two launches took 6.2 and 7.6.
+constexpr int64_t kSmallSlots = 8192, kSmallPairs = 32768;
+constexpr int kSmallBlocks = int(kSmallSlots / 128), kSmallThreads = 1024;
 
-bool small_layer(const MoeFwdPrep& p) { return p.N * p.B <= kSmallSlots && p.T * p.E <= kSmallPairs; }
+bool small_layer(const MoeFwdPrep& p) { return p.N * p.B <= kSmallSlots && p.T * p.E <= kSmallPairs && !p.x_by_slot; }
 
 // ---------------------------------------------------------------------------
 // X: a thread takes 8 columns, 4 lanes a group of 32.
@@ -41,10 +43,11 @@ __device__ __forceinline__ uint2 quant_x8(const uint4& v, int& X) {
   return make_uint2(encode_bf16x4<kE4M3>(clamp_bf16x2(w[0], lim), clamp_bf16x2(w[1], lim), s),
                     encode_bf16x4<kE4M3>(clamp_bf16x2(w[2], lim), clamp_bf16x2(w[3], lim), s));
 }
+template <int TH>
 __device__ __forceinline__ void quant_x(const MoeFwdPrep& p, unsigned wg, unsigned wgs) {
   constexpr int U = 4;   // chunks of a thread, their loads issued together
-  const uint32_t per = uint32_t(p.Hp / 8), n = uint32_t(p.T) * per, stride = wgs * kThreads;   // T * Hp < 2^32
-  for (uint32_t c0 = wg * kThreads + threadIdx.x; c0 < n; c0 += U * stride) {
+  const uint32_t per = uint32_t(p.Hp / 8), n = uint32_t(p.T) * per, stride = wgs * TH;   // T * Hp < 2^32
+  for (uint32_t c0 = wg * TH + threadIdx.x; c0 < n; c0 += U * stride) {
     uint4 v[U];
     uint32_t row[U], col[U];
 #pragma unroll
@@ -114,14 +117,15 @@ PairsJob pairs_job(const uint8_t* in, uint8_t* out, int64_t E, int64_t rows, int
   j.n = unsigned(E) * j.gx * j.gy;
   return j;
 }
+template <int TH>
 __device__ __forceinline__ void scale_pairs(const PairsJob& j, unsigned id, uint32_t (*tile)[65]) {
   const unsigned per = j.gx * j.gy, g = id / per, yx = id - g * per, y = yx / j.gx, x = yx - y * j.gx;
   const int64_t p0 = int64_t(x) * 32, r0 = int64_t(y) * 64;
   const uint8_t* src = j.in + g * j.rows * j.G;
   uint32_t* dst = j.out + g * j.rows * j.kp;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int i = threadIdx.x + kThreads * k, r = i >> 5, q = i & 31;
+  for (int k = 0; k < 2048 / TH; ++k) {
+    const int i = threadIdx.x + TH * k, r = i >> 5, q = i & 31;
     if (r0 + r < j.rows && p0 + q < j.kp) {
       const uint8_t* s = src + (r0 + r) * j.G + 4 * (p0 + q);
       uint32_t w = 0;
@@ -137,15 +141,15 @@ __device__ __forceinline__ void scale_pairs(const PairsJob& j, unsigned id, uint
   }
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int i = threadIdx.x + kThreads * k, q = i >> 6, r = i & 63;
+  for (int k = 0; k < 2048 / TH; ++k) {
+    const int i = threadIdx.x + TH * k, q = i >> 6, r = i & 63;
     if (r0 + r < j.rows && p0 + q < j.kp) dst[(p0 + q) * j.rows + r0 + r] = tile[q][r];
   }
 }
 
 // ---------------------------------------------------------------------------
 // Tile ranges (moe_tiles.hpp) of any number of blocks by one workgroup of TH
-// threads; ext(b): block b's extent.  One pass over the blocks for the totals,
+// threads, or (TH = 64) by one wave of any; ext(b): block b's extent.  One pass over the blocks for the totals,
 // one for the starts and the map: TH blocks at a time, a block's map entries
 // by as many lanes as it has tiles, from starts held in LDS (39 blocks of 448 tiles:
 // 12 us less than a thread a block).
@@ -156,13 +160,18 @@ struct RangeLds {
 };
 template <int TH, class Ext>
 __device__ __forceinline__ void make_ranges(const Ext& ext, int N, const TileRangeJob& j, RangeLds<TH>& lds) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, cmax = (j.blk + j.W - 1) / j.W * j.other;
+  const int tid = TH == 64 ? threadIdx.x & 63 : threadIdx.x;
+  auto sync = [] {
+    if constexpr (TH == 64) wave_lds_order();
+    else __syncthreads();
+  };
+  const int lane = tid & 63, wave = tid >> 6, cmax = (j.blk + j.W - 1) / j.W * j.other;
   // tiles of fully live blocks (with rr) in the high word, of the others in the low
   auto word = [&](int c) { return j.rr && c == cmax ? uint64_t(c) << 32 : uint64_t(c); };
   auto sum_waves = [&](uint64_t x, uint64_t& before) {   // x: lane 63's is the wave's; returns the sum, before: of earlier waves
-    __syncthreads();
+    sync();
     if (lane == 63) lds.wave[wave] = x;
-    __syncthreads();
+    sync();
     uint64_t all = 0;
     before = 0;
     for (int w = 0; w < TH / 64; ++w) {
@@ -173,14 +182,14 @@ __device__ __forceinline__ void make_ranges(const Ext& ext, int N, const TileRan
     return all;
   };
   uint64_t mine = 0, before;
-  for (int b = threadIdx.x; b < N; b += TH) mine += word((ext(b) + j.W - 1) / j.W * j.other);
+  for (int b = tid; b < N; b += TH) mine += word((ext(b) + j.W - 1) / j.W * j.other);
   for (int o = 32; o > 0; o >>= 1) mine += __shfl_xor(static_cast<unsigned long long>(mine), o, 64);
   const uint64_t sum = sum_waves(mine, before);
   const int nfull = int(sum >> 32), total = nfull + int32_t(sum);
   int32_t* map = j.start + N + 1;
   uint64_t carry = 0;   // of earlier blocks
   for (int b0 = 0; b0 < N; b0 += TH) {
-    const int b = b0 + threadIdx.x, c = b < N ? (ext(b) + j.W - 1) / j.W * j.other : 0;
+    const int b = b0 + tid, c = b < N ? (ext(b) + j.W - 1) / j.W * j.other : 0;
     uint64_t x = word(c);
     for (int o = 1; o < 64; o <<= 1) {
       const uint64_t y = __shfl_up(static_cast<unsigned long long>(x), o, 64);
@@ -191,31 +200,31 @@ __device__ __forceinline__ void make_ranges(const Ext& ext, int N, const TileRan
     carry += chunk;
     const int32_t start = j.rr && c == cmax ? int32_t(before >> 32) : nfull + int32_t(before);
     const int32_t dead = total + b * cmax - int32_t(before >> 32) - int32_t(before);
-    lds.c[threadIdx.x] = c;
-    lds.start[threadIdx.x] = start;
-    lds.dead[threadIdx.x] = dead;
+    lds.c[tid] = c;
+    lds.start[tid] = start;
+    lds.dead[tid] = dead;
     if (b < N) {
       j.start[b] = start;
       if (j.dead) j.dead[b] = dead;
     }
-    __syncthreads();
+    sync();
     const int L = cmax > 16 ? 64 : cmax > 4 ? 16 : 4, nb = min(TH, N - b0);
-    for (int k = threadIdx.x / L; k < nb; k += TH / L) {
+    for (int k = tid / L; k < nb; k += TH / L) {
       const int cc = lds.c[k], s = lds.start[k], d = lds.dead[k] - cc;
-      for (int t = threadIdx.x % L; t < (j.dead ? cmax : cc); t += L) map[t < cc ? s + t : d + t] = b0 + k;
+      for (int t = tid % L; t < (j.dead ? cmax : cc); t += L) map[t < cc ? s + t : d + t] = b0 + k;
     }
   }
-  if (threadIdx.x == 0) j.start[N] = total;
-  if (j.cut && threadIdx.x < 8) {   // the tail cut of each XCD
-    TailCut k = tail_cut_one(total, int(threadIdx.x), j.rr, j.conc, j.npairs);
+  if (tid == 0) j.start[N] = total;
+  if (j.cut && tid < 8) {   // the tail cut of each XCD
+    TailCut k = tail_cut_one(total, tid, j.rr, j.conc, j.npairs);
     const int mineb = k.tail * (k.S - 1);
     int base = mineb;
     for (int o = 1; o < 8; o <<= 1) {
       const int y = __shfl_up(base, o, 8);
-      if (int(threadIdx.x) >= o) base += y;
+      if (tid >= o) base += y;
     }
     k.base = base - mineb;
-    j.cut[threadIdx.x] = k;
+    j.cut[tid] = k;
   }
 }
 
@@ -251,45 +260,51 @@ __device__ __forceinline__ void put_slots(const MoeFwdPrep& p, int64_t s0, int64
     }
   }
 }
-__global__ void __launch_bounds__(kThreads) fwd_prep_kernel(MoeFwdPrep p, PairsJob j0, PairsJob j1, unsigned nq,
-                                                            unsigned nf, int small) {
+// SMALL: workgroup 0 does the whole set-up of the slots.
+template <bool SMALL>
+__global__ void __launch_bounds__(SMALL ? kSmallThreads : kThreads) fwd_prep_kernel(MoeFwdPrep p, PairsJob j0, PairsJob j1,
+                                                                                         unsigned nq, unsigned nf) {
+  constexpr int TH = SMALL ? kSmallThreads : kThreads;
   __shared__ uint32_t tile[32][65];
-  __shared__ int ext[kSmallBlocks];
-  __shared__ RangeLds<kThreads> lds;
   const unsigned wg = blockIdx.x;
-  if (small && wg == 0) {   // the whole set-up of the slots
-    for (int64_t k = threadIdx.x; k < p.T * p.E; k += kThreads) p.slot_of[k] = -1;
-    for (int b = threadIdx.x; b < p.N; b += kThreads) ext[b] = 0;
-    __syncthreads();
-    const int64_t Tv = valid_tokens(p);
-    const int P = int(p.N * p.B), B = int(p.B);
-    for (int s = threadIdx.x; s < P; s += 4 * kThreads)
-      put_slots(p, s, kThreads, P, Tv, [&](int64_t q) { return int64_t(p.b2e[int(q) / B]); },
-                [&](int64_t q) { atomicMax(&ext[int(q) / B], int(q) % B + 1); });
-    __syncthreads();
-    for (int b = threadIdx.x; b < p.N; b += kThreads) p.flag[b] = ext[b];
-    for (int k = 0; k < 2; ++k) make_ranges<kThreads>([&](int b) { return ext[b]; }, int(p.N), p.jobs[k], lds);
-    return;
+  if constexpr (SMALL) {
+    if (wg == 0) {
+      __shared__ int ext[kSmallBlocks];
+      __shared__ RangeLds<64> lds[2];
+      for (int64_t k = threadIdx.x; k < p.T * p.E; k += TH) p.slot_of[k] = -1;
+      for (int b = threadIdx.x; b < p.N; b += TH) ext[b] = 0;
+      __syncthreads();
+      const int64_t Tv = valid_tokens(p);
+      const int P = int(p.N * p.B), B = int(p.B);
+      for (int s = threadIdx.x; s < P; s += 4 * TH)
+        put_slots(p, s, TH, P, Tv, [&](int64_t q) { return int64_t(p.b2e[int(q) / B]); },
+                  [&](int64_t q) { atomicMax(&ext[int(q) / B], int(q) % B + 1); });
+      __syncthreads();
+      for (int b = threadIdx.x; b < p.N; b += TH) p.flag[b] = ext[b];
+      const int w = threadIdx.x >> 6;   // a wave for each product
+      if (w < 2) make_ranges<64>([&](int b) { return ext[b]; }, int(p.N), p.jobs[w], lds[w]);
+      return;
+    }
   }
-  unsigned id = wg - (small ? 1 : 0);
+  unsigned id = wg - (SMALL ? 1 : 0);
   if (id == 0 && threadIdx.x == 0) *p.done = 0;   // read by the next launch only
   if (id < nq) {
-    if (p.x_by_slot) return quant_slots(p, id);
-    quant_x(p, id, nq);
+    if (!SMALL && p.x_by_slot) return quant_slots(p, id);
+    quant_x<TH>(p, id, nq);
     return;
   }
   id -= nq;
   if (id < j0.n) {
-    scale_pairs(j0, id, tile);
+    scale_pairs<TH>(j0, id, tile);
     return;
   }
   id -= j0.n;
   if (id < j1.n) {
-    scale_pairs(j1, id, tile);
+    scale_pairs<TH>(j1, id, tile);
     return;
   }
   id -= j1.n;
-  const int64_t n = p.T * p.E, i = (int64_t(id) * kThreads + threadIdx.x) * 4;
+  const int64_t n = p.T * p.E, i = (int64_t(id) * TH + threadIdx.x) * 4;
   if (i + 4 <= n) {
     *reinterpret_cast<int4*>(p.slot_of + i) = int4{-1, -1, -1, -1};
   } else {
@@ -340,11 +355,13 @@ hipError_t launch_fwd_prep(const MoeFwdPrep& p, hipStream_t st) {
   const bool small = small_layer(p);
   const PairsJob j0 = pairs_job(p.wgu_scales, p.wgu_pairs, p.E, 2 * p.I, p.H);
   const PairsJob j1 = pairs_job(p.wd_scales, p.wd_pairs, p.E, p.H, p.I);
-  const int64_t chunks = p.T * (p.Hp / 8), want = (chunks + 4 * kThreads - 1) / (4 * kThreads);
+  const int64_t chunks = p.T * (p.Hp / 8), per = 4 * (small ? kSmallThreads : kThreads),
+                want = (chunks + per - 1) / per;
   const int64_t nq = p.x_by_slot ? p.N * p.B / 32 * ((p.Hp + 255) / 256) : want < 65536 ? want : 65536, nf = small ? 0 : (p.T * p.E + 4 * kThreads - 1) / (4 * kThreads);
   const int64_t ns = p.E * (int64_t(j0.gx) * j0.gy + int64_t(j1.gx) * j1.gy), grid = nq + ns + nf + (small ? 1 : 0);
   if (grid > kMaxGrid256) return hipErrorInvalidValue;
-  fwd_prep_kernel<<<unsigned(grid), kThreads, 0, st>>>(p, j0, j1, unsigned(nq), unsigned(nf), small ? 1 : 0);
+  if (small) fwd_prep_kernel<true><<<unsigned(grid), kSmallThreads, 0, st>>>(p, j0, j1, unsigned(nq), unsigned(nf));
+  else fwd_prep_kernel<false><<<unsigned(grid), kThreads, 0, st>>>(p, j0, j1, unsigned(nq), unsigned(nf));
   if (!small) {
     const bool ranges = p.N <= kListMax;
     fwd_slots_kernel<<<unsigned(p.N), kThreads, 0, st>>>(p, ranges ? 1 : 0);

@@ -254,6 +254,14 @@ __device__ __forceinline__ uint32_t encode_rt(int fmt, uint32_t vbits, int X) {
   return fmt == kE4M3 ? encode<kE4M3>(vbits, X) : encode<kE5M2>(vbits, X);
 }
 
+// Between a wave's writes to LDS and its own lanes' reads of them: the hardware runs them in order, the compiler too.
+__device__ __forceinline__ void wave_lds_order() {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+#endif
+}
+
 // ---- wavefront (64-lane) reductions ------------------------------------------------
 __device__ __forceinline__ uint32_t wave_max_xor(uint32_t v, int width) {
   for (int o = 1; o < width; o <<= 1) v = max(v, uint32_t(__shfl_xor(int(v), o, 64)));
