@@ -31,7 +31,7 @@ struct TokBias {
   const uint16_t* b2;      // [E][cols] bf16
   const int32_t* b2e;      // [rows / B]
   int64_t B;               // slots per block (a multiple of 128)
-  float* db2_acc;
+  double* db2_acc;
   float* part;             // null: no bias work
 };
 // x [rows][cols] along both axes in one pass, the same bytes as launch_quant_rows
@@ -245,8 +245,8 @@ hipError_t launch_finish(const float* dx_slot, const int32_t* slot_of, int64_t T
                          const int32_t* b2e, int64_t B, int64_t N, uint16_t* daff, hipStream_t st, bool accumulate);
 hipError_t launch_bias(const uint16_t* dy, const uint16_t* b2, const int32_t* slot_tok, const float* slot_aff,
                        const int32_t* b2e, const int32_t* flag, int64_t H, int64_t B, int64_t N, float* daff_slot,
-                       float* db2_acc, hipStream_t st);
-hipError_t launch_f32_to_bf16(const float* src, uint16_t* dst, int64_t n, hipStream_t st, bool accumulate = false);
+                       double* db2_acc, hipStream_t st);
+hipError_t launch_f64_to_bf16(const double* src, uint16_t* dst, int64_t n, hipStream_t st, bool accumulate = false);
 
 // moe_phase1_*.hip (product, epilogue), moe_phase3.hip
 struct Phase1Args {
@@ -284,7 +284,7 @@ struct Phase1Args {
                                 // affinity on I), slot groups
   uint8_t* inter_tok_scales;    // pair-major [P/128][I][4]
   float* daff_part;             // [I/32][P]: d(a) partial sums per 32 rows i
-  float* db1_acc;               // [E][2][I]
+  double* db1_acc;              // [E][2][I]
   int affinity_on_i;            // 1: the intermediate operand carries the affinity
   int has_bias;                 // 1: accumulate db1
   int fmt_act;                  // format of the intermediate operand (activation format)

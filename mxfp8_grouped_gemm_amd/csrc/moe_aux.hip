@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(256) bias_dot_kernel(const uint16_t* __restric
 __global__ void __launch_bounds__(256) db2_kernel(const uint16_t* __restrict__ dy, const int32_t* __restrict__ slot_tok,
                                                   const float* __restrict__ slot_aff, const int32_t* __restrict__ b2e,
                                                   const int32_t* __restrict__ flag, int64_t H, int64_t B,
-                                                  float* __restrict__ db2_acc) {
+                                                  double* __restrict__ db2_acc) {
   const int64_t b = blockIdx.y;
   const int64_t h = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 2;
   if (!flag[b] || h >= H) return;
@@ -570,13 +570,13 @@ __global__ void __launch_bounds__(256) db2_kernel(const uint16_t* __restrict__ d
       }
     }
   }
-  atomicAdd(db2_acc + e * H + h, ((lo[0] + lo[1]) + (lo[2] + lo[3])) + ((lo[4] + lo[5]) + (lo[6] + lo[7])));
-  atomicAdd(db2_acc + e * H + h + 1, ((hi[0] + hi[1]) + (hi[2] + hi[3])) + ((hi[4] + hi[5]) + (hi[6] + hi[7])));
+  atomicAdd(db2_acc + e * H + h, double(((lo[0] + lo[1]) + (lo[2] + lo[3])) + ((lo[4] + lo[5]) + (lo[6] + lo[7]))));
+  atomicAdd(db2_acc + e * H + h + 1, double(((hi[0] + hi[1]) + (hi[2] + hi[3])) + ((hi[4] + hi[5]) + (hi[6] + hi[7]))));
 }
 
 hipError_t launch_bias(const uint16_t* dy, const uint16_t* b2, const int32_t* slot_tok, const float* slot_aff,
                        const int32_t* b2e, const int32_t* flag, int64_t H, int64_t B, int64_t N, float* daff_slot,
-                       float* db2_acc, hipStream_t st) {
+                       double* db2_acc, hipStream_t st) {
   const int64_t P = N * B;
   bias_dot_kernel<<<unsigned((P + 3) / 4), 256, 0, st>>>(dy, b2, slot_tok, b2e, H, B, P, daff_slot);
   db2_kernel<<<dim3(unsigned((H + 511) / 512), unsigned(N)), 256, 0, st>>>(dy, slot_tok, slot_aff, b2e, flag, H, B,
@@ -585,12 +585,14 @@ hipError_t launch_bias(const uint16_t* dy, const uint16_t* b2, const int32_t* sl
 }
 
 // ---------------------------------------------------------------------------
-// Finalisation: fp32 accumulators -> bf16 outputs; d(a) scattered to t*E+e.
+// Finalisation: the bias sums -> bf16 outputs (fp32 terms of the blocks added by
+// atomics in fp64, so that their order, which varies, does not reach the result); d(a) scattered to t*E+e.
 // With ACC the output's old bf16 value is added before the one rounding.
 template <bool ACC>
-__global__ void f32_to_bf16_kernel(const float* __restrict__ src, uint16_t* __restrict__ dst, int64_t n) {
+__global__ void f64_to_bf16_kernel(const double* __restrict__ src, uint16_t* __restrict__ dst, int64_t n) {
   for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < n / 4; i += int64_t(gridDim.x) * blockDim.x) {
-    float4 v = reinterpret_cast<const float4*>(src)[i];
+    const double2 a = reinterpret_cast<const double2*>(src)[2 * i], b = reinterpret_cast<const double2*>(src)[2 * i + 1];
+    float4 v = make_float4(float(a.x), float(a.y), float(b.x), float(b.y));
     if (ACC) {
       const uint2 o = reinterpret_cast<const uint2*>(dst)[i];
       v.x += bf16_to_f32(uint16_t(o.x)); v.y += bf16_to_f32(uint16_t(o.x >> 16));
@@ -602,16 +604,16 @@ __global__ void f32_to_bf16_kernel(const float* __restrict__ src, uint16_t* __re
   }
   if (blockIdx.x == 0 && threadIdx.x < (n & 3)) {
     const int64_t i = (n & ~int64_t(3)) + threadIdx.x;
-    dst[i] = f32_to_bf16(src[i] + (ACC ? bf16_to_f32(dst[i]) : 0.f));
+    dst[i] = f32_to_bf16(float(src[i]) + (ACC ? bf16_to_f32(dst[i]) : 0.f));
   }
 }
 
-hipError_t launch_f32_to_bf16(const float* src, uint16_t* dst, int64_t n, hipStream_t st, bool accumulate) {
+hipError_t launch_f64_to_bf16(const double* src, uint16_t* dst, int64_t n, hipStream_t st, bool accumulate) {
   if (n <= 0) return hipSuccess;
   const int64_t want = (n / 4 + 255) / 256 + 1;
   const unsigned grid = unsigned(want < 16384 ? want : 16384);
-  if (accumulate) f32_to_bf16_kernel<true><<<grid, 256, 0, st>>>(src, dst, n);
-  else f32_to_bf16_kernel<false><<<grid, 256, 0, st>>>(src, dst, n);
+  if (accumulate) f64_to_bf16_kernel<true><<<grid, 256, 0, st>>>(src, dst, n);
+  else f64_to_bf16_kernel<false><<<grid, 256, 0, st>>>(src, dst, n);
   return hipGetLastError();
 }
 

@@ -447,8 +447,8 @@ __device__ __forceinline__ void epi_chunk(const Phase1Args& p, int b, int64_t ti
           su += __shfl_xor(su, o, 64);
         }
         if (c == 0) {
-          atomicAdd(p.db1_acc + (e * 2 + 0) * p.I + i, sg);
-          atomicAdd(p.db1_acc + (e * 2 + 1) * p.I + i, su);
+          atomicAdd(p.db1_acc + (e * 2 + 0) * p.I + i, double(sg));
+          atomicAdd(p.db1_acc + (e * 2 + 1) * p.I + i, double(su));
         }
       }
       // the intermediate operand (activation format)

@@ -365,7 +365,7 @@ __device__ __forceinline__ void quant_tok_tile(const uint16_t* __restrict__ x, i
       const float t = ((colsum[0][threadIdx.x] + colsum[1][threadIdx.x]) + colsum[2][threadIdx.x]) +
                       colsum[3][threadIdx.x];
       const int64_t e = bias.b2e[(int64_t(blockIdx.y) * kTokRows) / bias.B];
-      atomicAdd(bias.db2_acc + e * cols + int64_t(blockIdx.x) * kTokCols + threadIdx.x, t);
+      atomicAdd(bias.db2_acc + e * cols + int64_t(blockIdx.x) * kTokCols + threadIdx.x, double(t));
     }
   }
   tok_encode_pair<FMT, PAIRS>(w, rows, cols, colA, row0, codes_t, scales_t, stage_major != 0);
