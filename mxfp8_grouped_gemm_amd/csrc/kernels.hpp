@@ -5,13 +5,14 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "moe_fwd_plan.hpp"
 #include "philox.hpp"
 
 namespace mx {
 
-// Workgroups of 256 threads that one launch takes: the runtime runs a grid's
-// threads modulo 2^32, without an error.
-constexpr int64_t kMaxGrid256 = (int64_t(1) << 24) - 1;
+// Workgroups of 256 threads that one launch takes.
+constexpr int64_t kMaxGrid256 = kMaxLaunchThreads / 256;
+static_assert(kMaxGrid256 == (int64_t(1) << 24) - 1, "");
 
 // quantize.hip
 // Scale layouts: row-major [rows][K/32], or pair-major [K/128][rows][4] (pairs

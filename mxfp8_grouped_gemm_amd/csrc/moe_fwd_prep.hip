@@ -12,19 +12,15 @@
 // the rest is launches and latency (T = 256, E = 4: one launch of 5 us where four of
 // 2.5 to 4 us stood).
 #include "kernels.hpp"
+#include "moe_fwd_plan.hpp"
 #include "moe_tiles.hpp"
 #include "mx_device.hpp"
 
 namespace mx {
 
 namespace {
-constexpr int kThreads = 256;
-// A small layer (slots, T * E): one workgroup of kSmallThreads sets up its slots beside the others.  T = 1500, 23
-// blocks of 256: 10.0 us (15.6 with 256 threads), where two launches took 6.2 and 7.6.
-constexpr int64_t kSmallSlots = 8192, kSmallPairs = 32768;
-constexpr int kSmallBlocks = int(kSmallSlots / 128), kSmallThreads = 1024;
-
-bool small_layer(const MoeFwdPrep& p) { return p.N * p.B <= kSmallSlots && p.T * p.E <= kSmallPairs && !p.x_by_slot; }
+constexpr int kThreads = kPrepThreads;
+constexpr int kSmallBlocks = int(kSmallSlots / 128);
 
 // ---------------------------------------------------------------------------
 // X: a thread takes 8 columns, 4 lanes a group of 32.
@@ -352,17 +348,15 @@ __global__ void __launch_bounds__(kRangeThreads) fwd_ranges_kernel(MoeFwdPrep p)
 }  // namespace
 
 hipError_t launch_fwd_prep(const MoeFwdPrep& p, hipStream_t st) {
-  const bool small = small_layer(p);
+  const FwdPrepPlan plan = fwd_prep_plan(p.T, p.H, p.I, p.E, p.N, p.B, p.x_by_slot);
+  if (plan.grid > kMaxLaunchThreads / plan.threads) return hipErrorInvalidValue;
   const PairsJob j0 = pairs_job(p.wgu_scales, p.wgu_pairs, p.E, 2 * p.I, p.H);
   const PairsJob j1 = pairs_job(p.wd_scales, p.wd_pairs, p.E, p.H, p.I);
-  const int64_t chunks = p.T * (p.Hp / 8), per = 4 * (small ? kSmallThreads : kThreads),
-                want = (chunks + per - 1) / per;
-  const int64_t nq = p.x_by_slot ? p.N * p.B / 32 * ((p.Hp + 255) / 256) : want < 65536 ? want : 65536, nf = small ? 0 : (p.T * p.E + 4 * kThreads - 1) / (4 * kThreads);
-  const int64_t ns = p.E * (int64_t(j0.gx) * j0.gy + int64_t(j1.gx) * j1.gy), grid = nq + ns + nf + (small ? 1 : 0);
-  if (grid > kMaxGrid256) return hipErrorInvalidValue;
-  if (small) fwd_prep_kernel<true><<<unsigned(grid), kSmallThreads, 0, st>>>(p, j0, j1, unsigned(nq), unsigned(nf));
-  else fwd_prep_kernel<false><<<unsigned(grid), kThreads, 0, st>>>(p, j0, j1, unsigned(nq), unsigned(nf));
-  if (!small) {
+  const unsigned grid = unsigned(plan.grid), nq = unsigned(plan.nq), nf = unsigned(plan.nf);
+  if (plan.small) {
+    fwd_prep_kernel<true><<<grid, kSmallThreads, 0, st>>>(p, j0, j1, nq, nf);
+  } else {
+    fwd_prep_kernel<false><<<grid, kThreads, 0, st>>>(p, j0, j1, nq, nf);
     const bool ranges = p.N <= kListMax;
     fwd_slots_kernel<<<unsigned(p.N), kThreads, 0, st>>>(p, ranges ? 1 : 0);
     if (!ranges) fwd_ranges_kernel<<<2, kRangeThreads, 0, st>>>(p);
