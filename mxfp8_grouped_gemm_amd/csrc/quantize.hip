@@ -642,7 +642,7 @@ hipError_t launch_quant_rows(const uint16_t* x, int64_t rows, int64_t cols, int 
 
 hipError_t launch_tok_prep(const MoeTokensArgs& p, int ncol, hipStream_t st) {
   const int64_t nchunks = p.T * p.H / 8, nq = (nchunks + 1023) / 1024, M = p.T * p.K;
-  if (p.E > kTokExperts || M >= 1 << 14 || nq > 65535) return hipErrorInvalidValue;
+  if (p.E > kTokExperts || M >= 1 << 14 || nq >= kMaxGrid256) return hipErrorInvalidValue;
   tok_prep_kernel<<<unsigned(1 + nq), 256, 0, st>>>(reinterpret_cast<const uint4*>(p.x), reinterpret_cast<uint2*>(p.x_codes),
                                                     p.x_scales, nchunks, p.T, p.H / 32, p.idx, int(M), int(p.E), ncol,
                                                     p.units, p.list);

@@ -37,3 +37,26 @@ def test_small_layer_over_many_weight_rows():
     one = run(aff[:, -1].contiguous(), [t[-1:].contiguous() for t in (wgu, sgu, wd, sd)], 0)
     torch.cuda.synchronize()
     assert not one.isnan().any() and one.float().norm() > 0 and torch.equal(many, one)
+
+
+def test_tokens_of_the_longest_rows():
+    """The most tokens of the longest rows (X of 2^30 elements, 2^17 workgroups of its quantisation): what each 64 of them
+    give alone."""
+    T, H, I = 256, 2 ** 22, 32
+    print("tokens", T, H, I, flush=True)
+    g = torch.Generator("cuda").manual_seed(6)
+    w = [torch.randint(0x30, 0x38, s, generator=g, device="cuda", dtype=torch.uint8) for s in ((1, 2, I, H), (1, H, I))]
+    for c in w:
+        c |= torch.randint(0, 2, c.shape, generator=g, device="cuda", dtype=torch.uint8) << 7
+    sgu = torch.randint(112, 118, (1, 2, I, H // 32), generator=g, device="cuda", dtype=torch.uint8)
+    sd = torch.randint(120, 125, (1, H, I // 32), generator=g, device="cuda", dtype=torch.uint8)
+    x = torch.randn(T, H, generator=g, device="cuda", dtype=torch.bfloat16)
+    ids = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    a = torch.rand(T, 1, generator=g, device="cuda")
+
+    def run(r):
+        return mx.moe_tokens_fwd_mxfp8(x[r], ids[r], a[r], w[0], sgu, w[1], sd)
+    y = run(slice(0, T))
+    for t in range(0, T, 64):
+        part = run(slice(t, t + 64))
+        assert part.any(1).all() and not part.isnan().any() and torch.equal(y[t:t + 64], part), t
