@@ -368,7 +368,9 @@ typedef enum { MXFP8_ACT_SWIGLU = 0, MXFP8_ACT_GEGLU = 1 } mxfp8_activation;
  *   daff_slot [P] fp32 (the <dY, b2> term when it is computed on its own, else 0),
  *   daff_part [I/32 (+ H/128), P] fp32 (d(a) partials per 32 rows i; with a bias,
  *   H % 128 == 0 and no down_proj_act_checkpoint, then the <dY, b2> shares per
- *   128 columns h), db1_acc [E,2,I] fp32, db2_acc [E,H] fp32,
+ *   128 columns h), db1_acc [E,2,I] fp32, db2_acc [E,H] fp32 (the call's bias
+ *   gradients before their rounding to bf16, written by the last stage; the fp64
+ *   accumulators that they come from lie behind them in the same regions),
  *   expert_block_offsets [E+1] int32 and expert_block_list [N] int32: the blocks of
  *   expert e holding at least one routed slot are list[off[e] .. off[e+1]), ascending;
  *   slot_token [P] int32 (-1 = padding), slot_affinity [P] fp32, block_flag [N] int32

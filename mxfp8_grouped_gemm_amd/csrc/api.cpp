@@ -410,6 +410,10 @@ static bool moe_phase1_fused(const moe_bwd_mxfp8_args* a) {
          (!a->gate_up_checkpoint_codes || a->fmt_checkpoint == MXFP8_E4M3);
 }
 
+// db1_acc, db2_acc: n fp32 sums, which the last stage writes, and from this byte on the
+// fp64 accumulators that it takes them from.
+static int64_t moe_sums_at(int64_t n) { return int64_t(up256(size_t(n) * 4)); }
+
 static int moe_layout(const moe_bwd_mxfp8_args* a, moe_bwd_mxfp8_workspace_layout* L) {
   const int64_t T = a->T, H = a->H, I = a->I, E = a->E, N = a->N, B = a->block_size, P = N * B;
   size_t o = 0;
@@ -449,8 +453,8 @@ static int moe_layout(const moe_bwd_mxfp8_args* a, moe_bwd_mxfp8_workspace_layou
   put(L->slot_of, T * E * 4);
   put(L->daff_slot, P * 4);
   put(L->daff_part, (I / 32 + (moe_fuse_bias(a) ? H / 128 : 0)) * P * 4);
-  put(L->db1_acc, E * 2 * I * 8);
-  put(L->db2_acc, E * H * 8);
+  put(L->db1_acc, moe_sums_at(E * 2 * I) + E * 2 * I * 8);
+  put(L->db2_acc, moe_sums_at(E * H) + E * H * 8);
   put(L->expert_block_offsets, (E + 1) * 4);
   put(L->expert_block_list, N * 4);
   put(L->slot_token, P * 4);
@@ -577,8 +581,8 @@ static int moe_run(const moe_bwd_mxfp8_args* a, void* ws, size_t ws_bytes, void*
   float* dx_slot = reinterpret_cast<float*>(at(L.dx_slot));
   int32_t* slot_of = reinterpret_cast<int32_t*>(at(L.slot_of));
   float* daff_slot = reinterpret_cast<float*>(at(L.daff_slot));
-  double* db1_acc = reinterpret_cast<double*>(at(L.db1_acc));
-  double* db2_acc = reinterpret_cast<double*>(at(L.db2_acc));
+  double* db1_acc = reinterpret_cast<double*>(at(L.db1_acc + moe_sums_at(E * 2 * I)));
+  double* db2_acc = reinterpret_cast<double*>(at(L.db2_acc + moe_sums_at(E * H)));
   hipStream_t st = static_cast<hipStream_t>(stream);
   hipError_t e;
   // the second stream, for a whole backward (stages in order keep to the caller's)
@@ -788,8 +792,11 @@ static int moe_run(const moe_bwd_mxfp8_args* a, void* ws, size_t ws_bytes, void*
                          slot_tok, a->block_to_expert, B, N, a->expert_affinities_masked_grad, st, acc),
        "dX per-token sums and d(affinity) scatter");
   if (a->has_bias) {
-    STEP(mx::launch_f64_to_bf16(db1_acc, a->gate_and_up_proj_bias_grad, E * 2 * I, st, acc), "db1 to bf16");
-    STEP(mx::launch_f64_to_bf16(db2_acc, a->down_proj_bias_grad, E * H, st, acc), "db2 to bf16");
+    STEP(mx::launch_bias_sums(db1_acc, reinterpret_cast<float*>(at(L.db1_acc)), a->gate_and_up_proj_bias_grad, E * 2 * I,
+                              st, acc),
+         "db1 to bf16");
+    STEP(mx::launch_bias_sums(db2_acc, reinterpret_cast<float*>(at(L.db2_acc)), a->down_proj_bias_grad, E * H, st, acc),
+         "db2 to bf16");
   }
   // the caller's stream waits for Phases 2 and 4
   STEP(order(side ? &side->ev[3] : nullptr, s2, st), "join of the second stream");

@@ -247,7 +247,8 @@ hipError_t launch_finish(const float* dx_slot, const int32_t* slot_of, int64_t T
 hipError_t launch_bias(const uint16_t* dy, const uint16_t* b2, const int32_t* slot_tok, const float* slot_aff,
                        const int32_t* b2e, const int32_t* flag, int64_t H, int64_t B, int64_t N, float* daff_slot,
                        double* db2_acc, hipStream_t st);
-hipError_t launch_f64_to_bf16(const double* src, uint16_t* dst, int64_t n, hipStream_t st, bool accumulate = false);
+// n sums to fp32 (sum) and bf16 (dst, which it adds to with accumulate)
+hipError_t launch_bias_sums(const double* src, float* sum, uint16_t* dst, int64_t n, hipStream_t st, bool accumulate = false);
 
 // moe_phase1_*.hip (product, epilogue), moe_phase3.hip
 struct Phase1Args {

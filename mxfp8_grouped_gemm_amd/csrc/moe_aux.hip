@@ -585,14 +585,18 @@ hipError_t launch_bias(const uint16_t* dy, const uint16_t* b2, const int32_t* sl
 }
 
 // ---------------------------------------------------------------------------
-// Finalisation: the bias sums -> bf16 outputs (fp32 terms of the blocks added by
-// atomics in fp64, so that their order, which varies, does not reach the result); d(a) scattered to t*E+e.
+// Finalisation: the bias sums -> bf16 outputs, and fp32 in the workspace; d(a)
+// scattered to t*E+e.  The blocks' fp32 terms come added by atomics in fp64, whose
+// order varies: it moves a sum by some 2^-53 of its largest term, so an output
+// only if the sum lies that close to a border of two roundings.
 // With ACC the output's old bf16 value is added before the one rounding.
 template <bool ACC>
-__global__ void f64_to_bf16_kernel(const double* __restrict__ src, uint16_t* __restrict__ dst, int64_t n) {
+__global__ void bias_sums_kernel(const double* __restrict__ src, float* __restrict__ sum, uint16_t* __restrict__ dst,
+                                 int64_t n) {
   for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < n / 4; i += int64_t(gridDim.x) * blockDim.x) {
     const double2 a = reinterpret_cast<const double2*>(src)[2 * i], b = reinterpret_cast<const double2*>(src)[2 * i + 1];
     float4 v = make_float4(float(a.x), float(a.y), float(b.x), float(b.y));
+    reinterpret_cast<float4*>(sum)[i] = v;
     if (ACC) {
       const uint2 o = reinterpret_cast<const uint2*>(dst)[i];
       v.x += bf16_to_f32(uint16_t(o.x)); v.y += bf16_to_f32(uint16_t(o.x >> 16));
@@ -604,16 +608,17 @@ __global__ void f64_to_bf16_kernel(const double* __restrict__ src, uint16_t* __r
   }
   if (blockIdx.x == 0 && threadIdx.x < (n & 3)) {
     const int64_t i = (n & ~int64_t(3)) + threadIdx.x;
-    dst[i] = f32_to_bf16(float(src[i]) + (ACC ? bf16_to_f32(dst[i]) : 0.f));
+    sum[i] = float(src[i]);
+    dst[i] = f32_to_bf16(sum[i] + (ACC ? bf16_to_f32(dst[i]) : 0.f));
   }
 }
 
-hipError_t launch_f64_to_bf16(const double* src, uint16_t* dst, int64_t n, hipStream_t st, bool accumulate) {
+hipError_t launch_bias_sums(const double* src, float* sum, uint16_t* dst, int64_t n, hipStream_t st, bool accumulate) {
   if (n <= 0) return hipSuccess;
   const int64_t want = (n / 4 + 255) / 256 + 1;
   const unsigned grid = unsigned(want < 16384 ? want : 16384);
-  if (accumulate) f64_to_bf16_kernel<true><<<grid, 256, 0, st>>>(src, dst, n);
-  else f64_to_bf16_kernel<false><<<grid, 256, 0, st>>>(src, dst, n);
+  if (accumulate) bias_sums_kernel<true><<<grid, 256, 0, st>>>(src, sum, dst, n);
+  else bias_sums_kernel<false><<<grid, 256, 0, st>>>(src, sum, dst, n);
   return hipGetLastError();
 }
 
