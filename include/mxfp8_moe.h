@@ -706,8 +706,9 @@ int dropout_add_bwd(const dropout_add_args* args, void* stream);
  * below the largest of their eight; for g and u of few slots on the bf16 MFMA, from
  * the codes' exact values), g and u are not rounded before s, and y is rounded once.
  * In between, a slot's share of y is kept in fp32, or, with I below 4096 or no
- * multiple of 128, in fp16 times a power of two per 64 columns (off by at most 2^-12
- * of itself).  A token without a slot gets its residual, or 0.  E = 1 with every token
+ * multiple of 128, in fp16 times a power of two per 64 columns: a value is off by at
+ * most 2^-11 of itself, or, below 2^-28 of the largest of its 64, by at most 2^-39 of
+ * that one.  A token without a slot gets its residual, or 0.  E = 1 with every token
  * in a slot is a dense gated FFN.
  * Arguments (moe_fwd_mxfp8_args; [T], [N], ... and the block lists as for
  * moe_bwd_mxfp8):

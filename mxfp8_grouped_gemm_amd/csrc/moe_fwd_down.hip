@@ -7,9 +7,10 @@
 // short contraction the rows' trip through memory is most of the time (T = 32768,
 // I = 256, top-8: 1.6 GB written and read as fp32, against 0.2 TFLOP), so they are
 // stored as fp16 times a power of two per row and 64 columns: the largest value
-// lies in [2^14, 2^15), a value down to 2^-29 of it keeps 11 significant bits, so a
-// term of the sum is off by at most 2^-12 of itself, an eighth of half a step of
-// the bf16 result.  The scale is a row's own: no token's values touch another's.
+// lies in [2^14, 2^15), a value down to 2^-28 of it is a normal fp16 number of 11
+// significant bits, so a term of the sum is off by at most 2^-11 of itself, an eighth
+// of the 2^-8 of the bf16 result's rounding; a smaller one by at most 2^-25, that is
+// 2^-39 of the largest.  The scale is a row's own: no token's values touch another's.
 // With the slots as tile columns a lane holds 32 of a slot's 64 values, the lane 32
 // away the rest, and 4 of them in a row: one exchange a maximum, 8-byte stores.
 // 32768 slots, H = 2048, I = 1408: 135 us, 1.4 PFLOP/s.  I <= 256 has a kernel of its own
