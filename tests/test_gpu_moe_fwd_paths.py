@@ -1,0 +1,163 @@
+"""moe_fwd_mxfp8 on the GPU, path by path: every form of the scaled gate/up kernels, round-robin tiles with a checkpoint, and
+the products that have to be exact.  Against the layer in 64 bits (oracle/ffn.py, whose bounds the tolerances are)."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from ffn_common import HALF, Problem, bf16_values, check_rows
+from oracle import ffn
+from test_gpu_moe_fwd import _gate_up, _run
+
+pytestmark = pytest.mark.gpu
+
+
+def _few_tiles(p):
+    """The gate/up product takes exact products at 128 x 128 tiles."""
+    return p.N * (p.B // 128) * 2 * -(-p.I // 128) <= 512
+
+
+def _side(p):
+    """A gate/up tile's side."""
+    return 128 if p.I < 128 or p.B < 256 or p.H < 1024 or _few_tiles(p) else 256
+
+
+def _padded(args, N, seed):
+    """A problem whose block list is N long: those behind its own hold no token."""
+    p = Problem(**args, seed=seed)
+    assert p.N <= N
+    p.tpid = np.concatenate([p.tpid, np.full((N - p.N) * p.B, -1, np.int32)])
+    p.b2e = np.concatenate([p.b2e, np.full(N - p.N, p.E - 1, np.int32)])
+    p.N = N
+    return p
+
+
+def _check(p, what):
+    """y and every checkpoint: bf16 against the formula, both 8-bit formats as the bf16 one's codes."""
+    y, dy, gus = p.exact()
+    r = _run(p, "bf16")
+    check_rows(r["out"], y, dy, what)
+    ck, d = _gate_up(p, gus)
+    gu = bf16_values(r["checkpoint"])
+    assert (np.abs(gu - ck) <= d + (np.abs(ck) + d) * HALF).all()
+    assert not gu[(p.tpid < 0).reshape(p.N, 1, 1, p.B).repeat(2, 1).repeat(p.I, 2)].any()
+    assert torch.equal(_run(p)["out"], r["out"])
+    bits = r["checkpoint"].cpu().view(torch.int16).numpy().view(np.uint16)
+    for fmt in (oracle.E4M3, oracle.E5M2):
+        r8 = _run(p, "mxfp8", fmt_checkpoint=fmt)
+        codes, scales = oracle.quantize(bits.reshape(-1, p.B), 1, fmt)
+        assert np.array_equal(r8["checkpoint"][0].cpu().numpy().reshape(codes.shape), codes), fmt
+        assert np.array_equal(r8["checkpoint"][1].cpu().numpy().reshape(scales.shape), scales), fmt
+        assert torch.equal(r8["out"], r["out"]), fmt
+
+
+@pytest.mark.parametrize("geglu", [False, True])
+@pytest.mark.parametrize("ragged", [False, True])
+@pytest.mark.parametrize("side", [128, 256])
+def test_scaled_kernels(side, ragged, geglu):
+    """The scaled MFMA at both tile sides, contractions of whole pairs and not, both activations, every checkpoint."""
+    if side == 256:
+        p = _padded(dict(T=300, H=1056 if ragged else 1024, I=416 if ragged else 384, E=3, K=2, B=512 if ragged else 256,
+                         dropped=0.1, geglu=geglu, bias=not ragged), 60, 51)
+    else:
+        p = _padded(dict(T=200, H=608 if ragged else 384, I=224 if ragged else 256, E=4, K=2, B=128, dropped=0.1, geglu=geglu,
+                         residual=True), 160, 52)
+    assert not _few_tiles(p) and _side(p) == side
+    _check(p, (side, ragged, geglu))
+
+
+def test_blocks_that_are_full_partly_filled_and_empty():
+    """256 x 256 tiles in blocks of four: all live, some, none, in this order and mixed."""
+    idx = np.concatenate([np.full(90, 0), np.full(700, 1), np.full(1030, 2), np.full(40, -1)]).astype(np.int32)[:, None]
+    p = _padded(dict(T=len(idx), H=1024, I=256, E=4, K=1, B=1024, idx=idx), 20, 53)
+    assert _side(p) == 256
+    _check(p, "blocks")
+
+
+# Weights of 32 Mi codes and more: tiles go round robin, the blocks whose slot tiles are all live first.  Expert 0 has a
+# partly filled block, expert 1 a full one and one with a live and a dead tile.
+ROUND_ROBIN = {
+    # X in the slots' order, fp32 rows
+    "by_slot": dict(H=4096, I=4096),
+    # X by token, fp16 rows, the down projection round robin as well
+    "by_token": dict(H=16384, I=2048),
+    # weight rows that are no whole pair
+    "ragged": dict(H=4128, I=4128, on_i=True),
+}
+
+
+@pytest.mark.parametrize("name", ROUND_ROBIN)
+def test_round_robin_tiles_with_a_checkpoint(name):
+    """What every training forward of a large layer runs."""
+    print("round robin", name, flush=True)
+    idx = np.concatenate([np.full(60, 0), np.full(512 + 90, 1), np.full(5, -1)]).astype(np.int32)[:, None]
+    idx = idx[np.random.default_rng(1).permutation(len(idx))]
+    p = _padded(dict(T=len(idx), E=2, K=1, B=512, idx=idx, **ROUND_ROBIN[name]), 9, 54)
+    assert 2 * p.I * p.H >= 2 ** 25 and _side(p) == 256 and p.N * (p.B // 256) * -(-p.I // 128) > 256
+    _check(p, name)
+
+
+# ----------------------------------------------------------------------------- exact products
+class _Cancelling(Problem):
+    """Rows whose sums lie 2^13 below their largest products, which cancel: of 8 consecutive products two are +-2^17.6 and
+    the others +-1, which an instruction that truncates each product to 2^-13 of the largest drops.  g = 24 and u = 2 in
+    every element, SiLU(24) = 24 to 1e-9, so s = 48, an E4M3 value, and y = 48 a sum_i Wd, whatever the order of the sums."""
+
+    def __init__(self, T, H, I, E, K, B=128, seed=0, idx=None):
+        super().__init__(T, H, I, E, K, B=B, seed=seed, idx=idx)
+        r = np.random.default_rng(seed + 1)
+        x = np.ones((T, H), np.float32)
+        x[:, 0::8] = x[:, 1::8] = 448
+        self.x = torch.from_numpy(x).to(torch.bfloat16)
+        small = [k for k in range(H) if k % 8 > 1]
+        assert len(small) >= 96
+        w = np.zeros((E, 2, I, H))
+        w[..., 0::8], w[..., 1::8] = 448, -448
+        for part, total in ((0, 96), (1, 8)):
+            signs = np.zeros(len(small))
+            signs[:96] = 1
+            signs[:(96 - total) // 2] = -1
+            w[:, part][..., small] = r.permuted(np.broadcast_to(signs, (E, I, len(small))), axis=-1)
+        codes = torch.from_numpy(w.astype(np.float32)).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+        self.q[0], self.q[1] = codes, np.full((E, 2, I, H // 32), 127 - 2, np.uint8)      # scale 2^-2
+        wd = ffn.mx_values(self.q[2], self.q[3])
+        self.y = np.zeros((T, H))
+        for e, (t, a) in self.pairs.items():
+            np.add.at(self.y, t, 48 * np.asarray(a, np.float64)[:, None] * wd[e].sum(-1))
+        # the scaled MFMA of the down projection on equal s, the fp16 rows (blocks) and fp32 sums, per term
+        sq = np.full((1, I), 48.0)
+        self.dy = np.zeros((T, H))
+        for e, (t, a) in self.pairs.items():
+            term = np.abs(sq) @ np.abs(wd[e]).T * (8 * np.ceil(I / 64) + 8) * 2.0 ** -24 + ffn.product_rests(sq, wd[e])
+            row = np.abs(48 * wd[e].sum(-1))[None]
+            term = term + (row + term) * 2.0 ** -11 + row.max() * 2.0 ** -39
+            np.add.at(self.dy, t, np.abs(np.asarray(a, np.float64))[:, None] * term)
+        self.dy += np.abs(self.y) * 2.0 ** -22
+
+
+def test_the_cancelling_rows_are_lost_to_truncation():
+    """The formula the cases rest on: what truncation cuts off is all of g and u."""
+    p = _Cancelling(T=1, H=128, I=32, E=1, K=1)
+    v = ffn.mx_values(p.q[0], p.q[1])[0].reshape(64, 128)
+    x = bf16_values(p.x)
+    assert np.array_equal(x @ v.T, np.repeat([24.0, 2.0], 32)[None])
+    assert np.array_equal(ffn.mx_requant(x)[0], x)
+    assert (ffn.product_rests(x, v) == 96 / 4).all()
+
+
+@pytest.mark.parametrize("H,I", [(128, 32), (128, 256), (160, 96), (1024, 512)])
+def test_few_tiles_have_exact_products(H, I):
+    p = _Cancelling(T=150, H=H, I=I, E=3, K=2)
+    assert _few_tiles(p)
+    check_rows(_run(p)["out"], p.y, p.dy, (H, I))
+
+
+# T: the forms of 1 to 4, 8, 32 and 64 columns; tiles shared by a workgroup's waves, or whole ones a wave (1024 and more)
+@pytest.mark.parametrize("T,H,I,E,K", [(1, 128, 32, 1, 1), (2, 160, 96, 3, 2), (4, 128, 1088, 40, 32), (8, 128, 256, 4, 2),
+                                       (9, 160, 128, 30, 3), (40, 128, 1120, 32, 2), (100, 1024, 96, 2, 2),
+                                       (256, 128, 128, 2, 1)])
+def test_few_tokens_have_exact_products(T, H, I, E, K):
+    import mxfp8_grouped_gemm_amd as mx
+    p = _Cancelling(T=T, H=H, I=I, E=E, K=K)
+    pos, kw = p.tokens_on()
+    check_rows(mx.moe_tokens_fwd_mxfp8(*pos, **kw), p.y, p.dy, (T, H, I))
