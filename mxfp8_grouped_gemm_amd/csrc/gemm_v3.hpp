@@ -304,10 +304,10 @@ struct Tile {
 // next tile's descriptors spill, and the reloads' waits drain the ring at
 // every tile boundary).
 //
-// RAG (1: A, 2: B): that operand is row-major with rows of kend bytes, a multiple
-// of 32 that need not be one of 128, and nstages covers kend rounded up to 128:
-// 16-byte chunks from kend on read as zeros (they would be the next row's).
-template <int BM, int BN, int ELEM, int FA, int FB, class KMap, int RAG = 0>
+// RAG: A is row-major with rows of kend bytes, a multiple of 32 that need not be
+// one of 128, and nstages covers kend rounded up to 128: A's 16-byte chunks from
+// kend on read as zeros (they would be the next row's).
+template <int BM, int BN, int ELEM, int FA, int FB, class KMap, bool RAG = false>
 struct Ring {
   static constexpr int FM = BM / 64, FN = BN / 64;
   static constexpr int CS = code_slot(BM, BN), SSB = scale_slot(BM, BN);
@@ -353,9 +353,8 @@ struct Ring {
   uint32_t kend = 0;   // RAG: bytes of K
   // off, or past the descriptor where this lane's chunk of stage kc / 64 lies past kend (the logical chunk of
   // dma_row's rows is the same for every instruction: see swz)
-  template <bool R>
   __device__ __forceinline__ uint32_t in_row(uint32_t off, uint32_t kc) const {
-    if constexpr (!R) return off;
+    if constexpr (!RAG) return off;
     return kc + 16u * ((threadIdx.x & 3) ^ ((threadIdx.x >> 4) & 3)) < kend ? off : kOOB;
   }
 
@@ -370,12 +369,11 @@ struct Ring {
     if (J < FM) {
       v4i ra = dA;
       ra[2] = live ? ra[2] : 0;
-      dma16(ra, cs + uint32_t(wave * (BM / 4) + 16 * J) * SK, in_row<(RAG & 1) != 0>(x.A.off[J], kc), kc * x.A.kmul);
+      dma16(ra, cs + uint32_t(wave * (BM / 4) + 16 * J) * SK, in_row(x.A.off[J], kc), kc * x.A.kmul);
     } else {
       v4i rb = dB;
       rb[2] = live ? rb[2] : 0;
-      dma16(rb, cs + uint32_t(BM + wave * (BN / 4) + 16 * (J - FM)) * SK, in_row<(RAG & 2) != 0>(x.B.off[J - FM], kc),
-            kc * x.B.kmul);
+      dma16(rb, cs + uint32_t(BM + wave * (BN / 4) + 16 * (J - FM)) * SK, x.B.off[J - FM], kc * x.B.kmul);
     }
     // a pair's scale words go with its first (even) stage only: the odd stage
     // takes them from the registers its even stage read them into (read_item)
@@ -545,13 +543,13 @@ struct Ring {
 };
 
 // One tile per workgroup.
-template <int BM, int BN, int ELEM, int FA, int FB, class KMap, int RAG = 0>
+template <int BM, int BN, int ELEM, int FA, int FB, class KMap, bool RAG = false>
 __device__ __forceinline__ void mainloop(const Op<BM>& A, const Op<BN>& B, const ScaleDma<BM, BN>* sd, int nstages,
                                          const KMap& kmap, uint8_t* smem, v16f (&acc)[BM / 64][BN / 64],
                                          uint32_t kend = 0) {
   const Tile<BM, BN, KMap> tile{A, B, *sd, kmap, nstages};
   Ring<BM, BN, ELEM, FA, FB, KMap, RAG> ring{smem, tile};
-  if constexpr (RAG != 0) ring.kend = kend;
+  if constexpr (RAG) ring.kend = kend;
   ring.run(acc);
   // the look-ahead loads past the end still write (zeros) into the ring: let
   // them land before the caller reuses the LDS

@@ -393,7 +393,7 @@ bool fwd_x_by_slot(int64_t H, int64_t I, int64_t N, int64_t B);   // X quantised
 TileRangeJob fwd_gate_up_ranges(const MoeFwdArgs& p);
 hipError_t launch_fwd_gate_up(const MoeFwdArgs& p, hipStream_t st);
 
-// The down projection of short contractions, its rows in scaled fp16 (moe_fwd_down.hpp)
+// The down projection of short contractions, its rows in scaled fp16 (moe_fwd_down.hip)
 struct MoeFwdDownArgs {
   int64_t H, I, Ip, N, B;
   const uint8_t* inter_codes;

@@ -55,8 +55,8 @@ __global__ void __launch_bounds__(v2::kThreads) fwd_down_kernel(MoeFwdDownArgs p
     v3::setup_rows_sm(B, p.inter_codes, sbase + n0, sbase + p.B, P, p.Ip);
     v3::setup_scales(sd, p.w_scales + e * p.H * (p.Ip / 32), m0, p.H, p.H * (p.Ip / 32), p.inter_scales, sbase + n0, P,
                      P * (p.Ip / 32));
-    v3::mainloop<BM, BN, v3::kFp8, kE4M3, kE4M3, v3::KMapPlain, RAG ? 1 : 0>(A, B, &sd, int(p.Ip / v3::SK),
-                                                                            v3::KMapPlain{}, smem, acc, uint32_t(p.I));
+    v3::mainloop<BM, BN, v3::kFp8, kE4M3, kE4M3, v3::KMapPlain, RAG>(A, B, &sd, int(p.Ip / v3::SK), v3::KMapPlain{},
+                                                                   smem, acc, uint32_t(p.I));
   }
   __syncthreads();   // the ring is done
   const int lane = threadIdx.x & 63, h = lane >> 5, r = lane & 31, wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;

@@ -180,8 +180,8 @@ __global__ void __launch_bounds__(v2::kThreads) fwd_gate_up_kernel(MoeFwdArgs p)
     v3::setup_gather(A, wc, 2 * p.I, p.H, row_of);
     if (p.x_by_slot) v3::setup_rows_sm(B, p.x_codes, sbase + n0, sbase + p.B, P, p.Hp);
     else v3::setup_gather(B, p.x_codes, p.T, p.Hp, tok_of);
-    v3::mainloop<BM, BN, ELEM, kE4M3, kE4M3, v3::KMapPlain, RAG ? 1 : 0>(A, B, &sd, int(p.Hp / v3::SK),
-                                                                            v3::KMapPlain{}, smem, acc, uint32_t(p.H));
+    v3::mainloop<BM, BN, ELEM, kE4M3, kE4M3, v3::KMapPlain, RAG>(A, B, &sd, int(p.Hp / v3::SK), v3::KMapPlain{}, smem,
+                                                                   acc, uint32_t(p.H));
   }
   if constexpr (CK != 0) __syncthreads();   // every wave is done with the ring: its bytes stage the checkpoint
   uint32_t* stage = reinterpret_cast<uint32_t*>(smem + wave * kCkWaveBytes);

@@ -259,7 +259,7 @@ __device__ __forceinline__ void put_slots(const MoeFwdPrep& p, int64_t s0, int64
 // SMALL: workgroup 0 does the whole set-up of the slots.
 template <bool SMALL>
 __global__ void __launch_bounds__(SMALL ? kSmallThreads : kThreads) fwd_prep_kernel(MoeFwdPrep p, PairsJob j0, PairsJob j1,
-                                                                                         unsigned nq, unsigned nf) {
+                                                                                         unsigned nq) {
   constexpr int TH = SMALL ? kSmallThreads : kThreads;
   __shared__ uint32_t tile[32][65];
   const unsigned wg = blockIdx.x;
@@ -352,11 +352,11 @@ hipError_t launch_fwd_prep(const MoeFwdPrep& p, hipStream_t st) {
   if (plan.grid > kMaxLaunchThreads / plan.threads) return hipErrorInvalidValue;
   const PairsJob j0 = pairs_job(p.wgu_scales, p.wgu_pairs, p.E, 2 * p.I, p.H);
   const PairsJob j1 = pairs_job(p.wd_scales, p.wd_pairs, p.E, p.H, p.I);
-  const unsigned grid = unsigned(plan.grid), nq = unsigned(plan.nq), nf = unsigned(plan.nf);
+  const unsigned grid = unsigned(plan.grid), nq = unsigned(plan.nq);
   if (plan.small) {
-    fwd_prep_kernel<true><<<grid, kSmallThreads, 0, st>>>(p, j0, j1, nq, nf);
+    fwd_prep_kernel<true><<<grid, kSmallThreads, 0, st>>>(p, j0, j1, nq);
   } else {
-    fwd_prep_kernel<false><<<grid, kThreads, 0, st>>>(p, j0, j1, nq, nf);
+    fwd_prep_kernel<false><<<grid, kThreads, 0, st>>>(p, j0, j1, nq);
     const bool ranges = p.N <= kListMax;
     fwd_slots_kernel<<<unsigned(p.N), kThreads, 0, st>>>(p, ranges ? 1 : 0);
     if (!ranges) fwd_ranges_kernel<<<2, kRangeThreads, 0, st>>>(p);

@@ -1,9 +1,10 @@
 // moe_tokens.hip -- the MoE forward for few tokens (decoding): the layer of
 // moe_fwd.hip straight from the router's selections, without block lists.
 //
-// Bound by the bytes of the selected experts' weights, each read once: an
-// expert has a handful of rows, so a product is a stream of weights past a few
-// columns.  Selections ("pairs" t * K + k) keep their index as row of every
+// Bound by the bytes of the selected experts' weights: an expert has a handful
+// of rows, so a product is a stream of weights past a few columns.  They are read
+// once where an expert has no more pairs than a workgroup has columns (`columns`,
+// twice the average load up to 64), and once more for every further so many.  Selections ("pairs" t * K + k) keep their index as row of every
 // intermediate.  A tile is 64 weight rows of one expert (32 gate rows and the
 // same 32 up rows; or 64 rows of the down projection) times up to NCOL of the
 // expert's pairs.  Each wave streams whole 128-byte lines of weight rows
