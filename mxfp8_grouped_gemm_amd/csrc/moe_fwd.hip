@@ -22,10 +22,13 @@ int fwd_side(int64_t H, int64_t I, int64_t N, int64_t B) {
 }  // namespace
 
 // Every slot's X row by itself and stage-major costs the preparation 0.25 ns a KB of it and spares each 256-row
-// tile's reads half lines: H = 4096, I = 14336, 40k slots: preparation 62 -> 98 us, products 3.65 -> 3.44 ms;
-// H = 2048, I = 1408: 20 -> 43 us for 290 -> 287.
+// tile's reads half lines: H = 4096, I = 14336, 40k slots: preparation 62 -> 98 us, products 3.65 -> 3.44 ms.
+// The whole forward, by token -> by slot, top-2 (each row twice) and, in brackets, top-4, 32768 routed slots:
+// H = 4096: I = 4096 1.72 -> 1.73 ms (1.70 -> 1.75), 6144 2.47 -> 2.41 (2.42 -> 2.43), 8192 3.21 -> 3.11 (3.12 -> 3.07),
+// 14336 5.15 -> 4.96; H = 2048: I = 4096 (0.92 -> 0.94), 8192 1.85 -> 1.82 (1.73 -> 1.76), 11264 (2.31 -> 2.26).
+// 4096 routed slots: within 2% either way up to I = 14336.
 bool fwd_x_by_slot(int64_t H, int64_t I, int64_t N, int64_t B) {
-  return I >= 4096 && fwd_side(H, I, N, B) == 256 &&
+  return I >= 8192 && fwd_side(H, I, N, B) == 256 &&
          (H + 127) / 128 * 4 <= (int64_t(1) << 30) / (N * B);   // one launch, 32-bit offsets
 }
 

@@ -78,11 +78,15 @@ def test_blocks_that_are_full_partly_filled_and_empty():
 # partly filled block, expert 1 a full one and one with a live and a dead tile.
 ROUND_ROBIN = {
     # X in the slots' order, fp32 rows
-    "by_slot": dict(H=4096, I=4096),
+    "by_slot": dict(H=2048, I=8192),
+    # the same, weight rows that are no whole pair, fp16 rows
+    "by_slot_ragged": dict(H=2080, I=8224, on_i=True),
+    # X by token, fp32 rows
+    "by_token": dict(H=4096, I=4096),
     # X by token, fp16 rows, the down projection round robin as well
-    "by_token": dict(H=16384, I=2048),
+    "by_token_wide": dict(H=16384, I=2048),
     # weight rows that are no whole pair
-    "ragged": dict(H=4128, I=4128, on_i=True),
+    "by_token_ragged": dict(H=4128, I=4128),
 }
 
 
@@ -93,7 +97,7 @@ def test_round_robin_tiles_with_a_checkpoint(name):
     idx = np.concatenate([np.full(60, 0), np.full(512 + 90, 1), np.full(5, -1)]).astype(np.int32)[:, None]
     idx = idx[np.random.default_rng(1).permutation(len(idx))]
     p = _padded(dict(T=len(idx), E=2, K=1, B=512, idx=idx, **ROUND_ROBIN[name]), 9, 54)
-    assert 2 * p.I * p.H >= 2 ** 25 and _side(p) == 256 and p.N * (p.B // 256) * -(-p.I // 128) > 256
+    assert 2 * p.I * p.H >= 2 ** 25 and _side(p) == 256 and (p.I >= 8192) == name.startswith("by_slot") and p.N * (p.B // 256) * -(-p.I // 128) > 256
     _check(p, name)
 
 
