@@ -13,8 +13,7 @@
 // 2^-39 of the largest.  The scale is a row's own: no token's values touch another's.
 // With the slots as tile columns a lane holds 32 of a slot's 64 values, the lane 32
 // away the rest, and 4 of them in a row: one exchange a maximum, 8-byte stores.
-// 32768 slots, H = 2048, I = 1408: 135 us, 1.4 PFLOP/s.  I <= 256 has a kernel of its own
-// (moe_fwd_down_short.hip).  Long contractions (I >= 4096) keep fp32 rows and Phase 3's kernel
+// I <= 256 has a kernel of its own (moe_fwd_down_short.hip).  Long contractions (I >= 4096) keep fp32 rows and Phase 3's kernel
 // (moe_phase3.hip), whose last round of tiles is cut along K.
 #include "gemm_v3.hpp"
 #include "kernels.hpp"
@@ -116,9 +115,13 @@ __global__ void __launch_bounds__(v2::kThreads) fwd_down_kernel(MoeFwdDownArgs p
 struct Shape {
   int m, n;
 };
-// 256 x 256 from blocks and contractions that are long enough for one workgroup a CU, else 128 x 128, two a CU
+// 256 x 256 where a block's tiles are many and long enough for one workgroup a CU, else 128 x 128, two a CU.  The whole
+// forward at 128 -> 256, 32768 routed slots of 8 experts (in brackets 8192 of 4): H = 1024: I = 1024 195 -> 204 us,
+// 2048 326 -> 332, 2816 411 -> 416, 3968 561 -> 545; H = 2048: I = 1024 300 -> 313 (119 -> 129), 1408 369 -> 375 (127 -> 138),
+// 2112 525 -> 517 (181 -> 190), 2816 677 -> 647; H = 4096: I = 1024 527 -> 541 (194 -> 202), 1408 656 -> 649 (213 -> 218),
+// 2048 921 -> 905 (291 -> 287); H = 8192: I = 704 830 -> 845, 1024 1013 -> 1020 (338 -> 352).
 Shape down_shape(const MoeFwdDownArgs& p) {
-  if (p.I >= 1024 && p.B >= 256 && p.H >= 256) return {256, 256};
+  if (p.I >= 1024 && p.H * p.I > int64_t(1) << 22 && p.B >= 256 && p.H >= 256) return {256, 256};
   return {128, 128};
 }
 
@@ -133,6 +136,10 @@ hipError_t go(MoeFwdDownArgs p, hipStream_t st) {
 }
 }  // namespace
 
+// fp16 rows up to where their bytes no longer matter enough to give up bits for them.  The whole forward with fp32
+// rows -> fp16, 32768 routed slots: H = 4096: I = 1024 621 -> 545 us, 2048 986 -> 910, 4096 1762 -> 1651, 8192 3044 -> 3019;
+// H = 2048: 350 -> 316, 532 -> 500, 942 -> 908, 1770 -> 1761; 262144 slots of H = 1536, I = 256 1099 -> 775; T = 256,
+// H = 128, I = 256 21.5 -> 19.3.  (A ragged contraction takes them at any length: Phase 3's kernel reads whole pairs.)
 bool fwd_down_fits(int64_t I) { return I < 4096 || I % 128 != 0; }
 
 TileRangeJob fwd_down_ranges(const MoeFwdDownArgs& p) {

@@ -101,6 +101,16 @@ def test_round_robin_tiles_with_a_checkpoint(name):
     _check(p, name)
 
 
+# The down projection's tiles with fp16 rows: 128 x 128 and 256 x 256 (H * I past 2^22), contractions of whole pairs and not
+@pytest.mark.parametrize("H,I,side", [(288, 1024, 128), (288, 1056, 128), (1056, 3968, 128), (2080, 2176, 256), (2080, 2112, 256),
+                                      (256, 16416, 256)])
+def test_down_projection_tiles(H, I, side):
+    p = Problem(T=400, H=H, I=I, E=2, K=1, B=256, dropped=0.1, residual=True, seed=55)
+    assert (256 if I >= 1024 and H * I > 2 ** 22 and H >= 256 else 128) == side and (I < 4096 or I % 128)
+    y, dy, _ = p.exact()
+    check_rows(_run(p)["out"], y, dy, (H, I))
+
+
 # ----------------------------------------------------------------------------- exact products
 class _Cancelling(Problem):
     """Rows whose sums lie 2^13 below their largest products, which cancel: of 8 consecutive products two are +-2^17.6 and
