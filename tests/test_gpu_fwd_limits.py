@@ -60,3 +60,83 @@ def test_tokens_of_the_longest_rows():
     for t in range(0, T, 64):
         part = run(slice(t, t + 64))
         assert part.any(1).all() and not part.isnan().any() and torch.equal(y[t:t + 64], part), t
+
+
+def _weights(E, H, I, seed):
+    """E experts with the codes of one."""
+    g = torch.Generator("cuda").manual_seed(seed)
+
+    def codes(*s):
+        c = torch.randint(0x28, 0x38, s, generator=g, device="cuda", dtype=torch.uint8)
+        return c | torch.randint(0, 2, s, generator=g, device="cuda", dtype=torch.uint8) << 7
+
+    def scales(*s):
+        return torch.randint(118, 122, s, generator=g, device="cuda", dtype=torch.uint8)
+    one = codes(2, I, H), scales(2, I, H // 32), codes(H, I), scales(H, I // 32)
+    return [t.unsqueeze(0).expand(E, *t.shape).contiguous() for t in one]
+
+
+def test_most_tokens():
+    """T just below 2^24 and T * 128 below 2^31: a range of the tokens by itself gives the same bits."""
+    T, H, I, B = 16_700_000, 32, 32, 128
+    print("tokens", T, H, I, flush=True)
+    g = torch.Generator("cuda").manual_seed(7)
+    x = torch.randn(T, H, generator=g, device="cuda", dtype=torch.bfloat16)
+    aff = torch.rand(T, generator=g, device="cuda")
+    w = _weights(1, H, I, 8)
+
+    def run(a, b):
+        n = b - a
+        N = -(-n // B)
+        tpid = torch.full((N * B,), -1, dtype=torch.int32, device="cuda")
+        tpid[:n] = torch.arange(n, dtype=torch.int32, device="cuda")
+        op = mx.MoeFwd(x[a:b].contiguous(), aff[a:b].contiguous(), *w, tpid,
+                       torch.zeros(N, dtype=torch.int32, device="cuda"), B, checkpoint="mxfp8")
+        for t in (op.out["out"], *op.out["checkpoint"]):
+            t.fill_(77)
+        return op.run()
+    whole = run(0, T)
+    n = 1 << 18
+    for a in (0, T // 2 // B * B, (T - n) // B * B):   # the last one to the end, with a block partly filled
+        b = min(a + n + B, T)
+        part = run(a, b)
+        torch.cuda.synchronize()
+        assert part["out"].any() and torch.equal(part["out"], whole["out"][a:b]), a
+        for p, q in zip(part["checkpoint"], whole["checkpoint"]):
+            assert torch.equal(p, q[a // B:-(-b // B)]), a
+
+
+# name: sizes of a layer in which every token goes to all of 8 experts, and which operand passes 2^32 bytes
+FAR = {
+    "s_short_contraction": (64, 2176, 2 ** 18),      # fp16 rows
+    "s_long_contraction": (64, 4224, 2 ** 17),       # fp32 rows, Phase 3's kernel
+    "x_by_slot": (4224, 8224, 2 ** 17),              # X in the slots' order, s and the fp16 rows as well
+}
+
+
+@pytest.mark.parametrize("name", FAR)
+def test_operands_past_32_bits(name):
+    """The same 1024 tokens over and over: what they give once."""
+    H, I, T = FAR[name]
+    E, B, n = 8, 1024, 1024
+    print(name, T, H, I, flush=True)
+    assert T * E * (H if name == "x_by_slot" else I) > 1 << 32
+    g = torch.Generator("cuda").manual_seed(9)
+    x = torch.randn(n, H, generator=g, device="cuda", dtype=torch.bfloat16)
+    aff = torch.rand(n, E, generator=g, device="cuda")
+    w = _weights(E, H, I, 10)
+
+    def run(times):
+        t = n * times
+        tpid = torch.arange(t, dtype=torch.int32, device="cuda").repeat(E)
+        b2e = torch.arange(E, dtype=torch.int32, device="cuda").repeat_interleave(t // B)
+        y = mx.moe_fwd_mxfp8(x.repeat(times, 1), aff.repeat(times, 1).view(-1), *w, tpid, b2e, B)["out"]
+        torch.cuda.synchronize()
+        return y.view(times, n, H)
+    one, many = run(1), run(T // n)
+    assert one.float().norm() > 0 and not one.isnan().any()
+    if name == "s_long_contraction":     # how the last tiles are cut along I goes by their number
+        d = (many.float() - one.float()).norm(dim=(1, 2)) / one.float().norm()
+        assert float(d.max()) <= 2.0 ** -8
+    else:
+        assert (many == one).all()
