@@ -115,13 +115,18 @@ __global__ void __launch_bounds__(v2::kThreads) fwd_down_kernel(MoeFwdDownArgs p
 struct Shape {
   int m, n;
 };
-// 256 x 256 where a block's tiles are many and long enough for one workgroup a CU, else 128 x 128, two a CU.  The whole
-// forward at 128 -> 256, 32768 routed slots of 8 experts (in brackets 8192 of 4): H = 1024: I = 1024 195 -> 204 us,
-// 2048 326 -> 332, 2816 411 -> 416, 3968 561 -> 545; H = 2048: I = 1024 300 -> 313 (119 -> 129), 1408 369 -> 375 (127 -> 138),
-// 2112 525 -> 517 (181 -> 190), 2816 677 -> 647; H = 4096: I = 1024 527 -> 541 (194 -> 202), 1408 656 -> 649 (213 -> 218),
-// 2048 921 -> 905 (291 -> 287); H = 8192: I = 704 830 -> 845, 1024 1013 -> 1020 (338 -> 352).
+// 256 x 256 with one workgroup a CU where the work is several rounds of such tiles, else 128 x 128, two a CU.  The whole
+// forward at 128 -> 256 in us, by routed slots (of 4 to 16 experts; *: 64) and H; left of | the rule takes 128:
+//   8192, 2048   I = 1024 119 -> 129, 1408 127 -> 138, 2112 181 -> 190, 2816 199 -> 209 |
+//   32768, 1024  1024 195 -> 204, 2048 326 -> 332, 2816 411 -> 416 | 3968 561 -> 545
+//   32768, 2048  1024 300 -> 313, 1408 369 -> 375, 1664 421 -> 420 | 2048 508 -> 497, 2816 677 -> 647
+//   32768, 4096  512 352 -> 368, 704 435 -> 454 | 1024 527 -> 541, 1408 656 -> 649, 2048 921 -> 905
+//   65536, 1024  1024 351 -> 360, 1408 453 -> 458 | 2048 633 -> 609
+//   65536, 2048  512 380 -> 383, 704 469 -> 478 | 1024 581 -> 587, 1408 759 -> 732, 2048 1050 -> 973
+//   65536*, 2048 512 434 -> 434, 704 553 -> 529 | 1024 691 -> 655, 2048 1233 -> 1169
+//   131072, 2048 512 712 -> 713, 704 922 -> 899 | 1024 1162 -> 1117, 2048 2077 -> 1941
 Shape down_shape(const MoeFwdDownArgs& p) {
-  if (p.I >= 1024 && p.H * p.I > int64_t(1) << 22 && p.B >= 256 && p.H >= 256) return {256, 256};
+  if (p.I >= 1024 && p.N * p.B * p.H * p.I >= int64_t(1) << 37 && p.B >= 256 && p.H >= 256) return {256, 256};
   return {128, 128};
 }
 

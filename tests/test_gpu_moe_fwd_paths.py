@@ -101,12 +101,14 @@ def test_round_robin_tiles_with_a_checkpoint(name):
     _check(p, name)
 
 
-# The down projection's tiles with fp16 rows: 128 x 128 and 256 x 256 (H * I past 2^22), contractions of whole pairs and not
-@pytest.mark.parametrize("H,I,side", [(288, 1024, 128), (288, 1056, 128), (1056, 3968, 128), (2080, 2176, 256), (2080, 2112, 256),
-                                      (256, 16416, 256)])
-def test_down_projection_tiles(H, I, side):
-    p = Problem(T=400, H=H, I=I, E=2, K=1, B=256, dropped=0.1, residual=True, seed=55)
-    assert (256 if I >= 1024 and H * I > 2 ** 22 and H >= 256 else 128) == side and (I < 4096 or I % 128)
+# The down projection's tiles with fp16 rows: 128 x 128, and 256 x 256 from 2^37 products of the whole list on (the blocks
+# behind the layer's own hold no token); contractions of whole pairs and not
+@pytest.mark.parametrize("H,I,N,side", [(288, 1024, 4, 128), (288, 1056, 4, 128), (2080, 2176, 4, 128), (2080, 2176, 120, 256),
+                                        (2080, 2112, 123, 256), (256, 16416, 128, 256), (1056, 1024, 500, 256)])
+def test_down_projection_tiles(H, I, N, side):
+    p = _padded(dict(T=400, H=H, I=I, E=2, K=1, B=256, dropped=0.1, residual=True), N, 55)
+    large = I >= 1024 and H >= 256 and p.N * p.B * H * I >= 2 ** 37
+    assert large == (side == 256) and (I < 4096 or I % 128)
     y, dy, _ = p.exact()
     check_rows(_run(p)["out"], y, dy, (H, I))
 
