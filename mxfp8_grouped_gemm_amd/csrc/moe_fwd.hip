@@ -15,9 +15,12 @@ namespace {
 bool fwd_few_tiles(int64_t I, int64_t N, int64_t B) { return N * (B / 128) * ((I + 127) / 128 * 2) <= 512; }
 // The tile's side: 256 from contractions and blocks that are long enough for one workgroup a CU
 // (H = 4096: 3.6 ms against 5.1 at 128; H = 2048: 290 us against 308), else 128, two workgroups a CU
-// (blocks of 128 slots, H = 1536: 390 us against 420 at 256 x 128).
+// (blocks of 128 slots, H = 1536: 390 us against 420 at 256 x 128).  The whole forward of 32768 slots at 128 -> 256 in us,
+// in brackets of 131072: H = 1024: I = 512 123 -> 137 (395 -> 418), 1408 229 -> 248 (793 -> 874), 8192 1000 -> 1058
+// (3839 -> 4062); H = 1280: I = 1408 266 -> 276 (968 -> 1018); H = 1536: 165 -> 173 (571 -> 566), 322 -> 316 (1158 -> 1141),
+// 1439 -> 1402 (5588 -> 5363); H = 2048: 202 -> 209 (734 -> 705), 400 -> 372 (1536 -> 1412).
 int fwd_side(int64_t H, int64_t I, int64_t N, int64_t B) {
-  return I < 128 || B < 256 || H < 1024 || fwd_few_tiles(I, N, B) ? 128 : 256;
+  return I < 128 || B < 256 || H < 1536 || fwd_few_tiles(I, N, B) ? 128 : 256;
 }
 }  // namespace
 

@@ -19,7 +19,7 @@ def _few_tiles(p):
 
 def _side(p):
     """A gate/up tile's side."""
-    return 128 if p.I < 128 or p.B < 256 or p.H < 1024 or _few_tiles(p) else 256
+    return 128 if p.I < 128 or p.B < 256 or p.H < 1536 or _few_tiles(p) else 256
 
 
 def _padded(args, N, seed):
@@ -57,7 +57,7 @@ def _check(p, what):
 def test_scaled_kernels(side, ragged, geglu):
     """The scaled MFMA at both tile sides, contractions of whole pairs and not, both activations, every checkpoint."""
     if side == 256:
-        p = _padded(dict(T=300, H=1056 if ragged else 1024, I=416 if ragged else 384, E=3, K=2, B=512 if ragged else 256,
+        p = _padded(dict(T=300, H=1568 if ragged else 1536, I=416 if ragged else 384, E=3, K=2, B=512 if ragged else 256,
                          dropped=0.1, geglu=geglu, bias=not ragged), 60, 51)
     else:
         p = _padded(dict(T=200, H=608 if ragged else 384, I=224 if ragged else 256, E=4, K=2, B=128, dropped=0.1, geglu=geglu,
@@ -69,7 +69,7 @@ def test_scaled_kernels(side, ragged, geglu):
 def test_blocks_that_are_full_partly_filled_and_empty():
     """256 x 256 tiles in blocks of four: all live, some, none, in this order and mixed."""
     idx = np.concatenate([np.full(90, 0), np.full(700, 1), np.full(1030, 2), np.full(40, -1)]).astype(np.int32)[:, None]
-    p = _padded(dict(T=len(idx), H=1024, I=256, E=4, K=1, B=1024, idx=idx), 20, 53)
+    p = _padded(dict(T=len(idx), H=1536, I=256, E=4, K=1, B=1024, idx=idx), 20, 53)
     assert _side(p) == 256
     _check(p, "blocks")
 
