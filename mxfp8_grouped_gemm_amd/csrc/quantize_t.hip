@@ -11,6 +11,10 @@
 // 32-byte pieces.  Loads and stores go through the caches: nontemporal loads cost rows
 // that start inside a line a quarter (1184 x 2116: 41 -> 52 us) and the others a tenth,
 // nontemporal stores 3 us of the 48.
+// Widths that are no whole lines cost by the lines that a tile's 256-byte pieces of a row
+// touch, three in place of two: 22 x 1184 x 2176 31 us, 5.6 TB/s, 2116 36, 4.6, and 2115 42, 4.0,
+// where every other row is shifted by half a word besides (rows of whole lines in the
+// result, 1280 for 1184, change neither).
 #include <type_traits>
 
 #include "kernels.hpp"
@@ -45,7 +49,7 @@ __global__ void __launch_bounds__(256) quantize_t_kernel(const uint16_t* __restr
     }
   } else if (int64_t(blockIdx.x) + 1 < gridDim.x) {
     // odd C: every other row's pairs straddle two words, the second of which is the next lane's first
-    // (22 matrices of 1184 x 2115: 47 us, 75 with 2-byte loads).  A word may reach past the tile, not past x:
+    // (22 matrices of 1184 x 2115: 42 us, 75 with 2-byte loads).  A word may reach past the tile, not past x:
     // the last tile takes the other way.
     const uint32_t* words = reinterpret_cast<const uint32_t*>(x);
     if (r0 < R) {   // whole waves
