@@ -784,10 +784,11 @@ int moe_fwd_mxfp8(const moe_fwd_mxfp8_args* args, void* workspace, size_t worksp
  * g and u are summed on the bf16 MFMA from the codes' exact values, the down
  * projection on the scaled fp8 MFMA, all in fp32; otherwise rounded as in moe_fwd_mxfp8.
  * An expert's weights are read once for every 32 of its selections (64 where T * K is above
- * 16 * E).  With block lists at hand moe_fwd_mxfp8 is the faster form where every expert has many: from T = 64 on with
- * 16 experts of H = 2048, I = 1408, top-4 (53 against 52 us; T = 256 92 against 54), from 192 on
- * with 8 of H = 4096, I = 14336, top-2 (393 against 375; T = 128 356 against 370, T = 256 682
- * against 378), and up to 256 tokens not with 128 of H = 1536, I = 256, top-8 (53 against 68).
+ * 16 * E).  With block lists at hand moe_fwd_mxfp8 is the faster form where every expert has
+ * many: from T = 64 on with 16 experts of H = 2048, I = 1408, top-4 (53 against 52 us; T = 256
+ * 92 against 54), from 192 on with 8 of H = 4096, I = 14336, top-2 (393 against 375; T = 128 356
+ * against 370, T = 256 682 against 378), and up to 256 tokens not with 128 of H = 1536, I = 256,
+ * top-8 (53 against 68).
  * Arguments (moe_tokens_fwd_mxfp8_args):
  *   T <= MOE_TOKENS_FWD_MAX_TOKENS, 1 <= K <= MXFP8_ROUTER_MAX_K.
  *   hidden_states [T,H] bf16; topk_idx [T,K] int32, topk_scores [T,K] fp32.

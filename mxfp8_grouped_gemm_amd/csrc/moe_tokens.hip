@@ -4,7 +4,8 @@
 // Bound by the bytes of the selected experts' weights: an expert has a handful
 // of rows, so a product is a stream of weights past a few columns.  They are read
 // once where an expert has no more pairs than a workgroup has columns (`columns`:
-// 32, or 64 from an average of 16 on), and once more for every further so many.  Selections ("pairs" t * K + k) keep their index as row of every
+// 32, or 64 from an average of 16 on), and once more for every further so many.
+// Selections ("pairs" t * K + k) keep their index as row of every
 // intermediate.  A tile is 64 weight rows of one expert (32 gate rows and the
 // same 32 up rows; or 64 rows of the down projection) times up to NCOL of the
 // expert's pairs.  Each wave streams whole 128-byte lines of weight rows
