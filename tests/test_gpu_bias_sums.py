@@ -52,3 +52,24 @@ def test_repeated_runs_give_the_same_bits(name):
             assert np.array_equal(v.view(np.int32), sums[k].view(np.int32)), k
         for k, v in first.items():
             assert torch.equal(again[k].view(torch.int16), v.view(torch.int16)), k
+
+
+@pytest.mark.parametrize("name", CFGS)
+def test_accumulated_gradients_leave_the_sums_alone(name):
+    """With accumulate the regions hold this call's sums, and the outputs what they held plus those, rounded once."""
+    cfg = CFGS[name]
+    op = gpu_problem(cfg)["op"]
+    op.run()
+    sums = _sums(op, cfg)
+    g = torch.Generator("cuda").manual_seed(1)
+    for v in op.out.values():
+        if v is not None:
+            v.copy_(torch.randn(v.shape, generator=g, device="cuda"))
+    before = {k: op.out[k].cpu().reshape(-1).float() for k in sums}
+    op.args.accumulate = 1
+    op.workspace.fill_(0xC3)
+    op.run()
+    for k, v in _sums(op, cfg).items():
+        assert np.array_equal(v.view(np.int32), sums[k].view(np.int32)), k
+        want = (before[k] + torch.from_numpy(v)).to(torch.bfloat16)
+        assert torch.equal(op.out[k].cpu().reshape(-1).view(torch.int16), want.view(torch.int16)), k
